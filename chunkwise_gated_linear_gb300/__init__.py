@@ -22,3 +22,15 @@ from .kda import (  # noqa: F401
     lib,
     status_string,
 )
+from .mixer import (  # noqa: F401
+    block_norm_bwd,
+    block_norm_fwd,
+    causal_conv_bwd,
+    causal_conv_fwd,
+    causal_conv_step,
+    gated_norm_bwd,
+    gated_norm_fwd,
+    selective_scan_bwd,
+    selective_scan_fwd,
+    selective_scan_step,
+)

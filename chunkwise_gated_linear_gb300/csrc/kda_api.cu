@@ -183,6 +183,12 @@ int run_recurrent(const kda_fwd_params *p, const kda_frontend *fe, cudaStream_t 
 
 }  // namespace
 
+namespace kda {
+// for the entry points in other files
+cudaError_t device_error_word(unsigned int **out) { return device_error_ptr(out); }
+int status_of_cuda(cudaError_t e) { return status_of(e); }
+}  // namespace kda
+
 extern "C" {
 
 int kda_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

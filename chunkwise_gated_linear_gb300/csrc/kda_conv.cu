@@ -1,0 +1,472 @@
+// Short causal depthwise convolution and its gradient (kda_mixer.h: kda_conv_*).
+//
+//   y_t = act(b + sum_j w_j x_{t-W+1+j}),   W = 2..4 taps per channel,
+//
+// x before a sequence's first token being its initial state. One thread takes V neighbouring
+// channels through a tile of rows with the last W - 1 inputs in registers, so that each
+// input is read once (plus W - 1 rows per tile) and every access is V contiguous elements.
+// Tiles are cut over the rows of all sequences together: where a sequence ends inside
+// a tile its window is refilled from the next one's initial state, so ragged packed batches need
+// no table of tiles.
+//
+// Bound by memory: 2 bytes in and 2 out per bf16 element; about ten instructions per element,
+// under half of what the SMs issue in that time.
+#include "mixer_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace mix;
+
+constexpr int kConvThreads = 128;
+
+struct ConvArgs {
+    const void *x;
+    const float *w, *bias;
+    const void *s0;
+    void *y, *st;
+    const void *dy, *dst;
+    void *dx, *ds0;
+    float *partial;  // per tile: dweight [D][W], then dbias [D]
+    int64_t xs;      // elements between rows of x
+    int D, tile, silu;
+    int64_t tiles;
+    Seqs seqs;
+    unsigned int *err;
+};
+
+// The window before row r of a sequence: rows r - (W-1) .. r - 1, those before the sequence's
+// start from its initial state.
+template <typename T, int V, int W>
+__device__ __forceinline__ void fill_window(const ConvArgs &a, const SeqAt &at, int64_t r, int64_t c, float (&win)[W][V]) {
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        const int64_t pos = r - (W - 1) + i;
+        const int64_t slot = W - 1 + pos - at.start;  // >= 0 since r >= start
+        if (pos >= at.start)
+            load_vec<T, V>(win[i], static_cast<const T *>(a.x) + pos * a.xs + c);
+        else if (a.s0 != nullptr)
+            load_vec<T, V>(win[i], static_cast<const T *>(a.s0) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
+        else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) win[i][v] = 0.f;
+        }
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void copy_state(const void *from, void *to, int64_t at) {
+    Raw<T, V> r;
+    if (from != nullptr)
+        r.load(static_cast<const T *>(from) + at);
+    else
+        r.zero();
+    r.store(static_cast<T *>(to) + at);
+}
+
+constexpr int kBatch = 4;  // rows whose loads are issued together
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvArgs a) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
+    const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
+    if (c >= a.D) return;
+    // empty sequences keep their state; the tiles share them out
+    if (a.st != nullptr)
+        for (int64_t s = blockIdx.x; s < a.seqs.N; s += gridDim.x)
+            if (seq_empty(a.seqs, (int)s)) {
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) copy_state<T, V>(a.s0, a.st, (s * (W - 1) + i) * a.D + c);
+            }
+    const int64_t r0 = (int64_t)blockIdx.x * a.tile;
+    const int64_t r1 = r0 + a.tile < a.seqs.rows ? r0 + a.tile : a.seqs.rows;
+    if (r0 >= r1) return;
+
+    float w[W][V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        b[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][v] = a.w[(c + v) * W + j];
+    }
+    SeqAt at = seq_find(a.seqs, r0);
+    float win[W][V];
+    fill_window<T, V, W>(a, at, r0, c, win);
+
+    const T *x = static_cast<const T *>(a.x) + c;
+    T *y = static_cast<T *>(a.y) + c;
+    for (int64_t rb = r0; rb < r1; rb += kBatch) {
+        Raw<T, V> in[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (rb + i < r1) in[i].load(x + (rb + i) * a.xs);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t r = rb + i;
+            if (r >= r1) break;
+            if (r == at.end) {
+                seq_next(a.seqs, at);
+                fill_window<T, V, W>(a, at, r, c, win);
+            }
+            in[i].unpack(win[W - 1]);
+            float out[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float s = b[v];
+#pragma unroll
+                for (int j = 0; j < W; ++j) s = fmaf(w[j][v], win[j][v], s);
+                out[v] = SILU ? s * sigmoid(s) : s;
+            }
+            store_vec<T, V>(y + r * a.D, out);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
+            if (r + 1 == at.end && a.st != nullptr) {
+                T *st = static_cast<T *>(a.st) + (int64_t)at.s * (W - 1) * a.D + c;
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    float keep[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) keep[v] = win[j][v];
+                    store_vec<T, V>(st + (int64_t)j * a.D, keep);
+                }
+            }
+        }
+    }
+}
+
+// Gradient. With p_t the sum before the activation and g_t = dy_t act'(p_t),
+//   dx_p = sum_k g_{p+k} w_{W-1-k}   over the tokens p + k of the same sequence,
+//   dw_j = sum_t g_t x_{t-W+1+j},  db = sum_t g_t,
+// and the same sum gives ds0 at the W - 1 positions before the sequence; dst is added at
+// the positions that the final state holds. The thread walks its tile and W - 1 rows more with
+// the windows of x and g in registers and finishes position q - (W-1) at row q; where
+// a sequence ends, the open positions are finished with zeros.
+template <typename T, int V, int W>
+struct ConvBack {
+    const ConvArgs &a;
+    int64_t c, r0, r1;
+    float w[W][V], g[W][V];
+
+    __device__ __forceinline__ ConvBack(const ConvArgs &args) : a(args) {}
+    __device__ __forceinline__ void shift() {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[j][v] = g[j + 1][v];
+    }
+    // finish position p; `slot` of the final state holds it when slot >= 0
+    __device__ __forceinline__ void finish(const SeqAt &at, int64_t p, int slot) const {
+        const bool token = p >= at.start;
+        if (token ? (p < r0 || p >= r1) : (at.start < r0 || a.ds0 == nullptr)) return;
+        float s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = 0.f;
+        if (slot >= 0 && a.dst != nullptr)
+            load_vec<T, V>(s, static_cast<const T *>(a.dst) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = fmaf(g[k][v], w[W - 1 - k][v], s[v]);
+        T *to = token ? static_cast<T *>(a.dx) + p * a.D + c
+                      : static_cast<T *>(a.ds0) + ((int64_t)at.s * (W - 1) + (W - 1 + p - at.start)) * a.D + c;
+        store_vec<T, V>(to, s);
+    }
+    // the sequence has ended: its last W - 1 positions
+    __device__ __forceinline__ void flush(const SeqAt &at) {
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            shift();
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[W - 1][v] = 0.f;
+            finish(at, at.end - W + k, k - 1);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[j][v] = 0.f;
+    }
+};
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
+    const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
+    if (c >= a.D) return;
+    if (a.ds0 != nullptr)
+        for (int64_t s = blockIdx.x; s < a.seqs.N; s += gridDim.x)
+            if (seq_empty(a.seqs, (int)s)) {
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) copy_state<T, V>(a.dst, a.ds0, (s * (W - 1) + i) * a.D + c);
+            }
+    ConvBack<T, V, W> k(a);
+    k.c = c;
+    k.r0 = (int64_t)blockIdx.x * a.tile;
+    k.r1 = k.r0 + a.tile < a.seqs.rows ? k.r0 + a.tile : a.seqs.rows;
+    float b[V], dw[W][V], db[V], win[W][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        b[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
+        db[v] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            k.w[j][v] = a.w[(c + v) * W + j];
+            k.g[j][v] = dw[j][v] = 0.f;
+        }
+    }
+    if (k.r0 < k.r1) {
+        const int64_t qend = k.r1 + W - 1 < a.seqs.rows ? k.r1 + W - 1 : a.seqs.rows;
+        SeqAt at = seq_find(a.seqs, k.r0);
+        fill_window<T, V, W>(a, at, k.r0, c, win);
+        const T *x = static_cast<const T *>(a.x) + c;
+        const T *dy = static_cast<const T *>(a.dy) + c;
+        bool open = true;  // false once the last sequence with rows in the tile has been finished
+        for (int64_t qb = k.r0; qb < qend && open; qb += kBatch) {
+            Raw<T, V> in[kBatch], gr[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (qb + i < qend) {
+                    in[i].load(x + (qb + i) * a.xs);
+                    gr[i].load(dy + (qb + i) * a.D);
+                }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t q = qb + i;
+                if (q >= qend || !open) break;
+                if (q == at.end) {
+                    k.flush(at);
+                    if (q >= k.r1) {
+                        open = false;
+                        break;
+                    }
+                    seq_next(a.seqs, at);
+                    fill_window<T, V, W>(a, at, q, c, win);
+                }
+                in[i].unpack(win[W - 1]);
+                float gq[V];
+                gr[i].unpack(gq);
+                k.shift();
+                const bool mine = q < k.r1;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (SILU) {
+                        float s = b[v], val, der;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], win[j][v], s);
+                        act_both(s, true, val, der);
+                        gq[v] *= der;
+                    }
+                    k.g[W - 1][v] = gq[v];
+                    if (mine) {
+                        db[v] += gq[v];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gq[v], win[j][v], dw[j][v]);
+                    }
+                }
+                k.finish(at, q - (W - 1), -1);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
+            }
+        }
+        if (open && qend == at.end) k.flush(at);
+    }
+    float *part = a.partial + (int64_t)blockIdx.x * ((int64_t)a.D * (W + 1));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) part[(c + v) * W + j] = dw[j][v];
+        part[(int64_t)a.D * W + c + v] = db[v];
+    }
+}
+
+template <typename T, int V, int W>
+cudaError_t conv_launch(const ConvArgs &a, bool bwd, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.tiles, (unsigned)ceil_div(ceil_div(a.D, V), kConvThreads));
+    if (bwd) {
+        if (a.silu)
+            conv_bwd_kernel<T, V, W, true><<<grid, kConvThreads, 0, stream>>>(a);
+        else
+            conv_bwd_kernel<T, V, W, false><<<grid, kConvThreads, 0, stream>>>(a);
+    } else if (a.silu) {
+        conv_fwd_kernel<T, V, W, true><<<grid, kConvThreads, 0, stream>>>(a);
+    } else {
+        conv_fwd_kernel<T, V, W, false><<<grid, kConvThreads, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t conv_width(const ConvArgs &a, int W, bool bwd, cudaStream_t stream) {
+    if (W == 4) return conv_launch<T, V, 4>(a, bwd, stream);
+    if (W == 3) return conv_launch<T, V, 3>(a, bwd, stream);
+    return conv_launch<T, V, 2>(a, bwd, stream);
+}
+
+// V channels per thread when every row of every tensor lets V elements be read at once
+// (V * sizeof(T) aligned rows and pointers), one channel otherwise.
+cudaError_t conv_dispatch(const ConvArgs &a, int dtype, int W, bool bwd, int V, cudaStream_t stream) {
+    if (dtype == KDA_DTYPE_BF16) {
+        if (V == 8) return conv_width<bf16, 8>(a, W, bwd, stream);
+        if (V == 4) return conv_width<bf16, 4>(a, W, bwd, stream);
+        return conv_width<bf16, 1>(a, W, bwd, stream);
+    }
+    if (V == 4) return conv_width<float, 4>(a, W, bwd, stream);
+    return conv_width<float, 1>(a, W, bwd, stream);
+}
+
+int elem_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
+
+// Checks shared by the three entry points.
+int conv_check(const void *x, const float *weight, const float *bias, const void *s0, int64_t stride, int B, int T, int D, int W,
+               const int32_t *cu, int dtype, int activation) {
+    if (B < 1 || T < 0 || D < 1 || stride < 0 || (stride != 0 && stride < D)) return KDA_ERR_INVALID_ARG;
+    if (weight == nullptr || (T != 0 && x == nullptr)) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU)) return KDA_ERR_UNSUPPORTED;
+    const int e = elem_size(dtype);
+    if (!aligned(x, e) || !aligned(s0, e) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu, 4)) return KDA_ERR_ALIGNMENT;
+    const int64_t rows = cu != nullptr ? (int64_t)T : (int64_t)B * T;
+    if (rows > INT32_MAX || ceil_div(D, kConvThreads) > 65535) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// The widest V <= most that the sizes and pointers allow.
+int conv_vec(int dtype, int D, int64_t xs, int most, const void *const *ptrs, int n) {
+    const int e = elem_size(dtype);
+    for (int V = most; V > 1; V /= 2) {
+        if (V == 2 || (dtype == KDA_DTYPE_F32 && V > 4)) continue;
+        bool ok = D % V == 0 && xs % V == 0;
+        for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], (size_t)V * e);
+        if (ok) return V;
+    }
+    return 1;
+}
+
+// Rows per tile: enough tiles for `per_sm` blocks on every SM, between 8 rows (below that the
+// W - 1 rows read again weigh more than the parallelism gains) and `most`.
+int conv_tile(int64_t rows, int64_t chan_blocks, int per_sm, int most) {
+    const int64_t want = ceil_div((int64_t)per_sm * (sm_count() > 0 ? sm_count() : 1), chan_blocks);
+    int64_t tile = ceil_div(rows, want);
+    tile = tile < 8 ? 8 : (tile > most ? most : tile);
+    return (int)ceil_div(tile, kBatch) * kBatch;
+}
+
+int conv_run(const kda_conv_params &p, bool step, cudaStream_t stream) {
+    int st = conv_check(p.x, p.weight, p.bias, p.s0, p.x_stride, p.B, p.T, p.D, p.W, p.cu_seqlens, p.dtype, p.activation);
+    if (st != KDA_OK) return st;
+    if (p.T != 0 && p.y == nullptr) return KDA_ERR_INVALID_ARG;
+    if (step && (p.cu_seqlens != nullptr || p.s0 == nullptr || p.st == nullptr)) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(p.dtype);
+    if (!aligned(p.y, e) || !aligned(p.st, e)) return KDA_ERR_ALIGNMENT;
+    ConvArgs a{};
+    a.x = p.x;
+    a.w = p.weight;
+    a.bias = p.bias;
+    a.s0 = p.s0;
+    a.y = p.y;
+    a.st = p.st;
+    a.xs = p.x_stride != 0 ? p.x_stride : p.D;
+    a.D = p.D;
+    a.silu = p.activation == KDA_ACT_SILU;
+    a.seqs = Seqs{p.cu_seqlens, p.B, p.T, p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.B * p.T};
+    const cudaError_t e1 = device_error_word(&a.err);
+    if (e1 != cudaSuccess) return status_of_cuda(e1);
+    const void *ptrs[] = {p.x, p.s0, p.y, p.st};
+    const int V = conv_vec(p.dtype, p.D, a.xs, 8, ptrs, 4);
+    if (step) {
+        a.tile = p.T > 0 ? p.T : 1;  // one sequence per tile: its state is read and written by the same threads
+        a.tiles = p.B;
+    } else {
+        a.tile = conv_tile(a.seqs.rows, ceil_div(ceil_div(p.D, V), kConvThreads), 16, 64);
+        a.tiles = ceil_div(a.seqs.rows, a.tile);
+        if (a.tiles < 1) a.tiles = 1;
+    }
+    return status_of_cuda(conv_dispatch(a, p.dtype, p.W, false, V, stream));
+}
+
+struct ConvBwdPlan {
+    int V, tile;
+    int64_t tiles;
+    size_t bytes;
+};
+ConvBwdPlan conv_bwd_plan(const kda_conv_bwd_params &p) {
+    ConvBwdPlan q;
+    const void *ptrs[] = {p.x, p.s0, p.dy, p.dst, p.dx, p.ds0};
+    const int64_t rows = p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.B * p.T;
+    q.V = conv_vec(p.dtype, p.D, p.x_stride != 0 ? p.x_stride : p.D, 4, ptrs, 6);
+    q.tile = conv_tile(rows, ceil_div(ceil_div(p.D, q.V), kConvThreads), 16, 256);
+    q.tiles = ceil_div(rows, q.tile);
+    if (q.tiles < 1) q.tiles = 1;
+    q.bytes = (size_t)q.tiles * p.D * (p.W + 1) * sizeof(float);
+    return q;
+}
+
+int conv_bwd_check(const kda_conv_bwd_params &p) {
+    int st = conv_check(p.x, p.weight, p.bias, p.s0, p.x_stride, p.B, p.T, p.D, p.W, p.cu_seqlens, p.dtype, p.activation);
+    if (st != KDA_OK) return st;
+    if (p.dweight == nullptr || (p.T != 0 && (p.dy == nullptr || p.dx == nullptr))) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(p.dtype);
+    if (!aligned(p.dy, e) || !aligned(p.dst, e) || !aligned(p.dx, e) || !aligned(p.ds0, e) || !aligned(p.dweight, 4) ||
+        !aligned(p.dbias, 4))
+        return KDA_ERR_ALIGNMENT;
+    return KDA_OK;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+int kda_conv_fwd(const kda_conv_params *p, cudaStream_t stream) {
+    return p == nullptr ? KDA_ERR_INVALID_ARG : kda::conv_run(*p, false, stream);
+}
+
+int kda_conv_step(const kda_conv_params *p, cudaStream_t stream) {
+    return p == nullptr ? KDA_ERR_INVALID_ARG : kda::conv_run(*p, true, stream);
+}
+
+size_t kda_conv_bwd_workspace(const kda_conv_bwd_params *p) {
+    return p == nullptr || kda::conv_bwd_check(*p) != KDA_OK ? 0 : kda::conv_bwd_plan(*p).bytes;
+}
+
+int kda_conv_bwd(const kda_conv_bwd_params *p, cudaStream_t stream) {
+    using namespace kda;
+    if (p == nullptr) return KDA_ERR_INVALID_ARG;
+    const int st = conv_bwd_check(*p);
+    if (st != KDA_OK) return st;
+    const ConvBwdPlan q = conv_bwd_plan(*p);
+    if (p->workspace != nullptr && p->workspace_bytes < q.bytes) return KDA_ERR_INVALID_ARG;
+    if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;
+    ConvArgs a{};
+    a.x = p->x;
+    a.w = p->weight;
+    a.bias = p->bias;
+    a.s0 = p->s0;
+    a.dy = p->dy;
+    a.dst = p->dst;
+    a.dx = p->dx;
+    a.ds0 = p->ds0;
+    a.xs = p->x_stride != 0 ? p->x_stride : p->D;
+    a.D = p->D;
+    a.silu = p->activation == KDA_ACT_SILU;
+    a.tile = q.tile;
+    a.tiles = q.tiles;
+    a.seqs = Seqs{p->cu_seqlens, p->B, p->T, p->cu_seqlens != nullptr ? (int64_t)p->T : (int64_t)p->B * p->T};
+    cudaError_t e = device_error_word(&a.err);
+    if (e != cudaSuccess) return status_of_cuda(e);
+    Scratch ws;
+    e = ws.get(p->workspace, q.bytes, stream);
+    if (e != cudaSuccess) return status_of_cuda(e);
+    a.partial = static_cast<float *>(ws.ptr);
+    e = conv_dispatch(a, p->dtype, p->W, true, q.V, stream);
+    if (e == cudaSuccess) {
+        const SumOuts outs{{p->dweight, p->dbias, nullptr, nullptr}, {(int64_t)p->D * p->W, p->D, 0, 0}};
+        e = launch_sum_partials(a.partial, q.tiles, (int64_t)p->D * (p->W + 1), outs, stream);
+    }
+    return status_of_cuda(ws.release(e));
+}
+
+}  // extern "C"

@@ -1,0 +1,158 @@
+// What the forward and backward kernels of the selective scan share: arguments, the tile of
+// tokens in shared memory, step sizes, and the split of the tokens into chunks.
+//
+// Layout of a block: 256 threads take 64 channels; channel dl = tid / 4 is shared by four
+// neighbouring lanes, lane nl = tid % 4 holding states nl NP .. nl NP + NP - 1 of it (NP = 2, 4,
+// 8, 16: the smallest that holds N; the rest are zero states that stay zero).
+#pragma once
+
+#include "mixer_common.cuh"
+
+namespace kda {
+namespace scan {
+
+using namespace mix;
+
+constexpr int kThreads = 256;
+constexpr int kDB = 64;   // channels per block
+constexpr int kLN = 4;    // lanes that share a channel
+constexpr int kTK = 32;   // tokens per tile
+constexpr int kMaxN = 64;
+
+struct ScanArgs {
+    const void *u, *dt;
+    const float *A;
+    const void *B, *C;
+    const float *D;
+    const void *z;
+    const float *bias, *h0;
+    void *y;
+    float *ht;
+    int64_t us, dts, bs, cs, zs;  // elements between tokens
+    int ch, N, G, chg;            // channels, states, groups, channels per group
+    int blocks_per_group;
+    int softplus;
+    int vec;                      // every 8 channels of u, dt, z, y lie on 16 bytes
+    Seqs seqs;
+    int64_t chunk;                // rows per chunk (all sequences' rows together); 0: one block per sequence
+    int64_t nchunks;
+    float *hchunk;                // [nchunks][ch][N]: a chunk's end state, then the state it starts from
+    float *schunk;                // [nchunks][ch]: sum of the step sizes in a chunk
+    unsigned int *err;
+};
+
+inline int np_of(int N) { return N <= 8 ? 2 : (N <= 16 ? 4 : (N <= 32 ? 8 : 16)); }
+
+// A block's channels: group g, the first channel, and how many of the 64 exist.
+struct Chans {
+    int g, d0, n;
+};
+__device__ __forceinline__ Chans chans_of(const ScanArgs &a, int block) {
+    Chans c;
+    c.g = block / a.blocks_per_group;
+    const int first = (block % a.blocks_per_group) * kDB;
+    c.d0 = c.g * a.chg + first;
+    c.n = a.chg - first < kDB ? a.chg - first : kDB;
+    return c;
+}
+
+// 8 channels of one token, zeros where there are none
+template <typename T>
+__device__ __forceinline__ void load8(Raw<T, 8> &r, const void *base, int64_t at, int n, bool vec) {
+    const T *p = static_cast<const T *>(base) + at;
+    if (vec && n >= 8)
+        r.load(p);
+    else if (n > 0)
+        r.load_some(p, n);
+    else
+        r.zero();
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, int64_t at, const float (&f)[8], int n, bool vec) {
+    Raw<T, 8> r;
+    r.pack(f);
+    T *p = static_cast<T *>(base) + at;
+    if (vec && n >= 8)
+        r.store(p);
+    else if (n > 0)
+        r.store_some(p, n);
+}
+
+// Step size from dt + dt_bias. In fp32 by CUDA's log1pf and expf; for bf16 inputs, whose own
+// rounding is 2^-8, on the special-function unit and a polynomial (relative error under 1e-6).
+template <typename T>
+__device__ __forceinline__ float step_of(float s, bool softplus) {
+    if (!softplus) return s;
+    if constexpr (sizeof(T) == 4)
+        return softplus_f(s);
+    else
+        return tcu::softplus_fast(s);
+}
+
+// The four per-step sums p[0..3] of a lane, added over the kLN lanes of a channel: lane nl
+// returns the total of step nl. Three exchanges instead of the eight of four butterflies.
+__device__ __forceinline__ float sum_lanes(const float (&p)[4], int nl) {
+    const bool hi = nl & 2, odd = nl & 1;
+    const float a0 = hi ? p[0] : p[2], a1 = hi ? p[1] : p[3];
+    float b0 = hi ? p[2] : p[0], b1 = hi ? p[3] : p[1];
+    b0 += __shfl_xor_sync(0xffffffffu, a0, 2);
+    b1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+    const float s = odd ? b0 : b1, k = odd ? b1 : b0;
+    return k + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+
+// The states of channel d at `at` (of [..][ch][N]) for this lane, zeros past N and for no channel.
+template <int NP>
+__device__ __forceinline__ void load_states(float (&h)[NP], const float *base, int64_t at, int nl, int N, bool live) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int n = nl * NP + i;
+        h[i] = live && n < N ? base[at + n] : 0.f;
+    }
+}
+template <int NP>
+__device__ __forceinline__ void store_states(const float (&h)[NP], float *base, int64_t at, int nl, int N, bool live) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int n = nl * NP + i;
+        if (live && n < N) base[at + n] = h[i];
+    }
+}
+template <int NP>
+__device__ __forceinline__ void to_pairs(f2 (&p)[NP / 2], const float (&h)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) p[i] = pk(h[2 * i], h[2 * i + 1]);
+}
+template <int NP>
+__device__ __forceinline__ void from_pairs(float (&h)[NP], const f2 (&p)[NP / 2]) {
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) upk(p[i], h[2 * i], h[2 * i + 1]);
+}
+// NP floats of shared memory as pairs (8 or 16 bytes at a time)
+template <int NP>
+__device__ __forceinline__ void lds_pairs(f2 (&p)[NP / 2], const float *s) {
+    if constexpr (NP == 2) {
+        p[0] = *reinterpret_cast<const f2 *>(s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(s + 4 * i);
+            p[2 * i] = q.x;
+            p[2 * i + 1] = q.y;
+        }
+    }
+}
+
+// Slot of channel d (0..63) in a row of 64: rotated inside groups of 8 so that eight lanes
+// which write eight groups' same channel use different banks.
+__device__ __forceinline__ int slot_of(int d) { return (d & ~7) | ((d ^ (d >> 3)) & 7); }
+
+// ---- host ------------------------------------------------------------------------------------
+int scan_check(const kda_scan_params &p);
+// Arguments without chunk buffers and error word. `vec` covers u, dt, z and the given pointers.
+ScanArgs scan_args(const kda_scan_params &p, const void *const *more, int n);
+cudaError_t launch_scan_summary(const ScanArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_scan_carry(const ScanArgs &a, cudaStream_t stream);
+
+}  // namespace scan
+}  // namespace kda
