@@ -4,20 +4,24 @@
 //
 // per channel, so T x channels x N elements, each an exponential, two products and two
 // multiply-adds. No matrix product is hidden in it: the decay differs for every (t, channel,
-// state). On this GPU an SM does 32 exponentials and 128 fp32 multiply-adds per clock, so both
-// pipes allow 32 elements per clock and SM; reading u, dt, z and writing y takes
-// about as long (N = 16, bf16). The kernels are built to keep both pipes fed:
-//   - states stay in registers, four lanes per channel (enough threads without cutting T);
+// state). An SM does 32 exponentials and 128 fp32 multiply-adds per clock (measured), so both pipes
+// allow 32 elements per clock and SM; issuing an instruction per warp and clock on each of its
+// four schedulers allows 128 / (instructions per element). The layout is chosen for few
+// instructions and little shared-memory traffic per element:
+//   - a thread owns two neighbouring channels and up to 16 states of each in registers. B_t and C_t,
+//     the same for all channels of a group, come from shared memory once for 32 elements: 4
+//     bytes per element where the SM delivers 128 bytes per clock. (One channel and four states per
+//     thread, its predecessor, took 12 bytes per element and was bound by that at a third of the speed.)
+//   - no exchange between lanes up to 16 states; 17 to 64 states take 2 or 4 lanes per pair of channels;
 //   - fp32 pairs: two products or multiply-adds per instruction;
-//   - tiles of 32 tokens: step sizes and u are prepared once per (token, channel) by 16-byte
-//     vectors and handed over in shared memory, the next tile's loads are in flight meanwhile;
-//   - the sum over the states of four steps takes three exchanges between lanes.
-// Where channels x sequences fill the GPU, a block walks its sequence from start to end. Where
-// they do not, the rows are cut into chunks: every chunk's end state from a zero start is computed
-// (kSummary), the chunks' start states follow from
+//   - u, dt, z are read from memory by the thread that needs them (a warp reads whole 128-byte rows), four
+//     tokens ahead, and y is written from registers.
+// That is parallel only over channels and sequences. Where these do not fill the GPU, the rows are
+// cut into chunks: every chunk's end state from a zero start is computed (kSummary), the chunks'
+// start states follow from
 //   h_in[c + 1] = exp(A sum delta) h_in[c] + h_end[c]
 // (scan_carry_kernel), and every chunk is walked again with its start state (kChunk). The first
-// walk costs about 0.6 of the second.
+// walk costs about 0.7 of the second.
 #include "scan_common.cuh"
 
 namespace kda {
@@ -27,52 +31,86 @@ namespace {
 
 enum Mode { kWhole, kSummary, kChunk };
 
-// Steps t0 .. t0 + 3 of a tile for this thread's channel and states.
-template <int NP, bool OUT>
-__device__ __forceinline__ void step4(f2 (&h)[NP / 2], const f2 (&A)[NP / 2], const float4 (*sx)[kDB], const float *sB,
-                                      const float *sC, int nt, int t0, int slot, int nl, float (&p)[4]) {
+constexpr int kFThr = 128;      // threads per block
+constexpr int kTile = 32;       // tokens of B and C in shared memory
+// Blocks per SM: 128 registers per thread. 2 x 8192 tokens, 4096 channels, 16 states, bf16: 512 us,
+// with three blocks (168 registers) 542 us, with two 594 us.
+constexpr int kPerSM = 4;
+// Rows per chunk at least: 333 tokens of 2048 channels take 36 us with 12 or 16 rows, 49 us with
+// 32, 78 us with 64 (chunks are walked serially, and there are few).
+constexpr int kMinChunk = 16;
+
+// NS states per thread, LN lanes per pair of channels.
+template <int NS, int LN>
+struct FwdShape {
+    static constexpr int kNT = NS * LN;                 // states held per channel
+    static constexpr int kChan = 2 * kFThr / LN;        // channels per block
+    static constexpr int kBC = 2 * kTile * kNT / kFThr; // B and C elements per thread and tile
+};
+
+// A thread's NS states of a channel, at `at` = first state of [..][N], zeros past N.
+template <int NS>
+__device__ __forceinline__ void get_states(f2 (&h)[NS / 2], const float *base, int64_t at, int n0, int N, bool live, bool vec) {
+    if (live && vec) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int t = t0 + k;
-        const ulonglong2 dx = *reinterpret_cast<const ulonglong2 *>(&sx[t][slot]);  // (delta, delta), (delta u, delta u)
-        f2 B[NP / 2], C[NP / 2];
-        lds_pairs<NP>(B, sB + t * nt + nl * NP);
-        if (OUT) lds_pairs<NP>(C, sC + t * nt + nl * NP);
-        f2 s = 0;
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) {
-            h[i] = fma2(exp2_2(mul2(dx.x, A[i])), h[i], mul2(dx.y, B[i]));
-            if (OUT) s = i == 0 ? mul2(h[0], C[0]) : fma2(h[i], C[i], s);
+        for (int i = 0; i < NS / 4; ++i) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(base + at + n0 + 4 * i);
+            h[2 * i] = q.x;
+            h[2 * i + 1] = q.y;
         }
-        if (OUT) p[k] = hsum2(s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const int n = n0 + 2 * i;
+            h[i] = pk(live && n < N ? base[at + n] : 0.f, live && n + 1 < N ? base[at + n + 1] : 0.f);
+        }
+    }
+}
+template <int NS>
+__device__ __forceinline__ void put_states(const f2 (&h)[NS / 2], float *base, int64_t at, int n0, int N, bool live, bool vec) {
+    if (!live) return;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < NS / 4; ++i)
+            *reinterpret_cast<ulonglong2 *>(base + at + n0 + 4 * i) = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const int n = n0 + 2 * i;
+            float lo, hi;
+            upk(h[i], lo, hi);
+            if (n < N) base[at + n] = lo;
+            if (n + 1 < N) base[at + n + 1] = hi;
+        }
     }
 }
 
-template <typename T, int NP, Mode MODE>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanArgs a) {
+template <typename T, int NS, int LN, Mode MODE>
+__global__ void __launch_bounds__(kFThr, kPerSM) scan_fwd_kernel(const ScanArgs a) {
+    using S = FwdShape<NS, LN>;
     constexpr bool kOut = MODE != kSummary;
-    constexpr int kNT = kLN * NP;                      // states per channel held
-    constexpr int kBC = 2 * kTK * kNT / kThreads;      // B and C elements per thread and tile
-    constexpr int kYRow = kDB + 8;                     // padded: four steps x eight channels hit 32 banks
-    __shared__ __align__(16) float4 sx[kTK][kDB];
-    __shared__ __align__(16) float sB[kTK * kNT];
-    __shared__ __align__(16) float sC[kOut ? kTK * kNT : 4];
-    __shared__ __align__(16) float sy[kOut ? kTK : 1][kYRow];
+    constexpr int P2 = NS / 2;
+    __shared__ __align__(16) float sB[kTile * S::kNT];
+    __shared__ __align__(16) float sC[kOut ? kTile * S::kNT : 4];
 
     const int tid = threadIdx.x;
     const int nblk = a.G * a.blocks_per_group;
-    const Chans ch = chans_of(a, blockIdx.x % nblk);
+    const int blk = blockIdx.x % nblk;
     const int64_t part = blockIdx.x / nblk;  // sequence or chunk
-    if (blockIdx.x == 0 && MODE != kSummary) seq_check(a.seqs, a.err, tid, kThreads);
+    if (blockIdx.x == 0 && MODE != kSummary) seq_check(a.seqs, a.err, tid, kFThr);
 
-    const int dl = tid >> 2, nl = tid & 3, slot = slot_of(dl);
-    const int d = ch.d0 + dl;
-    const bool live = dl < ch.n;
-    const int64_t dn = (int64_t)d * a.N;
+    const int g = blk / a.blocks_per_group;
+    const int first = (blk % a.blocks_per_group) * S::kChan + 2 * (tid / LN);  // within the group
+    const int n0 = (tid % LN) * NS;
+    const int d = g * a.chg + first;
+    const int nch = a.chg - first < 2 ? (a.chg - first > 0 ? 1 : 0) : 2;  // channels that exist: 0, 1, 2
+    const int64_t cn = (int64_t)a.ch * a.N;
+    const int64_t dn0 = (int64_t)d * a.N, dn1 = dn0 + a.N;
+    const bool vst = a.vec_states && a.N == S::kNT;
 
     // rows of this block and the state it starts from
     int64_t c0, c1;
-    SeqAt at;
+    SeqAt at{};
     if (MODE == kWhole) {
         if (a.seqs.cu == nullptr) {
             c0 = part * a.seqs.T;
@@ -90,151 +128,184 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanArgs a) {
         // empty sequences keep their state; the chunks share them out
         if (MODE == kChunk && a.ht != nullptr)
             for (int64_t s = part; s < a.seqs.N; s += a.nchunks)
-                if (seq_empty(a.seqs, (int)s)) {
-                    float keep[NP];
-                    load_states<NP>(keep, a.h0, s * a.ch * a.N + dn, nl, a.N, live && a.h0 != nullptr);
-                    store_states<NP>(keep, a.ht, s * a.ch * a.N + dn, nl, a.N, live);
-                }
+                if (seq_empty(a.seqs, (int)s))
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        f2 keep[P2];
+                        get_states<NS>(keep, a.h0, s * cn + (r ? dn1 : dn0), n0, a.N, r < nch && a.h0 != nullptr, vst);
+                        put_states<NS>(keep, a.ht, s * cn + (r ? dn1 : dn0), n0, a.N, r < nch, vst);
+                    }
         if (c0 >= c1) return;
     }
-    float h[NP], An[NP];
+    f2 h[2][P2], A2[2][P2];
+    auto start = [&](const float *base, int64_t s) {
+        get_states<NS>(h[0], base, s * cn + dn0, n0, a.N, nch > 0 && base != nullptr, vst);
+        get_states<NS>(h[1], base, s * cn + dn1, n0, a.N, nch > 1 && base != nullptr, vst);
+    };
+    auto finish = [&](float *base, int64_t s) {
+        put_states<NS>(h[0], base, s * cn + dn0, n0, a.N, nch > 0, vst);
+        put_states<NS>(h[1], base, s * cn + dn1, n0, a.N, nch > 1, vst);
+    };
     if (c0 == at.start)
-        load_states<NP>(h, a.h0, (int64_t)at.s * a.ch * a.N + dn, nl, a.N, live && a.h0 != nullptr);
+        start(a.h0, at.s);
     else
-        load_states<NP>(h, a.hchunk, part * a.ch * a.N + dn, nl, a.N, live && MODE == kChunk);
-    load_states<NP>(An, a.A, dn, nl, a.N, live);
+        start(MODE == kChunk ? a.hchunk : nullptr, part);
+    get_states<NS>(A2[0], a.A, dn0, n0, a.N, nch > 0, vst);
+    get_states<NS>(A2[1], a.A, dn1, n0, a.N, nch > 1, vst);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) An[i] *= kLog2e;
-    f2 hp[NP / 2], A2[NP / 2];
-    to_pairs<NP>(hp, h);
-    to_pairs<NP>(A2, An);
-
-    // staging: token tr of a tile, channels 8 tc .. 8 tc + 7 of the block
-    const int tr = tid >> 3, tc = (tid & 7) * 8;
-    const int nc = ch.n - tc;  // channels that exist here (may be <= 0)
-    const int64_t dc = ch.d0 + tc;
-    float bias8[8], D8[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        bias8[j] = a.bias != nullptr && j < nc ? a.bias[dc + j] : 0.f;
-        D8[j] = kOut && a.D != nullptr && j < nc ? a.D[dc + j] : 0.f;
+    for (int i = 0; i < P2; ++i) {
+        A2[0][i] = mul2(A2[0][i], pk(kLog2e, kLog2e));
+        A2[1][i] = mul2(A2[1][i], pk(kLog2e, kLog2e));
     }
-    Raw<T, 8> nu, ndt, nz;
-    float nbc[kBC];
-    auto fetch = [&](int64_t t0) {
-        const int64_t r = t0 + tr;
-        const int n = r < c1 ? nc : 0;
-        load8<T>(nu, a.u, r * a.us + dc, n, a.vec);
-        load8<T>(ndt, a.dt, r * a.dts + dc, n, a.vec);
-        if (kOut && a.z != nullptr) load8<T>(nz, a.z, r * a.zs + dc, n, a.vec);
+    auto two = [&](const float *p) {
+        return pk(p != nullptr && nch > 0 ? p[d] : 0.f, p != nullptr && nch > 1 ? p[d + 1] : 0.f);
+    };
+    float bias0, bias1;
+    upk(two(a.bias), bias0, bias1);
+    float D0, D1;
+    upk(two(kOut ? a.D : nullptr), D0, D1);
+    const bool gate = kOut && a.z != nullptr;
+
+    // four tokens of this thread's channels, read ahead; a row's place is the same for all threads
+    Raw<T, 2> nu[4], ndt[4], nz[4];
+    auto fetch = [&](int64_t r0) {
+        const T *pu = static_cast<const T *>(a.u) + r0 * a.us;
+        const T *pd = static_cast<const T *>(a.dt) + r0 * a.dts;
+        const T *pz = static_cast<const T *>(a.z) + r0 * a.zs;
+        if (r0 + 4 <= c1 && a.vec && nch == 2) {
 #pragma unroll
-        for (int k = 0; k < kBC; ++k) {
-            const int e = (tid + k * kThreads) % (kTK * kNT);
-            const bool isC = k >= kBC / 2;  // the first half of the elements is B
-            const int64_t rr = t0 + e / kNT;
-            const int n2 = e % kNT;
-            float v = 0.f;
-            if (rr < c1 && n2 < a.N && (!isC || kOut)) {
-                const void *src = isC ? a.C : a.B;
-                v = to_f(static_cast<const T *>(src)[rr * (isC ? a.cs : a.bs) + (int64_t)ch.g * a.N + n2]);
+            for (int k = 0; k < 4; ++k) {
+                nu[k].load(pu + k * a.us + d);
+                ndt[k].load(pd + k * a.dts + d);
+                if (gate) nz[k].load(pz + k * a.zs + d);
             }
-            nbc[k] = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = r0 + k < c1 ? nch : 0;
+                nu[k].load_some(pu + k * a.us + d, n);
+                ndt[k].load_some(pd + k * a.dts + d, n);
+                if (gate) nz[k].load_some(pz + k * a.zs + d, n);
+            }
         }
     };
-    float sum_delta[8];
+    float nbc[S::kBC];
+    auto fetch_bc = [&](int64_t t0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum_delta[j] = 0.f;
-
-    if (c0 < c1) fetch(c0);
-    for (int64_t t0 = c0; t0 < c1; t0 += kTK) {
-        Raw<T, 8> cu_ = nu, cz = nz;
-        __syncthreads();  // the previous tile has been read
-        {
-            const bool row = t0 + tr < c1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // rows past the end: no step, the state stays
-                const float delta = row && j < nc ? step_of<T>(ndt.get(j) + bias8[j], a.softplus) : 0.f;
-                const float x = delta * cu_.get(j);
-                sx[tr][slot_of(tc + j)] = make_float4(delta, delta, x, x);
-                if (MODE == kSummary) sum_delta[j] += delta;
-            }
-#pragma unroll
-            for (int k = 0; k < kBC; ++k) {
-                const int e = (tid + k * kThreads) % (kTK * kNT);
-                if (k < kBC / 2)
-                    sB[e] = nbc[k];
-                else if (kOut)
-                    sC[e] = nbc[k];
-            }
+        for (int k = 0; k < S::kBC; ++k) {
+            const bool isC = k >= S::kBC / 2;  // the first half of the elements is B
+            const int e = (tid + k * kFThr) % (kTile * S::kNT);
+            const int64_t r = t0 + e / S::kNT;
+            const int n = e % S::kNT;
+            nbc[k] = r < c1 && n < a.N && (!isC || kOut)
+                         ? to_f(static_cast<const T *>(isC ? a.C : a.B)[r * (isC ? a.cs : a.bs) + (int64_t)g * a.N + n])
+                         : 0.f;
         }
-        __syncthreads();
-        if (t0 + kTK < c1) fetch(t0 + kTK);
-
-        const int64_t tile_end = t0 + kTK < c1 ? t0 + kTK : c1;
-        if (at.end >= tile_end) {  // one sequence in the whole tile
-#pragma unroll 2
-            for (int t = 0; t < kTK; t += 4) {
-                float p[4];
-                step4<NP, kOut>(hp, A2, sx, sB, sC, kNT, t, slot, nl, p);
-                if (kOut) sy[t + nl][dl] = sum_lanes(p, nl);
-            }
-        } else {  // sequences end inside the tile: token by token
-            for (int t = 0; t < (int)(tile_end - t0); ++t) {
-                if (t0 + t == at.end) {
-                    if (MODE == kChunk && a.ht != nullptr) {
-                        from_pairs<NP>(h, hp);
-                        store_states<NP>(h, a.ht, (int64_t)at.s * a.ch * a.N + dn, nl, a.N, live);
-                    }
-                    seq_next(a.seqs, at);
-                    load_states<NP>(h, a.h0, (int64_t)at.s * a.ch * a.N + dn, nl, a.N, live && a.h0 != nullptr);
-                    to_pairs<NP>(hp, h);
-                }
-                const ulonglong2 dx = *reinterpret_cast<const ulonglong2 *>(&sx[t][slot]);
-                float s = 0.f;
+    };
+    float sum0 = 0.f, sum1 = 0.f;
+    // one token: t in the tile, row r
+    auto token = [&](int t, int64_t r, const Raw<T, 2> &ru, const Raw<T, 2> &rdt, const Raw<T, 2> &rz) {
+        const float u0 = ru.get(0), u1 = ru.get(1);
+        const float d0 = step_of<T>(rdt.get(0) + bias0, a.softplus), d1 = step_of<T>(rdt.get(1) + bias1, a.softplus);
+        const float x0 = d0 * u0, x1 = d1 * u1;
+        const f2 dd0 = pk(d0, d0), dd1 = pk(d1, d1), xx0 = pk(x0, x0), xx1 = pk(x1, x1);
+        if (MODE == kSummary) {
+            sum0 += d0;
+            sum1 += d1;
+        }
+        f2 y0 = 0, y1 = 0;
 #pragma unroll
-                for (int i = 0; i < NP / 2; ++i) {
-                    const f2 B = *reinterpret_cast<const f2 *>(&sB[t * kNT + nl * NP + 2 * i]);
-                    hp[i] = fma2(exp2_2(mul2(dx.x, A2[i])), hp[i], mul2(dx.y, B));
-                    if (kOut) s += hsum2(mul2(hp[i], *reinterpret_cast<const f2 *>(&sC[t * kNT + nl * NP + 2 * i])));
-                }
-                if (kOut) {
-                    s += __shfl_xor_sync(0xffffffffu, s, 1);
-                    s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    if (nl == 0) sy[t][dl] = s;
-                }
+        for (int i = 0; i < P2; i += 2) {
+            const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sB[t * S::kNT + n0 + 2 * i]);
+            h[0][i] = fma2(exp2_2(mul2(dd0, A2[0][i])), h[0][i], mul2(xx0, B.x));
+            h[0][i + 1] = fma2(exp2_2(mul2(dd0, A2[0][i + 1])), h[0][i + 1], mul2(xx0, B.y));
+            h[1][i] = fma2(exp2_2(mul2(dd1, A2[1][i])), h[1][i], mul2(xx1, B.x));
+            h[1][i + 1] = fma2(exp2_2(mul2(dd1, A2[1][i + 1])), h[1][i + 1], mul2(xx1, B.y));
+            if (kOut) {
+                const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sC[t * S::kNT + n0 + 2 * i]);
+                y0 = i == 0 ? mul2(h[0][0], C.x) : fma2(h[0][i], C.x, y0);
+                y0 = fma2(h[0][i + 1], C.y, y0);
+                y1 = i == 0 ? mul2(h[1][0], C.x) : fma2(h[1][i], C.x, y1);
+                y1 = fma2(h[1][i + 1], C.y, y1);
             }
         }
         if (kOut) {
-            __syncthreads();
-            const int64_t r = t0 + tr;
-            if (r < c1 && nc > 0) {
-                float out[8];
+            float s0 = hsum2(y0), s1 = hsum2(y1);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    out[j] = fmaf(D8[j], cu_.get(j), sy[tr][tc + j]);
-                    if (a.z != nullptr) out[j] *= act_value(cz.get(j), true);
+            for (int o = 1; o < LN; o *= 2) {
+                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            }
+            float f[2] = {fmaf(D0, u0, s0), fmaf(D1, u1, s1)};
+            if (gate) {
+                f[0] *= act_value(rz.get(0), true);
+                f[1] *= act_value(rz.get(1), true);
+            }
+            if (LN == 1 || tid % LN == 0) {
+                Raw<T, 2> w;
+                w.pack(f);
+                T *py = static_cast<T *>(a.y) + r * a.ch;  // the same for all threads
+                if (a.vec && nch == 2)
+                    w.store(py + d);
+                else
+                    w.store_some(py + d, nch);
+            }
+        }
+    };
+
+    if (c0 < c1) {
+        fetch(c0);
+        fetch_bc(c0);
+    }
+    for (int64_t t0 = c0; t0 < c1; t0 += kTile) {
+        __syncthreads();  // the previous tile has been read
+#pragma unroll
+        for (int k = 0; k < S::kBC; ++k) {
+            const int e = (tid + k * kFThr) % (kTile * S::kNT);
+            if (k < S::kBC / 2)
+                sB[e] = nbc[k];
+            else if (kOut)
+                sC[e] = nbc[k];
+        }
+        __syncthreads();
+        if (t0 + kTile < c1) fetch_bc(t0 + kTile);
+#pragma unroll 1
+        for (int t = 0; t < kTile; t += 4) {
+            const int64_t r = t0 + t;
+            if (r >= c1) break;
+            Raw<T, 2> cu_[4], cdt[4], cz[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                cu_[k] = nu[k];
+                cdt[k] = ndt[k];
+                cz[k] = nz[k];
+            }
+            if (r + 4 < c1) fetch(r + 4);
+            if (r + 4 <= c1 && r + 4 <= at.end) {  // four tokens of one sequence
+#pragma unroll
+                for (int k = 0; k < 4; ++k) token(t + k, r + k, cu_[k], cdt[k], cz[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (r + k >= c1) break;
+                    if (r + k == at.end) {
+                        if (MODE == kChunk && a.ht != nullptr) finish(a.ht, at.s);
+                        seq_next(a.seqs, at);
+                        start(a.h0, at.s);
+                    }
+                    token(t + k, r + k, cu_[k], cdt[k], cz[k]);
                 }
-                store8<T>(a.y, r * a.ch + dc, out, nc, a.vec);
             }
         }
     }
-    from_pairs<NP>(h, hp);
     if (MODE == kSummary) {
-        store_states<NP>(h, a.hchunk, part * a.ch * a.N + dn, nl, a.N, live);
-        // sum of the step sizes over the 32 token rows of the staging threads, in a fixed order
-        __syncthreads();
-        float *red = reinterpret_cast<float *>(&sx[0][0]);  // [32][64]
-#pragma unroll
-        for (int j = 0; j < 8; ++j) red[tr * kDB + tc + j] = sum_delta[j];
-        __syncthreads();
-        if (tid < ch.n) {
-            float s = 0.f;
-            for (int i = 0; i < kTK; ++i) s += red[i * kDB + tid];
-            a.schunk[part * a.ch + ch.d0 + tid] = s;
+        finish(a.hchunk, part);
+        if (tid % LN == 0) {
+            if (nch > 0) a.schunk[part * a.ch + d] = sum0;
+            if (nch > 1) a.schunk[part * a.ch + d + 1] = sum1;
         }
     } else if (a.ht != nullptr && c1 == at.end) {
-        store_states<NP>(h, a.ht, (int64_t)at.s * a.ch * a.N + dn, nl, a.N, live);
+        finish(a.ht, at.s);
     }
 }
 
@@ -326,25 +397,22 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanArgs a) {
     }
 }
 
-template <typename T, Mode MODE>
-cudaError_t launch_mode(const ScanArgs &a, int64_t parts, cudaStream_t stream) {
+template <typename T, int NS, int LN, Mode MODE>
+cudaError_t launch_shape(ScanArgs a, int64_t parts, cudaStream_t stream) {
+    a.blocks_per_group = (int)ceil_div(a.chg, FwdShape<NS, LN>::kChan);
     const int64_t grid = parts * a.G * a.blocks_per_group;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    switch (np_of(a.N)) {
-        case 2:
-            scan_fwd_kernel<T, 2, MODE><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-            break;
-        case 4:
-            scan_fwd_kernel<T, 4, MODE><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-            break;
-        case 8:
-            scan_fwd_kernel<T, 8, MODE><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-            break;
-        default:
-            scan_fwd_kernel<T, 16, MODE><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-    }
+    scan_fwd_kernel<T, NS, LN, MODE><<<(unsigned)grid, kFThr, 0, stream>>>(a);
     return cudaGetLastError();
 }
+template <typename T, Mode MODE>
+cudaError_t launch_mode(const ScanArgs &a, int64_t parts, cudaStream_t stream) {
+    if (a.N <= 8) return launch_shape<T, 8, 1, MODE>(a, parts, stream);
+    if (a.N <= 16) return launch_shape<T, 16, 1, MODE>(a, parts, stream);
+    if (a.N <= 32) return launch_shape<T, 16, 2, MODE>(a, parts, stream);
+    return launch_shape<T, 16, 4, MODE>(a, parts, stream);
+}
+int fwd_channels(int N) { return N <= 16 ? 2 * kFThr : (N <= 32 ? kFThr : kFThr / 2); }
 
 template <typename T>
 cudaError_t launch_step(const ScanArgs &a, cudaStream_t stream) {
@@ -368,8 +436,8 @@ cudaError_t launch_step(const ScanArgs &a, cudaStream_t stream) {
 
 int elem_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
-// Chunks of the forward pass: none (0) where one block per sequence and 64 channels gives
-// about a block per SM, else as many as give three blocks per SM, of at least 64 rows.
+// Chunks of the forward pass: none (0) where one block per sequence and block of channels gives
+// three blocks per SM, else as many as fill the GPU's slots (kPerSM blocks per SM) once.
 struct FwdPlan {
     int64_t chunk, nchunks;
     size_t bytes;
@@ -377,15 +445,15 @@ struct FwdPlan {
 FwdPlan fwd_plan(const kda_scan_params &p) {
     FwdPlan q{};
     const int64_t rows = p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.batch * p.T;
-    const int64_t nblk = (int64_t)p.G * ceil_div(p.channels / p.G, kDB);
+    const int64_t nblk = (int64_t)p.G * ceil_div(p.channels / p.G, fwd_channels(p.N));
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
     const bool ragged = p.cu_seqlens != nullptr && rows > 4 * (int64_t)p.batch;
-    if (!ragged && nblk * p.batch * 10 >= sms * 8) return q;
-    const int64_t per_seq = ceil_div(rows, p.batch);
-    if (!ragged && per_seq < 128) return q;
-    int64_t n = ceil_div(3 * sms, nblk);
-    int64_t chunk = ceil_div(ceil_div(rows, n), kTK) * kTK;
-    if (chunk < 64) chunk = 64;
+    if (!ragged && nblk * p.batch >= 3 * sms) return q;
+    if (!ragged && ceil_div(rows, p.batch) < 64) return q;
+    int64_t n = kPerSM * sms / nblk;
+    if (n < 1) n = 1;
+    int64_t chunk = ceil_div(ceil_div(rows, n), 4) * 4;
+    if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk >= rows && !ragged) return q;
     q.chunk = chunk;
     q.nchunks = ceil_div(rows, chunk);
@@ -404,12 +472,6 @@ cudaError_t run_fwd(const ScanArgs &a, cudaStream_t stream) {
 }
 
 }  // namespace
-
-cudaError_t launch_scan_summary(const ScanArgs &a, int dtype, cudaStream_t stream) {
-    if (a.nchunks <= 1) return cudaSuccess;
-    return dtype == KDA_DTYPE_BF16 ? launch_mode<bf16, kSummary>(a, a.nchunks - 1, stream)
-                                   : launch_mode<float, kSummary>(a, a.nchunks - 1, stream);
-}
 
 cudaError_t launch_scan_carry(const ScanArgs &a, cudaStream_t stream) {
     scan_carry_kernel<<<(unsigned)ceil_div((int64_t)a.ch * a.N, 256), 256, 0, stream>>>(a);
@@ -496,8 +558,7 @@ int kda_scan_fwd(const kda_scan_params *p, cudaStream_t stream) {
     const FwdPlan q = fwd_plan(*p);
     if (p->workspace != nullptr && p->workspace_bytes < q.bytes) return KDA_ERR_INVALID_ARG;
     if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;
-    const void *more[] = {p->y};
-    ScanArgs a = scan_args(*p, more, 1);
+    ScanArgs a = scan_args(*p, nullptr, 0);
     a.y = p->y;
     a.ht = p->ht;
     a.chunk = q.chunk;
@@ -507,6 +568,10 @@ int kda_scan_fwd(const kda_scan_params *p, cudaStream_t stream) {
     Scratch ws;
     e = ws.get(p->workspace, q.bytes, stream);
     if (e != cudaSuccess) return status_of_cuda(e);
+    const size_t e2 = 2 * elem_size(p->dtype);  // pairs of channels
+    a.vec = a.us % 2 == 0 && a.dts % 2 == 0 && (p->z == nullptr || a.zs % 2 == 0) && a.ch % 2 == 0 && a.chg % 2 == 0 &&
+            aligned(p->u, e2) && aligned(p->dt, e2) && aligned(p->z, e2) && aligned(p->y, e2);
+    a.vec_states = aligned(p->A, 16) && aligned(p->h0, 16) && aligned(p->ht, 16) && p->N % 4 == 0;
     a.hchunk = static_cast<float *>(ws.ptr);
     a.schunk = a.hchunk + q.nchunks * (int64_t)p->channels * p->N;
     e = p->dtype == KDA_DTYPE_BF16 ? run_fwd<bf16>(a, stream) : run_fwd<float>(a, stream);

@@ -34,6 +34,15 @@ __device__ __forceinline__ bf16 from_f<bf16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
+// ---- pairs of fp32 in one 64-bit register: two lanes of an FMA per instruction ---------------
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void upk(f2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+
 // V consecutive elements as they lie in memory (V * sizeof(T) bytes, or one element).
 template <typename T, int V>
 struct Raw {
@@ -86,6 +95,7 @@ struct Raw {
         else
             return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
     }
+    __device__ __forceinline__ f2 pair(int i) const { return pk(get(2 * i), get(2 * i + 1)); }
     __device__ __forceinline__ void unpack(float (&f)[V]) const {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = get(i);
@@ -141,9 +151,14 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[V]) {
 }
 
 // ---- activations --------------------------------------------------------------------------
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 1 / (1 + e^-x): one exponential and one reciprocal on the special-function unit (relative
 // error about 3e-7; e^-x = inf gives 0)
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + tc5::ex2(-x * kLog2e)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + tc5::ex2(-x * kLog2e)); }
 // The value of the gate act(x), KDA_ACT_SILU or KDA_ACT_SIGMOID.
 __device__ __forceinline__ float act_value(float x, bool silu) {
     const float s = sigmoid(x);
@@ -156,14 +171,7 @@ __device__ __forceinline__ void act_both(float x, bool silu, float &val, float &
     der = silu ? s * fmaf(x, 1.f - s, 1.f) : s * (1.f - s);
 }
 
-// ---- pairs of fp32 in one 64-bit register: two lanes of an FMA per instruction ---------------
-using f2 = uint64_t;
-__device__ __forceinline__ f2 pk(float lo, float hi) {
-    f2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void upk(f2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+// ---- arithmetic on pairs -------------------------------------------------------------------
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     f2 d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

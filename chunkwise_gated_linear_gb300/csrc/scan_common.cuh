@@ -32,7 +32,8 @@ struct ScanArgs {
     int ch, N, G, chg;            // channels, states, groups, channels per group
     int blocks_per_group;
     int softplus;
-    int vec;                      // every 8 channels of u, dt, z, y lie on 16 bytes
+    int vec;                      // channels may be read several at a time (each file's kernels say how many)
+    int vec_states;               // A, h0, ht: 16 bytes at a time
     Seqs seqs;
     int64_t chunk;                // rows per chunk (all sequences' rows together); 0: one block per sequence
     int64_t nchunks;
@@ -151,7 +152,6 @@ __device__ __forceinline__ int slot_of(int d) { return (d & ~7) | ((d ^ (d >> 3)
 int scan_check(const kda_scan_params &p);
 // Arguments without chunk buffers and error word. `vec` covers u, dt, z and the given pointers.
 ScanArgs scan_args(const kda_scan_params &p, const void *const *more, int n);
-cudaError_t launch_scan_summary(const ScanArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_scan_carry(const ScanArgs &a, cudaStream_t stream);
 
 }  // namespace scan
