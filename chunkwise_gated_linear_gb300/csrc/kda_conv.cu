@@ -64,10 +64,18 @@ __device__ __forceinline__ void copy_state(const void *from, void *to, int64_t a
     r.store(static_cast<T *>(to) + at);
 }
 
-constexpr int kBatch = 4;  // rows whose loads are issued together
+// Rows that are loaded together, while the previous ones are worked on; inside a sequence and a tile they
+// are also worked on together, without a check or a move per row.
+constexpr int kBatch = 4;
+#ifndef FB
+#define FB 3
+#endif
+#ifndef BB
+#define BB 3
+#endif
 
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvArgs a) {
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
     const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.D) return;
@@ -93,44 +101,81 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvArgs a
     float win[W][V];
     fill_window<T, V, W>(a, at, r0, c, win);
 
-    const T *x = static_cast<const T *>(a.x) + c;
-    T *y = static_cast<T *>(a.y) + c;
+    Raw<T, V> next[kBatch];
+    auto fetch = [&](int64_t rb) {
+        const T *x = static_cast<const T *>(a.x) + rb * a.xs;  // the same for all threads
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (rb + i < r1) next[i].load(x + i * a.xs + c);
+    };
+    auto put = [&](int64_t r, const float (&s)[V]) {
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = SILU ? s[v] * sigmoid(s[v]) : s[v];
+        store_vec<T, V>(static_cast<T *>(a.y) + r * a.D + c, out);
+    };
+    auto keep_state = [&]() {
+        T *st = static_cast<T *>(a.st) + (int64_t)at.s * (W - 1) * a.D + c;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            float keep[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) keep[v] = win[j][v];
+            store_vec<T, V>(st + (int64_t)j * a.D, keep);
+        }
+    };
+    fetch(r0);
     for (int64_t rb = r0; rb < r1; rb += kBatch) {
         Raw<T, V> in[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (rb + i < r1) in[i].load(x + (rb + i) * a.xs);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t r = rb + i;
-            if (r >= r1) break;
-            if (r == at.end) {
-                seq_next(a.seqs, at);
-                fill_window<T, V, W>(a, at, r, c, win);
-            }
-            in[i].unpack(win[W - 1]);
-            float out[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float s = b[v];
-#pragma unroll
-                for (int j = 0; j < W; ++j) s = fmaf(w[j][v], win[j][v], s);
-                out[v] = SILU ? s * sigmoid(s) : s;
-            }
-            store_vec<T, V>(y + r * a.D, out);
+        for (int i = 0; i < kBatch; ++i) in[i] = next[i];
+        if (rb + kBatch < r1) fetch(rb + kBatch);
+        if (rb + kBatch <= r1 && rb + kBatch <= at.end) {
+            float ext[W - 1 + kBatch][V];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
-            if (r + 1 == at.end && a.st != nullptr) {
-                T *st = static_cast<T *>(a.st) + (int64_t)at.s * (W - 1) * a.D + c;
+                for (int v = 0; v < V; ++v) ext[j][v] = win[j][v];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    float keep[V];
+            for (int i = 0; i < kBatch; ++i) {
+                in[i].unpack(ext[W - 1 + i]);
+                float s[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) keep[v] = win[j][v];
-                    store_vec<T, V>(st + (int64_t)j * a.D, keep);
+                for (int v = 0; v < V; ++v) {
+                    s[v] = b[v];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s[v] = fmaf(w[j][v], ext[i + j][v], s[v]);
                 }
+                put(rb + i, s);
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[j][v] = ext[kBatch + j][v];
+            if (rb + kBatch == at.end && a.st != nullptr) keep_state();
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t r = rb + i;
+                if (r >= r1) break;
+                if (r == at.end) {
+                    seq_next(a.seqs, at);
+                    fill_window<T, V, W>(a, at, r, c, win);
+                }
+                in[i].unpack(win[W - 1]);
+                float s[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    s[v] = b[v];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s[v] = fmaf(w[j][v], win[j][v], s[v]);
+                }
+                put(r, s);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
+                if (r + 1 == at.end && a.st != nullptr) keep_state();
             }
         }
     }
@@ -190,7 +235,7 @@ struct ConvBack {
 };
 
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvArgs a) {
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
     const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.D) return;
@@ -219,17 +264,75 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a
         const int64_t qend = k.r1 + W - 1 < a.seqs.rows ? k.r1 + W - 1 : a.seqs.rows;
         SeqAt at = seq_find(a.seqs, k.r0);
         fill_window<T, V, W>(a, at, k.r0, c, win);
-        const T *x = static_cast<const T *>(a.x) + c;
-        const T *dy = static_cast<const T *>(a.dy) + c;
-        bool open = true;  // false once the last sequence with rows in the tile has been finished
-        for (int64_t qb = k.r0; qb < qend && open; qb += kBatch) {
-            Raw<T, V> in[kBatch], gr[kBatch];
+        Raw<T, V> nx[kBatch], ng[kBatch];
+        auto fetch = [&](int64_t qb) {
+            const T *x = static_cast<const T *>(a.x) + qb * a.xs, *dy = static_cast<const T *>(a.dy) + qb * a.D;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 if (qb + i < qend) {
-                    in[i].load(x + (qb + i) * a.xs);
-                    gr[i].load(dy + (qb + i) * a.D);
+                    nx[i].load(x + i * a.xs + c);
+                    ng[i].load(dy + (int64_t)i * a.D + c);
                 }
+        };
+        // gradient of the sum before the activation
+        auto before_act = [&](float s, float g) {
+            if (!SILU) return g;
+            float val, der;
+            act_both(s, true, val, der);
+            return g * der;
+        };
+        bool open = true;  // false once the last sequence with rows in the tile has been finished
+        fetch(k.r0);
+        for (int64_t qb = k.r0; qb < qend && open; qb += kBatch) {
+            Raw<T, V> in[kBatch], gr[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                in[i] = nx[i];
+                gr[i] = ng[i];
+            }
+            if (qb + kBatch < qend) fetch(qb + kBatch);
+            const int64_t p0 = qb - (W - 1);
+            if (qb + kBatch <= k.r1 && qb + kBatch <= at.end && p0 >= at.start && p0 >= k.r0) {
+                float ext[W - 1 + kBatch][V], gx[W - 1 + kBatch][V];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        ext[j][v] = win[j][v];
+                        gx[j][v] = k.g[j + 1][v];
+                    }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    in[i].unpack(ext[W - 1 + i]);
+                    gr[i].unpack(gx[W - 1 + i]);
+                    float out[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float &gq = gx[W - 1 + i][v];
+                        if (SILU) {
+                            float s = b[v];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], ext[i + j][v], s);
+                            gq = before_act(s, gq);
+                        }
+                        db[v] += gq;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gq, ext[i + j][v], dw[j][v]);
+                        out[v] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) out[v] = fmaf(gx[i + j][v], k.w[W - 1 - j][v], out[v]);
+                    }
+                    store_vec<T, V>(static_cast<T *>(a.dx) + (p0 + i) * a.D + c, out);
+                }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        win[j][v] = ext[kBatch + j][v];
+                        k.g[j + 1][v] = gx[kBatch + j][v];
+                    }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int64_t q = qb + i;
@@ -250,13 +353,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a
                 const bool mine = q < k.r1;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if (SILU) {
-                        float s = b[v], val, der;
+                    float s = b[v];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], win[j][v], s);
-                        act_both(s, true, val, der);
-                        gq[v] *= der;
-                    }
+                    for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], win[j][v], s);
+                    gq[v] = before_act(s, gq[v]);
                     k.g[W - 1][v] = gq[v];
                     if (mine) {
                         db[v] += gq[v];
@@ -375,7 +475,10 @@ int conv_run(const kda_conv_params &p, bool step, cudaStream_t stream) {
     const cudaError_t e1 = device_error_word(&a.err);
     if (e1 != cudaSuccess) return status_of_cuda(e1);
     const void *ptrs[] = {p.x, p.s0, p.y, p.st};
-    const int V = conv_vec(p.dtype, p.D, a.xs, 8, ptrs, 4);
+    #ifndef FV
+#define FV 8
+#endif
+    const int V = conv_vec(p.dtype, p.D, a.xs, FV, ptrs, 4);
     if (step) {
         a.tile = p.T > 0 ? p.T : 1;  // one sequence per tile: its state is read and written by the same threads
         a.tiles = p.B;
@@ -396,7 +499,10 @@ ConvBwdPlan conv_bwd_plan(const kda_conv_bwd_params &p) {
     ConvBwdPlan q;
     const void *ptrs[] = {p.x, p.s0, p.dy, p.dst, p.dx, p.ds0};
     const int64_t rows = p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.B * p.T;
-    q.V = conv_vec(p.dtype, p.D, p.x_stride != 0 ? p.x_stride : p.D, 4, ptrs, 6);
+    #ifndef BV
+#define BV 4
+#endif
+    q.V = conv_vec(p.dtype, p.D, p.x_stride != 0 ? p.x_stride : p.D, BV, ptrs, 6);
     q.tile = conv_tile(rows, ceil_div(ceil_div(p.D, q.V), kConvThreads), 16, 256);
     q.tiles = ceil_div(rows, q.tile);
     if (q.tiles < 1) q.tiles = 1;
