@@ -30,27 +30,143 @@ struct ConvArgs {
     float *partial;  // per tile: dweight [D][W], then dbias [D]
     int64_t xs;      // elements between rows of x
     int D, tile, silu;
+    int wvec;        // weight on 16 bytes
     int64_t tiles;
     Seqs seqs;
     unsigned int *err;
 };
 
+// V channels as pairs (or a single one): one instruction does a multiply-add for two channels.
+template <int V>
+struct Lanes {
+    using type = f2;
+    static constexpr int K = V / 2;
+};
+template <>
+struct Lanes<1> {
+    using type = float;
+    static constexpr int K = 1;
+};
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f2 fma_(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ f2 mul_(f2 a, f2 b) { return mul2(a, b); }
+__device__ __forceinline__ float add_(float a, float b) { return a + b; }
+__device__ __forceinline__ f2 add_(f2 a, f2 b) { return add2(a, b); }
+__device__ __forceinline__ float silu_(float s) { return s * sigmoid(s); }
+__device__ __forceinline__ f2 silu_(f2 s) {
+    float a, b;
+    upk(s, a, b);
+    return pk(silu_(a), silu_(b));
+}
+// silu'(s) = p (1 + s (1 - p)), p = 1 / (1 + e^-s)
+__device__ __forceinline__ float dsilu_(float s) {
+    const float p = sigmoid(s);
+    return fmaf(fmaf(-p, s, s), p, p);
+}
+__device__ __forceinline__ f2 dsilu_(f2 s) {
+    float a, b;
+    upk(s, a, b);
+    return pk(dsilu_(a), dsilu_(b));
+}
+
+template <typename T, int V>
+struct Row {
+    using L = typename Lanes<V>::type;
+    static constexpr int K = Lanes<V>::K;
+    L v[K];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = 0;
+    }
+    __device__ __forceinline__ void from(const Raw<T, V> &r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (V > 1)
+                v[k] = r.pair(k);
+            else
+                v[k] = r.get(k);
+        }
+    }
+    __device__ __forceinline__ void floats(float (&f)[V]) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (V > 1)
+                upk(v[k], f[2 * k], f[2 * k + 1]);
+            else
+                f[k] = v[k];
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (V > 1)
+                v[k] = pk(f[2 * k], f[2 * k + 1]);
+            else
+                v[k] = f[k];
+        }
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        Raw<T, V> r;
+        r.load(p);
+        from(r);
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        float f[V];
+        floats(f);
+        store_vec<T, V>(p, f);
+    }
+};
+// a += b c
+template <typename T, int V>
+__device__ __forceinline__ void mad(Row<T, V> &a, const Row<T, V> &b, const Row<T, V> &c) {
+#pragma unroll
+    for (int k = 0; k < Row<T, V>::K; ++k) a.v[k] = fma_(b.v[k], c.v[k], a.v[k]);
+}
+
+// The taps and the bias of V channels.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, Row<T, V> (&w)[W], Row<T, V> &b) {
+    float f[V * W], fb[V];
+    if (V > 1 && a.wvec) {
+#pragma unroll
+        for (int i = 0; i < V * W / 4; ++i) {
+            const float4 q = reinterpret_cast<const float4 *>(a.w + c * W)[i];
+            f[4 * i] = q.x;
+            f[4 * i + 1] = q.y;
+            f[4 * i + 2] = q.z;
+            f[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) f[i] = a.w[c * W + i];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) fb[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
+    b.set(fb);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float t[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) t[v] = f[v * W + j];
+        w[j].set(t);
+    }
+}
+
 // The window before row r of a sequence: rows r - (W-1) .. r - 1, those before the sequence's
 // start from its initial state.
 template <typename T, int V, int W>
-__device__ __forceinline__ void fill_window(const ConvArgs &a, const SeqAt &at, int64_t r, int64_t c, float (&win)[W][V]) {
+__device__ __forceinline__ void fill_window(const ConvArgs &a, const SeqAt &at, int64_t r, int64_t c, Row<T, V> (&win)[W]) {
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         const int64_t pos = r - (W - 1) + i;
         const int64_t slot = W - 1 + pos - at.start;  // >= 0 since r >= start
         if (pos >= at.start)
-            load_vec<T, V>(win[i], static_cast<const T *>(a.x) + pos * a.xs + c);
+            win[i].load(static_cast<const T *>(a.x) + pos * a.xs + c);
         else if (a.s0 != nullptr)
-            load_vec<T, V>(win[i], static_cast<const T *>(a.s0) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
-        else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[i][v] = 0.f;
-        }
+            win[i].load(static_cast<const T *>(a.s0) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
+        else
+            win[i].zero();
     }
 }
 
@@ -65,17 +181,19 @@ __device__ __forceinline__ void copy_state(const void *from, void *to, int64_t a
 }
 
 // Rows that are loaded together, while the previous ones are worked on; inside a sequence and a tile they
-// are also worked on together, without a check or a move per row.
-constexpr int kBatch = 4;
-#ifndef FB
-#define FB 3
-#endif
-#ifndef BB
-#define BB 3
-#endif
+// are also worked on together, without a check or a move per row. Blocks per SM (registers) go with
+// that: what keeps the memory busy is rows in flight times blocks.
+template <typename T>
+constexpr int kFwdBatch = sizeof(T) == 2 ? 8 : 4;
+constexpr int kBwdBatch = 4;
+constexpr int kFwdPerSM = 5;  // 32761 x 8192 bf16: 176 us; six blocks 194, four rows and eight blocks 183
+template <typename T>
+constexpr int kBwdPerSM = sizeof(T) == 2 ? 4 : 3;  // 16384 x 12288 bf16: 264 us; five blocks spill (512), three with 8 rows 296
 
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, kFwdPerSM) conv_fwd_kernel(const ConvArgs a) {
+    constexpr int kBatch = kFwdBatch<T>;
+    using R = Row<T, V>;
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
     const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.D) return;
@@ -90,15 +208,9 @@ __global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvAr
     const int64_t r1 = r0 + a.tile < a.seqs.rows ? r0 + a.tile : a.seqs.rows;
     if (r0 >= r1) return;
 
-    float w[W][V], b[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        b[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][v] = a.w[(c + v) * W + j];
-    }
+    R w[W], b, win[W];
+    load_weights<T, V, W>(a, c, w, b);
     SeqAt at = seq_find(a.seqs, r0);
-    float win[W][V];
     fill_window<T, V, W>(a, at, r0, c, win);
 
     Raw<T, V> next[kBatch];
@@ -108,21 +220,16 @@ __global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvAr
         for (int i = 0; i < kBatch; ++i)
             if (rb + i < r1) next[i].load(x + i * a.xs + c);
     };
-    auto put = [&](int64_t r, const float (&s)[V]) {
-        float out[V];
+    auto put = [&](int64_t r, R s) {
+        if (SILU)
 #pragma unroll
-        for (int v = 0; v < V; ++v) out[v] = SILU ? s[v] * sigmoid(s[v]) : s[v];
-        store_vec<T, V>(static_cast<T *>(a.y) + r * a.D + c, out);
+            for (int k = 0; k < R::K; ++k) s.v[k] = silu_(s.v[k]);
+        s.store(static_cast<T *>(a.y) + r * a.D + c);
     };
     auto keep_state = [&]() {
         T *st = static_cast<T *>(a.st) + (int64_t)at.s * (W - 1) * a.D + c;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            float keep[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) keep[v] = win[j][v];
-            store_vec<T, V>(st + (int64_t)j * a.D, keep);
-        }
+        for (int j = 0; j < W - 1; ++j) win[j].store(st + (int64_t)j * a.D);
     };
     fetch(r0);
     for (int64_t rb = r0; rb < r1; rb += kBatch) {
@@ -131,27 +238,19 @@ __global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvAr
         for (int i = 0; i < kBatch; ++i) in[i] = next[i];
         if (rb + kBatch < r1) fetch(rb + kBatch);
         if (rb + kBatch <= r1 && rb + kBatch <= at.end) {
-            float ext[W - 1 + kBatch][V];
+            R ext[W - 1 + kBatch];
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) ext[j][v] = win[j][v];
+            for (int j = 0; j < W - 1; ++j) ext[j] = win[j];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                in[i].unpack(ext[W - 1 + i]);
-                float s[V];
+                ext[W - 1 + i].from(in[i]);
+                R s = b;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = b[v];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) s[v] = fmaf(w[j][v], ext[i + j][v], s[v]);
-                }
+                for (int j = 0; j < W; ++j) mad(s, w[j], ext[i + j]);
                 put(rb + i, s);
             }
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[j][v] = ext[kBatch + j][v];
+            for (int j = 0; j < W - 1; ++j) win[j] = ext[kBatch + j];
             if (rb + kBatch == at.end && a.st != nullptr) keep_state();
         } else {
 #pragma unroll
@@ -162,19 +261,13 @@ __global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvAr
                     seq_next(a.seqs, at);
                     fill_window<T, V, W>(a, at, r, c, win);
                 }
-                in[i].unpack(win[W - 1]);
-                float s[V];
+                win[W - 1].from(in[i]);
+                R s = b;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = b[v];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) s[v] = fmaf(w[j][v], win[j][v], s[v]);
-                }
+                for (int j = 0; j < W; ++j) mad(s, w[j], win[j]);
                 put(r, s);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
+                for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
                 if (r + 1 == at.end && a.st != nullptr) keep_state();
             }
         }
@@ -190,52 +283,46 @@ __global__ void __launch_bounds__(kConvThreads, FB) conv_fwd_kernel(const ConvAr
 // a sequence ends, the open positions are finished with zeros.
 template <typename T, int V, int W>
 struct ConvBack {
+    using R = Row<T, V>;
     const ConvArgs &a;
     int64_t c, r0, r1;
-    float w[W][V], g[W][V];
+    R w[W], g[W];
 
     __device__ __forceinline__ ConvBack(const ConvArgs &args) : a(args) {}
     __device__ __forceinline__ void shift() {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[j][v] = g[j + 1][v];
+        for (int j = 0; j < W - 1; ++j) g[j] = g[j + 1];
     }
     // finish position p; `slot` of the final state holds it when slot >= 0
     __device__ __forceinline__ void finish(const SeqAt &at, int64_t p, int slot) const {
         const bool token = p >= at.start;
         if (token ? (p < r0 || p >= r1) : (at.start < r0 || a.ds0 == nullptr)) return;
-        float s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = 0.f;
+        R s;
+        s.zero();
         if (slot >= 0 && a.dst != nullptr)
-            load_vec<T, V>(s, static_cast<const T *>(a.dst) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
+            s.load(static_cast<const T *>(a.dst) + ((int64_t)at.s * (W - 1) + slot) * a.D + c);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = fmaf(g[k][v], w[W - 1 - k][v], s[v]);
-        T *to = token ? static_cast<T *>(a.dx) + p * a.D + c
-                      : static_cast<T *>(a.ds0) + ((int64_t)at.s * (W - 1) + (W - 1 + p - at.start)) * a.D + c;
-        store_vec<T, V>(to, s);
+        for (int k = 0; k < W; ++k) mad(s, g[k], w[W - 1 - k]);
+        s.store(token ? static_cast<T *>(a.dx) + p * a.D + c
+                      : static_cast<T *>(a.ds0) + ((int64_t)at.s * (W - 1) + (W - 1 + p - at.start)) * a.D + c);
     }
     // the sequence has ended: its last W - 1 positions
     __device__ __forceinline__ void flush(const SeqAt &at) {
 #pragma unroll
         for (int k = 1; k < W; ++k) {
             shift();
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[W - 1][v] = 0.f;
+            g[W - 1].zero();
             finish(at, at.end - W + k, k - 1);
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[j][v] = 0.f;
+        for (int j = 0; j < W; ++j) g[j].zero();
     }
 };
 
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, kBwdPerSM<T>) conv_bwd_kernel(const ConvArgs a) {
+    constexpr int kBatch = kBwdBatch;
+    using R = Row<T, V>;
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
     const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.D) return;
@@ -249,16 +336,13 @@ __global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvAr
     k.c = c;
     k.r0 = (int64_t)blockIdx.x * a.tile;
     k.r1 = k.r0 + a.tile < a.seqs.rows ? k.r0 + a.tile : a.seqs.rows;
-    float b[V], dw[W][V], db[V], win[W][V];
+    R b, dw[W], db, win[W];
+    load_weights<T, V, W>(a, c, k.w, b);
+    db.zero();
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        b[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
-        db[v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            k.w[j][v] = a.w[(c + v) * W + j];
-            k.g[j][v] = dw[j][v] = 0.f;
-        }
+    for (int j = 0; j < W; ++j) {
+        dw[j].zero();
+        k.g[j].zero();
     }
     if (k.r0 < k.r1) {
         const int64_t qend = k.r1 + W - 1 < a.seqs.rows ? k.r1 + W - 1 : a.seqs.rows;
@@ -274,12 +358,20 @@ __global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvAr
                     ng[i].load(dy + (int64_t)i * a.D + c);
                 }
         };
-        // gradient of the sum before the activation
-        auto before_act = [&](float s, float g) {
-            if (!SILU) return g;
-            float val, der;
-            act_both(s, true, val, der);
-            return g * der;
+        // g times the activation's derivative at the sum over the window `ext`
+        auto before_act = [&](R &g, const R *ext) {
+            if (!SILU) return;
+            R s = b;
+#pragma unroll
+            for (int j = 0; j < W; ++j) mad(s, k.w[j], ext[j]);
+#pragma unroll
+            for (int i = 0; i < R::K; ++i) g.v[i] = mul_(g.v[i], dsilu_(s.v[i]));
+        };
+        auto add_weights = [&](const R &g, const R *ext) {
+#pragma unroll
+            for (int i = 0; i < R::K; ++i) db.v[i] = add_(db.v[i], g.v[i]);
+#pragma unroll
+            for (int j = 0; j < W; ++j) mad(dw[j], g, ext[j]);
         };
         bool open = true;  // false once the last sequence with rows in the tile has been finished
         fetch(k.r0);
@@ -293,44 +385,29 @@ __global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvAr
             if (qb + kBatch < qend) fetch(qb + kBatch);
             const int64_t p0 = qb - (W - 1);
             if (qb + kBatch <= k.r1 && qb + kBatch <= at.end && p0 >= at.start && p0 >= k.r0) {
-                float ext[W - 1 + kBatch][V], gx[W - 1 + kBatch][V];
+                R ext[W - 1 + kBatch], gx[W - 1 + kBatch];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        ext[j][v] = win[j][v];
-                        gx[j][v] = k.g[j + 1][v];
-                    }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    in[i].unpack(ext[W - 1 + i]);
-                    gr[i].unpack(gx[W - 1 + i]);
-                    float out[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float &gq = gx[W - 1 + i][v];
-                        if (SILU) {
-                            float s = b[v];
-#pragma unroll
-                            for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], ext[i + j][v], s);
-                            gq = before_act(s, gq);
-                        }
-                        db[v] += gq;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gq, ext[i + j][v], dw[j][v]);
-                        out[v] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) out[v] = fmaf(gx[i + j][v], k.w[W - 1 - j][v], out[v]);
-                    }
-                    store_vec<T, V>(static_cast<T *>(a.dx) + (p0 + i) * a.D + c, out);
+                for (int j = 0; j < W - 1; ++j) {
+                    ext[j] = win[j];
+                    gx[j] = k.g[j + 1];
                 }
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
+                for (int i = 0; i < kBatch; ++i) {
+                    ext[W - 1 + i].from(in[i]);
+                    gx[W - 1 + i].from(gr[i]);
+                    before_act(gx[W - 1 + i], ext + i);
+                    add_weights(gx[W - 1 + i], ext + i);
+                    R out;
+                    out.zero();
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        win[j][v] = ext[kBatch + j][v];
-                        k.g[j + 1][v] = gx[kBatch + j][v];
-                    }
+                    for (int j = 0; j < W; ++j) mad(out, gx[i + j], k.w[W - 1 - j]);
+                    out.store(static_cast<T *>(a.dx) + (p0 + i) * a.D + c);
+                }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    win[j] = ext[kBatch + j];
+                    k.g[j + 1] = gx[kBatch + j];
+                }
                 continue;
             }
 #pragma unroll
@@ -346,39 +423,28 @@ __global__ void __launch_bounds__(kConvThreads, BB) conv_bwd_kernel(const ConvAr
                     seq_next(a.seqs, at);
                     fill_window<T, V, W>(a, at, q, c, win);
                 }
-                in[i].unpack(win[W - 1]);
-                float gq[V];
-                gr[i].unpack(gq);
+                win[W - 1].from(in[i]);
                 k.shift();
-                const bool mine = q < k.r1;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float s = b[v];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) s = fmaf(k.w[j][v], win[j][v], s);
-                    gq[v] = before_act(s, gq[v]);
-                    k.g[W - 1][v] = gq[v];
-                    if (mine) {
-                        db[v] += gq[v];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gq[v], win[j][v], dw[j][v]);
-                    }
-                }
+                k.g[W - 1].from(gr[i]);
+                before_act(k.g[W - 1], win);
+                if (q < k.r1) add_weights(k.g[W - 1], win);
                 k.finish(at, q - (W - 1), -1);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
+                for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
             }
         }
         if (open && qend == at.end) k.flush(at);
     }
     float *part = a.partial + (int64_t)blockIdx.x * ((int64_t)a.D * (W + 1));
+    float f[W][V], fb[V];
+    db.floats(fb);
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j].floats(f[j]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) part[(c + v) * W + j] = dw[j][v];
-        part[(int64_t)a.D * W + c + v] = db[v];
+        for (int j = 0; j < W; ++j) part[(c + v) * W + j] = f[j][v];
+        part[(int64_t)a.D * W + c + v] = fb[v];
     }
 }
 
@@ -405,16 +471,9 @@ cudaError_t conv_width(const ConvArgs &a, int W, bool bwd, cudaStream_t stream) 
     return conv_launch<T, V, 2>(a, bwd, stream);
 }
 
-// V channels per thread when every row of every tensor lets V elements be read at once
-// (V * sizeof(T) aligned rows and pointers), one channel otherwise.
 cudaError_t conv_dispatch(const ConvArgs &a, int dtype, int W, bool bwd, int V, cudaStream_t stream) {
-    if (dtype == KDA_DTYPE_BF16) {
-        if (V == 8) return conv_width<bf16, 8>(a, W, bwd, stream);
-        if (V == 4) return conv_width<bf16, 4>(a, W, bwd, stream);
-        return conv_width<bf16, 1>(a, W, bwd, stream);
-    }
-    if (V == 4) return conv_width<float, 4>(a, W, bwd, stream);
-    return conv_width<float, 1>(a, W, bwd, stream);
+    if (dtype == KDA_DTYPE_BF16) return V == 4 ? conv_width<bf16, 4>(a, W, bwd, stream) : conv_width<bf16, 1>(a, W, bwd, stream);
+    return V == 4 ? conv_width<float, 4>(a, W, bwd, stream) : conv_width<float, 1>(a, W, bwd, stream);
 }
 
 int elem_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
@@ -433,25 +492,26 @@ int conv_check(const void *x, const float *weight, const float *bias, const void
     return KDA_OK;
 }
 
-// The widest V <= most that the sizes and pointers allow.
-int conv_vec(int dtype, int D, int64_t xs, int most, const void *const *ptrs, int n) {
-    const int e = elem_size(dtype);
-    for (int V = most; V > 1; V /= 2) {
-        if (V == 2 || (dtype == KDA_DTYPE_F32 && V > 4)) continue;
-        bool ok = D % V == 0 && xs % V == 0;
-        for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], (size_t)V * e);
-        if (ok) return V;
-    }
-    return 1;
+// Four channels per thread where every row of every tensor lets them be read at once, else one. (Eight
+// channels take so many registers that fewer loads are in flight: 250 us for 32761 x 8192
+// where four take 213.)
+int conv_vec(int dtype, int D, int64_t xs, const void *const *ptrs, int n) {
+    bool ok = D % 4 == 0 && xs % 4 == 0;
+    for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], (size_t)4 * elem_size(dtype));
+    return ok ? 4 : 1;
 }
 
-// Rows per tile: enough tiles for `per_sm` blocks on every SM, between 8 rows (below that the
-// W - 1 rows read again weigh more than the parallelism gains) and `most`.
-int conv_tile(int64_t rows, int64_t chan_blocks, int per_sm, int most) {
-    const int64_t want = ceil_div((int64_t)per_sm * (sm_count() > 0 ? sm_count() : 1), chan_blocks);
-    int64_t tile = ceil_div(rows, want);
-    tile = tile < 8 ? 8 : (tile > most ? most : tile);
-    return (int)ceil_div(tile, kBatch) * kBatch;
+// Rows per tile: the tiles fill the GPU's slots (per_sm blocks per SM) `turns` times, or fewer
+// times where tiles would get shorter than 32 rows (the W - 1 rows that two tiles both read, and a tile's
+// first loads, then weigh more); where even one turn is not filled, tiles of at least 8 rows.
+int conv_tile(int64_t rows, int64_t chan_blocks, int per_sm, int turns, int batch) {
+    const int64_t slots = (int64_t)per_sm * (sm_count() > 0 ? sm_count() : 1);
+    int64_t tile = 0;
+    for (int t = turns; t >= 1 && tile < 32; --t) {
+        const int64_t n = t * slots / chan_blocks;
+        tile = ceil_div(ceil_div(rows, n < 1 ? 1 : n), batch) * batch;
+    }
+    return (int)(tile < 8 ? 8 : tile);
 }
 
 int conv_run(const kda_conv_params &p, bool step, cudaStream_t stream) {
@@ -471,19 +531,18 @@ int conv_run(const kda_conv_params &p, bool step, cudaStream_t stream) {
     a.xs = p.x_stride != 0 ? p.x_stride : p.D;
     a.D = p.D;
     a.silu = p.activation == KDA_ACT_SILU;
+    a.wvec = aligned(p.weight, 16);
     a.seqs = Seqs{p.cu_seqlens, p.B, p.T, p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.B * p.T};
     const cudaError_t e1 = device_error_word(&a.err);
     if (e1 != cudaSuccess) return status_of_cuda(e1);
     const void *ptrs[] = {p.x, p.s0, p.y, p.st};
-    #ifndef FV
-#define FV 8
-#endif
-    const int V = conv_vec(p.dtype, p.D, a.xs, FV, ptrs, 4);
+    const int V = conv_vec(p.dtype, p.D, a.xs, ptrs, 4);
     if (step) {
         a.tile = p.T > 0 ? p.T : 1;  // one sequence per tile: its state is read and written by the same threads
         a.tiles = p.B;
     } else {
-        a.tile = conv_tile(a.seqs.rows, ceil_div(ceil_div(p.D, V), kConvThreads), 16, 64);
+        a.tile = conv_tile(a.seqs.rows, ceil_div(ceil_div(p.D, V), kConvThreads), kFwdPerSM, 3,
+                           p.dtype == KDA_DTYPE_BF16 ? kFwdBatch<bf16> : kFwdBatch<float>);
         a.tiles = ceil_div(a.seqs.rows, a.tile);
         if (a.tiles < 1) a.tiles = 1;
     }
@@ -499,11 +558,9 @@ ConvBwdPlan conv_bwd_plan(const kda_conv_bwd_params &p) {
     ConvBwdPlan q;
     const void *ptrs[] = {p.x, p.s0, p.dy, p.dst, p.dx, p.ds0};
     const int64_t rows = p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.B * p.T;
-    #ifndef BV
-#define BV 4
-#endif
-    q.V = conv_vec(p.dtype, p.D, p.x_stride != 0 ? p.x_stride : p.D, BV, ptrs, 6);
-    q.tile = conv_tile(rows, ceil_div(ceil_div(p.D, q.V), kConvThreads), 16, 256);
+    q.V = conv_vec(p.dtype, p.D, p.x_stride != 0 ? p.x_stride : p.D, ptrs, 6);
+    q.tile = conv_tile(rows, ceil_div(ceil_div(p.D, q.V), kConvThreads), 
+                       p.dtype == KDA_DTYPE_BF16 ? kBwdPerSM<bf16> : kBwdPerSM<float>, 2, kBwdBatch);
     q.tiles = ceil_div(rows, q.tile);
     if (q.tiles < 1) q.tiles = 1;
     q.bytes = (size_t)q.tiles * p.D * (p.W + 1) * sizeof(float);
@@ -558,6 +615,7 @@ int kda_conv_bwd(const kda_conv_bwd_params *p, cudaStream_t stream) {
     a.xs = p->x_stride != 0 ? p->x_stride : p->D;
     a.D = p->D;
     a.silu = p->activation == KDA_ACT_SILU;
+    a.wvec = aligned(p->weight, 16);
     a.tile = q.tile;
     a.tiles = q.tiles;
     a.seqs = Seqs{p->cu_seqlens, p->B, p->T, p->cu_seqlens != nullptr ? (int64_t)p->T : (int64_t)p->B * p->T};

@@ -345,55 +345,88 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const ScanArgs a) {
     }
 }
 
-// The next T tokens of each sequence: 4 lanes per channel as above, no tiles. Bound by
-// reading and writing the states (8 bytes per state; everything else is 1 / 16 of that).
+// The next T tokens of each sequence. Four lanes share four channels: each lane holds a quarter of the
+// states of all four (a warp reads 512 contiguous bytes of states at a time, four such reads in flight
+// per thread), prepares the step size and the gate of one of them and passes the step size on to
+// the others; the four outputs are added across the lanes so that each lane ends with its own
+// channel's. Bound by reading and writing the states (8 bytes per state; the rest is 1 / 16 of that).
 template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanArgs a) {
-    const int tid = threadIdx.x, nl = tid & 3;
-    const int nblk = (a.ch + kDB - 1) / kDB;
+__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs a) {
+    const int tid = threadIdx.x, lane = tid & 31, nl = tid & 3, n0 = nl * NP;
+    const int nblk = (a.ch + 255) / 256;
     const int64_t seq = blockIdx.x / nblk;
-    const int d = (int)(blockIdx.x % nblk) * kDB + (tid >> 2);
-    const bool live = d < a.ch;
-    const int dd = live ? d : a.ch - 1;  // every lane takes part in the exchanges
-    const int64_t at = (seq * a.ch + dd) * a.N;
-    float h[NP], An[NP];
-    if (NP == 4 && a.N == 16 && a.vec) {  // whole vectors
-        load_vec<float, NP>(h, a.h0 + at + nl * NP);
-        load_vec<float, NP>(An, a.A + (int64_t)dd * a.N + nl * NP);
-    } else {
-        load_states<NP>(h, a.h0, at, nl, a.N, true);
-        load_states<NP>(An, a.A, (int64_t)dd * a.N, nl, a.N, true);
-    }
-    const float bias = a.bias != nullptr ? a.bias[dd] : 0.f, D = a.D != nullptr ? a.D[dd] : 0.f;
-    const int g = dd / a.chg;
-    for (int t = 0; t < a.seqs.T; ++t) {
-        const int64_t r = seq * a.seqs.T + t;
-        const float u = to_f(static_cast<const T *>(a.u)[r * a.us + dd]);
-        const float delta = step_of<T>(to_f(static_cast<const T *>(a.dt)[r * a.dts + dd]) + bias, a.softplus);
-        const float x = delta * u;
-        const T *B = static_cast<const T *>(a.B) + r * a.bs + (int64_t)g * a.N;
-        const T *C = static_cast<const T *>(a.C) + r * a.cs + (int64_t)g * a.N;
-        float s = 0.f;
+    const int base = (int)(blockIdx.x % nblk) * 256 + (tid >> 5) * 32 + (lane >> 2);
+    const int own = base + nl * 8;  // the channel that this lane prepares and finishes
+    const bool live = own < a.ch;
+    const bool vec = a.vec_states && a.N == 4 * NP;
+    const bool one_group = a.G == 1 || a.chg % 32 == 0;  // of a warp's 32 channels
+    const int64_t at = seq * a.ch * a.N;
+    float h[4][NP], A2[4][NP];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int n = nl * NP + i;
-            const bool in = n < a.N;
-            const float b = in ? to_f(B[n]) : 0.f, c = in ? to_f(C[n]) : 0.f;
-            h[i] = fmaf(tc5::ex2(delta * (An[i] * kLog2e)), h[i], x * b);
-            s = fmaf(c, h[i], s);
+    for (int r = 0; r < 4; ++r) {
+        const int d = base + r * 8;
+        const int64_t dn = (int64_t)d * a.N;
+        if (vec && d < a.ch) {
+            load_vec<float, NP>(h[r], a.h0 + at + dn + n0);
+            load_vec<float, NP>(A2[r], a.A + dn + n0);
+        } else {
+            load_states<NP>(h[r], a.h0, at + dn, nl, a.N, d < a.ch);
+            load_states<NP>(A2[r], a.A, dn, nl, a.N, d < a.ch);
         }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (nl == 0 && live) {
-            s = fmaf(D, u, s);
-            if (a.z != nullptr) s *= act_value(to_f(static_cast<const T *>(a.z)[r * a.zs + dd]), true);
-            static_cast<T *>(a.y)[r * a.ch + dd] = from_f<T>(s);
-        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) A2[r][i] *= kLog2e;
     }
-    if (NP == 4 && a.N == 16 && a.vec) {
-        if (live) store_vec<float, NP>(a.ht + at + nl * NP, h);
-    } else {
-        store_states<NP>(h, a.ht, at, nl, a.N, live);
+    const float bias = a.bias != nullptr && live ? a.bias[own] : 0.f, D = a.D != nullptr && live ? a.D[own] : 0.f;
+    float B[NP], C[NP];
+    auto load_bc = [&](int64_t r, int d) {
+        const int g = (d < a.ch ? d : a.ch - 1) / a.chg;
+        const T *pB = static_cast<const T *>(a.B) + r * a.bs + (int64_t)g * a.N + n0;
+        const T *pC = static_cast<const T *>(a.C) + r * a.cs + (int64_t)g * a.N + n0;
+        if (a.vec && a.N == 4 * NP) {
+            load_vec<T, NP>(B, pB);
+            load_vec<T, NP>(C, pC);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                B[i] = n0 + i < a.N ? to_f(pB[i]) : 0.f;
+                C[i] = n0 + i < a.N ? to_f(pC[i]) : 0.f;
+            }
+        }
+    };
+    for (int t = 0; t < a.seqs.T; ++t) {
+        const int64_t row = seq * a.seqs.T + t;
+        float u = 0.f, s = 0.f, z = 0.f;
+        if (live) {
+            u = to_f(static_cast<const T *>(a.u)[row * a.us + own]);
+            s = to_f(static_cast<const T *>(a.dt)[row * a.dts + own]);
+            if (a.z != nullptr) z = to_f(static_cast<const T *>(a.z)[row * a.zs + own]);
+        }
+        if (one_group) load_bc(row, base);
+        const float delta = step_of<T>(s + bias, a.softplus), x = delta * u;
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (!one_group) load_bc(row, base + r * 8);
+            const float dr = __shfl_sync(0xffffffffu, delta, (lane & ~3) + r), xr = __shfl_sync(0xffffffffu, x, (lane & ~3) + r);
+            p[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                h[r][i] = fmaf(tc5::ex2(dr * A2[r][i]), h[r][i], xr * B[i]);
+                p[r] = fmaf(C[i], h[r][i], p[r]);
+            }
+        }
+        float y = fmaf(D, u, sum_lanes(p, nl));
+        if (a.z != nullptr) y *= act_value(z, true);
+        if (live) static_cast<T *>(a.y)[row * a.ch + own] = from_f<T>(y);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int d = base + r * 8;
+        const int64_t dn = at + (int64_t)d * a.N;
+        if (vec && d < a.ch)
+            store_vec<float, NP>(a.ht + dn + n0, h[r]);
+        else
+            store_states<NP>(h[r], a.ht, dn, nl, a.N, d < a.ch);
     }
 }
 
@@ -416,20 +449,20 @@ int fwd_channels(int N) { return N <= 16 ? 2 * kFThr : (N <= 32 ? kFThr : kFThr 
 
 template <typename T>
 cudaError_t launch_step(const ScanArgs &a, cudaStream_t stream) {
-    const int64_t grid = (int64_t)a.seqs.N * ceil_div(a.ch, kDB);
+    const int64_t grid = (int64_t)a.seqs.N * ceil_div(a.ch, 256);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     switch (np_of(a.N)) {
         case 2:
-            scan_step_kernel<T, 2><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+            scan_step_kernel<T, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
             break;
         case 4:
-            scan_step_kernel<T, 4><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+            scan_step_kernel<T, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
             break;
         case 8:
-            scan_step_kernel<T, 8><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+            scan_step_kernel<T, 8><<<(unsigned)grid, 256, 0, stream>>>(a);
             break;
         default:
-            scan_step_kernel<T, 16><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+            scan_step_kernel<T, 16><<<(unsigned)grid, 256, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
@@ -588,7 +621,11 @@ int kda_scan_step(const kda_scan_params *p, cudaStream_t stream) {
     ScanArgs a = scan_args(*p, nullptr, 0);
     a.y = p->y;
     a.ht = p->ht;
-    a.vec = aligned(p->A, 16) && aligned(p->h0, 16) && aligned(p->ht, 16);  // the states and A here
+    // B and C by the lane's quarter of the states (at most 16 bytes at a time)
+    const int np = np_of(p->N), e = elem_size(p->dtype);
+    const int span = np * e > 16 ? 16 : np * e;
+    a.vec = a.bs * e % span == 0 && a.cs * e % span == 0 && aligned(p->B, span) && aligned(p->C, span);
+    a.vec_states = aligned(p->A, 16) && aligned(p->h0, 16) && aligned(p->ht, 16);
     return status_of_cuda(p->dtype == KDA_DTYPE_BF16 ? launch_step<bf16>(a, stream) : launch_step<float>(a, stream));
 }
 
