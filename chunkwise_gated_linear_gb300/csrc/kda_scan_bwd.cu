@@ -47,40 +47,38 @@ struct BwdArgs {
 };
 
 // ---- 1: every chunk from zero ---------------------------------------------------------------
-template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads) scan_bwd_local_kernel(const BwdArgs b) {
+// As the forward kernel: a thread owns its channel's states (NS of them, LN lanes per channel), B and C come
+// from shared memory, the rest from memory four tokens ahead. One channel per thread: a second one
+// would need 128 registers for states, decays, products and adjoints alone.
+constexpr int kLThr = 128;
+template <typename T, int NS, int LN>
+__global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs b) {
+    constexpr int kNT = NS * LN, P2 = NS / 2, kChan = kLThr / LN;
+    constexpr int kBC = 2 * kWin * kNT / kLThr;
+    __shared__ __align__(16) float sB[kWin * kNT], sC[kWin * kNT];
     const ScanArgs &a = b.f;
-    constexpr int kNT = kLN * NP;
-    constexpr int kBC = 2 * kTK * kNT / kThreads;
-    static_assert(kTK == kWin, "a staged tile is a window");
-    extern __shared__ __align__(16) unsigned char smem[];
-    float4 (*sx)[kDB] = reinterpret_cast<float4 (*)[kDB]>(smem);             // delta, delta, x, x
-    float2 (*sg)[kDB] = reinterpret_cast<float2 (*)[kDB]>(smem + kTK * kDB * 16);  // g, g
-    float *sB = reinterpret_cast<float *>(smem + kTK * kDB * 24), *sC = sB + kTK * kNT;
-
     const int tid = threadIdx.x;
     const int nblk = a.G * a.blocks_per_group;
-    const Chans ch = chans_of(a, blockIdx.x % nblk);
+    const int blk = blockIdx.x % nblk;
     const int64_t part = blockIdx.x / nblk;
-    const int dl = tid >> 2, nl = tid & 3, slot = slot_of(dl);
-    const int d = ch.d0 + dl;
-    const bool live = dl < ch.n;
-    const int64_t dn = (int64_t)d * a.N, cn = (int64_t)a.ch * a.N;
+    const int g = blk / a.blocks_per_group;
+    const int first = (blk % a.blocks_per_group) * kChan + tid / LN;
+    const int n0 = (tid % LN) * NS;
+    const bool live = first < a.chg;
+    const int d = g * a.chg + (live ? first : 0);
+    const int64_t cn = (int64_t)a.ch * a.N, dn = (int64_t)d * a.N;
+    const bool vst = a.vec_states && a.N == kNT;
     const int64_t c0 = part * a.chunk;
     const int64_t c1 = c0 + a.chunk < a.seqs.rows ? c0 + a.chunk : a.seqs.rows;
     if (c0 >= c1) return;
     SeqAt at = seq_find(a.seqs, c0);
 
-    float h[NP], An[NP];
-    load_states<NP>(h, a.h0, at.s * cn + dn, nl, a.N, live && c0 == at.start && a.h0 != nullptr);
-    load_states<NP>(An, a.A, dn, nl, a.N, live);
+    f2 h[P2], A2[P2], P[P2], f[P2];
+    get_states<NS>(h, a.h0, at.s * cn + dn, n0, a.N, live && c0 == at.start && a.h0 != nullptr, vst);
+    get_states<NS>(A2, a.A, dn, n0, a.N, live, vst);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) An[i] *= kLog2e;
-    f2 hp[NP / 2], A2[NP / 2], P[NP / 2], f[NP / 2];
-    to_pairs<NP>(hp, h);
-    to_pairs<NP>(A2, An);
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) {
+    for (int i = 0; i < P2; ++i) {
+        A2[i] = mul2(A2[i], pk(kLog2e, kLog2e));
         P[i] = pk(1.f, 1.f);
         f[i] = 0;
     }
@@ -88,101 +86,115 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_local_kernel(const BwdArgs 
     // the adjoint from the end of a sequence: dht, through the decays since the chunk's start
     auto add_dht = [&]() {
         if (b.dht == nullptr) return;
-        float t[NP];
-        load_states<NP>(t, b.dht, at.s * cn + dn, nl, a.N, live);
-        f2 t2[NP / 2];
-        to_pairs<NP>(t2, t);
+        f2 t[P2];
+        get_states<NS>(t, b.dht, at.s * cn + dn, n0, a.N, live, vst);
 #pragma unroll
-        for (int i = 0; i < NP / 2; ++i) f[i] = fma2(P[i], t2[i], f[i]);
+        for (int i = 0; i < P2; ++i) f[i] = fma2(P[i], t[i], f[i]);
     };
+    const float bias = a.bias != nullptr ? a.bias[d] : 0.f;
+    const bool gate = a.z != nullptr;
 
-    const int tr = tid >> 3, tc = (tid & 7) * 8;
-    const int nc = ch.n - tc;
-    const int64_t dc = ch.d0 + tc;
-    float bias8[8];
+    T nu[4], ndt[4], ndy[4], nz[4];
+    auto fetch = [&](int64_t r0) {
+        const T *pu = static_cast<const T *>(a.u) + r0 * a.us, *pd = static_cast<const T *>(a.dt) + r0 * a.dts;
+        const T *py = static_cast<const T *>(b.dy) + r0 * a.ch, *pz = static_cast<const T *>(a.z) + r0 * a.zs;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bias8[j] = a.bias != nullptr && j < nc ? a.bias[dc + j] : 0.f;
-    Raw<T, 8> nu, ndt, nz, ndy;
+        for (int k = 0; k < 4; ++k)
+            if (r0 + k < c1) {
+                nu[k] = pu[k * a.us + d];
+                ndt[k] = pd[k * a.dts + d];
+                ndy[k] = py[(int64_t)k * a.ch + d];
+                if (gate) nz[k] = pz[k * a.zs + d];
+            }
+    };
     float nbc[kBC];
-    auto fetch = [&](int64_t t0) {
-        const int64_t r = t0 + tr;
-        const int n = r < c1 ? nc : 0;
-        load8<T>(nu, a.u, r * a.us + dc, n, a.vec);
-        load8<T>(ndt, a.dt, r * a.dts + dc, n, a.vec);
-        load8<T>(ndy, b.dy, r * a.ch + dc, n, a.vec);
-        if (a.z != nullptr) load8<T>(nz, a.z, r * a.zs + dc, n, a.vec);
+    auto fetch_bc = [&](int64_t t0) {
 #pragma unroll
         for (int k = 0; k < kBC; ++k) {
-            const int e = (tid + k * kThreads) % (kTK * kNT);
             const bool isC = k >= kBC / 2;
-            const int64_t rr = t0 + e / kNT;
-            const int n2 = e % kNT;
-            nbc[k] = rr < c1 && n2 < a.N
-                         ? to_f(static_cast<const T *>(isC ? a.C : a.B)[rr * (isC ? a.cs : a.bs) + (int64_t)ch.g * a.N + n2])
+            const int e = (tid + k * kLThr) % (kWin * kNT);
+            const int64_t r = t0 + e / kNT;
+            const int n = e % kNT;
+            nbc[k] = r < c1 && n < a.N
+                         ? to_f(static_cast<const T *>(isC ? a.C : a.B)[r * (isC ? a.cs : a.bs) + (int64_t)g * a.N + n])
                          : 0.f;
         }
     };
+    auto token = [&](int t, T ru, T rdt, T rdy, T rz) {
+        const float delta = step_of<T>(to_f(rdt) + bias, a.softplus), x = delta * to_f(ru);
+        const float gy = gate ? to_f(rdy) * act_value(to_f(rz), true) : to_f(rdy);
+        const f2 d2 = pk(delta, delta), x2 = pk(x, x), g2 = pk(gy, gy);
+        S += delta;
+#pragma unroll
+        for (int i = 0; i < P2; i += 2) {
+            const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sB[t * kNT + n0 + 2 * i]);
+            const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sC[t * kNT + n0 + 2 * i]);
+            const f2 e0 = exp2_2(mul2(d2, A2[i])), e1 = exp2_2(mul2(d2, A2[i + 1]));
+            h[i] = fma2(e0, h[i], mul2(x2, B.x));
+            h[i + 1] = fma2(e1, h[i + 1], mul2(x2, B.y));
+            P[i] = mul2(P[i], e0);
+            P[i + 1] = mul2(P[i + 1], e1);
+            f[i] = fma2(P[i], mul2(g2, C.x), f[i]);
+            f[i + 1] = fma2(P[i + 1], mul2(g2, C.y), f[i + 1]);
+        }
+    };
     fetch(c0);
-    for (int64_t t0 = c0; t0 < c1; t0 += kTK) {
+    fetch_bc(c0);
+    for (int64_t t0 = c0; t0 < c1; t0 += kWin) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool in = t0 + tr < c1 && j < nc;
-            const float delta = in ? step_of<T>(ndt.get(j) + bias8[j], a.softplus) : 0.f;
-            const float x = delta * nu.get(j);
-            float g = in ? ndy.get(j) : 0.f;
-            if (a.z != nullptr) g *= in ? act_value(nz.get(j), true) : 0.f;
-            sx[tr][slot_of(tc + j)] = make_float4(delta, delta, x, x);
-            sg[tr][slot_of(tc + j)] = make_float2(g, g);
-        }
-#pragma unroll
-        for (int k = 0; k < kBC; ++k) {
-            const int e = (tid + k * kThreads) % (kTK * kNT);
-            (k < kBC / 2 ? sB : sC)[e] = nbc[k];
-        }
+        for (int k = 0; k < kBC; ++k) (k < kBC / 2 ? sB : sC)[(tid + k * kLThr) % (kWin * kNT)] = nbc[k];
         __syncthreads();
-        if (t0 + kTK < c1) fetch(t0 + kTK);
+        if (t0 + kWin < c1) fetch_bc(t0 + kWin);
         if (t0 > c0) {  // the state before this window
-            from_pairs<NP>(h, hp);
-            store_states<NP>(h, b.hwin, (t0 / kWin) * cn + dn, nl, a.N, live);
-            if (live && nl == 0) b.swin[(t0 / kWin) * a.ch + d] = S;
+            put_states<NS>(h, b.hwin, (t0 / kWin) * cn + dn, n0, a.N, live, a.N == kNT);
+            if (live && n0 == 0) b.swin[(t0 / kWin) * a.ch + d] = S;
         }
-        const int64_t tile_end = t0 + kTK < c1 ? t0 + kTK : c1;
-        const bool ragged = at.end < tile_end;
-        const int steps = ragged ? (int)(tile_end - t0) : kTK;  // rows past the end change nothing
-#pragma unroll 4
-        for (int t = 0; t < steps; ++t) {
-            if (ragged && t0 + t == at.end) {
-                add_dht();
+#pragma unroll 1
+        for (int t = 0; t < kWin; t += 4) {
+            const int64_t r = t0 + t;
+            if (r >= c1) break;
+            T cu_[4], cdt[4], cdy[4], cz[4];
 #pragma unroll
-                for (int i = 0; i < NP / 2; ++i) P[i] = 0;
-                seq_next(a.seqs, at);
-                load_states<NP>(h, a.h0, at.s * cn + dn, nl, a.N, live && a.h0 != nullptr);
-                to_pairs<NP>(hp, h);
+            for (int k = 0; k < 4; ++k) {
+                cu_[k] = nu[k];
+                cdt[k] = ndt[k];
+                cdy[k] = ndy[k];
+                cz[k] = nz[k];
             }
-            const ulonglong2 dx = *reinterpret_cast<const ulonglong2 *>(&sx[t][slot]);
-            const f2 g2 = *reinterpret_cast<const f2 *>(&sg[t][slot]);
-            f2 B[NP / 2], C[NP / 2];
-            lds_pairs<NP>(B, sB + t * kNT + nl * NP);
-            lds_pairs<NP>(C, sC + t * kNT + nl * NP);
-            float delta, same;
-            upk(dx.x, delta, same);
-            S += delta;
+            if (r + 4 < c1) fetch(r + 4);
+            if (r + 4 <= c1 && r + 4 <= at.end) {
 #pragma unroll
-            for (int i = 0; i < NP / 2; ++i) {
-                const f2 e = exp2_2(mul2(dx.x, A2[i]));
-                hp[i] = fma2(e, hp[i], mul2(dx.y, B[i]));
-                P[i] = mul2(P[i], e);
-                f[i] = fma2(P[i], mul2(g2, C[i]), f[i]);
+                for (int k = 0; k < 4; ++k) token(t + k, cu_[k], cdt[k], cdy[k], cz[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (r + k >= c1) break;
+                    if (r + k == at.end) {
+                        add_dht();
+#pragma unroll
+                        for (int i = 0; i < P2; ++i) P[i] = 0;
+                        seq_next(a.seqs, at);
+                        get_states<NS>(h, a.h0, at.s * cn + dn, n0, a.N, live && a.h0 != nullptr, vst);
+                    }
+                    token(t + k, cu_[k], cdt[k], cdy[k], cz[k]);
+                }
             }
         }
     }
     if (c1 == at.end) add_dht();
-    from_pairs<NP>(h, hp);
-    store_states<NP>(h, a.hchunk, part * cn + dn, nl, a.N, live);
-    from_pairs<NP>(h, f);
-    store_states<NP>(h, b.gchunk, part * cn + dn, nl, a.N, live);
-    if (live && nl == 0) a.schunk[part * a.ch + d] = S;
+    put_states<NS>(h, a.hchunk, part * cn + dn, n0, a.N, live, a.N == kNT);
+    put_states<NS>(f, b.gchunk, part * cn + dn, n0, a.N, live, a.N == kNT);
+    if (live && n0 == 0) a.schunk[part * a.ch + d] = S;
+}
+
+template <typename T, int NS, int LN>
+cudaError_t launch_local(BwdArgs b, cudaStream_t stream) {
+    b.f.blocks_per_group = (int)ceil_div(b.f.chg, kLThr / LN);
+    const int64_t grid = b.f.nchunks * b.f.G * b.f.blocks_per_group;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    scan_bwd_local_kernel<T, NS, LN><<<(unsigned)grid, kLThr, 0, stream>>>(b);
+    return cudaGetLastError();
 }
 
 // ---- 2: between the chunks, in place ----------------------------------------------------------
@@ -660,14 +672,13 @@ cudaError_t launch_np(const BwdArgs &b, cudaStream_t stream) {
     const int64_t nblk = (int64_t)a.G * a.blocks_per_group;
     if (nblk * a.nchunks > INT32_MAX) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(nblk * a.nchunks);
-    const int local_smem = kTK * kDB * 24 + 2 * kTK * kLN * NP * 4;
-    cudaError_t e = cudaFuncSetAttribute(scan_bwd_local_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, local_smem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(scan_bwd_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdShape<NP>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdShape<NP>::kSmem);
     if (e != cudaSuccess) return e;
     if (a.seqs.rows > kWin) {  // one window: nothing to hand over
-        scan_bwd_local_kernel<T, NP><<<grid, kThreads, local_smem, stream>>>(b);
-        e = cudaGetLastError();
+        if constexpr (NP == 2)
+            e = launch_local<T, 8, 1>(b, stream);
+        else
+            e = launch_local<T, 16, NP / 4>(b, stream);
         if (e != cudaSuccess) return e;
     }
     if (a.nchunks > 1) {
@@ -776,6 +787,7 @@ int kda_scan_bwd(const kda_scan_bwd_params *p, cudaStream_t stream) {
     b.f = scan_args(p->f, more, 4);
     b.f.chunk = q.chunk;
     b.f.nchunks = q.nchunks;
+    b.f.vec_states = aligned(p->f.A, 16) && aligned(p->f.h0, 16) && aligned(p->dht, 16) && p->f.N % 4 == 0;
     b.dy = p->dy;
     b.dht = p->dht;
     b.du = p->du;

@@ -144,6 +144,43 @@ __device__ __forceinline__ void lds_pairs(f2 (&p)[NP / 2], const float *s) {
     }
 }
 
+// A thread's NS states of a channel, at `at` = first state of [..][N], zeros past N.
+template <int NS>
+__device__ __forceinline__ void get_states(f2 (&h)[NS / 2], const float *base, int64_t at, int n0, int N, bool live, bool vec) {
+    if (live && vec) {
+#pragma unroll
+        for (int i = 0; i < NS / 4; ++i) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(base + at + n0 + 4 * i);
+            h[2 * i] = q.x;
+            h[2 * i + 1] = q.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const int n = n0 + 2 * i;
+            h[i] = pk(live && n < N ? base[at + n] : 0.f, live && n + 1 < N ? base[at + n + 1] : 0.f);
+        }
+    }
+}
+template <int NS>
+__device__ __forceinline__ void put_states(const f2 (&h)[NS / 2], float *base, int64_t at, int n0, int N, bool live, bool vec) {
+    if (!live) return;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < NS / 4; ++i)
+            *reinterpret_cast<ulonglong2 *>(base + at + n0 + 4 * i) = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const int n = n0 + 2 * i;
+            float lo, hi;
+            upk(h[i], lo, hi);
+            if (n < N) base[at + n] = lo;
+            if (n + 1 < N) base[at + n + 1] = hi;
+        }
+    }
+}
+
 // Slot of channel d (0..63) in a row of 64: rotated inside groups of 8 so that eight lanes
 // which write eight groups' same channel use different banks.
 __device__ __forceinline__ int slot_of(int d) { return (d & ~7) | ((d ^ (d >> 3)) & 7); }
