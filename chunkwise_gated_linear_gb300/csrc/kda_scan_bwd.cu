@@ -17,8 +17,8 @@
 //   2. scan_bwd_carry_kernel: true states at the chunk starts, true adjoints at the ends.
 //   3. scan_bwd_kernel: per chunk and 64 channels, windows last to first. A window's start state
 //      is its local state plus exp(A sum delta) times the chunk's start state; from there the
-//      states at every fourth token go to shared memory, and groups of four tokens are taken last to first:
-//      a and a h_{t-1} of four tokens in registers, then backwards.
+//      states before every group of (up to) four tokens go to shared memory, and the groups are taken
+//      last to first: a and a h_{t-1} of their tokens in registers, then backwards.
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
 // fixed order. About 20 instructions per (token, channel, state): bound by issue.
@@ -29,8 +29,8 @@ namespace scan {
 
 namespace {
 
-constexpr int kWin = 32;        // tokens per window
-constexpr int kGroups = kWin / 4;
+// Tokens per window: what the third kernel keeps states of in shared memory.
+__host__ __device__ constexpr int win_of(int np) { return np <= 4 ? 32 : (np == 8 ? 16 : 8); }
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdArgs {
@@ -51,11 +51,12 @@ struct BwdArgs {
 // from shared memory, the rest from memory four tokens ahead. One channel per thread: a second one
 // would need 128 registers for states, decays, products and adjoints alone.
 constexpr int kLThr = 128;
-template <typename T, int NS, int LN>
+template <typename T, int NS, int LN, int WIN>
 __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs b) {
     constexpr int kNT = NS * LN, P2 = NS / 2, kChan = kLThr / LN;
-    constexpr int kBC = 2 * kWin * kNT / kLThr;
-    __shared__ __align__(16) float sB[kWin * kNT], sC[kWin * kNT];
+    constexpr int kTile = 32;  // tokens of B and C in shared memory
+    constexpr int kBC = 2 * kTile * kNT / kLThr;
+    __shared__ __align__(16) float sB[kTile * kNT], sC[kTile * kNT];
     const ScanArgs &a = b.f;
     const int tid = threadIdx.x;
     const int nblk = a.G * a.blocks_per_group;
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
 #pragma unroll
         for (int k = 0; k < kBC; ++k) {
             const bool isC = k >= kBC / 2;
-            const int e = (tid + k * kLThr) % (kWin * kNT);
+            const int e = (tid + k * kLThr) % (kTile * kNT);
             const int64_t r = t0 + e / kNT;
             const int n = e % kNT;
             nbc[k] = r < c1 && n < a.N
@@ -140,20 +141,20 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
     };
     fetch(c0);
     fetch_bc(c0);
-    for (int64_t t0 = c0; t0 < c1; t0 += kWin) {
+    for (int64_t t0 = c0; t0 < c1; t0 += kTile) {
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kBC; ++k) (k < kBC / 2 ? sB : sC)[(tid + k * kLThr) % (kWin * kNT)] = nbc[k];
+        for (int k = 0; k < kBC; ++k) (k < kBC / 2 ? sB : sC)[(tid + k * kLThr) % (kTile * kNT)] = nbc[k];
         __syncthreads();
-        if (t0 + kWin < c1) fetch_bc(t0 + kWin);
-        if (t0 > c0) {  // the state before this window
-            put_states<NS>(h, b.hwin, (t0 / kWin) * cn + dn, n0, a.N, live, a.N == kNT);
-            if (live && n0 == 0) b.swin[(t0 / kWin) * a.ch + d] = S;
-        }
+        if (t0 + kTile < c1) fetch_bc(t0 + kTile);
 #pragma unroll 1
-        for (int t = 0; t < kWin; t += 4) {
+        for (int t = 0; t < kTile; t += 4) {
             const int64_t r = t0 + t;
             if (r >= c1) break;
+            if (t % WIN == 0 && r > c0) {  // the state before a window
+                put_states<NS>(h, b.hwin, (r / WIN) * cn + dn, n0, a.N, live, a.N == kNT);
+                if (live && n0 == 0) b.swin[(r / WIN) * a.ch + d] = S;
+            }
             T cu_[4], cdt[4], cdy[4], cz[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -188,12 +189,12 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
     if (live && n0 == 0) a.schunk[part * a.ch + d] = S;
 }
 
-template <typename T, int NS, int LN>
+template <typename T, int NS, int LN, int WIN>
 cudaError_t launch_local(BwdArgs b, cudaStream_t stream) {
     b.f.blocks_per_group = (int)ceil_div(b.f.chg, kLThr / LN);
     const int64_t grid = b.f.nchunks * b.f.G * b.f.blocks_per_group;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    scan_bwd_local_kernel<T, NS, LN><<<(unsigned)grid, kLThr, 0, stream>>>(b);
+    scan_bwd_local_kernel<T, NS, LN, WIN><<<(unsigned)grid, kLThr, 0, stream>>>(b);
     return cudaGetLastError();
 }
 
@@ -257,156 +258,163 @@ __device__ __forceinline__ float sum_channels(const float (&v)[8], int lane) {
     return k + __shfl_xor_sync(0xffffffffu, s, 4);
 }
 
-// R channels per thread: two while their states are few (half the exchanges per state).
+// A block: 128 threads, 64 channels. Warp w has channels 16 w .. 16 w + 15: thread (dl, nl) = (lane / 4,
+// lane % 4) has channels 16 w + dl and 16 w + 8 + dl, as the two halves of every pair, and states
+// nl NP .. nl NP + NP - 1 of both: step sizes, inputs and gradients of a pair come as pairs,
+// B and C (the same for all channels) are kept doubled in shared memory.
 template <int NP>
 struct BwdShape {
-    static constexpr int R = NP <= 4 ? 2 : 1;
-    static constexpr int E = R * NP;               // states per thread
-    static constexpr int kThr = kDB * kLN / R;
-    static constexpr int kWarps = kThr / 32;
+    static constexpr int kThr = 128, kWarps = 4;
     static constexpr int kNT = kLN * NP;
-    static constexpr int kCkpt = kGroups * E * kThr * 4;  // states at every fourth token
-    static constexpr int kTile = kWin * kDB * 16;         // delta, x, g; then s, w, y
-    static constexpr int kBCBytes = 2 * kWin * kNT * 4;
-    static constexpr int kFlags = kWin * 8;               // per row: sequence, start / end bits
-    static constexpr int kSmem = kCkpt + kTile + kBCBytes + kFlags;
+    static constexpr int kWin = win_of(NP);
+    // tokens whose decays are held in registers while they are walked back
+    static constexpr int kSC = NP <= 4 ? 4 : (NP == 8 ? 2 : 1);
+    static constexpr int kGroups = kWin / kSC;
+    static constexpr int kCkpt = kGroups * 2 * NP * kThr * 4;  // states before every group of tokens
+    static constexpr int kTileA = kWin * 32 * 16;              // delta and x of a pair; then s and w
+    static constexpr int kTileG = kWin * 32 * 8;               // g; then y
+    static constexpr int kTileD = kWin * 32 * 8;               // delta
+    static constexpr int kBCBytes = 2 * kWin * kNT * 8;
+    static constexpr int kFlags = kWin * 8;                    // per row: sequence, start / end bits
+    static constexpr int kSmem = kCkpt + kTileA + kTileG + kTileD + kBCBytes + kFlags;
 };
+
+// Place of pair dl of warp w in a tile's row t: rotated so that the threads that fill a tile row by row
+// (8 channels of one half each) do not all meet in the same banks.
+__device__ __forceinline__ int pair_slot(int t, int w, int dl) { return w * 8 + ((dl ^ (w + 4 * (t & 1))) & 7); }
 
 template <typename T, int NP>
 struct BwdBlock {
     using S = BwdShape<NP>;
-    static constexpr int R = S::R, P2 = NP / 2;
     const BwdArgs &b;
-    float4 *tile;        // [kWin][kDB]
-    const float *sB, *sC;
-    float4 *ckpt;        // [kGroups][kWarps][E / 4][32]
+    float4 *tileA;       // [kWin][32]
+    float2 *tileG;       // [kWin][32]
+    const f2 *sB, *sC;   // [kWin][kNT], doubled
+    float4 *ckpt;        // [kGroups][kWarps][NP / 2][32]
     const int *seq_of, *flag_of;
-    int lane, warp, nl;
-    int dl[R];           // the thread's channels in the block
-    int64_t dn[R];       // and their place in [ch][N]
-    bool live[R];
-    f2 A2[R][P2], G[R][P2], dA[R][P2];
+    int lane, warp, nl, dl;
+    int64_t dn0, dn1;    // the two channels' places in [ch][N]
+    bool live0, live1;
+    f2 A2[NP], G[NP], dA[NP];
 
     __device__ __forceinline__ BwdBlock(const BwdArgs &args) : b(args) {}
-    __device__ __forceinline__ float *group_mem(int g) const {
-        return reinterpret_cast<float *>(ckpt + (g * S::kWarps + warp) * (S::E / 4) * 32);
-    }
-    __device__ __forceinline__ void state_of(f2 (&h)[R][P2], const float *base, int s) const {
-        const ScanArgs &a = b.f;
+    __device__ __forceinline__ float4 *group_mem(int g) const { return ckpt + (g * S::kWarps + warp) * (NP / 2) * 32; }
+    // the pair's states at `at` (of [..][ch][N])
+    __device__ __forceinline__ void states(f2 (&h)[NP], const float *base, int64_t at) const {
+        float lo[NP], hi[NP];
+        load_states<NP>(lo, base, at + dn0, nl, b.f.N, live0 && base != nullptr);
+        load_states<NP>(hi, base, at + dn1, nl, b.f.N, live1 && base != nullptr);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float t[NP];
-            load_states<NP>(t, base, s * (int64_t)a.ch * a.N + dn[r], nl, a.N, live[r] && base != nullptr);
-            to_pairs<NP>(h[r], t);
+        for (int i = 0; i < NP; ++i) h[i] = pk(lo[i], hi[i]);
+    }
+    __device__ __forceinline__ void put(const f2 (&h)[NP], float *base, int64_t at) const {
+        float lo[NP], hi[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) upk(h[i], lo[i], hi[i]);
+        store_states<NP>(lo, base, at + dn0, nl, b.f.N, live0);
+        store_states<NP>(hi, base, at + dn1, nl, b.f.N, live1);
+    }
+    __device__ __forceinline__ int64_t seq_at(int t) const { return seq_of[t] * (int64_t)b.f.ch * b.f.N; }
+    __device__ __forceinline__ void row_bc(f2 (&v)[NP], const f2 *s, int t) const {
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            const ulonglong2 q = reinterpret_cast<const ulonglong2 *>(s + t * S::kNT + nl * NP)[i];
+            v[2 * i] = q.x;
+            v[2 * i + 1] = q.y;
         }
     }
-    // states before tokens 0, 4, .. of the window into shared memory, from the state h before it
+    // delta and x of the pair at token t
+    __device__ __forceinline__ void row_dx(f2 &d2, f2 &x2, int t) const {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(&tileA[t * 32 + pair_slot(t, warp, dl)]);
+        d2 = q.x;
+        x2 = q.y;
+    }
+    // states before every group of tokens into shared memory, from the state h before the window
     template <bool RAG>
-    __device__ __forceinline__ void forward(f2 (&h)[R][P2]) const {
-        for (int g = 0; g < kGroups; ++g) {
-            float4 *to = reinterpret_cast<float4 *>(group_mem(g));
+    __device__ __forceinline__ void forward(f2 (&h)[NP]) const {
+#pragma unroll 1
+        for (int g = 0; g < S::kGroups; ++g) {
+            float4 *to = group_mem(g);
 #pragma unroll
-            for (int q = 0; q < S::E / 4; ++q) {
-                const f2 lo = h[(4 * q) / NP][((4 * q) % NP) / 2], hi = h[(4 * q + 2) / NP][((4 * q + 2) % NP) / 2];
-                float4 v;
-                upk(lo, v.x, v.y);
-                upk(hi, v.z, v.w);
-                to[q * 32 + lane] = v;
-            }
-            if (g == kGroups - 1) break;
+            for (int q = 0; q < NP / 2; ++q) *reinterpret_cast<ulonglong2 *>(&to[q * 32 + lane]) = make_ulonglong2(h[2 * q], h[2 * q + 1]);
+            if (g == S::kGroups - 1) break;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = 4 * g + k;
-                if (RAG && (flag_of[t] & 1)) state_of(h, b.f.h0, seq_of[t]);
-                f2 B[P2];
-                lds_pairs<NP>(B, sB + t * S::kNT + nl * NP);
+            for (int k = 0; k < S::kSC; ++k) {
+                const int t = S::kSC * g + k;
+                if (RAG && (flag_of[t] & 1)) states(h, b.f.h0, seq_at(t));
+                f2 B[NP], d2, x2;
+                row_bc(B, sB, t);
+                row_dx(d2, x2, t);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float2 dx = *reinterpret_cast<const float2 *>(&tile[t * kDB + slot_of(dl[r])]);
-                    const f2 d2 = pk(dx.x, dx.x), x2 = pk(dx.y, dx.y);
-#pragma unroll
-                    for (int i = 0; i < P2; ++i) h[r][i] = fma2(exp2_2(mul2(d2, A2[r][i])), h[r][i], mul2(x2, B[i]));
-                }
+                for (int i = 0; i < NP; ++i) h[i] = fma2(exp2_2(mul2(d2, A2[i])), h[i], mul2(x2, B[i]));
             }
         }
     }
-    // tokens 4 g + 3 .. 4 g of the window
+    // the tokens of group g, last to first
     template <bool RAG>
     __device__ __forceinline__ void backward(int g) {
-        float *mem = group_mem(g);
-        f2 h[R][P2], e[4][R][P2], eh[4][R][P2];
-        float dlt[4][R], x[4][R], gr[4][R];
+        float4 *mem = group_mem(g);
+        f2 h[NP], e[S::kSC][NP], eh[S::kSC][NP];
 #pragma unroll
-        for (int q = 0; q < S::E / 4; ++q) {
-            const float4 v = reinterpret_cast<const float4 *>(mem)[q * 32 + lane];
-            h[(4 * q) / NP][((4 * q) % NP) / 2] = pk(v.x, v.y);
-            h[(4 * q + 2) / NP][((4 * q + 2) % NP) / 2] = pk(v.z, v.w);
+        for (int q = 0; q < NP / 2; ++q) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&mem[q * 32 + lane]);
+            h[2 * q] = v.x;
+            h[2 * q + 1] = v.y;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int t = 4 * g + k;
-            if (RAG && (flag_of[t] & 1)) state_of(h, b.f.h0, seq_of[t]);
-            f2 B[P2];
-            lds_pairs<NP>(B, sB + t * S::kNT + nl * NP);
+        for (int k = 0; k < S::kSC; ++k) {
+            const int t = S::kSC * g + k;
+            if (RAG && (flag_of[t] & 1)) states(h, b.f.h0, seq_at(t));
+            f2 B[NP], d2, x2;
+            row_bc(B, sB, t);
+            row_dx(d2, x2, t);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 q = tile[t * kDB + slot_of(dl[r])];
-                dlt[k][r] = q.x;
-                x[k][r] = q.y;
-                gr[k][r] = q.z;
-                const f2 d2 = pk(q.x, q.x), x2 = pk(q.y, q.y);
-#pragma unroll
-                for (int i = 0; i < P2; ++i) {
-                    e[k][r][i] = exp2_2(mul2(d2, A2[r][i]));
-                    eh[k][r][i] = mul2(e[k][r][i], h[r][i]);
-                    h[r][i] = fma2(x2, B[i], eh[k][r][i]);
-                }
+            for (int i = 0; i < NP; ++i) {
+                e[k][i] = exp2_2(mul2(d2, A2[i]));
+                eh[k][i] = mul2(e[k][i], h[i]);
+                h[i] = fma2(x2, B[i], eh[k][i]);
             }
         }
         __syncwarp();  // the group's states have been read: its memory takes dB and dC
-        float s[R][4], w[R][4], y[R][4];
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
-            const int t = 4 * g + k;
-            if (RAG && (flag_of[t] & 2)) state_of(G, b.dht, seq_of[t]);
-            f2 B[P2], C[P2], dB[P2], dC[P2];
-            lds_pairs<NP>(B, sB + t * S::kNT + nl * NP);
-            lds_pairs<NP>(C, sC + t * S::kNT + nl * NP);
+        for (int k = S::kSC - 1; k >= 0; --k) {
+            const int t = S::kSC * g + k;
+            if (RAG && (flag_of[t] & 2)) states(G, b.dht, seq_at(t));
+            f2 B[NP], C[NP], d2, x2, s2 = 0, w2 = 0, y2 = 0;
+            row_bc(B, sB, t);
+            row_bc(C, sC, t);
+            row_dx(d2, x2, t);
+            const int at = t * 32 + pair_slot(t, warp, dl);
+            const f2 g2 = *reinterpret_cast<const f2 *>(&tileG[at]);
+            float vb[NP], vc[NP];  // the pair's share of dB and dC
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const f2 d2 = pk(dlt[k][r], dlt[k][r]), x2 = pk(x[k][r], x[k][r]), g2 = pk(gr[k][r], gr[k][r]);
-                f2 s2 = 0, w2 = 0, y2 = 0;
-#pragma unroll
-                for (int i = 0; i < P2; ++i) {
-                    const f2 l = fma2(g2, C[i], G[r][i]);
-                    const f2 ht = fma2(x2, B[i], eh[k][r][i]);
-                    const f2 q = mul2(l, eh[k][r][i]);
-                    dB[i] = r == 0 ? mul2(l, x2) : fma2(l, x2, dB[i]);
-                    dC[i] = r == 0 ? mul2(ht, g2) : fma2(ht, g2, dC[i]);
-                    s2 = i == 0 ? mul2(l, B[i]) : fma2(l, B[i], s2);
-                    y2 = i == 0 ? mul2(ht, C[i]) : fma2(ht, C[i], y2);
-                    w2 = i == 0 ? mul2(q, A2[r][i]) : fma2(q, A2[r][i], w2);
-                    dA[r][i] = fma2(q, d2, dA[r][i]);
-                    G[r][i] = mul2(l, e[k][r][i]);
-                }
-                s[r][k] = hsum2(s2);
-                w[r][k] = hsum2(w2);
-                y[r][k] = hsum2(y2);
+            for (int i = 0; i < NP; ++i) {
+                const f2 l = fma2(g2, C[i], G[i]);
+                const f2 ht = fma2(x2, B[i], eh[k][i]);
+                const f2 q = mul2(l, eh[k][i]);
+                vb[i] = hsum2(mul2(l, x2));
+                vc[i] = hsum2(mul2(ht, g2));
+                s2 = i == 0 ? mul2(l, B[i]) : fma2(l, B[i], s2);
+                y2 = i == 0 ? mul2(ht, C[i]) : fma2(ht, C[i], y2);
+                w2 = i == 0 ? mul2(q, A2[i]) : fma2(q, A2[i], w2);
+                dA[i] = fma2(q, d2, dA[i]);
+                G[i] = mul2(l, e[k][i]);
             }
-            if (RAG && (flag_of[t] & 1) && b.dh0 != nullptr) {
-                const ScanArgs &a = b.f;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float o[NP];
-                    from_pairs<NP>(o, G[r]);
-                    store_states<NP>(o, b.dh0, seq_of[t] * (int64_t)a.ch * a.N + dn[r], nl, a.N, live[r]);
-                }
-            }
-            // [which][4 NP] of token t, this warp's channels added up
-            float vb[NP], vc[NP];
-            from_pairs<NP>(vb, dB);
-            from_pairs<NP>(vc, dC);
-            float *to = mem + k * 2 * S::kNT;
+            if (RAG && (flag_of[t] & 1) && b.dh0 != nullptr) put(G, b.dh0, seq_at(t));
+            // over the states: lane nl gets s of the first, of the second channel, w of the first, of the second
+            float v4[4], y0, y1;
+            upk(s2, v4[0], v4[1]);
+            upk(w2, v4[2], v4[3]);
+            upk(y2, y0, y1);
+            const float sw = sum_lanes(v4, nl);
+            const bool odd = nl & 1;
+            float yy = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+            yy += __shfl_xor_sync(0xffffffffu, yy, 2);
+            __syncwarp();  // all four lanes have read this token's tile words
+            reinterpret_cast<float *>(&tileA[at])[nl] = nl < 2 ? sw : sw * kLn2;
+            if (nl < 2) reinterpret_cast<float *>(&tileG[at])[nl] = yy;
+            // over this warp's channels: [which][4 NP] of token t
+            float *to = reinterpret_cast<float *>(mem) + k * 2 * S::kNT;
             const int j = lane >> 2;
             if constexpr (NP >= 8) {
 #pragma unroll
@@ -427,19 +435,13 @@ struct BwdBlock {
                 if (j < 2 * NP) to[(j / NP) * S::kNT + nl * NP + j % NP] = tot;
             }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float s1 = sum_lanes(s[r], nl), w1 = sum_lanes(w[r], nl), y1 = sum_lanes(y[r], nl);
-            __syncwarp();
-            tile[(4 * g + nl) * kDB + slot_of(dl[r])] = make_float4(s1, w1 * kLn2, y1, 0.f);
-        }
     }
 };
 
 template <typename T, int NP>
-__global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdArgs b) {
+__global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_kernel(const BwdArgs b) {
     using S = BwdShape<NP>;
-    constexpr int R = S::R, P2 = NP / 2, kThr = S::kThr;
+    constexpr int kThr = S::kThr, kWin = S::kWin;
     constexpr int kRowsAt = kThr / 8;  // token rows staged at a time
     extern __shared__ __align__(16) unsigned char smem[];
     const ScanArgs &a = b.f;
@@ -452,59 +454,56 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
     if (blockIdx.x == 0) seq_check(a.seqs, a.err, tid, kThr);
 
     BwdBlock<T, NP> k(b);
-    k.ckpt = reinterpret_cast<float4 *>(smem);
-    k.tile = reinterpret_cast<float4 *>(smem + S::kCkpt);
-    float *sB = reinterpret_cast<float *>(smem + S::kCkpt + S::kTile), *sC = sB + kWin * S::kNT;
-    int *seq_of = reinterpret_cast<int *>(smem + S::kCkpt + S::kTile + S::kBCBytes), *flag_of = seq_of + kWin;
-    k.sB = sB;
-    k.sC = sC;
+    unsigned char *mem = smem;
+    auto take = [&](int bytes) {
+        unsigned char *p = mem;
+        mem += bytes;
+        return p;
+    };
+    k.ckpt = reinterpret_cast<float4 *>(take(S::kCkpt));
+    k.tileA = reinterpret_cast<float4 *>(take(S::kTileA));
+    k.tileG = reinterpret_cast<float2 *>(take(S::kTileG));
+    float *tileD = reinterpret_cast<float *>(take(S::kTileD));
+    float2 *sB = reinterpret_cast<float2 *>(take(S::kBCBytes));
+    int *seq_of = reinterpret_cast<int *>(take(S::kFlags)), *flag_of = seq_of + kWin;
+    k.sB = reinterpret_cast<const f2 *>(sB);
+    k.sC = k.sB + kWin * S::kNT;
     k.seq_of = seq_of;
     k.flag_of = flag_of;
     k.lane = tid & 31;
     k.warp = tid >> 5;
     k.nl = tid & 3;
+    k.dl = k.lane >> 2;
+    const int own = k.warp * 16 + k.dl;  // and own + 8
+    k.live0 = own < ch.n;
+    k.live1 = own + 8 < ch.n;
+    k.dn0 = (int64_t)(ch.d0 + own) * a.N;
+    k.dn1 = k.dn0 + 8 * (int64_t)a.N;
+    k.states(k.A2, a.A, 0);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        k.dl[r] = (k.warp * R + r) * 8 + (k.lane >> 2);
-        k.live[r] = k.dl[r] < ch.n;
-        k.dn[r] = (int64_t)(ch.d0 + k.dl[r]) * a.N;
-        float t[NP];
-        load_states<NP>(t, a.A, k.dn[r], k.nl, a.N, k.live[r]);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) t[i] *= kLog2e;
-        to_pairs<NP>(k.A2[r], t);
-#pragma unroll
-        for (int i = 0; i < P2; ++i) k.G[r][i] = k.dA[r][i] = 0;
+    for (int i = 0; i < NP; ++i) {
+        k.A2[i] = mul2(k.A2[i], pk(kLog2e, kLog2e));
+        k.dA[i] = 0;
     }
     // empty sequences: their final state is their initial one
     if (b.dh0 != nullptr)
         for (int64_t s = part; s < a.seqs.N; s += a.nchunks)
-            if (seq_empty(a.seqs, (int)s))
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float t[NP];
-                    load_states<NP>(t, b.dht, s * cn + k.dn[r], k.nl, a.N, k.live[r] && b.dht != nullptr);
-                    store_states<NP>(t, b.dh0, s * cn + k.dn[r], k.nl, a.N, k.live[r]);
-                }
+            if (seq_empty(a.seqs, (int)s)) {
+                f2 t[NP];
+                k.states(t, b.dht, s * cn);
+                k.put(t, b.dh0, s * cn);
+            }
 
     const int64_t c0 = part * a.chunk;
     const int64_t c1 = c0 + a.chunk < a.seqs.rows ? c0 + a.chunk : a.seqs.rows;
     const int tr0 = tid >> 3, tc = (tid & 7) * 8;
+    const int tw = tc >> 4, half = (tc >> 3) & 1;  // whose pairs these 8 channels belong to, and which half
     const int nc = ch.n - tc;
     const int64_t dc = ch.d0 + tc;
     float accD[8], accb[8];  // over this thread's tokens
 #pragma unroll
     for (int j = 0; j < 8; ++j) accD[j] = accb[j] = 0.f;
-
-    f2 hin[R][P2];  // the state before the chunk
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float t[NP];
-        load_states<NP>(t, a.hchunk, part * cn + k.dn[r], k.nl, a.N, k.live[r] && part > 0);
-        to_pairs<NP>(hin[r], t);
-        load_states<NP>(t, b.gchunk, part * cn + k.dn[r], k.nl, a.N, k.live[r] && part + 1 < a.nchunks);
-        to_pairs<NP>(k.G[r], t);
-    }
+    k.states(k.G, part + 1 < a.nchunks ? b.gchunk : nullptr, part * cn);
 
     const int64_t windows = c1 > c0 ? (c1 - c0 + kWin - 1) / kWin : 0;
     for (int64_t wi = windows - 1; wi >= 0; --wi) {
@@ -526,7 +525,11 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
                 const float delta = in ? step_of<T>(rdt.get(j) + bias, a.softplus) : 0.f;
                 float g = in ? rdy.get(j) : 0.f;
                 if (a.z != nullptr) g *= in ? act_value(rz.get(j), true) : 0.f;
-                k.tile[tr * kDB + slot_of(tc + j)] = make_float4(delta, in ? delta * ru.get(j) : 0.f, g, 0.f);
+                const int at = tr * 32 + pair_slot(tr, tw, j);
+                reinterpret_cast<float *>(&k.tileA[at])[half] = delta;
+                reinterpret_cast<float *>(&k.tileA[at])[2 + half] = in ? delta * ru.get(j) : 0.f;
+                reinterpret_cast<float *>(&k.tileG[at])[half] = g;
+                tileD[2 * at + half] = delta;
             }
         }
         for (int e = tid; e < 2 * kWin * S::kNT; e += kThr) {
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
             float v = 0.f;
             if (row < w1 && n < a.N)
                 v = to_f(static_cast<const T *>(isC ? a.C : a.B)[row * (isC ? a.cs : a.bs) + (int64_t)ch.g * a.N + n]);
-            sB[e] = v;  // sC follows sB
+            sB[e] = make_float2(v, v);  // C follows B
         }
         const SeqAt last = seq_find(a.seqs, w1 - 1);
         const bool ragged = !(last.start < w0 && last.end > w1);  // a sequence starts or ends here
@@ -552,33 +555,31 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
             seq_of[tid] = s;
             flag_of[tid] = f;
         }
-        // the state before the window
-        f2 h[R][P2];
-        const bool fix = wi > 0 && seq_find(a.seqs, w0 - 1).start < c0;
+        // the state before the window: local, plus what the chunk's start state leaves of itself
+        f2 h[NP];
+        if (wi == 0) {
+            k.states(h, part > 0 ? a.hchunk : nullptr, part * cn);
+        } else {
+            const int64_t win = w0 / kWin;
+            k.states(h, b.hwin, win * cn);
+            if (part > 0 && seq_find(a.seqs, w0 - 1).start < c0) {
+                f2 in[NP];
+                k.states(in, a.hchunk, part * cn);
+                const float *sw = b.swin + win * a.ch + ch.d0 + own;
+                const f2 s2 = pk(k.live0 ? sw[0] : 0.f, k.live1 ? sw[8] : 0.f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (wi == 0) {
-#pragma unroll
-                for (int i = 0; i < P2; ++i) h[r][i] = hin[r][i];
-            } else {
-                float t[NP];
-                load_states<NP>(t, b.hwin, (w0 / kWin) * cn + k.dn[r], k.nl, a.N, k.live[r]);
-                to_pairs<NP>(h[r], t);
-                if (fix) {
-                    const float sw = k.live[r] ? b.swin[(w0 / kWin) * a.ch + ch.d0 + k.dl[r]] : 0.f;
-                    const f2 s2 = pk(sw, sw);
-#pragma unroll
-                    for (int i = 0; i < P2; ++i) h[r][i] = fma2(exp2_2(mul2(s2, k.A2[r][i])), hin[r][i], h[r][i]);
-                }
+                for (int i = 0; i < NP; ++i) h[i] = fma2(exp2_2(mul2(s2, k.A2[i])), in[i], h[i]);
             }
         }
         __syncthreads();
         if (ragged) {
             k.template forward<true>(h);
-            for (int g = kGroups - 1; g >= 0; --g) k.template backward<true>(g);
+#pragma unroll 1
+            for (int g = S::kGroups - 1; g >= 0; --g) k.template backward<true>(g);
         } else {
             k.template forward<false>(h);
-            for (int g = kGroups - 1; g >= 0; --g) k.template backward<false>(g);
+#pragma unroll 1
+            for (int g = S::kGroups - 1; g >= 0; --g) k.template backward<false>(g);
         }
         __syncthreads();
         // dB, dC of this block's channels: the warps' sums in order
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < S::kWarps; ++w)
-                    v += reinterpret_cast<const float *>(k.ckpt + ((t / 4) * S::kWarps + w) * (S::E / 4) * 32)[(t % 4) * 2 * S::kNT + q];
+                    v += reinterpret_cast<const float *>(k.ckpt + ((t / S::kSC) * S::kWarps + w) * (NP / 2) * 32)[(t % S::kSC) * 2 * S::kNT + q];
                 const int64_t row = ((int64_t)(blk % a.blocks_per_group) * a.seqs.rows + w0 + t) * a.G + ch.g;
                 b.pbc[(row * 2 + q / S::kNT) * a.N + n] = v;
             }
@@ -606,17 +607,19 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const bool in = j < nc;
-                const float4 q = k.tile[tr * kDB + slot_of(tc + j)];  // s, w, y
-                const float raw = rdt.get(j) + (a.bias != nullptr && in ? a.bias[dc + j] : 0.f);
-                const float delta = step_of<T>(raw, a.softplus), u = ru.get(j);
+                const int at = tr * 32 + pair_slot(tr, tw, j);
+                const float s = reinterpret_cast<const float *>(&k.tileA[at])[half];
+                const float w = reinterpret_cast<const float *>(&k.tileA[at])[2 + half];
+                const float y = reinterpret_cast<const float *>(&k.tileG[at])[half];
+                const float delta = tileD[2 * at + half], u = ru.get(j);
                 const float D = a.D != nullptr && in ? a.D[dc + j] : 0.f;
                 float val = 1.f, der = 0.f;
                 if (a.z != nullptr) act_both(rz.get(j), true, val, der);
                 const float g = rdy.get(j) * val;
-                du[j] = fmaf(D, g, delta * q.x);
-                ddt[j] = fmaf(u, q.x, q.y);
-                if (a.softplus) ddt[j] *= sigmoid(raw);
-                dz[j] = rdy.get(j) * fmaf(D, u, q.z) * der;
+                du[j] = fmaf(D, g, delta * s);
+                ddt[j] = fmaf(u, s, w);
+                if (a.softplus) ddt[j] *= sigmoid(rdt.get(j) + (a.bias != nullptr && in ? a.bias[dc + j] : 0.f));
+                dz[j] = rdy.get(j) * fmaf(D, u, y) * der;
                 accD[j] = fmaf(g, u, accD[j]);
                 accb[j] += ddt[j];
             }
@@ -627,12 +630,7 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr) scan_bwd_kernel(const BwdA
     }
     // sums over this chunk's tokens
     float *part_out = b.partial + part * (cn + 2 * (int64_t)a.ch);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float t[NP];
-        from_pairs<NP>(t, k.dA[r]);
-        store_states<NP>(t, part_out, k.dn[r], k.nl, a.N, k.live[r]);
-    }
+    k.put(k.dA, part_out, 0);
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem);  // [kRowsAt][2][kDB]
 #pragma unroll
@@ -674,11 +672,11 @@ cudaError_t launch_np(const BwdArgs &b, cudaStream_t stream) {
     const unsigned grid = (unsigned)(nblk * a.nchunks);
     cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdShape<NP>::kSmem);
     if (e != cudaSuccess) return e;
-    if (a.seqs.rows > kWin) {  // one window: nothing to hand over
+    if (a.seqs.rows > win_of(NP)) {  // one window: nothing to hand over
         if constexpr (NP == 2)
-            e = launch_local<T, 8, 1>(b, stream);
+            e = launch_local<T, 8, 1, win_of(NP)>(b, stream);
         else
-            e = launch_local<T, 16, NP / 4>(b, stream);
+            e = launch_local<T, 16, NP / 4, win_of(NP)>(b, stream);
         if (e != cudaSuccess) return e;
     }
     if (a.nchunks > 1) {
@@ -728,7 +726,10 @@ int bwd_check(const kda_scan_bwd_params &p) {
     return KDA_OK;
 }
 
-// Chunks: about four blocks of the third step per SM slot, of whole windows.
+// Chunks: so many that the third kernel's blocks fill the GPU's slots (three blocks per SM) kTurns
+// times, of at least a window. 2 x 4096 tokens of 4096 channels: 1356 us with one turn, 1225 with two, 1219
+// with five (the chunks' ends are better spread; more chunks cost little).
+constexpr int kTurns = 5;
 struct BwdPlan {
     int64_t chunk, nchunks, windows, rows, bpg;
     size_t h, g, s, hw, sw, pbc, partial, bytes;  // offsets in floats, then the size in bytes
@@ -739,11 +740,11 @@ BwdPlan bwd_plan(const kda_scan_params &p) {
     q.bpg = ceil_div(p.channels / p.G, kDB);
     const int64_t nblk = p.G * q.bpg;
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    int64_t n = ceil_div(12 * sms, nblk);
-    q.chunk = ceil_div(ceil_div(q.rows > 0 ? q.rows : 1, n), kWin) * kWin;
+    const int64_t n = kTurns * 3 * sms / nblk;
+    q.chunk = ceil_div(ceil_div(q.rows > 0 ? q.rows : 1, n < 1 ? 1 : n), 32) * 32;
     q.nchunks = ceil_div(q.rows, q.chunk);
     if (q.nchunks < 1) q.nchunks = 1;
-    q.windows = ceil_div(q.rows, kWin);
+    q.windows = ceil_div(q.rows, win_of(np_of(p.N)));
     const size_t cn = (size_t)p.channels * p.N, ch = p.channels;
     size_t at = 0;
     auto take = [&](size_t n2) {

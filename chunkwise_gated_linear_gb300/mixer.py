@@ -14,6 +14,7 @@ dimension is 1 and holds N packed sequences.
 from __future__ import annotations
 
 import ctypes
+import sys
 
 from .kda import KDA_DTYPE_BF16, KDA_DTYPE_F32, KDA_OK, KdaError, _ptr, lib
 
@@ -160,7 +161,7 @@ def kda_block_norm_bwd_workspace(params) -> int:
 # ---- checks -------------------------------------------------------------------------------
 
 def _dtype(t, name):
-    import torch
+    torch = sys.modules["torch"]
 
     if t.dtype == torch.bfloat16:
         return KDA_DTYPE_BF16
@@ -171,12 +172,11 @@ def _dtype(t, name):
 
 def _want(t, name, shape, dtype):
     """A tensor argument's dtype and shape (None passes)."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
 
 
 def _token_stride(t, name, lead=2):
@@ -204,7 +204,7 @@ def _token_stride(t, name, lead=2):
 def _device(strided, dense):
     """Every tensor on one CUDA device, those of ``dense`` contiguous."""
     for t in dense:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
             raise ValueError("every tensor must be a CUDA tensor, and all but the data inputs contiguous")
     for t in strided:
         if t is not None and not t.is_cuda:
@@ -213,7 +213,7 @@ def _device(strided, dense):
 
 def _sequences(cu_seqlens, B):
     """The number of sequences."""
-    import torch
+    torch = sys.modules["torch"]
 
     if cu_seqlens is None:
         return B
@@ -231,26 +231,30 @@ def _act(activation, allowed):
     return known[activation]
 
 
-def _stream(t, stream):
-    import torch
+def _stream(t):
+    """The handle of torch's current stream on the tensor's device. torch's own raw getter makes no
+    Stream object (2 us less per call); the public way where a torch version lacks it."""
+    torch = sys.modules["torch"]
 
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(t.device).cuda_stream if raw is None else raw(t.get_device())
 
 
 def _call(name, p, t, stream, workspace=False):
     """Run a C entry point; ``workspace``: give it torch memory for its scratch. On a stream
     that torch does not know of, the library takes the scratch from its own pool instead: torch
     would hand the memory out again before that stream is done with it."""
-    import torch
-
-    ws = None
-    if workspace and stream is None:
-        n = _fn(name + "_workspace")(p)
-        if n:
-            ws = torch.empty(n, dtype=torch.uint8, device=t.device)
-            p.workspace = ws.data_ptr()
-            p.workspace_bytes = n
-    st = _fn(name)(p, _stream(t, stream) or None)
+    ws = None  # keeps the scratch until the call has been queued
+    if stream is None:
+        stream = _stream(t)
+        if workspace:
+            n = _fn(name + "_workspace")(p)
+            if n:
+                torch = sys.modules["torch"]
+                ws = torch.empty(n, dtype=torch.uint8, device=t.device)
+                p.workspace = ws.data_ptr()
+                p.workspace_bytes = n
+    st = _fn(name)(p, stream or None)
     if st != KDA_OK:
         raise KdaError(st, name)
 
@@ -258,7 +262,7 @@ def _call(name, p, t, stream, workspace=False):
 # ---- short causal convolution -------------------------------------------------------------
 
 def _conv_check(x, weight, bias, s0, cu_seqlens):
-    import torch
+    torch = sys.modules["torch"]
 
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
@@ -283,7 +287,7 @@ def causal_conv_fwd(x, weight, bias=None, *, s0=None, activation="silu", cu_seql
     the inputs before each sequence (None: zeros), st the last ones, for the next call (None in
     the result unless ``output_final_state``). ``y`` and ``st`` may be given to write into.
     """
-    import torch
+    torch = sys.modules["torch"]
 
     B, T, D, W, N, dtype = _conv_check(x, weight, bias, s0, cu_seqlens)
     act = _act(activation, ("silu", None))
@@ -306,7 +310,7 @@ def causal_conv_fwd(x, weight, bias=None, *, s0=None, activation="silu", cu_seql
 def causal_conv_step(x, state, weight, bias=None, *, activation="silu", y=None, stream=None):
     """The convolution of the next tokens of B sequences: x [B, T, D] (T typically 1), ``state``
     [B, W - 1, D] updated in place. Returns y."""
-    import torch
+    torch = sys.modules["torch"]
 
     B, T, D, W, _, dtype = _conv_check(x, weight, bias, state, None)
     act = _act(activation, ("silu", None))
@@ -326,7 +330,7 @@ def causal_conv_bwd(x, weight, bias, dy, *, s0=None, dst=None, activation="silu"
     """Backward of :func:`causal_conv_fwd`: same inputs plus ``dy`` (of y) and ``dst`` (of st, or
     None). Returns ``(dx, dweight, dbias, ds0)``: dx and ds0 in the dtype of x, the others fp32;
     dbias is None without bias, ds0 None when ``want_ds0`` is False."""
-    import torch
+    torch = sys.modules["torch"]
 
     B, T, D, W, N, dtype = _conv_check(x, weight, bias, s0, cu_seqlens)
     act = _act(activation, ("silu", None))
@@ -348,7 +352,7 @@ def causal_conv_bwd(x, weight, bias, dy, *, s0=None, dst=None, activation="silu"
 
 def _scan_params(u, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, y, ht, dense=()):
     """Checks shared by the three calls; the argument struct and the number of sequences."""
-    import torch
+    torch = sys.modules["torch"]
 
     if u.dim() != 3:
         raise ValueError("u must be [B, T, channels]")
@@ -389,7 +393,7 @@ def selective_scan_fwd(u, dt, A, B, C, D=None, z=None, *, dt_bias=None, dt_softp
     channels of group g reading B and C of that group. ``ht`` is None in the result when
     ``output_final_state`` is False.
     """
-    import torch
+    torch = sys.modules["torch"]
 
     if not output_final_state:
         ht = None
@@ -406,7 +410,7 @@ def selective_scan_fwd(u, dt, A, B, C, D=None, z=None, *, dt_bias=None, dt_softp
 def selective_scan_step(u, dt, A, B, C, h, D=None, z=None, *, dt_bias=None, dt_softplus=True, y=None, stream=None):
     """The scan of the next tokens of B sequences (u [B, T, channels], T typically 1), the states
     ``h`` [B, channels, N] updated in place. Returns y."""
-    import torch
+    torch = sys.modules["torch"]
 
     if h is None:
         raise ValueError("h is required")
@@ -424,7 +428,7 @@ def selective_scan_bwd(u, dt, A, B, C, dy, D=None, z=None, *, dt_bias=None, dt_s
     None). Returns ``(du, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)``: du, ddt, dz, dB, dC in the
     dtype of u, the others fp32; dD, dz and ddt_bias are None where the argument is, dh0 when
     ``want_dh0`` is False."""
-    import torch
+    torch = sys.modules["torch"]
 
     _want(dy, "dy", u.shape, u.dtype)
     f, ns = _scan_params(u, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, None, None, (dy, dht))
@@ -448,7 +452,7 @@ def _rows(t):
 
 
 def _gated_norm_params(x, z, weight, eps, activation, y, dense=()):
-    import torch
+    torch = sys.modules["torch"]
 
     if x.dim() < 1 or not 1 <= x.shape[-1] <= 8192:
         raise ValueError("x must be [..., D] with 1 <= D <= 8192")
@@ -465,7 +469,7 @@ def gated_norm_fwd(x, z, weight, *, eps=1e-6, activation="silu", y=None, stream=
     """x / rms(x) * weight * act(z) over the last dimension (the recurrence's output x, normed per
     head, times its gate). x, z [..., D] bf16 or fp32, D up to 8192; weight fp32 [D];
     ``activation`` "silu" or "sigmoid". Returns y like x."""
-    import torch
+    torch = sys.modules["torch"]
 
     p = _gated_norm_params(x, z, weight, eps, activation, y)
     if y is None:
@@ -477,7 +481,7 @@ def gated_norm_fwd(x, z, weight, *, eps=1e-6, activation="silu", y=None, stream=
 
 def gated_norm_bwd(x, z, weight, dy, *, eps=1e-6, activation="silu", stream=None):
     """Backward of :func:`gated_norm_fwd`; returns ``(dx, dz, dweight)``, dweight fp32."""
-    import torch
+    torch = sys.modules["torch"]
 
     _want(dy, "dy", x.shape, x.dtype)
     f = _gated_norm_params(x, z, weight, eps, activation, None, (dy,))
@@ -490,7 +494,7 @@ def gated_norm_bwd(x, z, weight, dy, *, eps=1e-6, activation="silu", stream=None
 # ---- residual update and norm -------------------------------------------------------------------
 
 def _block_norm_params(x, residual, weight, post_weight, z, scale, eps, activation, y, new_residual, dense=()):
-    import torch
+    torch = sys.modules["torch"]
 
     if x.dim() < 1 or not 1 <= x.shape[-1] <= 8192:
         raise ValueError("x must be [..., D] with 1 <= D <= 8192")
@@ -521,7 +525,7 @@ def block_norm_fwd(x, residual, weight, *, post_weight=None, z=None, scale=None,
     post_weight, scale fp32 [D]. Without post_weight x is not normed, without z not gated,
     without scale not scaled. ``new_residual`` may be ``residual`` (updated in place).
     """
-    import torch
+    torch = sys.modules["torch"]
 
     p = _block_norm_params(x, residual, weight, post_weight, z, scale, eps, activation, y, new_residual)
     if y is None:
@@ -538,7 +542,7 @@ def block_norm_bwd(x, residual, weight, dy, dresidual=None, *, post_weight=None,
     """Backward of :func:`block_norm_fwd` for the gradients ``dy`` of y and ``dresidual`` of
     new_residual (None: none); ``residual`` is the tensor before the update. Returns
     ``(dx, dresidual, dweight, dpost_weight, dz, dscale)``, None where the argument is."""
-    import torch
+    torch = sys.modules["torch"]
 
     _want(dy, "dy", x.shape, x.dtype)
     _want(dresidual, "dresidual", residual.shape, residual.dtype)
