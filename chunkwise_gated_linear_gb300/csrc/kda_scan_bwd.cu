@@ -22,6 +22,8 @@
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
 // fixed order. About 20 instructions per (token, channel, state): bound by issue.
+#include <type_traits>
+
 #include "scan_common.cuh"
 
 namespace kda {
@@ -276,7 +278,8 @@ struct BwdShape {
     static constexpr int kTileD = kWin * 32 * 8;               // delta
     static constexpr int kBCBytes = 2 * kWin * kNT * 8;
     static constexpr int kFlags = kWin * 8;                    // per row: sequence, start / end bits
-    static constexpr int kSmem = kCkpt + kTileA + kTileG + kTileD + kBCBytes + kFlags;
+    static constexpr int kPar = 2 * kDB * 4;                   // dt_bias and D of the channels
+    static constexpr int kSmem = kCkpt + kTileA + kTileG + kTileD + kBCBytes + kFlags + kPar;
 };
 
 // Place of pair dl of warp w in a tile's row t: rotated so that the threads that fill a tile row by row
@@ -466,6 +469,11 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_
     float *tileD = reinterpret_cast<float *>(take(S::kTileD));
     float2 *sB = reinterpret_cast<float2 *>(take(S::kBCBytes));
     int *seq_of = reinterpret_cast<int *>(take(S::kFlags)), *flag_of = seq_of + kWin;
+    float *sbias = reinterpret_cast<float *>(take(S::kPar)), *sD = sbias + kDB;
+    if (tid < kDB) {
+        sbias[tid] = a.bias != nullptr && tid < ch.n ? a.bias[ch.d0 + tid] : 0.f;
+        sD[tid] = a.D != nullptr && tid < ch.n ? a.D[ch.d0 + tid] : 0.f;
+    }
     k.sB = reinterpret_cast<const f2 *>(sB);
     k.sC = k.sB + kWin * S::kNT;
     k.seq_of = seq_of;
@@ -510,19 +518,20 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_
         const int64_t w0 = c0 + wi * kWin;
         const int64_t w1 = w0 + kWin < c1 ? w0 + kWin : c1;
         __syncthreads();  // the previous window's results have been read
-        for (int tr = tr0; tr < kWin; tr += kRowsAt) {
-            const int64_t row = w0 + tr;
-            const int n = row < w1 ? nc : 0;
+        // ALL: the row and its eight channels exist
+        auto stage = [&](auto all, int tr, int64_t row, int n) {
+            constexpr bool ALL = decltype(all)::value;
             Raw<T, 8> ru, rdt, rz, rdy;
             load8<T>(ru, a.u, row * a.us + dc, n, a.vec);
             load8<T>(rdt, a.dt, row * a.dts + dc, n, a.vec);
             load8<T>(rdy, b.dy, row * a.ch + dc, n, a.vec);
             if (a.z != nullptr) load8<T>(rz, a.z, row * a.zs + dc, n, a.vec);
+            float bias[8];
+            load_vec<float, 8>(bias, sbias + tc);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool in = j < n;
-                const float bias = a.bias != nullptr && in ? a.bias[dc + j] : 0.f;
-                const float delta = in ? step_of<T>(rdt.get(j) + bias, a.softplus) : 0.f;
+                const bool in = ALL || j < n;
+                const float delta = in ? step_of<T>(rdt.get(j) + bias[j], a.softplus) : 0.f;
                 float g = in ? rdy.get(j) : 0.f;
                 if (a.z != nullptr) g *= in ? act_value(rz.get(j), true) : 0.f;
                 const int at = tr * 32 + pair_slot(tr, tw, j);
@@ -531,6 +540,13 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_
                 reinterpret_cast<float *>(&k.tileG[at])[half] = g;
                 tileD[2 * at + half] = delta;
             }
+        };
+        for (int tr = tr0; tr < kWin; tr += kRowsAt) {
+            const int64_t row = w0 + tr;
+            if (row < w1 && nc >= 8)
+                stage(std::true_type{}, tr, row, 8);
+            else
+                stage(std::false_type{}, tr, row, row < w1 ? nc : 0);
         }
         for (int e = tid; e < 2 * kWin * S::kNT; e += kThr) {
             const bool isC = e >= kWin * S::kNT;
@@ -594,7 +610,7 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_
                 b.pbc[(row * 2 + q / S::kNT) * a.N + n] = v;
             }
         }
-        // per (token, channel)
+        // per (token, channel); channels that do not exist are computed and not stored
         for (int tr = tr0; tr < kWin; tr += kRowsAt) {
             const int64_t row = w0 + tr;
             if (row >= w1 || nc <= 0) continue;
@@ -603,23 +619,23 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_
             load8<T>(rdt, a.dt, row * a.dts + dc, nc, a.vec);
             load8<T>(rdy, b.dy, row * a.ch + dc, nc, a.vec);
             if (a.z != nullptr) load8<T>(rz, a.z, row * a.zs + dc, nc, a.vec);
-            float du[8], ddt[8], dz[8];
+            float du[8], ddt[8], dz[8], bias[8], D[8];
+            load_vec<float, 8>(bias, sbias + tc);
+            load_vec<float, 8>(D, sD + tc);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool in = j < nc;
                 const int at = tr * 32 + pair_slot(tr, tw, j);
                 const float s = reinterpret_cast<const float *>(&k.tileA[at])[half];
                 const float w = reinterpret_cast<const float *>(&k.tileA[at])[2 + half];
                 const float y = reinterpret_cast<const float *>(&k.tileG[at])[half];
                 const float delta = tileD[2 * at + half], u = ru.get(j);
-                const float D = a.D != nullptr && in ? a.D[dc + j] : 0.f;
                 float val = 1.f, der = 0.f;
                 if (a.z != nullptr) act_both(rz.get(j), true, val, der);
                 const float g = rdy.get(j) * val;
-                du[j] = fmaf(D, g, delta * s);
+                du[j] = fmaf(D[j], g, delta * s);
                 ddt[j] = fmaf(u, s, w);
-                if (a.softplus) ddt[j] *= sigmoid(rdt.get(j) + (a.bias != nullptr && in ? a.bias[dc + j] : 0.f));
-                dz[j] = rdy.get(j) * fmaf(D, u, y) * der;
+                if (a.softplus) ddt[j] *= sigmoid(rdt.get(j) + bias[j]);
+                dz[j] = rdy.get(j) * fmaf(D[j], u, y) * der;
                 accD[j] = fmaf(g, u, accD[j]);
                 accb[j] += ddt[j];
             }
