@@ -519,6 +519,8 @@ int conv_run(const kda_conv_params &p, bool step, cudaStream_t stream) {
     if (st != KDA_OK) return st;
     if (p.T != 0 && p.y == nullptr) return KDA_ERR_INVALID_ARG;
     if (step && (p.cu_seqlens != nullptr || p.s0 == nullptr || p.st == nullptr)) return KDA_ERR_INVALID_ARG;
+    // a sequence's tiles read s0 and write st independently of each other
+    if (!step && p.st != nullptr && p.st == p.s0) return KDA_ERR_INVALID_ARG;
     const int e = elem_size(p.dtype);
     if (!aligned(p.y, e) || !aligned(p.st, e)) return KDA_ERR_ALIGNMENT;
     ConvArgs a{};

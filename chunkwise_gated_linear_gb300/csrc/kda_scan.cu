@@ -551,6 +551,8 @@ int kda_scan_fwd(const kda_scan_params *p, cudaStream_t stream) {
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     const int st = fwd_check(*p);
     if (st != KDA_OK) return st;
+    // chunks read h0 while others have already written ht
+    if (p->ht != nullptr && p->ht == p->h0) return KDA_ERR_INVALID_ARG;
     const FwdPlan q = fwd_plan(*p);
     if (p->workspace != nullptr && p->workspace_bytes < q.bytes) return KDA_ERR_INVALID_ARG;
     if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;

@@ -99,16 +99,27 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
 
     T nu[4], ndt[4], ndy[4], nz[4];
     auto fetch = [&](int64_t r0) {
+        // the rows' places are the same for all threads
         const T *pu = static_cast<const T *>(a.u) + r0 * a.us, *pd = static_cast<const T *>(a.dt) + r0 * a.dts;
         const T *py = static_cast<const T *>(b.dy) + r0 * a.ch, *pz = static_cast<const T *>(a.z) + r0 * a.zs;
+        if (r0 + 4 <= c1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (r0 + k < c1) {
-                nu[k] = pu[k * a.us + d];
-                ndt[k] = pd[k * a.dts + d];
-                ndy[k] = py[(int64_t)k * a.ch + d];
-                if (gate) nz[k] = pz[k * a.zs + d];
+            for (int k = 0; k < 4; ++k) {
+                nu[k] = (pu + k * a.us)[d];
+                ndt[k] = (pd + k * a.dts)[d];
+                ndy[k] = (py + (int64_t)k * a.ch)[d];
+                if (gate) nz[k] = (pz + k * a.zs)[d];
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k < c1) {
+                    nu[k] = (pu + k * a.us)[d];
+                    ndt[k] = (pd + k * a.dts)[d];
+                    ndy[k] = (py + (int64_t)k * a.ch)[d];
+                    if (gate) nz[k] = (pz + k * a.zs)[d];
+                }
+        }
     };
     float nbc[kBC];
     auto fetch_bc = [&](int64_t t0) {

@@ -64,7 +64,8 @@ extern "C" {
  *   x, y      [B, T, D] (or [1, T, D] packed), `dtype`; x with token stride x_stride
  *   weight    [D, W] fp32, W in {2, 3, 4};  bias [D] fp32 or NULL
  *   s0, st    [N, W - 1, D] `dtype`, the W - 1 inputs before the first token and up to the last
- *             one, oldest first, N the number of sequences; either may be NULL (s0: zeros)
+ *             one, oldest first, N the number of sequences; either may be NULL (s0: zeros);
+ *             st must not be s0 (KDA_ERR_INVALID_ARG; kda_conv_step updates in place)
  *   activation KDA_ACT_NONE or KDA_ACT_SILU
  */
 typedef struct kda_conv_params {
@@ -119,7 +120,8 @@ size_t kda_conv_bwd_workspace(const kda_conv_bwd_params *p);
  * with g = d / (channels / G), D and z each optional (NULL: no skip, no gate).
  *   u, dt, z, y  [B, T, channels] `dtype`;  B, C [B, T, G, N] `dtype`
  *   A [channels, N], D, dt_bias [channels] fp32 (dt_bias may be NULL)
- *   h0, ht       [N_seq, channels, N] fp32, either may be NULL (h0: zeros)
+ *   h0, ht       [N_seq, channels, N] fp32, either may be NULL (h0: zeros); ht must not be h0
+ *                (KDA_ERR_INVALID_ARG; kda_scan_step updates in place)
  * 1 <= N <= 64; channels divisible by G.
  * Where one pass over the tokens would leave most of the GPU idle (few channels and sequences)
  * the tokens are cut into pieces: scratch of kda_scan_fwd_workspace bytes.

@@ -52,7 +52,7 @@ def _set(p, **over):
 
 
 def _conv(**over):
-    return _set(mixer.kda_conv_params(A, A, A, A, A, A, 0, 2, 5, 64, 4, None, 0, 1), **over)
+    return _set(mixer.kda_conv_params(A, A, A, A, A, 2 * A, 0, 2, 5, 64, 4, None, 0, 1), **over)
 
 
 def _conv_bwd(**over):
@@ -60,7 +60,7 @@ def _conv_bwd(**over):
 
 
 def _scan(**over):
-    return _set(mixer.kda_scan_params(A, A, A, A, A, A, A, A, A, A, A, 0, 0, 0, 0, 0, 2, 5, 64, 16, 2, None, 0, 1, None, 0),
+    return _set(mixer.kda_scan_params(A, A, A, A, A, A, A, A, A, A, 2 * A, 0, 0, 0, 0, 0, 2, 5, 64, 16, 2, None, 0, 1, None, 0),
                 **over)
 
 
@@ -95,6 +95,7 @@ INV, UNS, ALI = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_AL
     ("conv_fwd", _conv, dict(dtype=2), UNS), ("conv_fwd", _conv, dict(activation=2), UNS),
     ("conv_fwd", _conv, dict(x=A + 1), ALI), ("conv_fwd", _conv, dict(weight=A + 2), ALI),
     ("conv_fwd", _conv, dict(st=A + 1), ALI), ("conv_fwd", _conv, dict(B=1 << 20, T=1 << 20), UNS),
+    ("conv_fwd", _conv, dict(st=A), INV), ("scan_fwd", _scan, dict(ht=A), INV),  # states in place: the step calls only
     ("conv_step", _conv, dict(s0=None), INV), ("conv_step", _conv, dict(st=None), INV),
     ("conv_step", _conv, dict(cu_seqlens=A), INV),
     ("conv_bwd", _conv_bwd, dict(dy=None), INV), ("conv_bwd", _conv_bwd, dict(dx=None), INV),

@@ -86,6 +86,22 @@ def test_block_norm_in_place(dtype, res):
     assert r3 is r and torch.equal(r, r2) and torch.equal(y, y3)
 
 
+def test_block_norm_gradient_in_place():
+    """kda_block_norm_bwd's dresidual may be dres."""
+    from chunkwise_gated_linear_gb300 import kda, mixer
+
+    g = torch.Generator().manual_seed(6)
+    x, r, w, dy, dr = _r(g, 9, 320), _r(g, 9, 320), _r(g, 320), _r(g, 9, 320), _r(g, 9, 320)
+    want = block_norm_bwd(x, r, w, dy, dr)
+    f = mixer._block_norm_params(x, r, w, None, None, None, EPS, "sigmoid", None, None)
+    dx, dw, got = torch.empty_like(x), torch.empty_like(w), dr.clone()
+    p = mixer.kda_block_norm_bwd_params(f, dy.data_ptr(), got.data_ptr(), dx.data_ptr(), got.data_ptr(), dw.data_ptr(), None, None,
+                                        None, None, 0)
+    assert mixer.kda_block_norm_bwd(p, torch.cuda.current_stream().cuda_stream) == kda.KDA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, want[1]) and torch.equal(dx, want[0]) and torch.equal(dw, want[2])
+
+
 def test_rows_of_zeros_and_large_values():
     """A row of zeros (the norm is eps alone) and rows near the type's largest squares stay finite."""
     g = torch.Generator().manual_seed(3)

@@ -58,7 +58,7 @@ def _forward(t, lens, packed, dtype, softplus=True):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("N", [1, 5, 8, 16, 31, 64])
-@pytest.mark.parametrize("ch,G", [(64, 1), (150, 3), (7, 1)])
+@pytest.mark.parametrize("ch,G", [(64, 1), (150, 3), (7, 1), (21, 3)])
 def test_forward(dtype, N, ch, G):
     for lens, packed in ((RAGGED, True), ([41, 41], False), ([300], False), ([1, 1, 1], False)):
         _forward(_make(lens, ch, N, G, dtype, seed=N + ch), lens, packed, dtype)
@@ -104,7 +104,7 @@ def _backward(t, lens, packed, dtype, softplus=True):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("N", [1, 5, 8, 16, 31, 64])
-@pytest.mark.parametrize("ch,G", [(64, 1), (150, 3), (7, 1)])
+@pytest.mark.parametrize("ch,G", [(64, 1), (150, 3), (7, 1), (21, 3)])
 def test_backward(dtype, N, ch, G):
     for lens, packed in ((RAGGED, True), ([41, 41], False), ([200], False), ([1, 1], False)):
         _backward(_make(lens, ch, N, G, dtype, seed=N + ch), lens, packed, dtype)
@@ -207,6 +207,37 @@ def test_extreme_values():
     assert not bool(torch.isfinite(ht[2, 7]).all())
     got = selective_scan_bwd(*a, dy, *dz, dht=t["dht"], **kw)
     assert bool(torch.isfinite(got[0][0, :73]).all()) and bool(torch.isfinite(got[3][0, :73]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_masked_tokens(dtype):
+    """Tokens masked by a step size of the type's lowest value or minus infinity: the state passes over
+    them unchanged, and their gradients are zero (dD and dz see u and z of the token itself)."""
+    lens = [70, 40]
+    t = _make(lens, 48, 16, 1, dtype, 18)
+    off = torch.zeros(sum(lens), dtype=torch.bool, device=dev)
+    off[[0, 1, 33, 34, 35, 69, 75]] = True
+    off[90:110] = True  # to the end of the sequence
+    t["dt"][off] = torch.finfo(dtype).min
+    t["dt"][35] = t["dt"][100] = float("-inf")
+    a, dy, dz, kw = _args(t, lens, True)
+    y, ht = selective_scan_fwd(*a, *dz, **kw)
+    # the same sequences without those tokens
+    keep = ~off
+    short = {k: (v[keep] if k in ("u", "dt", "B", "C", "z", "dy") else v) for k, v in t.items()}
+    l2 = [int(keep[:70].sum()), int(keep[70:].sum())]
+    a2, dy2, dz2, kw2 = _args(short, l2, True)
+    y2, ht2 = selective_scan_fwd(*a2, *dz2, **kw2)
+    ref.check("ht", ht, ht2.double().cpu(), F32, WORK)
+    ref.check("y", y[:, keep], y2.double().cpu(), dtype, WORK + 2.0 ** -8 * (dtype == BF))
+    t["dy"][off] = 0
+    got = selective_scan_bwd(*a, t["dy"][None], *dz, dht=t["dht"], **kw)
+    want = selective_scan_bwd(*a2, dy2, *dz2, dht=t["dht"], **kw2)
+    for i, (p, q) in enumerate(zip(got, want)):
+        if i in (0, 1, 3, 4, 6):
+            assert not bool(p[:, off].any())
+            p = p[:, keep]
+        ref.check(f"gradient {i}", p, q.double().cpu(), p.dtype, WORK_GRAD + ref.HALF[p.dtype])
 
 
 def test_no_tokens():
