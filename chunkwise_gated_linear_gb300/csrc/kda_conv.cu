@@ -126,12 +126,12 @@ __device__ __forceinline__ void mad(Row<T, V> &a, const Row<T, V> &b, const Row<
 
 // The taps and the bias of V channels.
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, Row<T, V> (&w)[W], Row<T, V> &b) {
+__device__ __forceinline__ void load_weights(const ConvArgs &a, uint32_t c, Row<T, V> (&w)[W], Row<T, V> &b) {
     float f[V * W], fb[V];
     if (V > 1 && a.wvec) {
 #pragma unroll
         for (int i = 0; i < V * W / 4; ++i) {
-            const float4 q = reinterpret_cast<const float4 *>(a.w + c * W)[i];
+            const float4 q = reinterpret_cast<const float4 *>(a.w + (int64_t)c * W)[i];
             f[4 * i] = q.x;
             f[4 * i + 1] = q.y;
             f[4 * i + 2] = q.z;
@@ -139,7 +139,7 @@ __device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, Row<T
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V * W; ++i) f[i] = a.w[c * W + i];
+        for (int i = 0; i < V * W; ++i) f[i] = a.w[(int64_t)c * W + i];
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) fb[v] = a.bias != nullptr ? a.bias[c + v] : 0.f;
@@ -156,7 +156,7 @@ __device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, Row<T
 // The window before row r of a sequence: rows r - (W-1) .. r - 1, those before the sequence's
 // start from its initial state.
 template <typename T, int V, int W>
-__device__ __forceinline__ void fill_window(const ConvArgs &a, const SeqAt &at, int64_t r, int64_t c, Row<T, V> (&win)[W]) {
+__device__ __forceinline__ void fill_window(const ConvArgs &a, const SeqAt &at, int64_t r, uint32_t c, Row<T, V> (&win)[W]) {
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         const int64_t pos = r - (W - 1) + i;
@@ -195,8 +195,10 @@ __global__ void __launch_bounds__(kConvThreads, kFwdPerSM) conv_fwd_kernel(const
     constexpr int kBatch = kFwdBatch<T>;
     using R = Row<T, V>;
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
-    const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
-    if (c >= a.D) return;
+    // 32 bits without a sign: a row's place is the same for all threads, and the thread's own part of an
+    // address then needs no 64-bit arithmetic
+    const uint32_t c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
+    if (c >= (uint32_t)a.D) return;
     // empty sequences keep their state; the tiles share them out
     if (a.st != nullptr)
         for (int64_t s = blockIdx.x; s < a.seqs.N; s += gridDim.x)
@@ -285,7 +287,8 @@ template <typename T, int V, int W>
 struct ConvBack {
     using R = Row<T, V>;
     const ConvArgs &a;
-    int64_t c, r0, r1;
+    uint32_t c;
+    int64_t r0, r1;
     R w[W], g[W];
 
     __device__ __forceinline__ ConvBack(const ConvArgs &args) : a(args) {}
@@ -324,8 +327,10 @@ __global__ void __launch_bounds__(kConvThreads, kBwdPerSM<T>) conv_bwd_kernel(co
     constexpr int kBatch = kBwdBatch;
     using R = Row<T, V>;
     if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.seqs, a.err, threadIdx.x, kConvThreads);
-    const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * V;
-    if (c >= a.D) return;
+    // 32 bits without a sign: a row's place is the same for all threads, and the thread's own part of an
+    // address then needs no 64-bit arithmetic
+    const uint32_t c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
+    if (c >= (uint32_t)a.D) return;
     if (a.ds0 != nullptr)
         for (int64_t s = blockIdx.x; s < a.seqs.N; s += gridDim.x)
             if (seq_empty(a.seqs, (int)s)) {
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(kConvThreads, kBwdPerSM<T>) conv_bwd_kernel(co
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) part[(c + v) * W + j] = f[j][v];
+        for (int j = 0; j < W; ++j) part[(int64_t)(c + v) * W + j] = f[j][v];
         part[(int64_t)a.D * W + c + v] = fb[v];
     }
 }

@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kFThr, kPerSM) scan_fwd_kernel(const ScanArgs 
     const int g = blk / a.blocks_per_group;
     const int first = (blk % a.blocks_per_group) * S::kChan + 2 * (tid / LN);  // within the group
     const int n0 = (tid % LN) * NS;
-    const int d = g * a.chg + first;
+    // without a sign: a row's place is the same for all threads, and the thread's own part of an address then
+    // needs no 64-bit arithmetic
+    const uint32_t d = g * a.chg + first;
     const int nch = a.chg - first < 2 ? (a.chg - first > 0 ? 1 : 0) : 2;  // channels that exist: 0, 1, 2
     const int64_t cn = (int64_t)a.ch * a.N;
     const int64_t dn0 = (int64_t)d * a.N, dn1 = dn0 + a.N;

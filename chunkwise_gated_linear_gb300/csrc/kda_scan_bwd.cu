@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
     const int first = (blk % a.blocks_per_group) * kChan + tid / LN;
     const int n0 = (tid % LN) * NS;
     const bool live = first < a.chg;
-    const int d = g * a.chg + (live ? first : 0);
+    const uint32_t d = g * a.chg + (live ? first : 0);
     const int64_t cn = (int64_t)a.ch * a.N, dn = (int64_t)d * a.N;
     const bool vst = a.vec_states && a.N == kNT;
     const int64_t c0 = part * a.chunk;
