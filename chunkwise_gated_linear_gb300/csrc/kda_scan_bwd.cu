@@ -11,13 +11,13 @@
 // The states are needed backwards and cannot be undone (a_t may underflow), so they are computed
 // again in three steps:
 //   1. scan_bwd_local_kernel: the rows are cut into chunks, all walked at once from a zero state.
-//      It leaves the local state at every 32 rows (a window), the chunk's end state, its adjoint
+//      It leaves the local state at every 16 rows (a window), the chunk's end state, its adjoint
 //      at the start from a zero adjoint at the end (in the same forward walk:
 //      sum_t (a_c0 .. a_t) C_t g_t), and sums of delta.
 //   2. scan_bwd_carry_kernel: true states at the chunk starts, true adjoints at the ends.
 //   3. scan_bwd_kernel: per chunk and 64 channels, windows last to first. A window's start state
 //      is its local state plus exp(A sum delta) times the chunk's start state; from there the
-//      states before every group of (up to) four tokens go to shared memory, and the groups are taken
+//      states before every group of two tokens go to shared memory, and the groups are taken
 //      last to first: a and a h_{t-1} of their tokens in registers, then backwards.
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
@@ -31,8 +31,10 @@ namespace scan {
 
 namespace {
 
-// Tokens per window: what the third kernel keeps states of in shared memory.
-__host__ __device__ constexpr int win_of(int np) { return np <= 4 ? 32 : (np == 8 ? 16 : 8); }
+// Tokens per window: what the third kernel keeps states of in shared memory. With 16 states, windows of 16
+// and groups of two tokens leave registers and shared memory for four blocks per SM (2 x 4096 tokens
+// of 4096 channels: 1135 us); windows of 32 and groups of four for three (1204 us).
+__host__ __device__ constexpr int win_of(int np) { return np <= 8 ? 16 : 8; }
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdArgs {
@@ -281,7 +283,7 @@ struct BwdShape {
     static constexpr int kNT = kLN * NP;
     static constexpr int kWin = win_of(NP);
     // tokens whose decays are held in registers while they are walked back
-    static constexpr int kSC = NP <= 4 ? 4 : (NP == 8 ? 2 : 1);
+    static constexpr int kSC = NP <= 8 ? 2 : 1;
     static constexpr int kGroups = kWin / kSC;
     static constexpr int kCkpt = kGroups * 2 * NP * kThr * 4;  // states before every group of tokens
     static constexpr int kTileA = kWin * 32 * 16;              // delta and x of a pair; then s and w
@@ -453,7 +455,7 @@ struct BwdBlock {
 };
 
 template <typename T, int NP>
-__global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 3 : 1) scan_bwd_kernel(const BwdArgs b) {
+__global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 4 : 1) scan_bwd_kernel(const BwdArgs b) {
     using S = BwdShape<NP>;
     constexpr int kThr = S::kThr, kWin = S::kWin;
     constexpr int kRowsAt = kThr / 8;  // token rows staged at a time
@@ -753,10 +755,10 @@ int bwd_check(const kda_scan_bwd_params &p) {
     return KDA_OK;
 }
 
-// Chunks: so many that the third kernel's blocks fill the GPU's slots (three blocks per SM) kTurns
-// times, of at least a window. 2 x 4096 tokens of 4096 channels: 1356 us with one turn, 1225 with two, 1219
-// with five (the chunks' ends are better spread; more chunks cost little).
-constexpr int kTurns = 5;
+// Chunks: so many that the third kernel's blocks fill the GPU's slots (four blocks per SM) kTurns
+// times, of at least a window. 2 x 4096 tokens of 4096 channels: 1136 us with two turns, 1158 with three,
+// 1135 with five, 1118 with eight (the last blocks end closer together; more chunks cost little).
+constexpr int kTurns = 8;
 struct BwdPlan {
     int64_t chunk, nchunks, windows, rows, bpg;
     size_t h, g, s, hw, sw, pbc, partial, bytes;  // offsets in floats, then the size in bytes
@@ -767,7 +769,7 @@ BwdPlan bwd_plan(const kda_scan_params &p) {
     q.bpg = ceil_div(p.channels / p.G, kDB);
     const int64_t nblk = p.G * q.bpg;
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    const int64_t n = kTurns * 3 * sms / nblk;
+    const int64_t n = kTurns * 4 * sms / nblk;
     q.chunk = ceil_div(ceil_div(q.rows > 0 ? q.rows : 1, n < 1 ? 1 : n), 32) * 32;
     q.nchunks = ceil_div(q.rows, q.chunk);
     if (q.nchunks < 1) q.nchunks = 1;
