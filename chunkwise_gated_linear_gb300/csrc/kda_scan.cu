@@ -39,6 +39,9 @@ constexpr int kPerSM = 4;
 // Rows per chunk at least: 333 tokens of 2048 channels take 36 us with 12 or 16 rows, 49 us with
 // 32, 78 us with 64 (chunks are walked serially, and there are few).
 constexpr int kMinChunk = 16;
+// Blocks per SM of the step kernel: two, with 128 registers, hold a sequence's states, the next one's and its
+// inputs (256 sequences of 4096 x 16 states: 31 us; three blocks spill: 46; one sequence per block: 35).
+constexpr int kStepPerSM = 2;
 
 // NS states per thread, LN lanes per pair of channels.
 template <int NS, int LN>
@@ -314,84 +317,127 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const ScanArgs a) {
 // states of all four (a warp reads 512 contiguous bytes of states at a time, four such reads in flight
 // per thread), prepares the step size and the gate of one of them and passes the step size on to
 // the others; the four outputs are added across the lanes so that each lane ends with its own
-// channel's. Bound by reading and writing the states (8 bytes per state; the rest is 1 / 16 of that).
+// channel's. A block goes through several sequences with the same channels, the next one's states on their
+// way meanwhile. Bound by reading and writing the states (8 bytes per state; the rest is 1 / 16 of that).
 template <typename T, int NP>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs a) {
-    const int tid = threadIdx.x, lane = tid & 31, nl = tid & 3, n0 = nl * NP;
-    const int nblk = (a.ch + 255) / 256;
-    const int64_t seq = blockIdx.x / nblk;
-    const int base = (int)(blockIdx.x % nblk) * 256 + (tid >> 5) * 32 + (lane >> 2);
-    const int own = base + nl * 8;  // the channel that this lane prepares and finishes
-    const bool live = own < a.ch;
-    const bool vec = a.vec_states && a.N == 4 * NP;
-    const bool one_group = a.G == 1 || a.chg % 32 == 0;  // of a warp's 32 channels
-    const int64_t at = seq * a.ch * a.N;
-    float h[4][NP], A2[4][NP];
+__global__ void __launch_bounds__(256, NP <= 4 ? kStepPerSM : 1) scan_step_kernel(const ScanArgs a) {
+    const uint32_t tid = threadIdx.x, lane = tid & 31, nl = tid & 3, n0 = nl * NP;
+    // places are a part that is the same for the block and the thread's own, in 32 bits without a sign
+    const uint32_t nblk = (a.ch + 255u) / 256u, blk = blockIdx.x % nblk;
+    const int per = gridDim.x / nblk;  // blocks that share the sequences
+    const uint32_t base = blk * 256 + (tid >> 5) * 32 + (lane >> 2), ch = a.ch, N = a.N;
+    const uint32_t own = base + nl * 8;  // the channel that this lane prepares and finishes
+    const bool live = own < ch;
+    const bool full = a.vec_states && N == 4 * NP && blk * 256 + 256 <= ch;  // whole vectors, all of them
+    const bool one_group = a.G == 1 || a.chg % 32 == 0;                      // of a warp's 32 channels
+    float next[4][NP], A2[4][NP];  // the states of the sequence whose turn is next
+    auto load = [&](float (&h)[4][NP], const float *from) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int d = base + r * 8;
-        const int64_t dn = (int64_t)d * a.N;
-        if (vec && d < a.ch) {
-            load_vec<float, NP>(h[r], a.h0 + at + dn + n0);
-            load_vec<float, NP>(A2[r], a.A + dn + n0);
-        } else {
-            load_states<NP>(h[r], a.h0, at + dn, nl, a.N, d < a.ch);
-            load_states<NP>(A2[r], a.A, dn, nl, a.N, d < a.ch);
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t d = base + r * 8;
+            if (full)
+                load_vec<float, NP>(h[r], from + (d * N + n0));
+            else
+                load_states<NP>(h[r], from, d * N, nl, N, d < ch);
         }
+    };
+    int64_t seq = blockIdx.x / nblk;
+    constexpr bool kNext = NP <= 8;  // registers for the next sequence's states
+    if (kNext) load(next, a.h0 + seq * ch * N);
+    load(A2, a.A);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int i = 0; i < NP; ++i) A2[r][i] *= kLog2e;
-    }
     const float bias = a.bias != nullptr && live ? a.bias[own] : 0.f, D = a.D != nullptr && live ? a.D[own] : 0.f;
     float B[NP], C[NP];
-    auto load_bc = [&](int64_t r, int d) {
-        const int g = (d < a.ch ? d : a.ch - 1) / a.chg;
-        const T *pB = static_cast<const T *>(a.B) + r * a.bs + (int64_t)g * a.N + n0;
-        const T *pC = static_cast<const T *>(a.C) + r * a.cs + (int64_t)g * a.N + n0;
-        if (a.vec && a.N == 4 * NP) {
-            load_vec<T, NP>(B, pB);
-            load_vec<T, NP>(C, pC);
+    auto load_bc = [&](const T *pB, const T *pC, uint32_t d) {  // of channel d's group
+        const uint32_t o = (a.G == 1 ? 0u : (d < ch ? d : ch - 1) / a.chg * N) + n0;
+        if (a.vec && N == 4 * NP) {
+            load_vec<T, NP>(B, pB + o);
+            load_vec<T, NP>(C, pC + o);
         } else {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                B[i] = n0 + i < a.N ? to_f(pB[i]) : 0.f;
-                C[i] = n0 + i < a.N ? to_f(pC[i]) : 0.f;
+                B[i] = n0 + i < N ? to_f(pB[o + i]) : 0.f;
+                C[i] = n0 + i < N ? to_f(pC[o + i]) : 0.f;
             }
         }
     };
-    for (int t = 0; t < a.seqs.T; ++t) {
-        const int64_t row = seq * a.seqs.T + t;
-        float u = 0.f, s = 0.f, z = 0.f;
+    // a token's inputs, read one token ahead
+    const bool ahead = one_group && a.vec && N == 4 * NP;  // B and C too
+    Raw<T, 1> nu, ns, nz;
+    Raw<T, NP> nB, nC;
+    const uint32_t obc = (a.G == 1 ? 0u : (base < ch ? base : ch - 1) / a.chg * N) + n0;
+    auto fetch = [&](int64_t row) {
         if (live) {
-            u = to_f(static_cast<const T *>(a.u)[row * a.us + own]);
-            s = to_f(static_cast<const T *>(a.dt)[row * a.dts + own]);
-            if (a.z != nullptr) z = to_f(static_cast<const T *>(a.z)[row * a.zs + own]);
+            nu.load(static_cast<const T *>(a.u) + row * a.us + own);
+            ns.load(static_cast<const T *>(a.dt) + row * a.dts + own);
+            if (a.z != nullptr) nz.load(static_cast<const T *>(a.z) + row * a.zs + own);
         }
-        if (one_group) load_bc(row, base);
-        const float delta = step_of<T>(s + bias, a.softplus), x = delta * u;
-        float p[4];
+        if (ahead) {
+            nB.load(static_cast<const T *>(a.B) + row * a.bs + obc);
+            nC.load(static_cast<const T *>(a.C) + row * a.cs + obc);
+        }
+    };
+    const int T_ = a.seqs.T;
+    nu.zero();
+    ns.zero();
+    nz.zero();
+    if (T_ > 0) fetch(seq * T_);
+    for (; seq < a.seqs.N; seq += per) {
+        float h[4][NP];
+        const bool more = seq + per < a.seqs.N;
+        if constexpr (kNext) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) h[r][i] = next[r][i];
+            if (more) load(next, a.h0 + (seq + per) * ch * N);
+        } else {
+            load(h, a.h0 + seq * ch * N);
+        }
+        for (int t = 0; t < T_; ++t) {
+            const int64_t row = seq * T_ + t;
+            const float u = nu.get(0), s = ns.get(0), z = nz.get(0);
+            if (ahead) {
+                nB.unpack(B);
+                nC.unpack(C);
+            } else if (one_group) {
+                load_bc(static_cast<const T *>(a.B) + row * a.bs, static_cast<const T *>(a.C) + row * a.cs, base);
+            }
+            if (t + 1 < T_)
+                fetch(row + 1);
+            else if (more)
+                fetch((seq + per) * T_);
+            const float delta = step_of<T>(s + bias, a.softplus), x = delta * u;
+            float p[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (!one_group)
+                    load_bc(static_cast<const T *>(a.B) + row * a.bs, static_cast<const T *>(a.C) + row * a.cs, base + r * 8);
+                const float dr = __shfl_sync(0xffffffffu, delta, (lane & ~3u) + r);
+                const float xr = __shfl_sync(0xffffffffu, x, (lane & ~3u) + r);
+                p[r] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    h[r][i] = fmaf(tc5::ex2(dr * A2[r][i]), h[r][i], xr * B[i]);
+                    p[r] = fmaf(C[i], h[r][i], p[r]);
+                }
+            }
+            float y = fmaf(D, u, sum_lanes(p, nl));
+            if (a.z != nullptr) y *= act_value(z, true);
+            if (live) (static_cast<T *>(a.y) + row * ch)[own] = from_f<T>(y);
+        }
+        float *ht = a.ht + seq * ch * N;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (!one_group) load_bc(row, base + r * 8);
-            const float dr = __shfl_sync(0xffffffffu, delta, (lane & ~3) + r), xr = __shfl_sync(0xffffffffu, x, (lane & ~3) + r);
-            p[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                h[r][i] = fmaf(tc5::ex2(dr * A2[r][i]), h[r][i], xr * B[i]);
-                p[r] = fmaf(C[i], h[r][i], p[r]);
-            }
+            const uint32_t d = base + r * 8;
+            if (full)
+                store_vec<float, NP>(ht + (d * N + n0), h[r]);
+            else
+                store_states<NP>(h[r], ht, d * N, nl, N, d < ch);
         }
-        float y = fmaf(D, u, sum_lanes(p, nl));
-        if (a.z != nullptr) y *= act_value(z, true);
-        if (live) static_cast<T *>(a.y)[row * a.ch + own] = from_f<T>(y);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int d = base + r * 8;
-        const int64_t dn = at + (int64_t)d * a.N;
-        if (vec && d < a.ch)
-            store_vec<float, NP>(a.ht + dn + n0, h[r]);
-        else
-            store_states<NP>(h[r], a.ht, dn, nl, a.N, d < a.ch);
     }
 }
 
@@ -414,7 +460,11 @@ int fwd_channels(int N) { return N <= 16 ? 2 * kFThr : (N <= 32 ? kFThr : kFThr 
 
 template <typename T>
 cudaError_t launch_step(const ScanArgs &a, cudaStream_t stream) {
-    const int64_t grid = (int64_t)a.seqs.N * ceil_div(a.ch, 256);
+    // the blocks of 256 channels, each as often as fills the GPU's slots once
+    const int64_t nblk = ceil_div(a.ch, 256);
+    int64_t per = (int64_t)kStepPerSM * (sm_count() > 0 ? sm_count() : 1) / nblk;
+    per = per < 1 ? 1 : (per > a.seqs.N ? a.seqs.N : per);
+    const int64_t grid = per * nblk;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     switch (np_of(a.N)) {
         case 2:
@@ -491,7 +541,7 @@ int scan_check(const kda_scan_params &p) {
     if (!aligned(p.A, 4) || !aligned(p.D, 4) || !aligned(p.dt_bias, 4) || !aligned(p.h0, 4) || !aligned(p.cu_seqlens, 4))
         return KDA_ERR_ALIGNMENT;
     const int64_t rows = p.cu_seqlens != nullptr ? (int64_t)p.T : (int64_t)p.batch * p.T;
-    if (rows > INT32_MAX || bc > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX || bc > INT32_MAX || (int64_t)p.channels * p.N > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
