@@ -185,10 +185,10 @@ __global__ void __launch_bounds__(kFThr, kPerSM) scan_fwd_kernel(const ScanArgs 
 #pragma unroll
         for (int i = 0; i < P2; i += 2) {
             const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sB[t * S::kNT + n0 + 2 * i]);
-            h[0][i] = fma2(exp2_2(mul2(dd0, A2[0][i])), h[0][i], mul2(xx0, B.x));
-            h[0][i + 1] = fma2(exp2_2(mul2(dd0, A2[0][i + 1])), h[0][i + 1], mul2(xx0, B.y));
-            h[1][i] = fma2(exp2_2(mul2(dd1, A2[1][i])), h[1][i], mul2(xx1, B.x));
-            h[1][i + 1] = fma2(exp2_2(mul2(dd1, A2[1][i + 1])), h[1][i + 1], mul2(xx1, B.y));
+            h[0][i] = fma2(decay2(dd0, A2[0][i]), h[0][i], mul2(xx0, B.x));
+            h[0][i + 1] = fma2(decay2(dd0, A2[0][i + 1]), h[0][i + 1], mul2(xx0, B.y));
+            h[1][i] = fma2(decay2(dd1, A2[1][i]), h[1][i], mul2(xx1, B.x));
+            h[1][i + 1] = fma2(decay2(dd1, A2[1][i + 1]), h[1][i + 1], mul2(xx1, B.y));
             if (kOut) {
                 const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sC[t * S::kNT + n0 + 2 * i]);
                 y0 = i == 0 ? mul2(h[0][0], C.x) : fma2(h[0][i], C.x, y0);
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(256, NP <= 4 ? kStepPerSM : 1) scan_step_kerne
                 p[r] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    h[r][i] = fmaf(tc5::ex2(dr * A2[r][i]), h[r][i], xr * B[i]);
+                    h[r][i] = fmaf(tc5::ex2(fmaf(dr, A2[r][i], kExpFix)), h[r][i], xr * B[i]);
                     p[r] = fmaf(C[i], h[r][i], p[r]);
                 }
             }

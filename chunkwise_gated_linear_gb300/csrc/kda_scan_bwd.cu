@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
         for (int i = 0; i < P2; i += 2) {
             const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sB[t * kNT + n0 + 2 * i]);
             const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sC[t * kNT + n0 + 2 * i]);
-            const f2 e0 = exp2_2(mul2(d2, A2[i])), e1 = exp2_2(mul2(d2, A2[i + 1]));
+            const f2 e0 = decay2(d2, A2[i]), e1 = decay2(d2, A2[i + 1]);
             h[i] = fma2(e0, h[i], mul2(x2, B.x));
             h[i + 1] = fma2(e1, h[i + 1], mul2(x2, B.y));
             P[i] = mul2(P[i], e0);
@@ -362,7 +362,7 @@ struct BwdBlock {
                 row_bc(B, sB, t);
                 row_dx(d2, x2, t);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) h[i] = fma2(exp2_2(mul2(d2, A2[i])), h[i], mul2(x2, B[i]));
+                for (int i = 0; i < NP; ++i) h[i] = fma2(decay2(d2, A2[i]), h[i], mul2(x2, B[i]));
             }
         }
     }
@@ -386,7 +386,7 @@ struct BwdBlock {
             row_dx(d2, x2, t);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                e[k][i] = exp2_2(mul2(d2, A2[i]));
+                e[k][i] = decay2(d2, A2[i]);
                 eh[k][i] = mul2(e[k][i], h[i]);
                 h[i] = fma2(x2, B[i], eh[k][i]);
             }

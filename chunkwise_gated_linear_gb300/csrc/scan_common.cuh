@@ -90,6 +90,13 @@ __device__ __forceinline__ float step_of(float s, bool softplus) {
         return tcu::softplus_fast(s);
 }
 
+// Decays exp(delta A) of a pair, A2 = A log2 e. The special-function unit's 2^x comes out low by 2e-8 on
+// average over the exponents that matter for a long memory (-1/2 to -1/256, measured), which a state that
+// remembers hundreds of steps adds up; kExpFix in the exponent (2e-8 log2 e, free in the multiply-add)
+// centres it. With delta = 0 the result is still exactly 1.
+constexpr float kExpFix = 3e-8f;
+__device__ __forceinline__ f2 decay2(f2 delta, f2 A2) { return exp2_2(fma2(delta, A2, pk(kExpFix, kExpFix))); }
+
 // The four per-step sums p[0..3] of a lane, added over the kLN lanes of a channel: lane nl
 // returns the total of step nl. Three exchanges instead of the eight of four butterflies.
 __device__ __forceinline__ float sum_lanes(const float (&p)[4], int nl) {

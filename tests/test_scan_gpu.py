@@ -238,6 +238,15 @@ def test_masked_tokens(dtype):
             assert not bool(p[:, off].any())
             p = p[:, keep]
         ref.check(f"gradient {i}", p, q.double().cpu(), p.dtype, WORK_GRAD + ref.HALF[p.dtype])
+    # nothing but masked tokens: the states are kept bit for bit, in one pass, in chunks and in steps
+    t["dt"].fill_(float("-inf"))
+    a, dy, dz, kw = _args(t, lens, True)
+    assert torch.equal(selective_scan_fwd(*a, *dz, **kw)[1], t["h0"])
+    for n in (1, 2):
+        u = t["u"][None, :n]
+        h = t["h0"][:1].clone()
+        selective_scan_step(u, t["dt"][None, :n], t["A"], t["B"][None, :n], t["C"][None, :n], h, dt_bias=t["bias"])
+        assert torch.equal(h, t["h0"][:1])
 
 
 def test_no_tokens():
