@@ -1,6 +1,8 @@
 """Chunkwise forward pass of the gated delta rule with a per-channel gate (Kimi Delta
 Attention) for GB300 (sm_103a): a C-ABI CUDA library (``include/kda.h``,
-``lib/libkda.so``) and its thin Python binding (:mod:`.kda`)."""
+``lib/libkda.so``) and its thin Python binding (:mod:`.kda`). The operators around the recurrence in
+a model's block (``include/kda_mixer.h``: short causal convolution, selective state space scan,
+gated output norm, residual update with norms) are bound in :mod:`.mixer`."""
 
 from .kda import (  # noqa: F401
     KdaError,

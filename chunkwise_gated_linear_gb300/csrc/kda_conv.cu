@@ -2,15 +2,15 @@
 //
 //   y_t = act(b + sum_j w_j x_{t-W+1+j}),   W = 2..4 taps per channel,
 //
-// x before a sequence's first token being its initial state. One thread takes V neighbouring
-// channels through a tile of rows with the last W - 1 inputs in registers, so that each
-// input is read once (plus W - 1 rows per tile) and every access is V contiguous elements.
+// x before a sequence's first token being its initial state. One thread takes four neighbouring
+// channels (one where rows are not aligned for that) through a tile of rows with the last W - 1 inputs in registers, so that each
+// input is read once (plus W - 1 rows per tile) and every access is four contiguous elements.
 // Tiles are cut over the rows of all sequences together: where a sequence ends inside
 // a tile its window is refilled from the next one's initial state, so ragged packed batches need
 // no table of tiles.
 //
-// Bound by memory: 2 bytes in and 2 out per bf16 element; about ten instructions per element,
-// under half of what the SMs issue in that time.
+// Bound by memory: 2 bytes in and 2 out per bf16 element. 32761 packed rows of 8192 channels in bf16: 174 us,
+// 6.2 TB/s. The gradient (16384 x 12288: 260 us, 4.7 TB/s) also issues 29 instructions per element.
 #include "mixer_common.cuh"
 
 namespace kda {

