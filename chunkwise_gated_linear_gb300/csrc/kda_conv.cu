@@ -10,7 +10,7 @@
 // no table of tiles.
 //
 // Bound by memory: 2 bytes in and 2 out per bf16 element. 32761 packed rows of 8192 channels in bf16: 174 us,
-// 6.2 TB/s. The gradient (16384 x 12288: 260 us, 4.7 TB/s) also issues 29 instructions per element.
+// 6.2 TB/s. The gradient (16384 x 12288: 250 us, 4.8 TB/s) also issues 29 instructions per element.
 #include "mixer_common.cuh"
 
 namespace kda {

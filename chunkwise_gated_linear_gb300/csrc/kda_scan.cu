@@ -278,41 +278,7 @@ __global__ void __launch_bounds__(kFThr, kPerSM) scan_fwd_kernel(const ScanArgs 
     }
 }
 
-// Chunk end states to chunk start states, in place; one thread per (channel, state) walks
-// the chunks, eight loads ahead. A chunk in which a sequence starts does not pass its start
-// state on. Chunk 0 starts a sequence: its own start state is not read.
-__global__ void __launch_bounds__(256) scan_carry_kernel(const ScanArgs a) {
-    constexpr int kAhead = 8;
-    __shared__ bool starts[256];  // whether a sequence starts in a chunk, 256 chunks at a time
-    const int64_t total = (int64_t)a.ch * a.N;
-    const int64_t at_e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t e = at_e < total ? at_e : total - 1;  // the block's barriers want every thread
-    const int d = (int)(e / a.N);
-    const float A = a.A[e] * kLog2e;
-    float in = 0.f;
-    for (int64_t cb = 0; cb < a.nchunks; cb += kAhead) {
-        if (cb % 256 == 0) {
-            __syncthreads();
-            const int64_t c0 = (cb + threadIdx.x) * a.chunk, c1 = c0 + a.chunk;
-            starts[threadIdx.x] = c1 <= a.seqs.rows && seq_find(a.seqs, c1 - 1).start >= c0;
-            __syncthreads();
-        }
-        float end[kAhead], sum[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (cb + i + 1 < a.nchunks) {  // the last chunk passes nothing on
-                end[i] = a.hchunk[(cb + i) * total + e];
-                sum[i] = a.schunk[(cb + i) * a.ch + d];
-            }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t c = cb + i;
-            if (c >= a.nchunks) break;
-            if (at_e < total) a.hchunk[c * total + e] = in;
-            if (c + 1 < a.nchunks) in = starts[c % 256] ? end[i] : fmaf(tc5::ex2(A * sum[i]), in, end[i]);
-        }
-    }
-}
+__global__ void __launch_bounds__(256) scan_carry_kernel(const ScanArgs a) { carry_states(a); }
 
 // The next T tokens of each sequence. Four lanes share four channels: each lane holds a quarter of the
 // states of all four (a warp reads 512 contiguous bytes of states at a time, four such reads in flight
@@ -515,17 +481,15 @@ cudaError_t run_fwd(const ScanArgs &a, cudaStream_t stream) {
     if (a.nchunks == 0) return launch_mode<T, kWhole>(a, a.seqs.N, stream);
     cudaError_t e = cudaSuccess;
     if (a.nchunks > 1) e = launch_mode<T, kSummary>(a, a.nchunks - 1, stream);  // nothing follows the last
-    if (e == cudaSuccess && a.nchunks > 1) e = launch_scan_carry(a, stream);
+    if (e == cudaSuccess && a.nchunks > 1) {
+        scan_carry_kernel<<<(unsigned)ceil_div((int64_t)a.ch * a.N, 256), 256, 0, stream>>>(a);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) e = launch_mode<T, kChunk>(a, a.nchunks, stream);
     return e;
 }
 
 }  // namespace
-
-cudaError_t launch_scan_carry(const ScanArgs &a, cudaStream_t stream) {
-    scan_carry_kernel<<<(unsigned)ceil_div((int64_t)a.ch * a.N, 256), 256, 0, stream>>>(a);
-    return cudaGetLastError();
-}
 
 int scan_check(const kda_scan_params &p) {
     if (p.batch < 1 || p.T < 0 || p.channels < 1 || p.N < 1 || p.G < 1 || p.channels % p.G != 0) return KDA_ERR_INVALID_ARG;

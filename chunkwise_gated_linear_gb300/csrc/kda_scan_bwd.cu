@@ -22,7 +22,7 @@
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
 // fixed order. Bound by issue: about 11 instructions per (token, channel, state) in the first kernel, 34 in the
-// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1120 us, of which 240 and 830.
+// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1104 us, of which 236 and 810.
 #include <type_traits>
 
 #include "scan_common.cuh"
@@ -215,11 +215,11 @@ cudaError_t launch_local(BwdArgs b, cudaStream_t stream) {
 }
 
 // ---- 2: between the chunks, in place ----------------------------------------------------------
-// Adjoints (states: scan_carry_kernel): the adjoint that enters chunk c - 1 at its end is chunk
+// Adjoints: the adjoint that enters chunk c - 1 at its end is chunk
 // c's local one plus, when no sequence ends in chunk c, exp(A sum delta) times what enters c.
-__global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdArgs b) {
+__device__ __forceinline__ void carry_adjoints(const BwdArgs &b) {
     const ScanArgs &a = b.f;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     __shared__ bool ends[256];
     const int64_t total = (int64_t)a.ch * a.N;
     const int64_t at_e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -252,6 +252,14 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdArgs b) {
             if (c > 0) in = ends[(k + i) % 256] ? loc[i] : fmaf(tc5::ex2(A * sum[i]), in, loc[i]);
         }
     }
+}
+
+// Both ways at once: half the blocks each.
+__global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdArgs b) {
+    if (blockIdx.y == 0)
+        carry_states(b.f);
+    else
+        carry_adjoints(b);
 }
 
 // ---- 3: the gradients -------------------------------------------------------------------------
@@ -710,9 +718,7 @@ cudaError_t launch_np(const BwdArgs &b, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     if (a.nchunks > 1) {
-        e = launch_scan_carry(a, stream);
-        if (e != cudaSuccess) return e;
-        scan_bwd_carry_kernel<<<(unsigned)ceil_div((int64_t)a.ch * a.N, 256), 256, 0, stream>>>(b);
+        scan_bwd_carry_kernel<<<dim3((unsigned)ceil_div((int64_t)a.ch * a.N, 256), 2), 256, 0, stream>>>(b);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

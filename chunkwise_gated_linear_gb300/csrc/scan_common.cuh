@@ -192,11 +192,46 @@ __device__ __forceinline__ void put_states(const f2 (&h)[NS / 2], float *base, i
 // which write eight groups' same channel use different banks.
 __device__ __forceinline__ int slot_of(int d) { return (d & ~7) | ((d ^ (d >> 3)) & 7); }
 
+// Chunk end states to chunk start states, in place; one thread per (channel, state) walks
+// the chunks, 16 loads ahead, in blocks of 256. A chunk in which a sequence starts does not pass its start
+// state on. Chunk 0 starts a sequence: its own start state is not read.
+__device__ __forceinline__ void carry_states(const ScanArgs &a) {
+    constexpr int kAhead = 16;
+    __shared__ bool starts[256];  // whether a sequence starts in a chunk, 256 chunks at a time
+    const int64_t total = (int64_t)a.ch * a.N;
+    const int64_t at_e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t e = at_e < total ? at_e : total - 1;  // the block's barriers want every thread
+    const int d = (int)(e / a.N);
+    const float A = a.A[e] * kLog2e;
+    float in = 0.f;
+    for (int64_t cb = 0; cb < a.nchunks; cb += kAhead) {
+        if (cb % 256 == 0) {
+            __syncthreads();
+            const int64_t c0 = (cb + threadIdx.x) * a.chunk, c1 = c0 + a.chunk;
+            starts[threadIdx.x] = c1 <= a.seqs.rows && seq_find(a.seqs, c1 - 1).start >= c0;
+            __syncthreads();
+        }
+        float end[kAhead], sum[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (cb + i + 1 < a.nchunks) {  // the last chunk passes nothing on
+                end[i] = a.hchunk[(cb + i) * total + e];
+                sum[i] = a.schunk[(cb + i) * a.ch + d];
+            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t c = cb + i;
+            if (c >= a.nchunks) break;
+            if (at_e < total) a.hchunk[c * total + e] = in;
+            if (c + 1 < a.nchunks) in = starts[c % 256] ? end[i] : fmaf(tc5::ex2(A * sum[i]), in, end[i]);
+        }
+    }
+}
+
 // ---- host ------------------------------------------------------------------------------------
 int scan_check(const kda_scan_params &p);
 // Arguments without chunk buffers and error word. `vec` covers u, dt, z and the given pointers.
 ScanArgs scan_args(const kda_scan_params &p, const void *const *more, int n);
-cudaError_t launch_scan_carry(const ScanArgs &a, cudaStream_t stream);
 
 }  // namespace scan
 }  // namespace kda
