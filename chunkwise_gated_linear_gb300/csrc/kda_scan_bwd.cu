@@ -21,8 +21,8 @@
 //      last to first: a and a h_{t-1} of their tokens in registers, then backwards.
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
-// fixed order. Bound by issue: about 11 instructions per (token, channel, state) in the first kernel, 34 in the
-// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1104 us, of which 236 and 810.
+// fixed order. Bound by issue: about 11 instructions per (token, channel, state) in the first kernel, 37 in the
+// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1080 us, of which 236 and 785.
 #include <type_traits>
 
 #include "scan_common.cuh"
@@ -34,7 +34,7 @@ namespace {
 
 // Tokens per window: what the third kernel keeps states of in shared memory. With 16 states, windows of 16
 // and groups of two tokens leave registers and shared memory for four blocks per SM (2 x 4096 tokens
-// of 4096 channels: 1135 us); windows of 32 and groups of four for three (1204 us).
+// of 4096 channels: 1135 us, 1080 since); windows of 32 and groups of four for three (1204 us).
 __host__ __device__ constexpr int win_of(int np) { return np <= 8 ? 16 : 8; }
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -284,8 +284,9 @@ __device__ __forceinline__ float sum_channels(const float (&v)[8], int lane) {
 
 // A block: 128 threads, 64 channels. Warp w has channels 16 w .. 16 w + 15: thread (dl, nl) = (lane / 4,
 // lane % 4) has channels 16 w + dl and 16 w + 8 + dl, as the two halves of every pair, and states
-// nl NP .. nl NP + NP - 1 of both: step sizes, inputs and gradients of a pair come as pairs,
-// B and C (the same for all channels) are kept doubled in shared memory.
+// nl NP .. nl NP + NP - 1 of both: step sizes, inputs and gradients of a pair come as pairs, B and C (the
+// same for all channels) are doubled in registers (doubled in shared memory they took a quarter of
+// the load/store wavefronts: 1104 us for the sizes below where this takes 1080).
 template <int NP>
 struct BwdShape {
     static constexpr int kThr = 128, kWarps = 4;
@@ -298,7 +299,7 @@ struct BwdShape {
     static constexpr int kTileA = kWin * 32 * 16;              // delta and x of a pair; then s and w
     static constexpr int kTileG = kWin * 32 * 8;               // g; then y
     static constexpr int kTileD = kWin * 32 * 8;               // delta
-    static constexpr int kBCBytes = 2 * kWin * kNT * 8;
+    static constexpr int kBCBytes = 2 * kWin * kNT * 4;
     static constexpr int kFlags = kWin * 8;                    // per row: sequence, start / end bits
     static constexpr int kPar = 2 * kDB * 4;                   // dt_bias and D of the channels
     static constexpr int kSmem = kCkpt + kTileA + kTileG + kTileD + kBCBytes + kFlags + kPar;
@@ -314,7 +315,7 @@ struct BwdBlock {
     const BwdArgs &b;
     float4 *tileA;       // [kWin][32]
     float2 *tileG;       // [kWin][32]
-    const f2 *sB, *sC;   // [kWin][kNT], doubled
+    const float *sB, *sC;   // [kWin][kNT]
     float4 *ckpt;        // [kGroups][kWarps][NP / 2][32]
     const int *seq_of, *flag_of;
     int lane, warp, nl, dl;
@@ -340,13 +341,24 @@ struct BwdBlock {
         store_states<NP>(hi, base, at + dn1, nl, b.f.N, live1);
     }
     __device__ __forceinline__ int64_t seq_at(int t) const { return seq_of[t] * (int64_t)b.f.ch * b.f.N; }
-    __device__ __forceinline__ void row_bc(f2 (&v)[NP], const f2 *s, int t) const {
+    __device__ __forceinline__ void row_bc(f2 (&v)[NP], const float *s, int t) const {
+        float f[NP];
+        if constexpr (NP >= 4) {
 #pragma unroll
-        for (int i = 0; i < NP / 2; ++i) {
-            const ulonglong2 q = reinterpret_cast<const ulonglong2 *>(s + t * S::kNT + nl * NP)[i];
-            v[2 * i] = q.x;
-            v[2 * i + 1] = q.y;
+            for (int i = 0; i < NP / 4; ++i) {
+                const float4 q = reinterpret_cast<const float4 *>(s + t * S::kNT + nl * NP)[i];
+                f[4 * i] = q.x;
+                f[4 * i + 1] = q.y;
+                f[4 * i + 2] = q.z;
+                f[4 * i + 3] = q.w;
+            }
+        } else {
+            const float2 q = *reinterpret_cast<const float2 *>(s + t * S::kNT + nl * NP);
+            f[0] = q.x;
+            f[1] = q.y;
         }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[i] = pk(f[i], f[i]);
     }
     // delta and x of the pair at token t
     __device__ __forceinline__ void row_dx(f2 &d2, f2 &x2, int t) const {
@@ -489,14 +501,14 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 4 : 1) scan_bwd_
     k.tileA = reinterpret_cast<float4 *>(take(S::kTileA));
     k.tileG = reinterpret_cast<float2 *>(take(S::kTileG));
     float *tileD = reinterpret_cast<float *>(take(S::kTileD));
-    float2 *sB = reinterpret_cast<float2 *>(take(S::kBCBytes));
+    float *sB = reinterpret_cast<float *>(take(S::kBCBytes));
     int *seq_of = reinterpret_cast<int *>(take(S::kFlags)), *flag_of = seq_of + kWin;
     float *sbias = reinterpret_cast<float *>(take(S::kPar)), *sD = sbias + kDB;
     if (tid < kDB) {
         sbias[tid] = a.bias != nullptr && tid < ch.n ? a.bias[ch.d0 + tid] : 0.f;
         sD[tid] = a.D != nullptr && tid < ch.n ? a.D[ch.d0 + tid] : 0.f;
     }
-    k.sB = reinterpret_cast<const f2 *>(sB);
+    k.sB = sB;
     k.sC = k.sB + kWin * S::kNT;
     k.seq_of = seq_of;
     k.flag_of = flag_of;
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(BwdShape<NP>::kThr, NP <= 4 ? 4 : 1) scan_bwd_
             float v = 0.f;
             if (row < w1 && n < a.N)
                 v = to_f(static_cast<const T *>(isC ? a.C : a.B)[row * (isC ? a.cs : a.bs) + (int64_t)ch.g * a.N + n]);
-            sB[e] = make_float2(v, v);  // C follows B
+            sB[e] = v;  // C follows B
         }
         const SeqAt last = seq_find(a.seqs, w1 - 1);
         const bool ragged = !(last.start < w0 && last.end > w1);  // a sequence starts or ends here

@@ -159,7 +159,8 @@ int kda_scan_step(const kda_scan_params *p, cudaStream_t stream);
  *   du, ddt, dz like u (contiguous); dB, dC like B (contiguous; sums over the channels of a
  *   group); dA [channels, N], dD, ddt_bias [channels], dh0 like h0: fp32
  * ddt is the gradient with respect to dt as given (before bias and softplus). Scratch:
- * kda_scan_bwd_workspace bytes.
+ * kda_scan_bwd_workspace bytes: per token about channels N / 4 bytes of states (at every 16th token, fp32)
+ * and channels N / 8 bytes of the blocks' shares of dB and dC, and what the chunks hand over.
  */
 typedef struct kda_scan_bwd_params {
     kda_scan_params f;
