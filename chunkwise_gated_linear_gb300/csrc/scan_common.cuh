@@ -1,9 +1,10 @@
-// What the forward and backward kernels of the selective scan share: arguments, the tile of
-// tokens in shared memory, step sizes, and the split of the tokens into chunks.
+// What the kernels of the selective scan share: arguments, step sizes and decays, states in memory, and
+// the carry between chunks.
 //
-// Layout of a block: 256 threads take 64 channels; channel dl = tid / 4 is shared by four
-// neighbouring lanes, lane nl = tid % 4 holding states nl NP .. nl NP + NP - 1 of it (NP = 2, 4,
-// 8, 16: the smallest that holds N; the rest are zero states that stay zero).
+// Two layouts. The walks (forward, and the gradient's local pass): a thread owns up to 16 states of one or two
+// channels, 17 to 64 states take 2 or 4 lanes. The step and the gradient's third kernel: four neighbouring lanes
+// share channels, lane nl holding states nl NP .. nl NP + NP - 1 (NP = 2, 4, 8, 16: the smallest that
+// holds N; the rest are zero states that stay zero).
 #pragma once
 
 #include "mixer_common.cuh"
@@ -13,10 +14,8 @@ namespace scan {
 
 using namespace mix;
 
-constexpr int kThreads = 256;
-constexpr int kDB = 64;   // channels per block
-constexpr int kLN = 4;    // lanes that share a channel
-constexpr int kTK = 32;   // tokens per tile
+constexpr int kDB = 64;  // channels per block of the gradient's third kernel
+constexpr int kLN = 4;   // lanes that share a channel in the second layout
 constexpr int kMaxN = 64;
 
 struct ScanArgs {
@@ -44,7 +43,7 @@ struct ScanArgs {
 
 inline int np_of(int N) { return N <= 8 ? 2 : (N <= 16 ? 4 : (N <= 32 ? 8 : 16)); }
 
-// A block's channels: group g, the first channel, and how many of the 64 exist.
+// A block's channels (gradient's third kernel): group g, the first channel, and how many of the 64 exist.
 struct Chans {
     int g, d0, n;
 };
@@ -97,8 +96,8 @@ __device__ __forceinline__ float step_of(float s, bool softplus) {
 constexpr float kExpFix = 3e-8f;
 __device__ __forceinline__ f2 decay2(f2 delta, f2 A2) { return exp2_2(fma2(delta, A2, pk(kExpFix, kExpFix))); }
 
-// The four per-step sums p[0..3] of a lane, added over the kLN lanes of a channel: lane nl
-// returns the total of step nl. Three exchanges instead of the eight of four butterflies.
+// Four values of each lane, added over the kLN lanes that share channels: lane nl returns the total of
+// value nl. Three exchanges instead of the eight of four butterflies.
 __device__ __forceinline__ float sum_lanes(const float (&p)[4], int nl) {
     const bool hi = nl & 2, odd = nl & 1;
     const float a0 = hi ? p[0] : p[2], a1 = hi ? p[1] : p[3];
@@ -126,31 +125,6 @@ __device__ __forceinline__ void store_states(const float (&h)[NP], float *base, 
         if (live && n < N) base[at + n] = h[i];
     }
 }
-template <int NP>
-__device__ __forceinline__ void to_pairs(f2 (&p)[NP / 2], const float (&h)[NP]) {
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) p[i] = pk(h[2 * i], h[2 * i + 1]);
-}
-template <int NP>
-__device__ __forceinline__ void from_pairs(float (&h)[NP], const f2 (&p)[NP / 2]) {
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) upk(p[i], h[2 * i], h[2 * i + 1]);
-}
-// NP floats of shared memory as pairs (8 or 16 bytes at a time)
-template <int NP>
-__device__ __forceinline__ void lds_pairs(f2 (&p)[NP / 2], const float *s) {
-    if constexpr (NP == 2) {
-        p[0] = *reinterpret_cast<const f2 *>(s);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) {
-            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(s + 4 * i);
-            p[2 * i] = q.x;
-            p[2 * i + 1] = q.y;
-        }
-    }
-}
-
 // A thread's NS states of a channel, at `at` = first state of [..][N], zeros past N.
 template <int NS>
 __device__ __forceinline__ void get_states(f2 (&h)[NS / 2], const float *base, int64_t at, int n0, int N, bool live, bool vec) {
@@ -187,10 +161,6 @@ __device__ __forceinline__ void put_states(const f2 (&h)[NS / 2], float *base, i
         }
     }
 }
-
-// Slot of channel d (0..63) in a row of 64: rotated inside groups of 8 so that eight lanes
-// which write eight groups' same channel use different banks.
-__device__ __forceinline__ int slot_of(int d) { return (d & ~7) | ((d ^ (d >> 3)) & 7); }
 
 // Chunk end states to chunk start states, in place; one thread per (channel, state) walks
 // the chunks, 16 loads ahead, in blocks of 256. A chunk in which a sequence starts does not pass its start
