@@ -122,7 +122,7 @@ size_t kda_conv_bwd_workspace(const kda_conv_bwd_params *p);
  *   A [channels, N], D, dt_bias [channels] fp32 (dt_bias may be NULL)
  *   h0, ht       [N_seq, channels, N] fp32, either may be NULL (h0: zeros); ht must not be h0
  *                (KDA_ERR_INVALID_ARG; kda_scan_step updates in place)
- * 1 <= N <= 64; channels divisible by G.
+ * 1 <= N <= 64; channels divisible by G; channels N and the number of tokens below 2^31.
  * Where one pass over the tokens would leave most of the GPU idle (few channels and sequences)
  * the tokens are cut into pieces: scratch of kda_scan_fwd_workspace bytes.
  */

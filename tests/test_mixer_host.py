@@ -105,7 +105,7 @@ INV, UNS, ALI = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_AL
     ("scan_fwd", _scan, dict(G=3), INV), ("scan_fwd", _scan, dict(G=0), INV), ("scan_fwd", _scan, dict(N=0), INV),
     ("scan_fwd", _scan, dict(N=65), UNS), ("scan_fwd", _scan, dict(dtype=5), UNS), ("scan_fwd", _scan, dict(B_stride=31), INV),
     ("scan_fwd", _scan, dict(z_stride=8), INV), ("scan_fwd", _scan, dict(u=A + 1), ALI), ("scan_fwd", _scan, dict(h0=A + 2), ALI),
-    ("scan_fwd", _scan, dict(batch=1 << 16, T=1 << 16), UNS),
+    ("scan_fwd", _scan, dict(batch=1 << 16, T=1 << 16), UNS), ("scan_fwd", _scan, dict(channels=1 << 28), UNS),
     ("scan_step", _scan, dict(h0=None), INV), ("scan_step", _scan, dict(ht=None), INV), ("scan_step", _scan, dict(cu_seqlens=A), INV),
     ("scan_bwd", _scan_bwd, dict(dy=None), INV), ("scan_bwd", _scan_bwd, dict(dA=None), INV), ("scan_bwd", _scan_bwd, dict(dB=None), INV),
     ("scan_bwd", _scan_bwd, dict(D=None), INV), ("scan_bwd", _scan_bwd, dict(z=None), INV), ("scan_bwd", _scan_bwd, dict(N=100), UNS),
