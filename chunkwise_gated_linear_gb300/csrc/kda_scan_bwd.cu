@@ -89,13 +89,19 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
         f[i] = 0;
     }
     float S = 0.f;
-    // the adjoint from the end of a sequence: dht, through the decays since the chunk's start
-    auto add_dht = [&]() {
-        if (b.dht == nullptr) return;
-        f2 t[P2];
-        get_states<NS>(t, b.dht, at.s * cn + dn, n0, a.N, live, vst);
+    // The chunk's start adjoint is that of the sequence which holds its first row: it is complete, and leaves,
+    // where that sequence or the chunk ends, with dht (if the sequence ends) through the decays since
+    // the chunk's start. What f and P become in later sequences of the chunk is not used. (Were
+    // they held at zero instead, an infinity there would come back as NaN in the sequence before.)
+    auto open = [&] { return at.start <= c0; };
+    auto leave = [&](bool ends) {
+        if (ends && b.dht != nullptr) {
+            f2 t[P2];
+            get_states<NS>(t, b.dht, at.s * cn + dn, n0, a.N, live, vst);
 #pragma unroll
-        for (int i = 0; i < P2; ++i) f[i] = fma2(P[i], t[i], f[i]);
+            for (int i = 0; i < P2; ++i) f[i] = fma2(P[i], t[i], f[i]);
+        }
+        put_states<NS>(f, b.gchunk, part * cn + dn, n0, a.N, live, a.N == kNT);
     };
     const float bias = a.bias != nullptr ? a.bias[d] : 0.f;
     const bool gate = a.z != nullptr;
@@ -188,9 +194,7 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
                 for (int k = 0; k < 4; ++k) {
                     if (r + k >= c1) break;
                     if (r + k == at.end) {
-                        add_dht();
-#pragma unroll
-                        for (int i = 0; i < P2; ++i) P[i] = 0;
+                        if (open()) leave(true);
                         seq_next(a.seqs, at);
                         get_states<NS>(h, a.h0, at.s * cn + dn, n0, a.N, live && a.h0 != nullptr, vst);
                     }
@@ -199,9 +203,8 @@ __global__ void __launch_bounds__(kLThr, 4) scan_bwd_local_kernel(const BwdArgs 
             }
         }
     }
-    if (c1 == at.end) add_dht();
+    if (open()) leave(c1 == at.end);
     put_states<NS>(h, a.hchunk, part * cn + dn, n0, a.N, live, a.N == kNT);
-    put_states<NS>(f, b.gchunk, part * cn + dn, n0, a.N, live, a.N == kNT);
     if (live && n0 == 0) a.schunk[part * a.ch + d] = S;
 }
 

@@ -329,3 +329,31 @@ def test_agrees_with_the_decay_only_recurrence():
     y, ht = selective_scan_fwd(u, delta.expand(1, T, ch).contiguous(), A, B, C, dt_softplus=False)
     o, h = chunk_kda_fwd(C, B, (delta * u).unsqueeze(2).contiguous(), (-delta).contiguous(), None, scale=1.0)
     assert ref.rel(y, o.double().cpu()[:, :, 0]) < 1e-5 and ref.rel(ht, h.double().cpu()[:, 0].transpose(1, 2)) < 1e-5
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("what", ["u", "dt", "B", "C", "z", "dy", "h0", "dht"])
+@pytest.mark.parametrize("dtype,N", [(BF, 16), (F32, 5), (F32, 40)])
+def test_nonfinite_values_stay_in_their_sequence(dtype, N, what, value):
+    """Values that are not finite in one sequence leave the outputs and gradients of the others as
+    they are, bit for bit: packed (the sequence before it runs over several chunks and ends in
+    the same chunk as the bad one and the start of the next) and in a batch."""
+    for lens, packed in (([100, 10, 60, 40], True), ([41, 41, 41], False)):
+        t = _make(lens, 64, N, 1, dtype, 21)
+        run = lambda: [selective_scan_fwd(*a, *dz, **kw), selective_scan_bwd(*a, dy, *dz, dht=t["dht"], **kw)]  # noqa: E731
+        a, dy, dz, kw = _args(t, lens, packed)
+        clean = run()
+        t = dict(t, **{what: t[what].clone()})
+        first, last = lens[0], lens[0] + lens[1]
+        t[what][1 if what in ("h0", "dht") else slice(first + 3, first + 5)] = value
+        a, dy, dz, kw = _args(t, lens, packed)
+        bad = run()
+        rows = torch.ones(sum(lens), dtype=torch.bool, device=dev)
+        rows[first:last] = False
+        seqs = torch.tensor([True, False] + [True] * (len(lens) - 2), device=dev)
+        (y, ht), (du, ddt, _, dB, dC, _, dzg, _, dh0) = (tuple(zip(p, q)) for p, q in zip(clean, bad))
+        for name, (p, q) in dict(y=y, du=du, ddt=ddt, dB=dB, dC=dC, dz=dzg).items():
+            p, q = (x.reshape(sum(lens), -1)[rows] for x in (p, q))
+            assert torch.equal(p, q), (name, packed)
+        for name, (p, q) in dict(ht=ht, dh0=dh0).items():
+            assert torch.equal(p[seqs], q[seqs]), (name, packed)
