@@ -203,12 +203,18 @@ def _token_stride(t, name, lead=2):
 
 def _device(strided, dense):
     """Every tensor on one CUDA device, those of ``dense`` contiguous."""
-    for t in dense:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            raise ValueError("every tensor must be a CUDA tensor, and all but the data inputs contiguous")
-    for t in strided:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor, and all but the data inputs contiguous")
+    dev = -1
+    for tensors, contiguous in ((dense, True), (strided, False)):
+        for t in tensors:
+            if t is None:
+                continue
+            d = t.get_device()  # -1 on the host
+            if d < 0 or (contiguous and not t.is_contiguous()):
+                raise ValueError("every tensor must be a CUDA tensor, and all but the data inputs contiguous")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError("every tensor must be on one CUDA device")
+                dev = d
 
 
 def _sequences(cu_seqlens, B):
@@ -231,22 +237,36 @@ def _act(activation, allowed):
     return known[activation]
 
 
-def _stream(t):
-    """The handle of torch's current stream on the tensor's device. torch's own raw getter makes no
-    Stream object (2 us less per call); the public way where a torch version lacks it."""
+# torch's own raw getters: no Stream object, no check that CUDA has been initialised (2 us less per
+# call). The public ways where a torch version lacks them.
+
+def _stream(device):
+    """The handle of torch's current stream on a device."""
     torch = sys.modules["torch"]
 
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream(t.device).cuda_stream if raw is None else raw(t.get_device())
+    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device)
+
+
+def _current_device():
+    torch = sys.modules["torch"]
+
+    raw = getattr(torch._C, "_cuda_getDevice", None)
+    return torch.cuda.current_device() if raw is None else raw()
 
 
 def _call(name, p, t, stream, workspace=False):
     """Run a C entry point; ``workspace``: give it torch memory for its scratch. On a stream
     that torch does not know of, the library takes the scratch from its own pool instead: torch
-    would hand the memory out again before that stream is done with it."""
+    would hand the memory out again before that stream is done with it. The library launches on the
+    current device: that of the tensors, of which ``t`` is one, is made current for the call."""
+    device = t.get_device()
+    if device != _current_device():
+        with sys.modules["torch"].cuda.device(device):
+            return _call(name, p, t, stream, workspace)
     ws = None  # keeps the scratch until the call has been queued
     if stream is None:
-        stream = _stream(t)
+        stream = _stream(device)
         if workspace:
             n = _fn(name + "_workspace")(p)
             if n:

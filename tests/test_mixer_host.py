@@ -274,3 +274,92 @@ def test_reference_gradients_against_differences():
         diff = float((value(eps) - value(-eps)) / (2 * eps))
         want = float(sum((a * w).sum() for a, w in zip(got, way)))
         assert abs(diff - want) <= 1e-7 * (1 + abs(want))
+
+
+class _OnGpu(torch.Tensor):
+    """A host tensor that says it lies on the GPU ``gpu``: what the binding's checks see of a device."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+    def get_device(self):
+        return self.gpu
+
+
+def _on(gpu, *shape, dtype=torch.bfloat16):
+    t = _t(*shape, dtype=dtype).as_subclass(_OnGpu)
+    t.gpu = gpu
+    return t
+
+
+def _device_calls():
+    """Every call of the binding with all its tensor arguments: (function, {name: (shape, dtype)}, other arguments)."""
+    bf, i32 = torch.bfloat16, torch.int32
+    conv = dict(x=((1, 5, 16), bf), weight=((16, 4), F), bias=((16,), F), s0=((2, 3, 16), bf), cu_seqlens=((3,), i32))
+    scan = dict(u=((1, 5, 12), bf), dt=((1, 5, 12), bf), A=((12, 7), F), B=((1, 5, 3, 7), bf), C=((1, 5, 3, 7), bf), D=((12,), F),
+                z=((1, 5, 12), bf), dt_bias=((12,), F))
+    packed = dict(scan, h0=((2, 12, 7), F), cu_seqlens=((3,), i32))
+    gated = dict(x=((5, 16), bf), z=((5, 16), bf), weight=((16,), F))
+    block = dict(x=((5, 16), bf), residual=((5, 16), F), weight=((16,), F), post_weight=((16,), F), z=((5, 16), bf), scale=((16,), F))
+    return [
+        (pkg.causal_conv_fwd, dict(conv, y=((1, 5, 16), bf), st=((2, 3, 16), bf)), dict(output_final_state=True)),
+        (pkg.causal_conv_step, dict(x=((2, 1, 16), bf), state=((2, 3, 16), bf), weight=((16, 4), F), bias=((16,), F), y=((2, 1, 16), bf)), {}),
+        (pkg.causal_conv_bwd, dict(conv, dy=((1, 5, 16), bf), dst=((2, 3, 16), bf)), {}),
+        (pkg.selective_scan_fwd, dict(packed, y=((1, 5, 12), bf), ht=((2, 12, 7), F)), {}),
+        (pkg.selective_scan_step, dict(scan, h=((1, 12, 7), F), y=((1, 5, 12), bf)), {}),
+        (pkg.selective_scan_bwd, dict(packed, dy=((1, 5, 12), bf), dht=((2, 12, 7), F)), {}),
+        (pkg.gated_norm_fwd, dict(gated, y=((5, 16), bf)), {}),
+        (pkg.gated_norm_bwd, dict(gated, dy=((5, 16), bf)), {}),
+        (pkg.block_norm_fwd, dict(block, y=((5, 16), bf), new_residual=((5, 16), F)), {}),
+        (pkg.block_norm_bwd, dict(block, dy=((5, 16), bf), dresidual=((5, 16), F)), {}),
+    ]
+
+
+@pytest.fixture
+def on_gpus(monkeypatch):
+    """Device 0 is current; the library's calls are recorded with the device that is current then."""
+    current, calls = [0], []
+
+    class device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            current.append(self.d)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    def fn(name):
+        def call(p, *stream):
+            calls.append((name, current[-1]))
+            return 0
+        return call
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(mixer, "_current_device", lambda: current[-1])
+    monkeypatch.setattr(mixer, "_fn", fn)
+    monkeypatch.setattr(mixer, "_stream", lambda device: 0)
+    return calls
+
+
+@pytest.mark.parametrize("fn,tensors,more", _device_calls(), ids=lambda v: getattr(v, "__name__", ""))
+def test_tensors_of_two_devices_are_rejected(on_gpus, fn, tensors, more):
+    make = lambda other: {k: _on(1 if k == other else 0, *s, dtype=d) for k, (s, d) in tensors.items()}  # noqa: E731
+    fn(**make(None), **more)
+    assert [d for _, d in on_gpus] == [0] * len(on_gpus) and on_gpus
+    on_gpus.clear()
+    for other in tensors:
+        with pytest.raises(ValueError, match="one CUDA device"):
+            fn(**make(other), **more)
+    assert not on_gpus
+
+
+@pytest.mark.parametrize("fn,tensors,more", _device_calls(), ids=lambda v: getattr(v, "__name__", ""))
+def test_calls_run_on_the_tensors_device(on_gpus, fn, tensors, more):
+    """Workspace query and call with the tensors' device current, also where a stream is given."""
+    for kw in ({}, dict(stream=7)):
+        fn(**{k: _on(1, *s, dtype=d) for k, (s, d) in tensors.items()}, **more, **kw)
+    assert [d for _, d in on_gpus] == [1] * len(on_gpus)
+    assert len([n for n, _ in on_gpus if not n.endswith("_workspace")]) == 2
