@@ -178,6 +178,32 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _one_device(tensors):
+    """Every tensor (None passes) contiguous and on one CUDA device; returns its index."""
+    device = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()  # -1 on the host
+        if d < 0 or not t.is_contiguous():
+            raise ValueError("every tensor must be a contiguous CUDA tensor")
+        if d != device:
+            if device >= 0:
+                raise ValueError("every tensor must be on one CUDA device")
+            device = d
+    return device
+
+
+def _on_device(device, call, *args):
+    """``call(*args)`` with ``device`` current: the library launches on the current device."""
+    import torch
+
+    if device == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
 def chunk_kda_fwd(q, k, v, g, beta, *, h0=None, scale=None, cu_seqlens=None,
                   output_final_state=True, chunk_size=64, o=None, ht=None, stream=None,
                   one_cta_per_unit=False, recurrent=False, qk_l2norm=False, beta_sigmoid=False,
@@ -252,9 +278,7 @@ def chunk_kda_fwd(q, k, v, g, beta, *, h0=None, scale=None, cu_seqlens=None,
         raise ValueError("o must be [B, T, H_v, d_v] in the dtype of q")
     if ht is not None and output_final_state and (ht.dtype != torch.float32 or tuple(ht.shape) != (N, H_v, d_k, d_v)):
         raise ValueError("ht must be fp32 [N, H_v, d_k, d_v]")
-    for t in (q, k, v, g, beta, h0, cu_seqlens, A_log, dt_bias, o, ht if output_final_state else None):
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("every tensor must be a contiguous CUDA tensor")
+    device = _one_device((q, k, v, g, beta, h0, cu_seqlens, A_log, dt_bias, o, ht if output_final_state else None))
     if o is None:
         o = torch.empty((B, T, H_v, d_v), dtype=q.dtype, device=q.device)
     if output_final_state and ht is None:
@@ -277,10 +301,10 @@ def chunk_kda_fwd(q, k, v, g, beta, *, h0=None, scale=None, cu_seqlens=None,
         fe = kda_frontend(1 if qk_l2norm else 0, 1 if beta_sigmoid else 0, _ptr(A_log) or None,
                           _ptr(dt_bias) or None)
         name = "kda_recurrent_fwd_fused" if recurrent else "kda_chunk_fwd_fused"
-        st = (kda_recurrent_fwd_fused if recurrent else kda_chunk_fwd_fused)(p, fe, stream)
+        st = _on_device(device, kda_recurrent_fwd_fused if recurrent else kda_chunk_fwd_fused, p, fe, stream)
     else:
         name = "kda_recurrent_fwd_ex" if recurrent else "kda_chunk_fwd_ex"
-        st = (kda_recurrent_fwd_ex if recurrent else kda_chunk_fwd_ex)(p, stream)
+        st = _on_device(device, kda_recurrent_fwd_ex if recurrent else kda_chunk_fwd_ex, p, stream)
     if st != KDA_OK:
         raise KdaError(st, name)
     return o, ht
@@ -331,9 +355,7 @@ def chunk_kda_bwd(q, k, v, g, beta, do, *, h0=None, dht=None, scale=None, cu_seq
     for name, t in (("h0", h0), ("dht", dht)):
         if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (N, H_v, d_k, d_v)):
             raise ValueError(f"{name} must be fp32 [N, H_v, d_k, d_v]")
-    for t in (q, k, v, g, beta, do, h0, dht, cu_seqlens):
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("every tensor must be a contiguous CUDA tensor")
+    device = _one_device((q, k, v, g, beta, do, h0, dht, cu_seqlens))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dg = torch.empty_like(g)
     dbeta = None if beta is None else torch.empty_like(beta)
@@ -346,7 +368,7 @@ def chunk_kda_bwd(q, k, v, g, beta, do, *, h0=None, dht=None, scale=None, cu_seq
                        _ptr(do), _ptr(dht) or None, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
                        _ptr(dbeta) or None, _ptr(dh0) or None, nb, T, H_k, H_v, d_k, d_v, chunk_size,
                        float(scale), _ptr(cu_seqlens) or None, dtype, gate, 0)
-    st = kda_chunk_bwd(p, stream)
+    st = _on_device(device, kda_chunk_bwd, p, stream)
     if st != KDA_OK:
         raise KdaError(st, "kda_chunk_bwd")
     return dq, dk, dv, dg, dbeta, dh0
