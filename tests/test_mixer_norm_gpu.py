@@ -171,3 +171,78 @@ def test_repeats_bitwise_and_in_a_graph():
     torch.cuda.synchronize()
     for a, b in zip(first, got):
         assert torch.equal(a, b)
+
+
+# More rows than one grid covers: a block then takes several row groups, the next one's loads ahead. The
+# blocks per SM are at most 4 (gated norm) and 16 (block norm) of 256 threads, of half as many 512. The
+# definition runs on the GPU in 64 bits. A block adds at most tens of rows' products to a column, and the
+# blocks' sums (below 3000) are added in several lanes: the tolerances above hold.
+def _grids(per_sm, D, threads):
+    """Rows of two and a half grids, for `threads` per row."""
+    blocks = (per_sm if threads <= 256 else (per_sm + 1) // 2) * torch.cuda.get_device_properties(0).multi_processor_count
+    return 5 * blocks * max(1, 256 // threads) // 2 + 1
+
+
+def _on_gpu(seed):
+    g = torch.Generator(dev).manual_seed(seed)
+    return lambda *s, dt=F32, std=1.0: (torch.randn(*s, generator=g, device=dev) * std).to(dt)
+
+
+def _gpu_reference(fn, inputs, cotangents):
+    v = {k: x.double().requires_grad_() for k, x in inputs.items()}
+    outs = fn(v)
+    got = torch.autograd.grad(sum((o * c.double()).sum() for o, c in zip(outs, cotangents)), list(v.values()))
+    return [o.detach().cpu() for o in outs], {k: x.cpu() for k, x in zip(v, got)}
+
+
+@pytest.mark.parametrize("dtype,act", [(BF, "silu"), (F32, "sigmoid")])
+@pytest.mark.parametrize("D,threads", [(1024, 128), (2048, 256), (1000, 128), (1001, 128), (4096, 512), (6144, 512)])
+def test_gated_norm_in_several_turns(dtype, act, D, threads):
+    rows, r = _grids(4, D, threads), _on_gpu(D)
+    x, z, dy, w = r(rows, D, dt=dtype), r(rows, D, dt=dtype, std=2), r(rows, D, dt=dtype), r(D)
+    (y_r,), g_r = _gpu_reference(lambda v: (ref.gated_norm(v["x"], v["z"], v["w"], EPS, act),), dict(x=x, z=z, w=w), (dy,))
+    ref.check("y", gated_norm_fwd(x, z, w, eps=EPS, activation=act), y_r, dtype, WORK)
+    for name, o, dt in zip("xzw", gated_norm_bwd(x, z, w, dy, eps=EPS, activation=act), (dtype, dtype, F32)):
+        ref.check("d" + name, o, g_r[name], dt, WORK)
+
+
+@pytest.mark.parametrize("dtype,res", [(BF, F32), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("D,threads", [(2048, 256), (2047, 512), (4096, 512), (8192, 512)])
+def test_block_norm_in_several_turns(dtype, res, D, threads):
+    """In place as well; with a SiLU gate in both passes."""
+    rows, rnd = _grids(16, D, threads), _on_gpu(D)
+    x, z, r = rnd(rows, D, dt=dtype), rnd(rows, D, dt=dtype), rnd(rows, D, dt=res, std=2)
+    w, kw = rnd(D), dict(post_weight=rnd(D), z=z, scale=rnd(D))
+    dy, dr = rnd(rows, D, dt=dtype), rnd(rows, D, dt=res)
+    (y_r, r_r), g_r = _gpu_reference(
+        lambda v: ref.block_norm(v["x"], v["r"], v["w"], v["post_weight"], v["z"], v["scale"], EPS, "silu"),
+        dict(x=x, r=r, w=w, **kw), (dy, dr))
+    got = block_norm_bwd(x, r, w, dy, dr, eps=EPS, activation="silu", **kw)
+    y, r2 = block_norm_fwd(x, r, w, eps=EPS, activation="silu", **kw)
+    y3, r3 = block_norm_fwd(x, r, w, eps=EPS, activation="silu", new_residual=r, **kw)
+    assert r3 is r and torch.equal(r, r2) and torch.equal(y, y3)
+    ref.check("y", y, y_r, dtype, WORK)
+    ref.check("r", r2, r_r, res, WORK)
+    for name, o, dt in zip(("x", "r", "w", "post_weight", "z", "scale"), got, (dtype, res, F32, F32, dtype, F32)):
+        ref.check("d" + name, o, g_r[name], dt, WORK)
+
+
+@pytest.mark.parametrize("dtype,res", [(BF, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,D", [(37, 256), (11, 130), (5, 1000), (3, 4096), (2, 8192), (2, 8190)])
+@pytest.mark.parametrize("parts", ["pzs", "z"])
+def test_block_norm_with_a_silu_gate(dtype, res, rows, D, parts):
+    g = torch.Generator().manual_seed(D + 1)
+    x, z, r = _r(g, rows, D, dt=dtype), _r(g, rows, D, dt=dtype, std=2), _r(g, rows, D, dt=res, std=2)
+    w, kw = _r(g, D), dict(post_weight=_r(g, D) if "p" in parts else None, scale=_r(g, D) if "s" in parts else None, z=z)
+    dy, dr = _r(g, rows, D, dt=dtype), _r(g, rows, D, dt=res)
+    v = ref.leaves(dict(x=x, r=r, w=w, **kw))
+    y_r, r_r = ref.block_norm(v["x"], v["r"], v["w"], v["post_weight"], v["z"], v["scale"], EPS, "silu")
+    g_r = ref.grads((y_r, r_r), (dy, dr), v)
+    y, r2 = block_norm_fwd(x, r, w, eps=EPS, activation="silu", **kw)
+    ref.check("y", y, y_r, dtype, WORK)
+    ref.check("r", r2, r_r, res, WORK)
+    got = block_norm_bwd(x, r, w, dy, dr, eps=EPS, activation="silu", **kw)
+    for name, o, key, dt in zip(("dx", "dr", "dw", "dpw", "dz", "dscale"), got, ("x", "r", "w", "post_weight", "z", "scale"),
+                                (dtype, res, F32, F32, dtype, F32)):
+        if v[key] is not None:
+            ref.check(name, o, g_r[key], dt, WORK)

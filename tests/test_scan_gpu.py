@@ -357,3 +357,88 @@ def test_nonfinite_values_stay_in_their_sequence(dtype, N, what, value):
             assert torch.equal(p, q), (name, packed)
         for name, (p, q) in dict(ht=ht, dh0=dh0).items():
             assert torch.equal(p[seqs], q[seqs]), (name, packed)
+
+
+# The sizes below follow from the GPU's SMs, so that the kernels' loops take more than one turn. Their
+# sequences are longer than the 300 tokens of the tolerances above; the states still remember about 1000
+# steps, whose independent errors of 2^-20 add up to 2^-15, and to twice that in gradients.
+LONG, LONG_GRAD = 2.0 ** -15, 2.0 ** -14
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("dtype,ch,N,G", [(BF, 256, 16, 1), (F32, 256, 16, 1), (BF, 512, 8, 2), (F32, 300, 5, 3), (BF, 256, 32, 1),
+                                          (F32, 256, 64, 1), (BF, 90, 40, 2)])
+@pytest.mark.parametrize("T", [1, 2])
+def test_steps_of_more_sequences_than_blocks(dtype, ch, N, G, T):
+    """A block of 256 channels takes several sequences one after another, the next one's states and inputs
+    on their way meanwhile: here three, two for the last blocks."""
+    per = 2 * _sms() // -(-ch // 256)
+    n = 3 * per - per // 2
+    t = _make([T] * n, ch, N, G, dtype, 22)
+    v = {k: None if x is None else x.double().cpu() for k, x in t.items()}
+    ch_of = torch.arange(ch) // (ch // G)
+    rows = lambda x: x.reshape(n, T, *x.shape[1:])  # noqa: E731
+    h, ys = v["h0"], []
+    for i in range(T):  # all sequences at once
+        u, dt, B, C, z = (rows(v[k])[:, i] for k in ("u", "dt", "B", "C", "z"))
+        delta = torch.nn.functional.softplus(dt + v["bias"], threshold=50.0)
+        h = torch.exp(delta[..., None] * v["A"]) * h + (delta * u)[..., None] * B[:, ch_of]
+        ys.append(((h * C[:, ch_of]).sum(-1) + v["D"] * u) * ref.act(z, "silu"))
+    h_r = t["h0"].clone()
+    a = [rows(t["u"]), rows(t["dt"]), t["A"], rows(t["B"]), rows(t["C"])]
+    y = selective_scan_step(*a, h_r, t["D"], rows(t["z"]), dt_bias=t["bias"])
+    for name, got, want, dt in (("y", y, torch.stack(ys, 1), dtype), ("h", h_r, h, F32)):
+        ref.check(name, got, want, dt, WORK)
+        for s in (0, per - 1, per, 2 * per - 1, 2 * per, n - 1):  # first and last of each turn
+            ref.check(f"{name} {s}", got[s], want[s], dt, WORK)
+
+
+@pytest.mark.parametrize("dtype,N", [(BF, 16), (F32, 16), (F32, 20)])
+def test_forward_one_block_per_sequence(dtype, N):
+    """Enough blocks of channels and sequences for three per SM, and more than 64 tokens: no chunks."""
+    G = 64  # a block of channels holds one group
+    n = -(-3 * _sms() // G)
+    _forward(_make([70] * n, 4 * G, N, G, dtype, 23), [70] * n, False, dtype)
+
+
+def _on_gpu(t, lens):
+    """Outputs and gradients of the 64-bit definition, computed on the GPU (many channels and tokens)."""
+    names = ("u", "dt", "A", "B", "C", "D", "z", "bias", "h0")
+    v = {k: t[k].double().requires_grad_() for k in names}
+    y, ht = ref.scan(*(v[k] for k in names[:8]), True, v["h0"], lens)
+    g = torch.autograd.grad((y * t["dy"].double()).sum() + (ht * t["dht"].double()).sum(), [v[k] for k in names])
+    return y.detach().cpu(), ht.detach().cpu(), {k: x.cpu() for k, x in zip(names, g)}
+
+
+def _both(t, lens, dtype):
+    y_r, ht_r, g_r = _on_gpu(t, lens)
+    a, dy, dz, kw = _args(t, lens, True)
+    y, ht = selective_scan_fwd(*a, *dz, **kw)
+    ref.check("y", y, y_r, dtype, LONG)
+    ref.check("ht", ht, ht_r, F32, LONG)
+    got = selective_scan_bwd(*a, dy, *dz, dht=t["dht"], **kw)
+    for k, o in zip(("u", "dt", "A", "B", "C", "D", "z", "bias", "h0"), got):
+        ref.check("d" + k, o, g_r[k], dtype if k in ("u", "dt", "B", "C", "z") else F32, LONG_GRAD)
+    assert kda.kda_get_device_error(0) == 0
+
+
+@pytest.mark.parametrize("dtype,N", [(BF, 10), (F32, 3)])
+def test_chunks_of_several_tiles(dtype, N):
+    """Chunks of more than 64 rows in both passes, so that B and C come in several tiles of 32 tokens, with
+    sequences that start, end and cross inside them."""
+    ch = 64 * _sms()
+    rows = 70 * 32  # gradient: blocks of 64 channels, 32 chunks; forward: of 256 channels, 16 chunks
+    lens = [0, 300, 1, 33, 700, 0, 150]
+    _both(_make([*lens, rows - sum(lens)], ch, N, 1, dtype, 24), [*lens, rows - sum(lens)], dtype)
+
+
+@pytest.mark.parametrize("dtype,N,ch", [(BF, 16, 6), (F32, 2, 5)])
+def test_more_than_256_chunks(dtype, N, ch):
+    """Few channels: chunks of 16 rows forward and 32 backward, more than 256 of either, so that the carries
+    look up where sequences start and end more than once. A sequence crosses each of those places."""
+    lens = [4000, 0, 37, 4500, 1, 500]
+    t = _make(lens, ch, N, 1, dtype, 25)
+    _both(t, lens, dtype)
