@@ -201,20 +201,23 @@ def _token_stride(t, name, lead=2):
     return 0 if step is None or step == inner else step
 
 
-def _device(strided, dense):
-    """Every tensor on one CUDA device, those of ``dense`` contiguous."""
-    dev = -1
-    for tensors, contiguous in ((dense, True), (strided, False)):
-        for t in tensors:
-            if t is None:
-                continue
-            d = t.get_device()  # -1 on the host
-            if d < 0 or (contiguous and not t.is_contiguous()):
-                raise ValueError("every tensor must be a CUDA tensor, and all but the data inputs contiguous")
-            if d != dev:
-                if dev >= 0:
-                    raise ValueError("every tensor must be on one CUDA device")
-                dev = d
+def _device(lead, strided, dense):
+    """Every tensor on the CUDA device of ``lead``, those of ``dense`` contiguous."""
+    device = lead.get_device()  # -1 on the host
+    good = device >= 0
+    for t in dense:
+        if t is not None and (t.get_device() != device or not t.is_contiguous()):
+            good = False
+    for t in strided:
+        if t is not None and t.get_device() != device:
+            good = False
+    if good:
+        return
+    devices = {t.get_device() for t in (lead, *strided, *dense) if t is not None}
+    if len(devices) > 1 and -1 not in devices:
+        raise ValueError("every tensor must be on one CUDA device")
+    raise ValueError("every tensor must be a CUDA tensor and contiguous (the data inputs of the convolution and the scan: "
+                     "evenly spaced tokens)")
 
 
 def _sequences(cu_seqlens, B):
@@ -316,7 +319,7 @@ def causal_conv_fwd(x, weight, bias=None, *, s0=None, activation="silu", cu_seql
         st = None
     _want(st, "st", (N, W - 1, D), x.dtype)
     stride = _token_stride(x, "x")
-    _device((x,), (weight, bias, s0, cu_seqlens, y, st))
+    _device(x, (), (weight, bias, s0, cu_seqlens, y, st))
     if y is None:
         y = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
     if output_final_state and st is None:
@@ -336,7 +339,7 @@ def causal_conv_step(x, state, weight, bias=None, *, activation="silu", y=None, 
     act = _act(activation, ("silu", None))
     _want(y, "y", (B, T, D), x.dtype)
     stride = _token_stride(x, "x")
-    _device((x,), (weight, bias, state, y))
+    _device(x, (), (weight, bias, state, y))
     if y is None:
         y = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
     p = kda_conv_params(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state), stride, B, T, D, W,
@@ -357,7 +360,7 @@ def causal_conv_bwd(x, weight, bias, dy, *, s0=None, dst=None, activation="silu"
     _want(dy, "dy", (B, T, D), x.dtype)
     _want(dst, "dst", (N, W - 1, D), x.dtype)
     stride = _token_stride(x, "x")
-    _device((x,), (weight, bias, s0, cu_seqlens, dy, dst))
+    _device(x, (), (weight, bias, s0, cu_seqlens, dy, dst))
     dx = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
     dweight = torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
@@ -396,7 +399,7 @@ def _scan_params(u, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, y, 
     _want(y, "y", u.shape, u.dtype)
     _want(ht, "ht", (ns, ch, N), torch.float32)
     strides = [0 if t is None else _token_stride(t, name) for name, t in (("u", u), ("dt", dt), ("B", B), ("C", C), ("z", z))]
-    _device((u, dt, B, C, z), (A, D, dt_bias, h0, cu_seqlens, y, ht, *dense))
+    _device(u, (dt, B, C, z), (A, D, dt_bias, h0, cu_seqlens, y, ht, *dense))
     p = kda_scan_params(_ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), None,
                         None, *strides, ns, T, ch, N, G, _ptr(cu_seqlens), dtype, 1 if dt_softplus else 0, None, 0)
     return p, ns
@@ -481,7 +484,7 @@ def _gated_norm_params(x, z, weight, eps, activation, y, dense=()):
     _want(z, "z", x.shape, x.dtype)
     _want(weight, "weight", x.shape[-1:], torch.float32)
     _want(y, "y", x.shape, x.dtype)
-    _device((), (x, z, weight, y, *dense))
+    _device(x, (), (x, z, weight, y, *dense))
     return kda_gated_norm_params(_ptr(x), _ptr(z), _ptr(weight), None, _rows(x), x.shape[-1], eps, dtype, act)
 
 
@@ -530,7 +533,7 @@ def _block_norm_params(x, residual, weight, post_weight, z, scale, eps, activati
     _want(scale, "scale", ch, torch.float32)
     _want(y, "y", x.shape, x.dtype)
     _want(new_residual, "new_residual", x.shape, residual.dtype)
-    _device((), (x, residual, weight, post_weight, z, scale, y, new_residual, *dense))
+    _device(x, (), (x, residual, weight, post_weight, z, scale, y, new_residual, *dense))
     return kda_block_norm_params(_ptr(x), _ptr(residual), _ptr(weight), _ptr(post_weight), _ptr(z), _ptr(scale), None, None,
                                  _rows(x), x.shape[-1], eps, dtype, _dtype(residual, "residual"), act)
 
