@@ -186,9 +186,9 @@ __device__ __forceinline__ void copy_state(const void *from, void *to, int64_t a
 template <typename T>
 constexpr int kFwdBatch = sizeof(T) == 2 ? 8 : 4;
 constexpr int kBwdBatch = 4;
-constexpr int kFwdPerSM = 5;  // 32761 x 8192 bf16: 176 us; six blocks 194, four rows and eight blocks 183
+constexpr int kFwdPerSM = 5;  // 32761 x 8192 bf16: 174 us; six blocks 192, four rows and eight blocks 181
 template <typename T>
-constexpr int kBwdPerSM = sizeof(T) == 2 ? 4 : 3;  // 16384 x 12288 bf16: 264 us; five blocks spill (512), three with 8 rows 296
+constexpr int kBwdPerSM = sizeof(T) == 2 ? 4 : 3;  // 16384 x 12288 bf16: 250 us; five blocks spill (500), three with 8 rows 283
 
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, kFwdPerSM) conv_fwd_kernel(const ConvArgs a) {
@@ -498,8 +498,8 @@ int conv_check(const void *x, const float *weight, const float *bias, const void
 }
 
 // Four channels per thread where every row of every tensor lets them be read at once, else one. (Eight
-// channels take so many registers that fewer loads are in flight: 250 us for 32761 x 8192
-// where four take 213.)
+// channels take so many registers that they spill at five blocks per SM: 300 us for 32761 x 8192
+// where four take 174.)
 int conv_vec(int dtype, int D, int64_t xs, const void *const *ptrs, int n) {
     bool ok = D % 4 == 0 && xs % 4 == 0;
     for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], (size_t)4 * elem_size(dtype));

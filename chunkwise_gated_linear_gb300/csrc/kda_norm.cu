@@ -7,7 +7,7 @@
 // read and written once. Sums over a row are shuffles, above 256 channels with one exchange through
 // shared memory and one barrier each. The next row's loads are issued before the current row is
 // worked on. Bound by memory: 16384 x 4096 block norm (bf16, fp32 residual) 144 us, 6.5 TB/s, its gradient on 8192
-// rows 138 us, 5.4 TB/s; 524288 x 128 gated norm 68 us, 5.9 TB/s, its gradient on half the rows 64 us, 5.3 TB/s.
+// rows 140 us, 5.3 TB/s; 524288 x 128 gated norm 68 us, 5.9 TB/s, its gradient on half the rows 64 us, 5.3 TB/s.
 //
 // Gradient of n = x i, i = (mean x^2 + eps)^(-1/2), for the gradient g of n:
 //   dx = i (g - n mean(g n)) = i (g - x i^2 mean(g x)),
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, TPR > 256 ? 1 : 3) gated_no
 
 // The block norm's parameters of a row group in shared memory: weight, and post_weight scale (what
 // multiplies n act(z) in r'). Registers do not hold them beside a row, and from memory they would be
-// fetched behind the next row's loads (216 against 180 us for the gradient of 8192 x 4096).
+// fetched behind the next row's loads (216 against 180 us for the gradient of 8192 x 4096 when this was chosen).
 template <int V, int E, int TPR>
 struct BlockParams {
     float *w, *f;
@@ -502,8 +502,8 @@ struct NormPlan {
 // needs. They lie in vectors where every row of every tensor starts on 16 bytes; single channels
 // otherwise, in three sizes only. `wide`: vectors of 8 channels, else of 4. Eight suit bf16 (16
 // bytes). With fp32 tensors four let neighbouring threads read neighbouring 16 bytes, which the block norm's
-// gradient gains from (8192 x 4096, fp32 residual: 145 -> 139 us) and its forward pass, already at
-// the memory's rate, does not (16384 x 4096: 161 us with four, 145 with eight).
+// gradient gains from (8192 x 4096, fp32 residual: 145 -> 140 us) and its forward pass, already at
+// the memory's rate, does not (16384 x 4096: 161 us with four, 144 with eight).
 NormPlan norm_plan(int64_t rows, int D, bool vec, bool block, bool wide, int per_sm) {
     NormPlan q{};
     q.V = !vec ? 1 : (wide ? 8 : 4);

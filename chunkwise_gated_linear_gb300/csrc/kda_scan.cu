@@ -22,7 +22,7 @@
 //   h_in[c + 1] = exp(A sum delta) h_in[c] + h_end[c]
 // (scan_carry_kernel), and every chunk is walked again with its start state (kChunk). The first
 // walk costs about 0.7 of the second. Bound by issue and the fp32 pipes: 4.8 and 7.0 instructions per element, 0.55
-// per clock and scheduler. 2 x 8192 tokens of 4096 channels, 16 states, bf16: 527 us (2.0e12 elements/s).
+// per clock and scheduler. 2 x 8192 tokens of 4096 channels, 16 states, bf16: 526 us (2.0e12 elements/s).
 #include "scan_common.cuh"
 
 namespace kda {
@@ -34,14 +34,14 @@ enum Mode { kWhole, kSummary, kChunk };
 
 constexpr int kFThr = 128;      // threads per block
 constexpr int kTile = 32;       // tokens of B and C in shared memory
-// Blocks per SM: 128 registers per thread. 2 x 8192 tokens, 4096 channels, 16 states, bf16: 512 us,
-// with three blocks (168 registers) 542 us, with two 594 us.
+// Blocks per SM: 128 registers per thread. 2 x 8192 tokens, 4096 channels, 16 states, bf16: 525 us,
+// with three blocks (168 registers) 533 us, with two 589 us.
 constexpr int kPerSM = 4;
-// Rows per chunk at least: 333 tokens of 2048 channels take 36 us with 12 or 16 rows, 49 us with
-// 32, 78 us with 64 (chunks are walked serially, and there are few).
+// Rows per chunk at least: 333 tokens of 2048 channels take 36 us with 16 rows (35 with 12), 48 us with
+// 32, 77 us with 64 (chunks are walked serially, and there are few).
 constexpr int kMinChunk = 16;
 // Blocks per SM of the step kernel: two, with 128 registers, hold a sequence's states, the next one's and its
-// inputs (256 sequences of 4096 x 16 states: 31 us; three blocks spill: 46; one sequence per block: 35).
+// inputs (256 sequences of 4096 x 16 states: 31 us; three blocks spill: 46; one sequence per block: 46).
 constexpr int kStepPerSM = 2;
 
 // NS states per thread, LN lanes per pair of channels.

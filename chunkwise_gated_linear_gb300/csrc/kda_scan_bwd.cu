@@ -11,7 +11,7 @@
 // The states are needed backwards and cannot be undone (a_t may underflow), so they are computed
 // again in three steps:
 //   1. scan_bwd_local_kernel: the rows are cut into chunks, all walked at once from a zero state.
-//      It leaves the local state at every 16 rows (a window), the chunk's end state, its adjoint
+//      It leaves the local state at every 16 rows (a window; 8 above 32 states), the chunk's end state, its adjoint
 //      at the start from a zero adjoint at the end (in the same forward walk:
 //      sum_t (a_c0 .. a_t) C_t g_t), and sums of delta.
 //   2. scan_bwd_carry_kernel: true states at the chunk starts, true adjoints at the ends.
@@ -22,7 +22,7 @@
 // Sums over the states go across 4 lanes, sums over channels across 8 lanes (one exchange per
 // value and halving, so that each lane ends with one total), then over warps and blocks in a
 // fixed order. Bound by issue: about 11 instructions per (token, channel, state) in the first kernel, 37 in the
-// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1080 us, of which 236 and 785.
+// third. 2 x 4096 tokens of 4096 channels, 16 states, bf16: 1075 us, of which 236 and 780.
 #include <type_traits>
 
 #include "scan_common.cuh"
@@ -34,7 +34,7 @@ namespace {
 
 // Tokens per window: what the third kernel keeps states of in shared memory. With 16 states, windows of 16
 // and groups of two tokens leave registers and shared memory for four blocks per SM (2 x 4096 tokens
-// of 4096 channels: 1135 us, 1080 since); windows of 32 and groups of four for three (1204 us).
+// of 4096 channels: 1072 us); windows of 32 and groups of four for three (1120 us).
 __host__ __device__ constexpr int win_of(int np) { return np <= 8 ? 16 : 8; }
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -289,7 +289,7 @@ __device__ __forceinline__ float sum_channels(const float (&v)[8], int lane) {
 // lane % 4) has channels 16 w + dl and 16 w + 8 + dl, as the two halves of every pair, and states
 // nl NP .. nl NP + NP - 1 of both: step sizes, inputs and gradients of a pair come as pairs, B and C (the
 // same for all channels) are doubled in registers (doubled in shared memory they took a quarter of
-// the load/store wavefronts: 1104 us for the sizes below where this takes 1080).
+// the load/store wavefronts: 1104 us for the sizes above where this then took 1080).
 template <int NP>
 struct BwdShape {
     static constexpr int kThr = 128, kWarps = 4;
@@ -777,9 +777,10 @@ int bwd_check(const kda_scan_bwd_params &p) {
     return KDA_OK;
 }
 
-// Chunks: so many that the third kernel's blocks fill the GPU's slots (four blocks per SM) kTurns
-// times, of at least a window. 2 x 4096 tokens of 4096 channels: 1136 us with two turns, 1158 with three,
-// 1135 with five, 1118 with eight (the last blocks end closer together; more chunks cost little).
+// Chunks: so many that the third kernel's blocks fill the GPU's slots (four blocks per SM, which is what fits
+// up to 16 states) kTurns times, of at least a window. 2 x 4096 tokens of 4096 channels: 1096 us with two
+// turns, 1117 with three, 1087 with five, 1072 with eight (the last blocks end closer together; more
+// chunks cost little).
 constexpr int kTurns = 8;
 struct BwdPlan {
     int64_t chunk, nchunks, windows, rows, bpg;

@@ -156,8 +156,8 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 1 / (1 + e^-x): one exponential and one reciprocal on the special-function unit (relative
-// error about 3e-7; e^-x = inf gives 0)
+// 1 / (1 + e^-x): one exponential and one reciprocal on the special-function unit. Relative error below
+// 4e-7, for negative x plus 8e-8 |x| (the exponent -x log2 e is rounded once); e^-x = inf gives 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + tc5::ex2(-x * kLog2e)); }
 // The value of the gate act(x), KDA_ACT_SILU or KDA_ACT_SIGMOID.
 __device__ __forceinline__ float act_value(float x, bool silu) {
@@ -298,8 +298,8 @@ struct Scratch {
 // SMs of the current device (0 when it cannot be asked).
 int sm_count();
 
-// out[c] = sum over p of partial[p * total + c], in the order of p; the columns go to up to
-// four outputs one after another, an output that is null is left out.
+// out[c] = sum over p of partial[p * total + c], in an order that the sizes alone fix (every 8th or 32nd part,
+// then those sums); the columns go to up to four outputs one after another, an output that is null is left out.
 struct SumOuts {
     float *out[4];
     int64_t len[4];

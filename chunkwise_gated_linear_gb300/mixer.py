@@ -5,9 +5,10 @@ block's residual update with its norms, each with its gradient.
 As in :mod:`.kda`, the functions take torch CUDA tensors, check shapes and dtypes, allocate
 the outputs with torch and call the C ABI on the current torch stream (or ``stream``); every
 step of the computation runs in the library's CUDA kernels. Data tensors are bf16 or fp32;
-parameters and recurrence states are fp32. The data inputs may be slices of wider tensors as
-long as their tokens are evenly spaced and each token's channels contiguous; gradients and
-states passed in are contiguous. With ``cu_seqlens`` (int32 [N + 1] on the device) the batch
+parameters and recurrence states are fp32. The data inputs of the convolution and the scan may be
+slices of wider tensors as long as their tokens are evenly spaced and each token's channels
+contiguous; all other tensors are contiguous. All tensors of a call lie on one device, which need
+not be the current one. With ``cu_seqlens`` (int32 [N + 1] on the device) the batch
 dimension is 1 and holds N packed sequences.
 """
 

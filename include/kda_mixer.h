@@ -13,7 +13,7 @@
  * each with its backward pass; the convolution and the scan also with a form for single
  * tokens that updates the sequences' states in place.
  *
- * Common to all calls, as in kda.h: tensor pointers are DEVICE pointers; data tensors are
+ * Common to all calls, as in kda.h: tensor pointers are DEVICE pointers of the current device; data tensors are
  * bf16 or fp32 (`dtype`, KDA_DTYPE_*), parameters and recurrence states fp32; sums, states and
  * norms are held in fp32 and a result is rounded to its tensor's type once. Calls are
  * asynchronous on `stream`, thread-safe, and fully overwrite their outputs, which must not
@@ -24,11 +24,11 @@
  * the tensors, and raises KDA_DEVICE_ERR_SEQLENS (kda_get_device_error). Empty sequences and
  * T == 0 are valid.
  *
- * Token strides: the inputs x, u, dt, B, C and z may be slices of wider tensors. Their
- * `*_stride` is the distance in elements between consecutive tokens (all B x T tokens evenly
- * spaced, the channels of a token contiguous); 0 means contiguous. Pointers are aligned to
- * their element type; 16-byte aligned rows are read 16 bytes at a time, others one
- * element at a time. Outputs and all other tensors are contiguous.
+ * Token strides: the convolution's x and the scan's u, dt, B, C and z may be slices of wider
+ * tensors. Their `*_stride` is the distance in elements between consecutive tokens (all B x T tokens
+ * evenly spaced, the channels of a token contiguous); 0 means contiguous. Outputs and all other
+ * tensors, the norms' x and z among them, are contiguous. Pointers are aligned to their element
+ * type; where all rows are aligned for it several elements are read at a time, otherwise one.
  *
  * Scratch: the calls that need it say so; it is `workspace` (16-byte aligned, at least the
  * bytes that the matching *_workspace function returns, free for reuse when the call's work on
@@ -159,8 +159,10 @@ int kda_scan_step(const kda_scan_params *p, cudaStream_t stream);
  *   du, ddt, dz like u (contiguous); dB, dC like B (contiguous; sums over the channels of a
  *   group); dA [channels, N], dD, ddt_bias [channels], dh0 like h0: fp32
  * ddt is the gradient with respect to dt as given (before bias and softplus). Scratch:
- * kda_scan_bwd_workspace bytes: per token about channels N / 4 bytes of states (at every 16th token, fp32)
- * and channels N / 8 bytes of the blocks' shares of dB and dC, and what the chunks hand over.
+ * kda_scan_bwd_workspace bytes, all fp32: per token channels (N + 1) / 4 bytes of states and step sizes (at
+ * every 16th token; channels (N + 1) / 2, at every 8th, for N > 32) and 8 N bytes for every block of 64
+ * channels (shares of dB and dC; a group's last block may be smaller); per chunk 12 channels (N + 1) bytes of
+ * what the chunks hand over. Chunks have 32 tokens or, where so many are not needed to fill the GPU, more.
  */
 typedef struct kda_scan_bwd_params {
     kda_scan_params f;
