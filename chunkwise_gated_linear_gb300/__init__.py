@@ -2,8 +2,20 @@
 Attention) for GB300 (sm_103a): a C-ABI CUDA library (``include/kda.h``,
 ``lib/libkda.so``) and its thin Python binding (:mod:`.kda`). The operators around the recurrence in
 a model's block (``include/kda_mixer.h``: short causal convolution, selective state space scan,
-gated output norm, residual update with norms) are bound in :mod:`.mixer`."""
+gated output norm, residual update with norms) are bound in :mod:`.mixer`, those of a softmax-attention
+layer between recurrent ones (``include/kda_attention.h``: norms of queries and keys with the position
+rotation, paged key-value cache, attention of the next tokens over it) in :mod:`.attention`."""
 
+from .attention import (  # noqa: F401
+    KVCache,
+    kv_cache_read,
+    kv_cache_write,
+    paged_attn_step,
+    qk_norm_bwd,
+    qk_norm_fwd,
+    qk_norm_step,
+    rope_frequencies,
+)
 from .kda import (  # noqa: F401
     KdaError,
     chunk_kda_bwd,

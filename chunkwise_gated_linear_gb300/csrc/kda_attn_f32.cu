@@ -1,0 +1,232 @@
+// Attention over a paged cache, computed on the fp32 pipes: fp32 data (cache fp32 or 8-bit). See attn_common.cuh
+// for how the work is cut.
+//
+// A step of a warp is KEYS keys: lane (key, part) takes every (32 / KEYS)-th 16-byte chunk of its key against all query rows,
+// the parts are added across lanes; the running maximum of each row is that of the warp's keys alone (joined at the
+// end); then a lane owns columns lane + 32 j of O and goes through the keys.
+#include "attn_common.cuh"
+#include "attn_launch.h"
+
+namespace kda {
+namespace attn {
+namespace {
+
+template <typename C>
+__device__ __forceinline__ void unpack16(float (&f)[16 / sizeof(C)], const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(C) == 4) {
+            f[i] = __uint_as_float(w[i]);
+        } else if constexpr (sizeof(C) == 2) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            e4m3_to_f(w[i] & 0xffffu, f[4 * i], f[4 * i + 1]);
+            e4m3_to_f(w[i] >> 16, f[4 * i + 2], f[4 * i + 3]);
+        }
+    }
+}
+__device__ __forceinline__ float elem(const float *p) { return *p; }
+__device__ __forceinline__ float elem(const bf16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float elem(const uint8_t *p) {
+    float lo, hi;
+    e4m3_to_f(*p, lo, hi);
+    return lo;
+}
+
+template <typename T, typename C, int DP, int RB, int KEYS, int STAGES>
+struct Fma {
+    using S = Stream<C, DP, KEYS, STAGES>;
+    static constexpr int kParts = 32 / KEYS;
+    static constexpr int kE = 16 / (int)sizeof(C);
+    static constexpr int kCols = DP / 32;
+    static_assert(S::kBytes >= RB * DP * 4, "a warp's ring holds its O at the end");
+    // shared memory: rings, q [RB][DP], p [warps][KEYS][RB], (m, l) [warps][RB], rows' limits, the plan, exponent bytes
+    static constexpr int kQ = kWarps * S::kBytes;
+    static constexpr int kP = kQ + RB * DP * 4;
+    static constexpr int kMl = kP + kWarps * KEYS * RB * 4;
+    static constexpr int kLim = kMl + kWarps * RB * 8;
+    static constexpr int kPlan = kLim + RB * 4 + (RB * 4) % 8;
+    static constexpr int kSc = kPlan + (kWarps + 2) * 8;
+    static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
+};
+
+template <typename T, typename C, int DP, int RB, int KEYS, int STAGES>
+__global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constant__ Args a) {
+    using F = Fma<T, C, DP, RB, KEYS, STAGES>;
+    extern __shared__ __align__(128) unsigned char mem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Start at = find_start(a, blockIdx.x, reinterpret_cast<int64_t *>(mem + F::kPlan));
+    if ((int)blockIdx.x >= at.grid) return;
+    float *qs = reinterpret_cast<float *>(mem + F::kQ);
+    float *pw = reinterpret_cast<float *>(mem + F::kP) + warp * KEYS * RB;
+    float2 *ml = reinterpret_cast<float2 *>(mem + F::kMl);
+    int *lim = reinterpret_cast<int *>(mem + F::kLim);
+    unsigned char *own = mem + warp * F::S::kBytes;
+    typename F::S st(a, own, mem + F::kSc + warp * F::S::kScaleBytes, lane, warp);
+    const int D = a.cache.D, key = lane & (KEYS - 1), part = lane / KEYS;
+    const int cpr = D * (int)sizeof(C) / 16;
+
+    int64_t cur = share(at.total, blockIdx.x, at.grid);
+    const int64_t stop = share(at.total, blockIdx.x + 1, at.grid);
+    int b = at.b, len = cache_len(a.cache, b);
+    int64_t before = at.before;
+    while (cur < stop) {
+        int64_t all = (int64_t)tiles_of(len) * a.per_seq;
+        while (cur >= before + all) {
+            before += all;
+            len = cache_len(a.cache, ++b);
+            all = (int64_t)tiles_of(len) * a.per_seq;
+        }
+        const Piece p = piece_at(a, b, len, cur - before, stop - cur);
+        cur += p.t1 - p.t0;
+        const int s0 = p.t0 * (kTile / F::S::kStep), s1 = p.t1 * (kTile / F::S::kStep);
+        st.begin(p, s0, s1);
+        for (int i = threadIdx.x; i < p.rows * DP; i += kThreads) {
+            const int r = i / DP, d = i - r * DP;
+            qs[i] = d < D ? to_f(static_cast<const T *>(a.q)[q_at(a, p, r) + d]) * a.scale_log2 : 0.f;
+        }
+        if (threadIdx.x < RB) lim[threadIdx.x] = threadIdx.x < p.rows ? seen(a, p.len, p.row0 + threadIdx.x) : 0;
+        __syncthreads();
+        const int least = lim[0];  // keys from here on are not seen by all rows
+        float m[RB], l[RB], acc[RB][F::kCols];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < F::kCols; ++j) acc[r][j] = 0.f;
+        }
+        int slot = 0;
+        for (int s = s0; s < s1; ++s) {
+            st.ready();
+            const unsigned char *ks = own + slot * 2 * F::S::kHalf, *vs = ks + F::S::kHalf;
+            const uint8_t *sc = st.scales + slot * 2 * KEYS;
+            const int pos0 = s * F::S::kStep + warp * KEYS;
+            if (pos0 < p.last) {  // the same for the whole warp
+                float x[RB];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) x[r] = 0.f;
+                for (int c = part; c < cpr; c += F::kParts) {
+                    float kf[F::kE];
+                    unpack16<C>(kf, *reinterpret_cast<const uint4 *>(ks + key * F::S::kPitch + ((c ^ (key & 7)) << 4)));
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        if (r >= p.rows) break;
+#pragma unroll
+                        for (int e = 0; e < F::kE; e += 4) {
+                            const float4 qv = *reinterpret_cast<const float4 *>(qs + r * DP + c * F::kE + e);
+                            x[r] = fmaf(kf[e], qv.x, x[r]);
+                            x[r] = fmaf(kf[e + 1], qv.y, x[r]);
+                            x[r] = fmaf(kf[e + 2], qv.z, x[r]);
+                            x[r] = fmaf(kf[e + 3], qv.w, x[r]);
+                        }
+                    }
+                }
+                float kscale = 1.f, vscale = 1.f;
+                if constexpr (F::S::kScaled) {
+                    kscale = __uint_as_float((uint32_t)sc[key] << 23);
+                    vscale = __uint_as_float((uint32_t)sc[KEYS + key] << 23);
+                }
+                const int pos = pos0 + key;
+                bool grew = false;
+                float alpha[RB];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    alpha[r] = 1.f;
+                    if (r >= p.rows) continue;
+#pragma unroll
+                    for (int o = KEYS; o < 32; o <<= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], o);
+                    x[r] = pos < lim[r] ? x[r] * kscale : -INFINITY;
+                    float top = x[r];
+#pragma unroll
+                    for (int o = 1; o < KEYS; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (top > m[r]) {
+                        alpha[r] = tc5::ex2(m[r] - top);
+                        m[r] = top;
+                        grew = true;
+                    }
+                    // no key seen so far: 2^(-inf - 0) = 0
+                    const float w = tc5::ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                    l[r] = l[r] * alpha[r] + (part == 0 ? w : 0.f);
+                    if (part == 0) pw[key * RB + r] = w * vscale;
+                }
+                __syncwarp();
+                if (grew) {
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+#pragma unroll
+                        for (int j = 0; j < F::kCols; ++j) acc[r][j] *= alpha[r];
+                }
+                const bool edge = pos0 + KEYS > least;
+#pragma unroll 2
+                for (int k = 0; k < KEYS; ++k) {
+                    float v[F::kCols];
+#pragma unroll
+                    for (int j = 0; j < F::kCols; ++j) {
+                        const int byte = (lane + 32 * j) * (int)sizeof(C);
+                        v[j] = elem(reinterpret_cast<const C *>(vs + k * F::S::kPitch + ((((byte >> 4) ^ (k & 7)) << 4) | (byte & 15))));
+                    }
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        if (r >= p.rows) break;
+                        // a value that this row does not see must not reach it, not even times zero
+                        if (edge && pos0 + k >= lim[r]) continue;
+                        const float w = pw[k * RB + r];
+#pragma unroll
+                        for (int j = 0; j < F::kCols; ++j) acc[r][j] = fmaf(w, v[j], acc[r][j]);
+                    }
+                }
+            }
+            __syncwarp();
+            st.fetch(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+            slot = slot == STAGES - 1 ? 0 : slot + 1;
+        }
+        copies_wait<0>();
+        __syncwarp();
+        // the warps' results side by side in their rings, then one sum over them
+        float *mine = reinterpret_cast<float *>(own);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            if (r >= p.rows) break;
+            float t = l[r];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == 0) ml[warp * RB + r] = make_float2(m[r], t);
+#pragma unroll
+            for (int j = 0; j < F::kCols; ++j) mine[r * DP + lane + 32 * j] = acc[r][j];
+        }
+        __syncthreads();
+        finish<T, DP, RB>(a, p, mem, F::S::kBytes, ml, blockIdx.x);
+        __syncthreads();
+    }
+}
+
+template <typename T, typename C, int DP, int RB, int KEYS>
+cudaError_t launch(const Args &a, cudaStream_t stream) {
+    constexpr int kStages = 3;
+    return launch_kernel<attn_fma_kernel<T, C, DP, RB, KEYS, kStages>, Fma<T, C, DP, RB, KEYS, kStages>::kSmem>(a, stream);
+}
+template <typename T, typename C, int RB>
+cudaError_t launch_d(const Args &a, cudaStream_t stream) {
+    if (a.cache.D <= 64) return launch<T, C, 64, RB, 16>(a, stream);
+    if (a.cache.D <= 128) return launch<T, C, 128, RB, 16>(a, stream);
+    return launch<T, C, 256, RB, sizeof(C) == 4 ? 8 : 16>(a, stream);
+}
+template <typename T, typename C>
+cudaError_t launch_rows(const Args &a, cudaStream_t stream) {
+    return a.rows <= 4 ? launch_d<T, C, 4>(a, stream) : launch_d<T, C, 16>(a, stream);
+}
+
+}  // namespace
+
+int fma_rows(int all) { return all <= 4 ? 4 : 16; }
+
+cudaError_t launch_attn_fma(const Args &a, bool f32, cudaStream_t stream) {
+    if (f32) return a.cache.ks != nullptr ? launch_rows<float, uint8_t>(a, stream) : launch_rows<float, float>(a, stream);
+    return a.cache.ks != nullptr ? launch_rows<bf16, uint8_t>(a, stream) : launch_rows<bf16, bf16>(a, stream);
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -1,0 +1,319 @@
+"""Attention of the next tokens over a paged cache on the GPU against its 64-bit definition (attention_reference). Every
+place of the caches that no position of a sequence holds is NaN, and every entry of a table beyond a sequence's
+length names no page.
+
+Tolerances: the result is rounded once to its type. fp32: a score is a sum of at most 256 products (below 2^-20 of
+|q| |k| scale, at most 20 here), its exponential adds 2^-22, the sums over keys are pairwise over warps and
+blocks: 2^-17 together. bf16: scores as in fp32 (products of bf16 numbers are exact in it), each probability rounded
+to bf16 once more, off by 2^-8 at most; on values without a common sign those errors add up as the values
+themselves do: 2^-8 of the result. lse: the scores' error, absolute.
+"""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import attention_reference as aref
+import mixer_reference as ref
+from attention_cases import BF, E4M3, F32, filled, index, to_gpu
+from chunkwise_gated_linear_gb300 import KVCache, attention, kda, paged_attn_step
+
+pytestmark = pytest.mark.gpu
+dev = "cuda"
+WORK = {BF: 2.0 ** -8 + 2.0 ** -17, F32: 2.0 ** -17}
+KINDS = [(BF, BF), (BF, E4M3), (F32, F32), (F32, E4M3)]
+
+
+def _q(g, B, T, Hq, D, dtype, kind):
+    # scores of a spread of about 2
+    std = 2.0 / (1.5 if kind == E4M3 else 1.0)
+    return (torch.randn(B, T, Hq, D, generator=g) * std).to(dtype)
+
+
+def _int32(x):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+def _check(q, cache, table, lens, dtype, scale=None):
+    """The call on the GPU against the definition; cache and table on the CPU."""
+    D = q.shape[3]
+    want, lse_w = aref.attention(q, cache, table, lens, D ** -0.5 if scale is None else scale)
+    o, lse = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens), scale=scale, want_lse=True)
+    ref.check("o", o, want, dtype, WORK[dtype])
+    lse = lse.double().cpu()
+    empty = torch.isinf(lse_w)
+    assert torch.equal(torch.isinf(lse), empty) and bool((lse[empty] < 0).all())
+    assert not o.cpu()[empty].any()
+    if not bool(empty.all()):
+        off = float((lse - lse_w)[~empty].abs().max())
+        print(f"lse: {off:.2e}")
+        assert off <= 2.0 ** -16
+    assert torch.equal(o, paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens), scale=scale))
+    return o
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 192, 256])
+@pytest.mark.parametrize("heads,group", [(2, 1), (3, 4), (1, 8), (2, 5), (1, 16), (1, 33), (1, 71)])
+def test_head_layouts(dtype, kind, D, heads, group):
+    lens = [1, 63, 64, 65, 0, 300]
+    g = torch.Generator().manual_seed(D + group)
+    cache, table = filled(g, lens, 16, heads, D, kind)
+    _check(_q(g, len(lens), 1, heads * group, D, dtype, kind), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 64, 100, 256])
+def test_pages(dtype, kind, page):
+    lens = [5, 129, 640, 17, 1]
+    g = torch.Generator().manual_seed(page)
+    cache, table = filled(g, lens, page, 2, 128, kind)
+    _check(_q(g, len(lens), 1, 8, 128, dtype, kind), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("T,group", [(2, 1), (4, 8), (3, 5), (8, 4), (17, 2), (70, 1), (5, 16)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_several_tokens(dtype, kind, T, group, D):
+    """Each sees the ones before it; sequences shorter than the new tokens have rows that see nothing."""
+    lens = [T, T + 1, 200, 2, 0, 64 + T // 2]
+    g = torch.Generator().manual_seed(T)
+    cache, table = filled(g, lens, 16, 2, D, kind)
+    _check(_q(g, len(lens), T, 2 * group, D, dtype, kind), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("lens", [[5000], [0], [1], [40000, 3], [20000] + [1] * 40, list(range(0, 700, 3))])
+def test_lengths(dtype, kind, lens):
+    """One long sequence over all SMs, uneven batches, more sequences than threads that plan them."""
+    g = torch.Generator().manual_seed(len(lens))
+    cache, table = filled(g, lens, 32, 2, 64, kind)
+    _check(_q(g, len(lens), 1, 8, 64, dtype, kind), cache, table, lens, dtype)
+
+
+def test_more_sequences_than_a_block_has_threads():
+    lens = [(7 * i) % 90 for i in range(1000)]
+    g = torch.Generator().manual_seed(1)
+    cache, table = filled(g, lens, 16, 1, 64, BF)
+    _check(_q(g, len(lens), 1, 2, 64, BF, BF), cache, table, lens, BF)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("size", [0.0, 30.0, -1.0])
+def test_sharp_and_flat_scores(dtype, kind, size):
+    """Scores that all agree, that leave one key (growing along the sequence, so that the running maximum keeps
+    changing), and that fall from the first key on. A score of 300 is off by 2^-24 of it times 16 in 32 bits."""
+    lens = [1000, 77]
+    g = torch.Generator().manual_seed(2)
+    cache, table = filled(g, lens, 16, 1, 64, F32 if kind == E4M3 else kind)
+    q = torch.zeros(2, 1, 4, 64)
+    q[..., 0] = 8.0 if size else 0.0
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        ramp = torch.arange(n).float() / n * abs(size)
+        cache.k[table[b].long()[pos // 16], 0, pos % 16, 0] = (ramp if size > 0 else -ramp).to(cache.k.dtype)
+    if kind == E4M3:
+        nan = torch.isnan(cache.k)
+        made = []
+        for t in (cache.k, cache.v):
+            x = torch.nan_to_num(t).double()
+            unit = aref.row_unit(x)
+            made.append(((x / unit[..., None]).float().to(E4M3), torch.log2(unit).add(127).to(torch.uint8).view(torch.float8_e8m0fnu)))
+        cache = KVCache(made[0][0], made[1][0], made[0][1], made[1][1])
+        index(cache.k)[nan] = 0x7F
+        index(cache.v)[nan] = 0x7F
+    _check(q.to(dtype), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+def test_values_without_a_meaning_stay_where_no_row_sees_them(dtype, kind):
+    """NaN and infinities at positions that only later tokens of the call see do not reach earlier ones."""
+    lens, T = [70, 9, 200], 5
+    g = torch.Generator().manual_seed(3)
+    cache, table = filled(g, lens, 16, 2, 64, kind)
+    q = _q(g, 3, T, 4, 64, dtype, kind)
+    clean = _check(q, cache, table, lens, dtype)
+    bad = KVCache(*(None if t is None else t.clone() for t in cache))
+    for b, n in enumerate(lens):
+        pos = n - 2  # seen by the last two tokens
+        for t, at in ((bad.k, 3), (bad.v, 5)):
+            index(t)[table[b, pos // 16].long(), 0, pos % 16, at] = 0x7F if kind == E4M3 else float("nan")
+            if kind != E4M3:
+                t[table[b, (pos + 1) // 16].long(), 0, (pos + 1) % 16, at] = float("inf")
+    o = paged_attn_step(q.to(dev), to_gpu(bad), table.to(dev), _int32(lens))
+    assert torch.equal(o[:, :T - 2], clean[:, :T - 2])
+    assert torch.equal(o[:, :, 2:], clean[:, :, 2:])  # the other key head
+    assert bool(torch.isnan(o[:, T - 2:, :2]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_values_that_are_not_finite_are_kept_where_seen(dtype):
+    """A NaN value reaches its own channel alone, a NaN key the whole row."""
+    lens = [90]
+    g = torch.Generator().manual_seed(4)
+    cache, table = filled(g, lens, 16, 2, 64, dtype)
+    cache.v[table[0, 2].long(), 0, 3, 7] = float("nan")
+    cache.k[table[0, 1].long(), 1, 3, 7] = float("nan")
+    o = paged_attn_step(_q(g, 1, 1, 4, 64, dtype, dtype).to(dev), to_gpu(cache), table.to(dev), _int32(lens)).cpu()
+    bad = torch.isnan(o)
+    want = torch.zeros_like(bad)
+    want[..., :2, 7] = True
+    want[..., 2:, :] = True
+    assert torch.equal(bad, want)
+
+
+def test_scale_and_large_scales_of_rows():
+    g = torch.Generator().manual_seed(5)
+    lens = [130, 31]
+    cache, table = filled(g, lens, 16, 2, 128, BF)
+    q = _q(g, 2, 1, 4, 128, BF, BF)
+    for scale in (0.0, 0.25, -0.1):
+        _check(q, cache, table, lens, BF, scale=scale)
+    # rows of an 8-bit cache whose values differ by 2^60 between keys
+    cache, table = filled(g, lens, 16, 2, 128, E4M3)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        at = table[b].long()[pos // 16]
+        index(cache.v_scale)[at, :, pos % 16] = (90 + 60 * (pos % 2))[:, None].to(torch.uint8)
+    _check(q / 2, cache, table, lens, BF)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+def test_slices(dtype, kind):
+    """q out of one projection, pages of one layer out of a buffer of several, a table's first columns."""
+    g = torch.Generator().manual_seed(6)
+    lens = [100, 33, 1]
+    cache, table = filled(g, lens, 16, 2, 64, kind)
+    qkv = (torch.randn(3, 2, 12 * 64, generator=g)).to(dtype).to(dev)
+    q = qkv[..., 2 * 64:10 * 64].unflatten(-1, (8, 64))
+    c = to_gpu(cache)
+    wide = KVCache(*(None if t is None else torch.stack([index(t)] * 3, 1).view(t.dtype)[:, 1] for t in c))
+    more = torch.full((3, 40), -1, dtype=torch.int32, device=dev)
+    more[:, :table.shape[1]] = table.to(dev)
+    want = paged_attn_step(q.contiguous(), c, table.to(dev), _int32(lens))
+    assert torch.equal(paged_attn_step(q, wide, more[:, :table.shape[1]], _int32(lens)), want)
+
+
+def test_places_beyond_32_bits():
+    """Pages whose offsets pass 2^31 elements and 2^32 bytes."""
+    g = torch.Generator().manual_seed(7)
+    lens = [200]
+    small, table = filled(g, lens, 64, 1, 256, BF)
+    pages = (1 << 32) // (64 * 256) + 8
+    cache = KVCache(*(torch.zeros(pages, 1, 64, 256, dtype=BF, device=dev) for _ in "kv"))
+    far = table.clone()
+    for i in range(4):
+        far[0, i] = pages - 1 - 2 * i
+        for a, b in zip(cache, small):
+            if a is not None:
+                a[pages - 1 - 2 * i] = b[table[0, i].long()].to(dev)
+    q = _q(g, 1, 1, 4, 256, BF, BF)
+    want = paged_attn_step(q.to(dev), to_gpu(small), table.to(dev), _int32(lens))
+    assert torch.equal(paged_attn_step(q.to(dev), cache, far.to(dev), _int32(lens)), want)
+
+
+def test_shared_pages_and_joined_caches():
+    """Two sequences with one prefix's pages; lse joins the results over a cache cut in two."""
+    g = torch.Generator().manual_seed(8)
+    cache, table = filled(g, [96], 16, 2, 64, F32)
+    q = _q(g, 1, 1, 4, 64, F32, F32).to(dev)
+    c, t = to_gpu(cache), table.to(dev)
+    both = paged_attn_step(q.expand(2, -1, -1, -1).contiguous(), c, t.expand(2, -1).contiguous(), _int32([96, 96]))
+    whole = paged_attn_step(q, c, t, _int32([96]))
+    for i in range(2):  # a batch may cut its sequences elsewhere
+        ref.check("shared", both[i:i + 1], whole.double().cpu(), F32, WORK[F32])
+    o1, l1 = paged_attn_step(q, c, t, _int32([64]), want_lse=True)
+    o2, l2 = paged_attn_step(q, c, t[:, 4:].contiguous(), _int32([32]), want_lse=True)
+    w = torch.sigmoid(l1 - l2)[..., None]
+    ref.check("joined", o1 * w + o2 * (1 - w), whole.double().cpu(), F32, 2 * WORK[F32])
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+def test_bad_pages_and_lengths_are_reported(dtype, kind):
+    g = torch.Generator().manual_seed(9)
+    stream = torch.cuda.current_stream().cuda_stream
+    cache, table = filled(g, [60, 60], 16, 1, 64, kind)
+    q = _q(g, 2, 1, 4, 64, dtype, kind).to(dev)
+    c = to_gpu(cache)
+    kda.kda_get_device_error(stream)
+    bad = table.clone()
+    bad[1, 2] = cache.k.shape[0]
+    o = paged_attn_step(q, c, bad.to(dev), _int32([60, 60]))
+    assert kda.kda_get_device_error(stream) == attention.KDA_DEVICE_ERR_CACHE
+    assert bool(torch.isfinite(o).all())
+    want = paged_attn_step(q, c, table.to(dev), _int32([60, 60]))
+    assert kda.kda_get_device_error(stream) == 0 and torch.equal(o[0], want[0])
+    short = table[:, :4].contiguous().to(dev)
+    o = paged_attn_step(q, c, short, _int32([-3, 60]))
+    assert kda.kda_get_device_error(stream) == attention.KDA_DEVICE_ERR_CACHE
+    assert not o[0].any() and bool(torch.isfinite(o).all())
+    filled_up = to_gpu(filled(g, [64, 64], 16, 1, 64, kind)[0])
+    o = paged_attn_step(q, filled_up, short, _int32([64, 1 << 30]))
+    assert kda.kda_get_device_error(stream) == attention.KDA_DEVICE_ERR_CACHE
+
+
+@pytest.mark.parametrize("dtype,kind", [(BF, E4M3), (F32, F32)])
+def test_graphs_streams_and_growing_lengths(dtype, kind):
+    """Two captured calls, each with scratch of its own, replayed in turn on another stream while the lengths grow in
+    place: the plan is made on the device, from the lengths of the moment."""
+    g = torch.Generator().manual_seed(10)
+    most = [700, 90, 2000]
+    cache, table = filled(g, most, 16, 2, 64, kind)
+    c, t, lens = to_gpu(cache), table.to(dev), _int32([1, 90, 500])
+    qs = [_q(g, 3, 1, 8, 64, dtype, kind).to(dev) for _ in range(2)]
+    outs, graphs = [], []
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for q in qs:
+            paged_attn_step(q, c, t, lens)
+    torch.cuda.synchronize()
+    for q in qs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(paged_attn_step(q, c, t, lens))
+        graphs.append(gr)
+    for now in ([1, 90, 500], [2, 0, 501], [700, 64, 2000]):
+        lens.copy_(_int32(now))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for gr in graphs + graphs:
+                gr.replay()
+        torch.cuda.synchronize()
+        for q, o in zip(qs, outs):
+            assert torch.equal(o, paged_attn_step(q, c, t, lens))
+            want, _ = aref.attention(q.cpu(), cache, table, now, 64 ** -0.5)
+            ref.check("replayed", o, want, dtype, WORK[dtype])
+
+
+def test_calls_on_two_streams_at_once():
+    g = torch.Generator().manual_seed(11)
+    cache, table = filled(g, [9000], 64, 4, 128, BF)
+    c, t, lens = to_gpu(cache), table.to(dev), _int32([9000])
+    qs = [_q(g, 1, 1, 16, 128, BF, BF).to(dev) for _ in range(2)]
+    want = [paged_attn_step(q, c, t, lens) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(20):
+        got = []
+        for s, q in zip(streams, qs):
+            with torch.cuda.stream(s):
+                got.append(paged_attn_step(q, c, t, lens))
+        # and with the library's own scratch, on a stream given by its handle
+        got.append(paged_attn_step(qs[0], c, t, lens, o=torch.empty_like(qs[0]), stream=streams[1].cuda_stream))
+        torch.cuda.synchronize()
+        for o, w in zip(got, want + want[:1]):
+            assert torch.equal(o, w)
+
+
+def test_no_tokens_and_given_outputs():
+    g = torch.Generator().manual_seed(12)
+    cache, table = filled(g, [20], 16, 1, 64, BF)
+    c, t, lens = to_gpu(cache), table.to(dev), _int32([20])
+    assert paged_attn_step(torch.empty(1, 0, 4, 64, dtype=BF, device=dev), c, t, lens).shape == (1, 0, 4, 64)
+    q = _q(g, 1, 1, 4, 64, BF, BF).to(dev)
+    o, lse = torch.empty_like(q), torch.empty(1, 1, 4, device=dev)
+    got = paged_attn_step(q, c, t, lens, want_lse=True, o=o, lse=lse)
+    assert got[0] is o and got[1] is lse and math.isfinite(float(lse.sum()))
