@@ -8,12 +8,18 @@
 namespace kda {
 namespace attn {
 
-int fma_rows(int all);  // query rows of an item for `all` rows of a sequence and key head
-cudaError_t launch_attn_fma(const Args &a, bool f32, cudaStream_t stream);
+// Query rows of an item for `all` rows of a sequence and key head, blocks on an SM, and the launch, of the kernel for
+// fp32 data and of that for bf16.
+int fma_rows(int all);
+int fma_blocks(const Args &a);
+cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream);
+int mma_rows(int all, int D);
+int mma_blocks(const Args &a);
+cudaError_t launch_attn_mma(const Args &a, cudaStream_t stream);
 
-// The warps' results of a piece, O [rows][DP] at `mem` + warp * `stride` bytes and (m, l) in ml [warp][RB], put together: into
+// The warps' results of a piece, O [rows][PITCH] at `mem` + warp * `stride` bytes and (m, l) in ml [warp][RB], put together: into
 // o and lse where the piece is a whole item, otherwise into the block's piece of scratch.
-template <typename T, int DP, int RB>
+template <typename T, int DP, int RB, int PITCH>
 __device__ __forceinline__ void finish(const Args &a, const Piece &p, const unsigned char *mem, int stride, const float2 *ml, int block) {
     const bool whole = p.t0 == 0 && p.t1 == p.tiles;
     const int D = a.cache.D;
@@ -31,7 +37,7 @@ __device__ __forceinline__ void finish(const Args &a, const Piece &p, const unsi
         for (int w = 0; w < kWarps; ++w) {
             const float2 x = ml[w * RB + r];
             const float f = tc5::ex2(x.x - ref);
-            const float4 v = *reinterpret_cast<const float4 *>(mem + w * stride + (r * DP + d) * 4);
+            const float4 v = *reinterpret_cast<const float4 *>(mem + w * stride + (r * PITCH + d) * 4);
             l = fmaf(x.y, f, l);
             s.x = fmaf(v.x, f, s.x);
             s.y = fmaf(v.y, f, s.y);

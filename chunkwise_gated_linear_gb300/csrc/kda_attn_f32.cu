@@ -18,9 +18,6 @@ __device__ __forceinline__ void unpack16(float (&f)[16 / sizeof(C)], const uint4
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(C) == 4) {
             f[i] = __uint_as_float(w[i]);
-        } else if constexpr (sizeof(C) == 2) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         } else {
             e4m3_to_f(w[i] & 0xffffu, f[4 * i], f[4 * i + 1]);
             e4m3_to_f(w[i] >> 16, f[4 * i + 2], f[4 * i + 3]);
@@ -28,14 +25,13 @@ __device__ __forceinline__ void unpack16(float (&f)[16 / sizeof(C)], const uint4
     }
 }
 __device__ __forceinline__ float elem(const float *p) { return *p; }
-__device__ __forceinline__ float elem(const bf16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float elem(const uint8_t *p) {
     float lo, hi;
     e4m3_to_f(*p, lo, hi);
     return lo;
 }
 
-template <typename T, typename C, int DP, int RB, int KEYS, int STAGES>
+template <typename C, int DP, int RB, int KEYS, int STAGES>
 struct Fma {
     using S = Stream<C, DP, KEYS, STAGES>;
     static constexpr int kParts = 32 / KEYS;
@@ -52,9 +48,9 @@ struct Fma {
     static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
 };
 
-template <typename T, typename C, int DP, int RB, int KEYS, int STAGES>
+template <typename C, int DP, int RB, int KEYS, int STAGES>
 __global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constant__ Args a) {
-    using F = Fma<T, C, DP, RB, KEYS, STAGES>;
+    using F = Fma<C, DP, RB, KEYS, STAGES>;
     extern __shared__ __align__(128) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Start at = find_start(a, blockIdx.x, reinterpret_cast<int64_t *>(mem + F::kPlan));
@@ -85,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constan
         st.begin(p, s0, s1);
         for (int i = threadIdx.x; i < p.rows * DP; i += kThreads) {
             const int r = i / DP, d = i - r * DP;
-            qs[i] = d < D ? to_f(static_cast<const T *>(a.q)[q_at(a, p, r) + d]) * a.scale_log2 : 0.f;
+            qs[i] = d < D ? static_cast<const float *>(a.q)[q_at(a, p, r) + d] * a.scale_log2 : 0.f;
         }
         if (threadIdx.x < RB) lim[threadIdx.x] = threadIdx.x < p.rows ? seen(a, p.len, p.row0 + threadIdx.x) : 0;
         __syncthreads();
@@ -198,34 +194,40 @@ __global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constan
             for (int j = 0; j < F::kCols; ++j) mine[r * DP + lane + 32 * j] = acc[r][j];
         }
         __syncthreads();
-        finish<T, DP, RB>(a, p, mem, F::S::kBytes, ml, blockIdx.x);
+        finish<float, DP, RB, DP>(a, p, mem, F::S::kBytes, ml, blockIdx.x);
         __syncthreads();
     }
 }
 
-template <typename T, typename C, int DP, int RB, int KEYS>
-cudaError_t launch(const Args &a, cudaStream_t stream) {
-    constexpr int kStages = 3;
-    return launch_kernel<attn_fma_kernel<T, C, DP, RB, KEYS, kStages>, Fma<T, C, DP, RB, KEYS, kStages>::kSmem>(a, stream);
+template <typename C, int DP, int RB, int KEYS>
+struct Variant {
+    using F = Fma<C, DP, RB, KEYS, 3>;
+    static cudaError_t launch(const Args &a, cudaStream_t stream) {
+        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, 3>, F::kSmem>(a, stream);
+    }
+    static int blocks() { return 1; }
+};
+// Calls f with the variant for these sizes.
+template <typename C, int RB, typename F>
+auto pick(const Args &a, F f) {
+    if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16>{});
+    if (a.cache.D <= 128) return f(Variant<C, 128, RB, 16>{});
+    return f(Variant<C, 256, RB, sizeof(C) == 4 ? 8 : 16>{});
 }
-template <typename T, typename C, int RB>
-cudaError_t launch_d(const Args &a, cudaStream_t stream) {
-    if (a.cache.D <= 64) return launch<T, C, 64, RB, 16>(a, stream);
-    if (a.cache.D <= 128) return launch<T, C, 128, RB, 16>(a, stream);
-    return launch<T, C, 256, RB, sizeof(C) == 4 ? 8 : 16>(a, stream);
-}
-template <typename T, typename C>
-cudaError_t launch_rows(const Args &a, cudaStream_t stream) {
-    return a.rows <= 4 ? launch_d<T, C, 4>(a, stream) : launch_d<T, C, 16>(a, stream);
+template <typename F>
+auto pick(const Args &a, F f) {
+    if (a.cache.ks != nullptr) return a.rows == 4 ? pick<uint8_t, 4>(a, f) : pick<uint8_t, 16>(a, f);
+    return a.rows == 4 ? pick<float, 4>(a, f) : pick<float, 16>(a, f);
 }
 
 }  // namespace
 
 int fma_rows(int all) { return all <= 4 ? 4 : 16; }
-
-cudaError_t launch_attn_fma(const Args &a, bool f32, cudaStream_t stream) {
-    if (f32) return a.cache.ks != nullptr ? launch_rows<float, uint8_t>(a, stream) : launch_rows<float, float>(a, stream);
-    return a.cache.ks != nullptr ? launch_rows<bf16, uint8_t>(a, stream) : launch_rows<bf16, bf16>(a, stream);
+int fma_blocks(const Args &a) {
+    return pick(a, [](auto v) { return decltype(v)::blocks(); });
+}
+cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream) {
+    return pick(a, [&](auto v) { return decltype(v)::launch(a, stream); });
 }
 
 }  // namespace attn

@@ -81,10 +81,11 @@ Args make(const kda_attn_step_params &p, unsigned int *err) {
     a.scale_log2 = p.scale * kLog2e;
     a.cache = cache_args(p.cache, err);
     const int all = a.T * a.group;
-    a.rows = fma_rows(all);
+    const bool f32 = p.dtype == KDA_DTYPE_F32;
+    a.rows = f32 ? fma_rows(all) : mma_rows(all, a.cache.D);
     a.row_blocks = (int)ceil_div(all, a.rows);
     a.per_seq = a.row_blocks * a.cache.heads;
-    a.grid = sm_count();
+    a.grid = sm_count() * (f32 ? fma_blocks(a) : mma_blocks(a));
     return a;
 }
 size_t bytes_of(const Args &a) { return (size_t)2 * a.grid * a.rows * (a.cache.D + 2) * sizeof(float); }
@@ -121,7 +122,7 @@ int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
     if (e != cudaSuccess) return status_of_cuda(e);
     a.pieces = static_cast<float *>(ws.ptr);
     const bool f32 = p->dtype == KDA_DTYPE_F32;
-    e = launch_attn_fma(a, f32, stream);
+    e = f32 ? launch_attn_fma(a, stream) : launch_attn_mma(a, stream);
     if (e == cudaSuccess) {
         const dim3 grid((unsigned)(a.B * a.per_seq), (unsigned)ceil_div(a.rows, kJoinWarps));
         if (f32)

@@ -317,3 +317,31 @@ def test_no_tokens_and_given_outputs():
     o, lse = torch.empty_like(q), torch.empty(1, 1, 4, device=dev)
     got = paged_attn_step(q, c, t, lens, want_lse=True, o=o, lse=lse)
     assert got[0] is o and got[1] is lse and math.isfinite(float(lse.sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("zeros", ["first", "all", "most"])
+def test_rows_of_zeros_in_an_8_bit_cache(dtype, zeros):
+    """A row of zeros has the least power of two, 2^-126: it counts in the softmax's sum like any other."""
+    g = torch.Generator().manual_seed(13)
+    lens = [150, 16, 1]
+    cache, table = filled(g, lens, 16, 2, 64, E4M3)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        pos = pos[:40] if zeros == "first" else pos if zeros == "all" else pos[pos % 37 != 5]
+        at = table[b].long()[pos // 16]
+        index(cache.v)[at, :, pos % 16] = 0
+        index(cache.v_scale)[at, :, pos % 16] = 1
+    _check(_q(g, 3, 1, 8, 64, dtype, E4M3), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tiny_values_in_an_8_bit_cache(dtype):
+    """All values near the least power of two: nothing of them is lost before the result is rounded."""
+    g = torch.Generator().manual_seed(14)
+    lens = [300, 40]
+    cache, table = filled(g, lens, 16, 2, 64, E4M3)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        index(cache.v_scale)[table[b].long()[pos // 16], :, pos % 16] = (5 + 20 * (pos % 2))[:, None].to(torch.uint8)
+    _check(_q(g, 2, 1, 8, 64, dtype, E4M3), cache, table, lens, dtype)
