@@ -1,9 +1,8 @@
 // Attention over a paged cache, computed on the fp32 pipes: fp32 data (cache fp32 or 8-bit). See attn_common.cuh
 // for how the work is cut.
 //
-// A step of a warp is KEYS keys: lane (key, part) takes every (32 / KEYS)-th 16-byte chunk of its key against all query rows,
-// the parts are added across lanes; the running maximum of each row is that of the warp's keys alone (joined at the
-// end); then a lane owns columns lane + 32 j of O and goes through the keys.
+// A unit is KEYS keys: lane (key, part) takes every (32 / KEYS)-th 16-byte chunk of its key against all query rows, the
+// parts are added across lanes; then a lane owns columns lane + 32 j of O and goes through the keys.
 #include "attn_common.cuh"
 #include "attn_launch.h"
 
@@ -37,54 +36,42 @@ struct Fma {
     static constexpr int kParts = 32 / KEYS;
     static constexpr int kE = 16 / (int)sizeof(C);
     static constexpr int kCols = DP / 32;
-    static_assert(S::kBytes >= RB * DP * 4, "a warp's ring holds its O at the end");
-    // shared memory: rings, q [RB][DP], p [warps][KEYS][RB], (m, l) [warps][RB], rows' limits, the plan, exponent bytes
+    // shared memory: rings, q [warps][RB][DP], p [warps][KEYS][RB], rows' limits [warps][RB], the plan, exponent bytes
     static constexpr int kQ = kWarps * S::kBytes;
-    static constexpr int kP = kQ + RB * DP * 4;
-    static constexpr int kMl = kP + kWarps * KEYS * RB * 4;
-    static constexpr int kLim = kMl + kWarps * RB * 8;
-    static constexpr int kPlan = kLim + RB * 4 + (RB * 4) % 8;
-    static constexpr int kSc = kPlan + (kWarps + 2) * 8;
+    static constexpr int kP = kQ + kWarps * RB * DP * 4;
+    static constexpr int kLim = kP + kWarps * KEYS * RB * 4;
+    static constexpr int kPlan = kLim + kWarps * RB * 4;
+    static constexpr int kSc = kPlan + kPlanBytes;
     static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+    static constexpr int kBlocks = (228 * 1024) / (kSmem + 1024) < 2 ? 1 : 2;
 };
 
 template <typename C, int DP, int RB, int KEYS, int STAGES>
-__global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlocks) attn_fma_kernel(const __grid_constant__ Args a) {
     using F = Fma<C, DP, RB, KEYS, STAGES>;
     extern __shared__ __align__(128) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Start at = find_start(a, blockIdx.x, reinterpret_cast<int64_t *>(mem + F::kPlan));
-    if ((int)blockIdx.x >= at.grid) return;
-    float *qs = reinterpret_cast<float *>(mem + F::kQ);
+    launch_dependents();
+    Walk walk = find_walk(a, reinterpret_cast<int64_t *>(mem + F::kPlan));
+    if (walk.left <= 0) return;
+    float *qs = reinterpret_cast<float *>(mem + F::kQ) + warp * RB * DP;
     float *pw = reinterpret_cast<float *>(mem + F::kP) + warp * KEYS * RB;
-    float2 *ml = reinterpret_cast<float2 *>(mem + F::kMl);
-    int *lim = reinterpret_cast<int *>(mem + F::kLim);
+    int *lim = reinterpret_cast<int *>(mem + F::kLim) + warp * RB;
     unsigned char *own = mem + warp * F::S::kBytes;
-    typename F::S st(a, own, mem + F::kSc + warp * F::S::kScaleBytes, lane, warp);
+    typename F::S st(a, own, mem + F::kSc + warp * F::S::kScaleBytes, lane, walk);
     const int D = a.cache.D, key = lane & (KEYS - 1), part = lane / KEYS;
     const int cpr = D * (int)sizeof(C) / 16;
 
-    int64_t cur = share(at.total, blockIdx.x, at.grid);
-    const int64_t stop = share(at.total, blockIdx.x + 1, at.grid);
-    int b = at.b, len = cache_len(a.cache, b);
-    int64_t before = at.before;
-    while (cur < stop) {
-        int64_t all = (int64_t)tiles_of(len) * a.per_seq;
-        while (cur >= before + all) {
-            before += all;
-            len = cache_len(a.cache, ++b);
-            all = (int64_t)tiles_of(len) * a.per_seq;
+    int slot = 0;
+    while (walk.left > 0) {
+        const Piece p = walk.piece(a);
+        for (int r = 0; r < p.rows; ++r) {
+            const float *from = static_cast<const float *>(a.q) + q_at(a, p, r);
+            for (int d = lane; d < DP; d += 32) qs[r * DP + d] = d < D ? from[d] * a.scale_log2 : 0.f;
         }
-        const Piece p = piece_at(a, b, len, cur - before, stop - cur);
-        cur += p.t1 - p.t0;
-        const int s0 = p.t0 * (kTile / F::S::kStep), s1 = p.t1 * (kTile / F::S::kStep);
-        st.begin(p, s0, s1);
-        for (int i = threadIdx.x; i < p.rows * DP; i += kThreads) {
-            const int r = i / DP, d = i - r * DP;
-            qs[i] = d < D ? static_cast<const float *>(a.q)[q_at(a, p, r) + d] * a.scale_log2 : 0.f;
-        }
-        if (threadIdx.x < RB) lim[threadIdx.x] = threadIdx.x < p.rows ? seen(a, p.len, p.row0 + threadIdx.x) : 0;
-        __syncthreads();
+        if (lane < RB) lim[lane] = lane < p.rows ? seen(a, p.len, p.row0 + lane) : 0;
+        __syncwarp();
         const int least = lim[0];  // keys from here on are not seen by all rows
         float m[RB], l[RB], acc[RB][F::kCols];
 #pragma unroll
@@ -94,12 +81,11 @@ __global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < F::kCols; ++j) acc[r][j] = 0.f;
         }
-        int slot = 0;
-        for (int s = s0; s < s1; ++s) {
+        for (int u = p.u0; u < p.u1; ++u) {
             st.ready();
             const unsigned char *ks = own + slot * 2 * F::S::kHalf, *vs = ks + F::S::kHalf;
             const uint8_t *sc = st.scales + slot * 2 * KEYS;
-            const int pos0 = s * F::S::kStep + warp * KEYS;
+            const int pos0 = u * KEYS;
             if (pos0 < p.last) {  // the same for the whole warp
                 float x[RB];
 #pragma unroll
@@ -175,44 +161,51 @@ __global__ void __launch_bounds__(kThreads) attn_fma_kernel(const __grid_constan
                     }
                 }
             }
-            __syncwarp();
-            st.fetch(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
-            slot = slot == STAGES - 1 ? 0 : slot + 1;
+            slot = st.next(slot);
         }
-        copies_wait<0>();
-        __syncwarp();
-        // the warps' results side by side in their rings, then one sum over them
-        float *mine = reinterpret_cast<float *>(own);
+        float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             if (r >= p.rows) break;
             float t = l[r];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            if (lane == 0) ml[warp * RB + r] = make_float2(m[r], t);
+            const bool whole = p.whole();
+            const int64_t row = out_row(a, p, r);
+            const float f = whole ? (t == 0.f ? 0.f : 1.f / t) : 1.f;
+            float *to = whole ? static_cast<float *>(a.o) + row * D : piece + r * D;
 #pragma unroll
-            for (int j = 0; j < F::kCols; ++j) mine[r * DP + lane + 32 * j] = acc[r][j];
+            for (int j = 0; j < F::kCols; ++j)
+                if (lane + 32 * j < D) to[lane + 32 * j] = acc[r][j] * f;
+            if (lane == 0) {
+                if (!whole)
+                    reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(m[r], t);
+                else if (a.lse != nullptr)
+                    a.lse[row] = lse_of(m[r], t);
+            }
         }
-        __syncthreads();
-        finish<float, DP, RB, DP>(a, p, mem, F::S::kBytes, ml, blockIdx.x);
-        __syncthreads();
+        __syncwarp();
+        walk.step(a, p);
     }
+    copies_wait<0>();
 }
 
-template <typename C, int DP, int RB, int KEYS>
+template <typename C, int DP, int RB, int KEYS, int STAGES>
 struct Variant {
-    using F = Fma<C, DP, RB, KEYS, 3>;
+    using F = Fma<C, DP, RB, KEYS, STAGES>;
     static cudaError_t launch(const Args &a, cudaStream_t stream) {
-        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, 3>, F::kSmem>(a, stream);
+        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, STAGES>, F::kSmem>(a, stream);
     }
-    static int blocks() { return 1; }
+    static int blocks() { return F::kBlocks; }
+    static int unit() { return KEYS; }
 };
-// Calls f with the variant for these sizes.
+// Calls f with the variant for these sizes: rings that fill the shared memory of an SM, in one block or two.
 template <typename C, int RB, typename F>
 auto pick(const Args &a, F f) {
-    if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16>{});
-    if (a.cache.D <= 128) return f(Variant<C, 128, RB, 16>{});
-    return f(Variant<C, 256, RB, sizeof(C) == 4 ? 8 : 16>{});
+    constexpr bool k4 = sizeof(C) == 4;
+    if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16, 3>{});
+    if (a.cache.D <= 128) return f(Variant<C, 128, RB, k4 ? 8 : 16, k4 && RB == 16 ? 5 : 3>{});
+    return f(Variant<C, 256, RB == 16 ? 8 : RB, k4 ? 8 : 16, 3>{});
 }
 template <typename F>
 auto pick(const Args &a, F f) {
@@ -222,7 +215,10 @@ auto pick(const Args &a, F f) {
 
 }  // namespace
 
-int fma_rows(int all) { return all <= 4 ? 4 : 16; }
+int fma_rows(int all, int D) { return all <= 4 ? 4 : D > 128 ? 8 : 16; }
+int fma_unit(const Args &a) {
+    return pick(a, [](auto v) { return decltype(v)::unit(); });
+}
 int fma_blocks(const Args &a) {
     return pick(a, [](auto v) { return decltype(v)::blocks(); });
 }

@@ -20,7 +20,6 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kKeys = 16;
 constexpr float kGrow = 8.f;  // scores may pass their reference by 2^kGrow before it moves
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -61,20 +60,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 template <typename C, int DP, int NT, int STAGES>
 struct Mma {
-    using S = Stream<C, DP, kKeys, STAGES>;
     static constexpr bool kScaled = sizeof(C) == 1;
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kSteps = DP / 16;      // products of S^T, and blocks of 16 channels of O^T
-    static constexpr int kOPitch = DP + 4;      // floats; rows 2 c, 2 c + 1 of the four lanes c in different banks
-    static_assert(S::kBytes >= kRows * kOPitch * 4, "a warp's ring holds its O at the end");
-    // shared memory: rings, (m, l) [warps][rows], the plan, exponent bytes
-    static constexpr int kMl = kWarps * S::kBytes;
-    static constexpr int kPlan = kMl + kWarps * kRows * 8;
-    static constexpr int kSc = kPlan + (kWarps + 2) * 8;
+    // blocks of 16 keys in a unit: two of 8-bit values, where the registers hold the scores of both beside O^T
+    static constexpr int kHalves = kScaled && DP * NT <= 256 ? 2 : 1;
+    static constexpr int kKeys = 16 * kHalves;
+    using S = Stream<C, DP, kKeys, STAGES>;
+    static constexpr int kSteps = DP / 16;  // products of S^T, and blocks of 16 channels of O^T
+    // shared memory: rings, the plan, exponent bytes
+    static constexpr int kPlan = kWarps * S::kBytes;
+    static constexpr int kSc = kPlan + kPlanBytes;
     static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
-    static constexpr int kFit = (227 * 1024 + 1024) / (kSmem + 1024);
+    static constexpr int kFit = (228 * 1024) / (kSmem + 1024);
     // registers: O^T and Q^T alone are (4 + 2) kSteps NT of a lane's
-    static constexpr int kLive = 6 * kSteps * NT + 72;
+    static constexpr int kLive = 6 * kSteps * NT + 90;
     static constexpr int kByRegs = 65536 / (kThreads * (kLive < 96 ? 96 : kLive > 255 ? 255 : kLive));
     static constexpr int kBlocks = kFit < kByRegs ? kFit : kByRegs;
 };
@@ -83,32 +81,20 @@ template <typename C, int DP, int NT, int STAGES>
 __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) attn_mma_kernel(const __grid_constant__ Args a) {
     using M = Mma<C, DP, NT, STAGES>;
     using S = typename M::S;
-    constexpr int kSteps = M::kSteps;
+    constexpr int kSteps = M::kSteps, kHalves = M::kHalves, kKeys = M::kKeys;
     extern __shared__ __align__(1024) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const Start at = find_start(a, blockIdx.x, reinterpret_cast<int64_t *>(mem + M::kPlan));
-    if ((int)blockIdx.x >= at.grid) return;
-    float2 *ml = reinterpret_cast<float2 *>(mem + M::kMl);
+    launch_dependents();
+    Walk walk = find_walk(a, reinterpret_cast<int64_t *>(mem + M::kPlan));
+    if (walk.left <= 0) return;
     unsigned char *own = mem + warp * S::kBytes;
-    S st(a, own, mem + M::kSc + warp * S::kScaleBytes, lane, warp);
+    S st(a, own, mem + M::kSc + warp * S::kScaleBytes, lane, walk);
     const int D = a.cache.D;
 
-    int64_t cur = share(at.total, blockIdx.x, at.grid);
-    const int64_t stop = share(at.total, blockIdx.x + 1, at.grid);
-    int b = at.b, len = cache_len(a.cache, b);
-    int64_t before = at.before;
-    while (cur < stop) {
-        int64_t all = (int64_t)tiles_of(len) * a.per_seq;
-        while (cur >= before + all) {
-            before += all;
-            len = cache_len(a.cache, ++b);
-            all = (int64_t)tiles_of(len) * a.per_seq;
-        }
-        const Piece p = piece_at(a, b, len, cur - before, stop - cur);
-        cur += p.t1 - p.t0;
-        st.begin(p, p.t0, p.t1);
-
+    int slot = 0;
+    while (walk.left > 0) {
+        const Piece p = walk.piece(a);
         // Q^T: row 8 n + g, the lane's channels of each block of 16 in the order in which K's come out of the ring
         uint32_t q[NT][kSteps][2];
         float rowf[NT][2];  // what a score of rows 8 n + 2 c, + 1 is multiplied with
@@ -177,69 +163,84 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) att
                 for (int i = 0; i < 4; ++i) o[k][n][i] = 0.f;
         }
 
-        int slot = 0;
-        for (int s = p.t0; s < p.t1; ++s) {
+        for (int u = p.u0; u < p.u1; ++u) {
             st.ready();
-            const int pos0 = s * kTile + warp * kKeys;
+            const int pos0 = u * kKeys;
             if (pos0 < p.last) {  // the same for the whole warp
                 const uint32_t ks = st.ring + slot * 2 * S::kHalf, vs = ks + S::kHalf;
-                float x[NT][4];
+                // scores, base 2; element i of half h: key 16 h + g + 8 (i / 2), row 8 n + 2 c + i % 2
+                float x[kHalves][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[h][n][i] = 0.f;
                 const uint32_t krow = ks + (lane & 15) * S::kPitch;
 #pragma unroll
                 for (int k = 0; k < kSteps; k += M::kScaled ? 2 : 1) {
-                    uint32_t r[4];
-                    if constexpr (M::kScaled) {
-                        // 16-byte chunks k and k + 1 are channels 16 k .. 16 k + 31: keys g and g + 8, channels 4 c .. 4 c + 3 of each
-                        ldsm(r, krow + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
-                        uint32_t f[4];
-                        widen(r[0], f[0], f[2]);
-                        widen(r[1], f[1], f[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(x[n], f, q[n][k][0], q[n][k][1]);
-                        widen(r[2], f[0], f[2]);
-                        widen(r[3], f[1], f[3]);
+                    for (int h = 0; h < kHalves; ++h) {
+                        uint32_t r[4];
+                        if constexpr (M::kScaled) {
+                            // 16-byte chunks k and k + 1 are channels 16 k .. 16 k + 31: keys g and g + 8, channels 4 c .. 4 c + 3 of each
+                            ldsm(r, krow + 16 * h * S::kPitch + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
+                            uint32_t f[4];
+                            widen(r[0], f[0], f[2]);
+                            widen(r[1], f[1], f[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(x[n], f, q[n][k + 1][0], q[n][k + 1][1]);
-                    } else {
-                        ldsm(r, krow + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
+                            for (int n = 0; n < NT; ++n) mma_f16(x[h][n], f, q[n][k][0], q[n][k][1]);
+                            widen(r[2], f[0], f[2]);
+                            widen(r[3], f[1], f[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_bf16(x[n], r, q[n][k][0], q[n][k][1]);
+                            for (int n = 0; n < NT; ++n) mma_f16(x[h][n], f, q[n][k + 1][0], q[n][k + 1][1]);
+                        } else {
+                            ldsm(r, krow + 16 * h * S::kPitch + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_bf16(x[h][n], r, q[n][k][0], q[n][k][1]);
+                        }
                     }
                 }
-                // scores, base 2; element i: key g + 8 (i / 2), row 8 n + 2 c + i % 2
-                float fk[2] = {1.f, 1.f}, fv[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
-                if constexpr (M::kScaled) {
-                    const uint8_t *sc = st.scales + slot * 2 * kKeys;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        fk[i] = __uint_as_float((uint32_t)sc[g + 8 * i] << 23);
-                        const uint32_t e = sc[kKeys + g + 8 * i];
-                        fv[i] = __uint_as_float(e << 23);
-                        ev[i] = (float)((int)e - 127);
-                    }
-                }
+                float fv[kHalves][2], ev[kHalves][2];  // 8-bit: the values' powers of two and their exponents
                 const bool edge = pos0 + kKeys > least;
                 bool grows = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int h = 0; h < kHalves; ++h) {
+                    float fk[2] = {1.f, 1.f};
+                    if constexpr (M::kScaled) {
+                        const uint8_t *sc = st.scales + slot * 2 * kKeys + 16 * h;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[n][i] *= M::kScaled ? rowf[n][i & 1] * fk[i >> 1] : rowf[n][i & 1];
-                        if (edge && pos0 + g + 8 * (i >> 1) >= seen(a, p.len, p.row0 + 8 * n + 2 * c + (i & 1))) x[n][i] = -INFINITY;
-                        grows |= x[n][i] > big[n][i & 1];
-                        if constexpr (M::kScaled) grows |= x[n][i] + ev[i >> 1] > bigv[n][i & 1];
+                        for (int i = 0; i < 2; ++i) {
+                            fk[i] = __uint_as_float((uint32_t)sc[g + 8 * i] << 23);
+                            const uint32_t e = sc[kKeys + g + 8 * i];
+                            fv[h][i] = __uint_as_float(e << 23);
+                            ev[h][i] = (float)((int)e - 127);
+                        }
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float &y = x[h][n][i];
+                            y *= M::kScaled ? rowf[n][i & 1] * fk[i >> 1] : rowf[n][i & 1];
+                            if (edge && pos0 + 16 * h + g + 8 * (i >> 1) >= seen(a, p.len, p.row0 + 8 * n + 2 * c + (i & 1))) y = -INFINITY;
+                            grows |= y > big[n][i & 1];
+                            if constexpr (M::kScaled) grows |= y + ev[h][i >> 1] > bigv[n][i & 1];
+                        }
+                }
                 if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float top = fmaxf(x[n][j], x[n][j + 2]);
-                            float topv = M::kScaled ? fmaxf(x[n][j] + ev[0], x[n][j + 2] + ev[1]) : 0.f;
+                            float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                                for (int i = j; i < 4; i += 2) {
+                                    top = fmaxf(top, x[h][n][i]);
+                                    if constexpr (M::kScaled) topv = fmaxf(topv, x[h][n][i] + ev[h][i >> 1]);
+                                }
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) {
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -275,30 +276,33 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) att
                             }
                         }
                 }
-                uint32_t pb[NT][2];
+                uint32_t pb[kHalves][NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[n][i] = tc5::ex2(x[n][i] - m[n][i & 1]);
-                        l[n][i & 1] += x[n][i];
-                        if constexpr (M::kScaled) x[n][i] *= fv[i >> 1] * turn[n][i & 1];
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float &y = x[h][n][i];
+                            y = tc5::ex2(y - m[n][i & 1]);
+                            l[n][i & 1] += y;
+                            if constexpr (M::kScaled) y *= fv[h][i >> 1] * turn[n][i & 1];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float lo = x[h][n][2 * i], hi = x[h][n][2 * i + 1];
+                            pb[h][n][i] = transpose8(M::kScaled ? pack_f16(lo, hi) : pack_bf16(lo, hi));
+                        }
                     }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t two = M::kScaled ? pack_f16(x[n][2 * i], x[n][2 * i + 1]) : pack_bf16(x[n][2 * i], x[n][2 * i + 1]);
-                        pb[n][i] = transpose8(two);
-                    }
-                }
                 if (edge && a.T > 1) {
                     // Values that are not finite would reach rows that do not see them, as 0 * NaN: such keys' shares are added one by
                     // one to the rows that do, and their values then count as zeros.
-                    unsigned char *rows = own + slot * 2 * S::kHalf + S::kHalf;
+                    unsigned char *vals = own + slot * 2 * S::kHalf + S::kHalf;
                     uint32_t odd = 0;
                     for (int r = 0; r < kKeys; ++r) {
                         bool bad = false;
                         for (int w = lane; w < S::kPitch / 4; w += 32) {
-                            const uint32_t v = *reinterpret_cast<const uint32_t *>(rows + r * S::kPitch + 4 * w);
+                            const uint32_t v = *reinterpret_cast<const uint32_t *>(vals + r * S::kPitch + 4 * w);
                             if constexpr (M::kScaled)
                                 bad |= (v & 0x7fu) == 0x7fu || (v >> 8 & 0x7fu) == 0x7fu || (v >> 16 & 0x7fu) == 0x7fu || (v >> 24 & 0x7fu) == 0x7fu;
                             else
@@ -306,98 +310,123 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) att
                         }
                         if (__any_sync(0xffffffffu, bad)) odd |= 1u << r;
                     }
-                    for (int r = 0; odd >> r != 0; ++r) {
-                        if ((odd >> r & 1) == 0) continue;
+                    if (odd != 0) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int h = 0; h < kHalves; ++h)
+#pragma unroll 1
+                            for (int r = 0; r < 16; ++r) {
+                                if ((odd >> (16 * h + r) & 1) == 0) continue;
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float lo = __shfl_sync(0xffffffffu, x[n][j], 4 * (r & 7) + c);
-                                const float hi = __shfl_sync(0xffffffffu, x[n][j + 2], 4 * (r & 7) + c);
-                                const float w = r < 8 ? lo : hi;
-                                if (pos0 + r >= seen(a, p.len, p.row0 + 8 * n + 2 * c + j)) continue;
+                                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                for (int k = 0; k < kSteps; ++k)
+                                    for (int j = 0; j < 2; ++j) {
+                                        const float lo = __shfl_sync(0xffffffffu, x[h][n][j], 4 * (r & 7) + c);
+                                        const float hi = __shfl_sync(0xffffffffu, x[h][n][j + 2], 4 * (r & 7) + c);
+                                        const float w = r < 8 ? lo : hi;
+                                        if (pos0 + 16 * h + r >= seen(a, p.len, p.row0 + 8 * n + 2 * c + j)) continue;
 #pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        const int d = 16 * k + (M::kScaled ? 2 * g + h : g + 8 * h);
-                                        const int byte = d * (int)sizeof(C);
-                                        const unsigned char *e = rows + r * S::kPitch + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-                                        float v, no;
-                                        if constexpr (M::kScaled)
-                                            e4m3_to_f(*e, v, no);
-                                        else
-                                            v = to_f(*reinterpret_cast<const bf16 *>(e));
-                                        o[k][n][j + 2 * h] = fmaf(w, v, o[k][n][j + 2 * h]);
+                                        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                                            for (int t = 0; t < 2; ++t) {
+                                                const int byte = (16 * k + (M::kScaled ? 2 * g + t : g + 8 * t)) * (int)sizeof(C);
+                                                const unsigned char *e = vals + (16 * h + r) * S::kPitch + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+                                                float v, no;
+                                                if constexpr (M::kScaled)
+                                                    e4m3_to_f(*e, v, no);
+                                                else
+                                                    v = to_f(*reinterpret_cast<const bf16 *>(e));
+                                                o[k][n][j + 2 * t] = fmaf(w, v, o[k][n][j + 2 * t]);
+                                            }
                                     }
                             }
+                        __syncwarp();
+                        for (int r = 0; r < kKeys; ++r)
+                            if (odd >> r & 1)
+                                for (int w = lane; w < S::kPitch / 4; w += 32) *reinterpret_cast<uint32_t *>(vals + r * S::kPitch + 4 * w) = 0u;
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    for (int r = 0; r < kKeys; ++r)
-                        if (odd >> r & 1)
-                            for (int w = lane; w < S::kPitch / 4; w += 32) *reinterpret_cast<uint32_t *>(rows + r * S::kPitch + 4 * w) = 0u;
-                    __syncwarp();
                 }
-                if constexpr (M::kScaled) {
-                    // 16 keys x 16-byte chunks k, k + 1, transposed in units of two bytes: channels 2 g, 2 g + 1 of keys 2 c, 2 c + 1
-                    const uint32_t vrow = vs + (lane & 15) * S::kPitch;
 #pragma unroll
-                    for (int k = 0; k < kSteps; k += 2) {
-                        uint32_t r[4];
-                        ldsm_t(r, vrow + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
+                for (int h = 0; h < kHalves; ++h) {
+                    if constexpr (M::kScaled) {
+                        // 16 keys x 16-byte chunks k, k + 1, transposed in units of two bytes: channels 2 g, 2 g + 1 of keys 2 c, 2 c + 1
+                        const uint32_t vrow = vs + (16 * h + (lane & 15)) * S::kPitch;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // bytes (key 2c, channel 2g), (2c, 2g + 1), (2c + 1, 2g), (2c + 1, 2g + 1): pair the keys
-                            uint32_t f[4];
-                            widen(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
-                            widen(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
+                        for (int k = 0; k < kSteps; k += 2) {
+                            uint32_t r[4];
+                            ldsm_t(r, vrow + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(o[k + h][n], f, pb[n][0], pb[n][1]);
+                            for (int t = 0; t < 2; ++t) {
+                                // bytes (key 2c, channel 2g), (2c, 2g + 1), (2c + 1, 2g), (2c + 1, 2g + 1): pair the keys
+                                uint32_t f[4];
+                                widen(__byte_perm(r[2 * t], 0, 0x3120), f[0], f[1]);
+                                widen(__byte_perm(r[2 * t + 1], 0, 0x3120), f[2], f[3]);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) mma_f16(o[k + t][n], f, pb[h][n][0], pb[h][n][1]);
+                            }
                         }
-                    }
-                } else {
-                    const uint32_t vrow = vs + ((lane & 7) + ((lane >> 4) << 3)) * S::kPitch;
+                    } else {
+                        const uint32_t vrow = vs + (16 * h + (lane & 7) + ((lane >> 4) << 3)) * S::kPitch;
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        uint32_t r[4];
-                        ldsm_t(r, vrow + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+                        for (int k = 0; k < kSteps; ++k) {
+                            uint32_t r[4];
+                            ldsm_t(r, vrow + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_bf16(o[k][n], r, pb[n][0], pb[n][1]);
+                            for (int n = 0; n < NT; ++n) mma_bf16(o[k][n], r, pb[h][n][0], pb[h][n][1]);
+                        }
                     }
                 }
             }
-            __syncwarp();
-            st.fetch(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
-            slot = slot == STAGES - 1 ? 0 : slot + 1;
+            slot = st.next(slot);
         }
-        copies_wait<0>();
-        __syncwarp();
-        // the warps' results side by side in their rings, then one sum over them
-        float *mine = reinterpret_cast<float *>(own);
+        float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
+        const bool whole = p.whole();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
-                if (g == 0) ml[warp * M::kRows + 8 * n + 2 * c + j] = make_float2(big[n][j] == -INFINITY ? -INFINITY : m[n][j], l[n][j]);
-                const float f = M::kScaled ? tc5::ex2(mv[n][j] - m[n][j]) : 1.f;
+                const int r = 8 * n + 2 * c + j;
+                if (r >= p.rows) continue;
+                const float top = big[n][j] == -INFINITY ? -INFINITY : m[n][j];
+                float f = M::kScaled ? tc5::ex2(mv[n][j] - m[n][j]) : 1.f;
+                if (whole) {
+                    f = l[n][j] == 0.f ? 0.f : f / l[n][j];
+                    const int64_t row = out_row(a, p, r);
+                    bf16 *to = static_cast<bf16 *>(a.o) + row * D;
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    float *to = mine + (8 * n + 2 * c + j) * M::kOPitch + 16 * k;
-                    if constexpr (M::kScaled) {
-                        *reinterpret_cast<float2 *>(to + 2 * g) = make_float2(o[k][n][j] * f, o[k][n][j + 2] * f);
-                    } else {
-                        to[g] = o[k][n][j];
-                        to[g + 8] = o[k][n][j + 2];
+                    for (int k = 0; k < kSteps; ++k) {
+                        if (16 * k >= D) break;
+                        const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
+                        if constexpr (M::kScaled) {
+                            *reinterpret_cast<uint32_t *>(to + 16 * k + 2 * g) = pack_bf16(lo, hi);
+                        } else {
+                            to[16 * k + g] = from_f<bf16>(lo);
+                            to[16 * k + g + 8] = from_f<bf16>(hi);
+                        }
                     }
+                    if (g == 0 && a.lse != nullptr) a.lse[row] = lse_of(top, l[n][j]);
+                } else {
+                    float *to = piece + r * D;
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        if (16 * k >= D) break;
+                        const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
+                        if constexpr (M::kScaled) {
+                            *reinterpret_cast<float2 *>(to + 16 * k + 2 * g) = make_float2(lo, hi);
+                        } else {
+                            to[16 * k + g] = lo;
+                            to[16 * k + g + 8] = hi;
+                        }
+                    }
+                    if (g == 0) reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(top, l[n][j]);
                 }
             }
         }
-        __syncthreads();
-        finish<bf16, DP, M::kRows, M::kOPitch>(a, p, mem, S::kBytes, ml, blockIdx.x);
-        __syncthreads();
+        walk.step(a, p);
     }
+    copies_wait<0>();
 }
 
 template <typename C, int DP, int NT, int STAGES>
@@ -407,18 +436,16 @@ struct Variant {
         return launch_kernel<attn_mma_kernel<C, DP, NT, STAGES>, M::kSmem>(a, stream);
     }
     static int blocks() { return M::kBlocks; }
+    static int unit() { return M::kKeys; }
 };
 
 // Calls f with the variant for these sizes. Query rows: 8, 16 or 32 (16 where O^T of wide heads fills the registers).
 template <typename C, typename F>
 auto pick(const Args &a, F f) {
-    constexpr bool k8 = sizeof(C) == 1;
     if (a.cache.D <= 64)
         return a.rows == 8 ? f(Variant<C, 64, 1, 4>{}) : a.rows == 16 ? f(Variant<C, 64, 2, 4>{}) : f(Variant<C, 64, 4, 4>{});
     if (a.cache.D <= 128)
-        return a.rows == 8    ? f(Variant<C, 128, 1, k8 ? 4 : 3>{})
-               : a.rows == 16 ? f(Variant<C, 128, 2, k8 ? 4 : 3>{})
-                              : f(Variant<C, 128, 4, k8 ? 6 : 3>{});
+        return a.rows == 8 ? f(Variant<C, 128, 1, 3>{}) : a.rows == 16 ? f(Variant<C, 128, 2, 3>{}) : f(Variant<C, 128, 4, sizeof(C) == 1 ? 6 : 3>{});
     return a.rows == 8 ? f(Variant<C, 256, 1, 3>{}) : f(Variant<C, 256, 2, 3>{});
 }
 
@@ -426,6 +453,10 @@ auto pick(const Args &a, F f) {
 
 int mma_rows(int all, int D) { return all <= 8 ? 8 : (all <= 16 || D > 128) ? 16 : 32; }
 
+int mma_unit(const Args &a) {
+    auto f = [](auto v) { return decltype(v)::unit(); };
+    return a.cache.ks != nullptr ? pick<uint8_t>(a, f) : pick<bf16>(a, f);
+}
 int mma_blocks(const Args &a) {
     auto f = [](auto v) { return decltype(v)::blocks(); };
     return a.cache.ks != nullptr ? pick<uint8_t>(a, f) : pick<bf16>(a, f);
