@@ -30,114 +30,133 @@ struct Args {
     float *lse;
     int64_t q_stride;
     int B, T, Hq, group;
-    int rows;          // query rows of an item (at most)
-    int per_seq;       // items of a sequence: blocks of query rows * key heads
-    int unit;          // keys of a unit
+    uint32_t group_magic;  // ceil(2^32 / group): row / group is the upper half of row * group_magic while row * group < 2^32
+    int rows;              // query rows of an item (at most)
+    int row_blocks, per_seq;  // items of a sequence: blocks of query rows * key heads
+    int unit_shift;        // keys of a unit, as a power of two
     int workers;
-    float scale_log2;  // scale * log2 e
+    float scale_log2;      // scale * log2 e
     Cache cache;
-    float *pieces;     // [2 workers][rows * (D + 2)]: O [rows][D], then (m, l) [rows]
+    float *pieces;         // [2 workers][rows * (D + 2)]: O [rows][D], then (m, l) [rows]
 };
 
-__device__ __forceinline__ int units_of(int len, int unit) { return len <= unit ? 1 : (len + unit - 1) / unit; }
+__device__ __forceinline__ int token_of(const Args &a, int row) {
+    return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_magic);
+}
+__device__ __forceinline__ uint32_t units_of(const Args &a, int len) {
+    const uint32_t n = ((uint32_t)len + (1u << a.unit_shift) - 1) >> a.unit_shift;
+    return n == 0 ? 1 : n;
+}
 
-// How many workers have a share (each then has a unit at least), the first unit of share w, and whose share unit x is in.
-__device__ __forceinline__ int sharers(const Args &a, int64_t total) { return total < a.workers ? (int)total : a.workers; }
-__device__ __forceinline__ int64_t share(int64_t total, int w, int n) { return total * w / n; }
-__device__ __forceinline__ int owner(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
-
-// A scan over the sequences by the NT threads of a block: thread i adds up the sequences i * each .. i * each + each - 1.
-template <int NT>
-struct Scan {
-    int each, first;
-    int64_t sum, before, total;  // units of the thread's sequences, of those before, of all
-    // `mem`: NT / 32 int64
-    __device__ __forceinline__ void run(const Args &a, int64_t *mem) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        each = (a.B + NT - 1) / NT;
-        first = threadIdx.x * each;
-        sum = 0;
-        for (int b = first; b < first + each && b < a.B; ++b) sum += units_of(cache_len(a.cache, b), a.unit);
-        sum *= a.per_seq;
-        int64_t scan = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += x;
-        }
-        if (lane == 31) mem[warp] = scan;
-        __syncthreads();
-        before = scan - sum;
-        total = 0;
-#pragma unroll
-        for (int v = 0; v < NT / 32; ++v) {
-            if (v < warp) before += mem[v];
-            total += mem[v];
-        }
+// The units of all items (below 2^32, checked on the host for the longest sequences) dealt out: how many workers have a
+// share (each then has a unit at least), where share w begins, and whose share unit x is in.
+struct Deal {
+    uint32_t n, base, more;  // the first `more` shares have base + 1 units
+    __device__ __forceinline__ Deal(const Args &a, uint32_t total) {
+        n = total < (uint32_t)a.workers ? total : (uint32_t)a.workers;
+        base = total / n;
+        more = total - base * n;
+    }
+    __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * base + (w < more ? w : more); }
+    __device__ __forceinline__ int owner(uint32_t x) const {
+        const uint32_t big = more * (base + 1);
+        return (int)(x < big ? x / (base + 1) : more + (x - big) / base);
     }
 };
+
+// A scan over the sequences by the threads of a block: thread i adds up the sequences i * each .. i * each + each - 1.
+struct Scan {
+    int each, first;
+    uint32_t sum, before, total;  // units of the thread's sequences, of those before, of all
+};
+// `mem`: an int for each warp.
+__device__ __forceinline__ Scan scan_sequences(const Args &a, uint32_t *mem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+    Scan s;
+    s.each = (a.B + threads - 1) / threads;
+    s.first = threadIdx.x * s.each;
+    s.sum = 0;
+#pragma unroll 1
+    for (int b = s.first; b < s.first + s.each && b < a.B; ++b) s.sum += units_of(a, cache_len(a.cache, b));
+    s.sum *= a.per_seq;
+    uint32_t scan = s.sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += x;
+    }
+    if (lane == 31) mem[warp] = scan;
+    __syncthreads();
+    s.before = scan - s.sum;
+    s.total = 0;
+#pragma unroll 1
+    for (int v = 0; v < threads / 32; ++v) {
+        if (v < warp) s.before += mem[v];
+        s.total += mem[v];
+    }
+    return s;
+}
 
 // One piece of work: units u0 .. u1 - 1 of an item's `units`.
 struct Piece {
     int b, len, head, row0, rows;  // first query row of the item and how many it has
-    int u0, u1, units;
+    uint32_t u0, u1, units;
     int last;  // keys that the last of its rows sees: no key at or after this one counts
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
 };
 __device__ __forceinline__ int seen(const Args &a, int len, int row) {
-    const int n = len - a.T + row / a.group + 1;
+    const int n = len - a.T + token_of(a, row) + 1;
     return n < 0 ? 0 : n;
 }
-__device__ __forceinline__ Piece piece_of(const Args &a, int b, int len, int item, int u0, int64_t left) {
-    Piece p;
-    p.b = b;
-    p.len = len;
-    p.units = units_of(len, a.unit);
-    p.u0 = u0;
-    p.u1 = left < p.units - u0 ? u0 + (int)left : p.units;
-    const int rb = item / a.cache.heads;
-    p.head = item - rb * a.cache.heads;
-    p.row0 = rb * a.rows;
-    const int all = a.T * a.group;
-    p.rows = all - p.row0 < a.rows ? all - p.row0 : a.rows;
-    p.last = seen(a, len, p.row0 + p.rows - 1);
-    return p;
-}
 
-// A worker's way through its share, piece by piece.
+// A worker's way through its share, piece by piece: items in the order (sequence, block of rows, key head).
 struct Walk {
-    int b, len, item, u0, next_len;  // next_len: of sequence b + 1, read ahead
-    int64_t left;
+    int b, len, rb, head;
+    uint32_t u0, left;
+    int next_len;  // of sequence b + 1, read ahead
     __device__ __forceinline__ void read_ahead(const Args &a) { next_len = b + 1 < a.B ? cache_len(a.cache, b + 1) : 0; }
-    __device__ __forceinline__ Piece piece(const Args &a) const { return piece_of(a, b, len, item, u0, left); }
-    __device__ __forceinline__ void step(const Args &a, const Piece &p) {
-        left -= p.u1 - p.u0;
+    __device__ __forceinline__ Piece piece(const Args &a) const {
+        Piece p;
+        p.b = b;
+        p.len = len;
+        p.units = units_of(a, len);
+        p.u0 = u0;
+        p.u1 = left < p.units - u0 ? u0 + left : p.units;
+        p.head = head;
+        p.row0 = rb * a.rows;
+        const int all = a.T * a.group;
+        p.rows = all - p.row0 < a.rows ? all - p.row0 : a.rows;
+        p.last = seen(a, len, p.row0 + p.rows - 1);
+        return p;
+    }
+    __device__ __forceinline__ void step(const Args &a, uint32_t done) {
+        left -= done;
         u0 = 0;
-        if (++item == a.per_seq) {
-            item = 0;
-            ++b;
-            len = next_len;
-            read_ahead(a);
-        }
+        if (++head < a.cache.heads) return;
+        head = 0;
+        if (++rb < a.row_blocks) return;
+        rb = 0;
+        ++b;
+        len = next_len;
+        read_ahead(a);
     }
 };
-// The start of every warp's share; `mem`: 2 kWarps int64 each. Ends with a barrier; `left` 0: no share.
-__device__ __forceinline__ Walk find_walk(const Args &a, int64_t *mem) {
-    Scan<kThreads> sc;
-    sc.run(a, mem);
-    const int n = sharers(a, sc.total), w0 = blockIdx.x * kWarps;
-    int64_t *found = mem + kWarps;  // [kWarps]: sequence in the upper half, and (u0 + units * item) fits the lower
-    int64_t *rest = found + kWarps;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-        if (w0 + v >= n) break;
-        const int64_t at = share(sc.total, w0 + v, n);
-        if (at >= sc.before && at < sc.before + sc.sum) {  // one thread's
+// The start of every warp's share; `mem`: 3 kWarps ints. Ends with a barrier; `left` 0: no share.
+__device__ __forceinline__ Walk find_walk(const Args &a, uint32_t *mem) {
+    const Scan sc = scan_sequences(a, mem);
+    const Deal deal(a, sc.total);
+    const uint32_t w0 = blockIdx.x * kWarps;
+    uint32_t *found = mem + kWarps, *rest = found + kWarps;
+#pragma unroll 1
+    for (uint32_t v = 0; v < kWarps && w0 + v < deal.n; ++v) {
+        const uint32_t at = deal.start(w0 + v);
+        if (at - sc.before < sc.sum) {  // one thread's
             int b = sc.first;
-            int64_t before = sc.before;
+            uint32_t before = sc.before;
+#pragma unroll 1
             for (;;) {
-                const int64_t x = (int64_t)units_of(cache_len(a.cache, b), a.unit) * a.per_seq;
-                if (at < before + x) break;
+                const uint32_t x = units_of(a, cache_len(a.cache, b)) * a.per_seq;
+                if (at - before < x) break;
                 before += x;
                 ++b;
             }
@@ -146,30 +165,31 @@ __device__ __forceinline__ Walk find_walk(const Args &a, int64_t *mem) {
         }
     }
     __syncthreads();
-    const int v = threadIdx.x >> 5;
+    const uint32_t v = threadIdx.x >> 5;
     Walk k;
     k.left = 0;
-    k.b = k.len = k.item = k.u0 = k.next_len = 0;
-    if (w0 + v < n) {
-        k.left = share(sc.total, w0 + v + 1, n) - share(sc.total, w0 + v, n);
+    k.b = k.len = k.rb = k.head = k.u0 = k.next_len = 0;
+    if (w0 + v < deal.n) {
+        k.left = deal.start(w0 + v + 1) - deal.start(w0 + v);
         k.b = (int)found[v];
         k.len = cache_len(a.cache, k.b);
-        const int units = units_of(k.len, a.unit);
-        k.item = (int)(rest[v] / units);
-        k.u0 = (int)(rest[v] - (int64_t)k.item * units);
+        const uint32_t units = units_of(a, k.len), item = rest[v] / units;
+        k.rb = (int)(item / a.cache.heads);
+        k.head = (int)item - k.rb * a.cache.heads;
+        k.u0 = rest[v] - item * units;
         k.read_ahead(a);
     }
     return k;
 }
-constexpr int kPlanBytes = 3 * kWarps * 8;
+constexpr int kPlanBytes = 4 * kWarps * 4;
 
 // Offsets (elements) of a query row in q, and of its row in o and lse.
 __device__ __forceinline__ int64_t q_at(const Args &a, const Piece &p, int r) {
-    const int row = p.row0 + r, t = row / a.group;
+    const int row = p.row0 + r, t = token_of(a, row);
     return ((int64_t)p.b * a.T + t) * a.q_stride + (int64_t)(p.head * a.group + row - t * a.group) * a.cache.D;
 }
 __device__ __forceinline__ int64_t out_row(const Args &a, const Piece &p, int r) {
-    const int row = p.row0 + r, t = row / a.group;
+    const int row = p.row0 + r, t = token_of(a, row);
     return ((int64_t)p.b * a.T + t) * a.Hq + p.head * a.group + row - t * a.group;
 }
 // A worker's scratch for a piece: the first when the item began before, the second when it goes on (or both).
@@ -194,67 +214,78 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// The stream of a worker's keys and values, through a ring of STAGES slots of shared memory. A slot holds a unit: KEYS rows of K
-// and of V, kPitch bytes each, 16-byte chunk c of row r at chunk c ^ (r & 7): 8 rows at one chunk lie in
-// different banks. Rows that no query of the piece sees, or without a page, are zeros. It runs ahead of the
-// computation over the borders of pieces. The page of a row is read from the table two units before its copies are
-// issued, and the rows' exponent bytes one unit before, so that neither is waited for.
-template <typename C, int DP, int KEYS, int STAGES>
+// The stream of a worker's keys and values, through a ring of SLOTS slots of shared memory: K of a unit, V of it, K of the
+// next one, and so on, so that half a unit is enough to keep and the rest of the ring is on its way. A slot holds KEYS
+// rows of kPitch bytes, 16-byte chunk c of row r at chunk c ^ (r & 7): 8 rows at one chunk lie in different banks.
+// Rows that no query of the piece sees, or without a page, are zeros. The stream runs ahead of the computation over the
+// borders of pieces. The page of a row is read from the table two units before its copies are issued, and the rows'
+// exponent bytes one unit before, so that neither is waited for.
+template <typename C, int DP, int KEYS, int SLOTS>
 struct Stream {
     static constexpr int kPitch = DP * (int)sizeof(C) < 128 ? 128 : DP * (int)sizeof(C);
-    static constexpr int kHalf = KEYS * kPitch;  // K or V of a slot
-    static constexpr int kBytes = STAGES * 2 * kHalf;
-    static constexpr int kScaleBytes = STAGES * 2 * KEYS;
-    static constexpr int kChunks = kPitch / 16;            // of a row
-    static constexpr int kTurns = KEYS * kChunks / 32;     // copies of a lane for KEYS rows
+    static constexpr int kSlot = KEYS * kPitch;
+    static constexpr int kBytes = SLOTS * kSlot;
+    static constexpr int kUnits = SLOTS / 2 + 2;  // whose exponent bytes may be held at a time
+    static constexpr int kScaleBytes = sizeof(C) == 1 ? kUnits * 2 * KEYS : 0;
+    static constexpr int kChunks = kPitch / 16;         // of a row
+    static constexpr int kTurns = KEYS * kChunks / 32;  // copies of a lane for KEYS rows
     static constexpr bool kScaled = sizeof(C) == 1;
 
     const Args &a;
-    uint32_t ring;         // shared address
-    uint8_t *scales;       // [STAGES][2][KEYS] exponent bytes
+    uint32_t ring;           // shared address
+    uint8_t *scales;         // [kUnits][2][KEYS] exponent bytes
     int lane;
-    Walk walk;             // of the unit that is looked up next
-    Piece p;
-    int u;
-    int entry, place;      // of this lane's row (lane % KEYS), looked up: the table's entry, the row within the page and head (-1: none)
-    int row;               // and of the unit before that: the row of the cache (-1: zeros)
-    uint32_t sk, sv;       // its exponent bytes
+    Walk walk;               // of the unit that is looked up next
+    uint32_t u, u1;          // that unit, and where its piece ends
+    int last;                // keys of its piece that count
+    int entry, place;        // of this lane's row (lane % KEYS), looked up: the table's entry, the row within the page and head (-1: none)
+    int row;                 // and of the unit that is copied next: the row of the cache (-1: zeros)
+    uint32_t sk, sv;         // its exponent bytes
+    int slot, unit_in, unit_out;  // the oldest slot, and where exponent bytes are written and read
 
     __device__ __forceinline__ Stream(const Args &a_, unsigned char *mem, uint8_t *sc, int lane_, const Walk &w)
-        : a(a_), ring(smem_u32(mem)), scales(sc), lane(lane_), walk(w), sk(0), sv(0) {
-        if (walk.left > 0) {
-            p = walk.piece(a);
-            u = p.u0;
+        : a(a_), ring(smem_u32(mem)), scales(sc), lane(lane_), walk(w), sk(0), sv(0), slot(0), unit_in(0), unit_out(0) {
+        enter();
+        place = -1;
+        // one unit looked up, then one resolved and the next looked up; then the slots in order
+#pragma unroll 1
+        for (int i = -2; i < SLOTS; ++i) {
+            if (i < 0 || (i & 1)) {
+                if (i > 0) copy_rows(a.cache.v, i);
+                resolve();
+                look();
+            } else {
+                fetch_k(i);
+            }
         }
-        look();
-        resolve();
-        look();
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    }
+    __device__ __forceinline__ void enter() {
+        if (walk.left == 0) return;
+        const Piece p = walk.piece(a);
+        u = p.u0;
+        u1 = p.u1;
+        last = p.last;
     }
     __device__ __forceinline__ void look() {
         place = -1;
-        if (walk.left <= 0) return;
-        const int pos = u * KEYS + (lane & (KEYS - 1));
-        if (pos < p.last) {
-            int at, slot;
-            cache_split(a.cache, pos, at, slot);
-            entry = a.cache.table[(int64_t)p.b * a.cache.table_stride + at];
-            place = p.head * a.cache.page + slot;
+        if (walk.left == 0) return;
+        const int pos = (int)u * KEYS + (lane & (KEYS - 1));
+        if (pos < last) {
+            int at, s;
+            cache_split(a.cache, pos, at, s);
+            entry = a.cache.table[(int64_t)walk.b * a.cache.table_stride + at];
+            place = walk.head * a.cache.page + s;
         }
-        if (++u == p.u1) {
-            walk.step(a, p);
-            if (walk.left > 0) {
-                p = walk.piece(a);
-                u = p.u0;
-            }
+        if (++u == u1) {
+            walk.step(a, u1 - walk.u0);
+            enter();
         }
     }
     __device__ __forceinline__ void resolve() {
         row = -1;
         if (place < 0) return;
         if ((unsigned)entry < (unsigned)a.cache.pages) {
-            row = (int)((int64_t)entry * a.cache.page_rows) + place;
+            row = entry * (int)a.cache.page_rows + place;
             if constexpr (kScaled) {
                 const int64_t x = (int64_t)entry * a.cache.scale_stride + place;
                 sk = a.cache.ks[x];
@@ -264,41 +295,53 @@ struct Stream {
             atomicOr(a.cache.err, kDeviceErrCache);
         }
     }
-    __device__ __forceinline__ void fetch(int slot) {
-        const int width = a.cache.D * (int)sizeof(C);
-        const uint32_t to = ring + slot * 2 * kHalf;
+    __device__ __forceinline__ void copy_rows(const void *base, int to_slot) {
+        const uint32_t to = ring + to_slot * kSlot;
+        const uint32_t width = a.cache.D * (uint32_t)sizeof(C);
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
             const int r = kChunks <= 32 ? i * (32 / kChunks) + lane / kChunks : i / (kChunks / 32);
             const int c = kChunks <= 32 ? lane % kChunks : (i % (kChunks / 32)) * 32 + lane;
             const int from = __shfl_sync(0xffffffffu, row, r);
-            const bool ok = from >= 0 && c * 16 < width;
-            const int64_t byte = ok ? (int64_t)from * width + c * 16 : 0;
-            const uint32_t at = to + r * kPitch + ((c ^ (r & 7)) << 4);
-            copy16(at, static_cast<const char *>(a.cache.k) + byte, ok);
-            copy16(at + kHalf, static_cast<const char *>(a.cache.v) + byte, ok);
+            const bool ok = from >= 0 && c * 16u < width;
+            copy16(to + r * kPitch + ((c ^ (r & 7)) << 4), static_cast<const char *>(base) + (uint64_t)(uint32_t)(ok ? from : 0) * width + (ok ? c * 16u : 0u), ok);
         }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+    __device__ __forceinline__ void fetch_k(int to_slot) {
+        copy_rows(a.cache.k, to_slot);
         if constexpr (kScaled) {
-            uint8_t *x = scales + slot * 2 * KEYS;
+            uint8_t *x = scales + unit_in * 2 * KEYS;
             if (lane < KEYS) {
                 x[lane] = (uint8_t)sk;
                 x[KEYS + lane] = (uint8_t)sv;
             }
+            unit_in = unit_in == kUnits - 1 ? 0 : unit_in + 1;
         }
-        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+    __device__ __forceinline__ void fetch_v(int to_slot) {
+        copy_rows(a.cache.v, to_slot);
         resolve();
         look();
     }
-    // The oldest slot on its way is complete and seen by the warp.
+    // The oldest slot is complete and seen by the warp.
     __device__ __forceinline__ void ready() {
-        copies_wait<STAGES - 2>();
+        copies_wait<SLOTS - 1>();
         __syncwarp();
     }
-    // The warp is done with slot `slot`, the oldest: the next unit goes into the one before it. Returns the new oldest.
-    __device__ __forceinline__ int next(int slot) {
+    // Shared address of the oldest slot; the exponent bytes of the oldest unit.
+    __device__ __forceinline__ uint32_t oldest() const { return ring + slot * kSlot; }
+    __device__ __forceinline__ const uint8_t *bytes() const { return scales + unit_out * 2 * KEYS; }
+    // The warp is done with the oldest slot, K or V (`V`): what comes SLOTS slots later goes into it.
+    template <bool V>
+    __device__ __forceinline__ void release() {
         __syncwarp();
-        fetch(slot == 0 ? STAGES - 1 : slot - 1);
-        return slot == STAGES - 1 ? 0 : slot + 1;
+        if constexpr (V == (SLOTS % 2 == 0))
+            fetch_v(slot);
+        else
+            fetch_k(slot);
+        slot = slot == SLOTS - 1 ? 0 : slot + 1;
+        if constexpr (V) unit_out = unit_out == kUnits - 1 ? 0 : unit_out + 1;
     }
 };
 

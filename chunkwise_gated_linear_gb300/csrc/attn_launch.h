@@ -8,14 +8,14 @@
 namespace kda {
 namespace attn {
 
-// Query rows of an item for `all` rows of a sequence and key head, keys of a unit, blocks on an SM, and the launch, of the
+// Query rows of an item for `all` rows of a sequence and key head, keys of a unit (its power of two), blocks on an SM, and the launch, of the
 // kernel for fp32 data and of that for bf16.
 int fma_rows(int all, int D);
-int fma_unit(const Args &a);
+int fma_unit_shift(const Args &a);
 int fma_blocks(const Args &a);
 cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream);
 int mma_rows(int all, int D);
-int mma_unit(const Args &a);
+int mma_unit_shift(const Args &a);
 int mma_blocks(const Args &a);
 cudaError_t launch_attn_mma(const Args &a, cudaStream_t stream);
 

@@ -24,7 +24,7 @@ struct Cache {
     const int32_t *lens;
     int pages, heads, page, D, max_pages;
     int shift;       // page == 1 << shift, or -1
-    int most;        // max_pages * page, at most INT_MAX
+    int most;        // max_pages * page, at most 2^31 - 65 (sums with a few more stay in range)
     unsigned int *err;
 };
 
@@ -129,7 +129,7 @@ inline Cache cache_args(const kda_kv_cache &c, unsigned int *err) {
     for (int s = 0; s < 31; ++s)
         if (c.page_size == 1 << s) a.shift = s;
     const int64_t most = (int64_t)c.max_pages * c.page_size;
-    a.most = (int)(most > INT32_MAX ? INT32_MAX : most);
+    a.most = (int)(most > INT32_MAX - 64 ? INT32_MAX - 64 : most);
     a.err = err;
     return a;
 }

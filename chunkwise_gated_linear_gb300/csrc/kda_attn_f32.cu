@@ -30,9 +30,9 @@ __device__ __forceinline__ float elem(const uint8_t *p) {
     return lo;
 }
 
-template <typename C, int DP, int RB, int KEYS, int STAGES>
+template <typename C, int DP, int RB, int KEYS, int SLOTS>
 struct Fma {
-    using S = Stream<C, DP, KEYS, STAGES>;
+    using S = Stream<C, DP, KEYS, SLOTS>;
     static constexpr int kParts = 32 / KEYS;
     static constexpr int kE = 16 / (int)sizeof(C);
     static constexpr int kCols = DP / 32;
@@ -44,17 +44,18 @@ struct Fma {
     static constexpr int kSc = kPlan + kPlanBytes;
     static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
-    static constexpr int kBlocks = (228 * 1024) / (kSmem + 1024) < 2 ? 1 : 2;
+    static constexpr int kFit = (228 * 1024) / (kSmem + 1024);
+    static constexpr int kBlocks = kFit < 2 ? 1 : RB > 4 || kFit == 2 ? 2 : 3;
 };
 
-template <typename C, int DP, int RB, int KEYS, int STAGES>
-__global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlocks) attn_fma_kernel(const __grid_constant__ Args a) {
-    using F = Fma<C, DP, RB, KEYS, STAGES>;
+template <typename C, int DP, int RB, int KEYS, int SLOTS>
+__global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks) attn_fma_kernel(const __grid_constant__ Args a) {
+    using F = Fma<C, DP, RB, KEYS, SLOTS>;
     extern __shared__ __align__(128) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     launch_dependents();
-    Walk walk = find_walk(a, reinterpret_cast<int64_t *>(mem + F::kPlan));
-    if (walk.left <= 0) return;
+    Walk walk = find_walk(a, reinterpret_cast<uint32_t *>(mem + F::kPlan));
+    if (walk.left == 0) return;
     float *qs = reinterpret_cast<float *>(mem + F::kQ) + warp * RB * DP;
     float *pw = reinterpret_cast<float *>(mem + F::kP) + warp * KEYS * RB;
     int *lim = reinterpret_cast<int *>(mem + F::kLim) + warp * RB;
@@ -63,9 +64,10 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlock
     const int D = a.cache.D, key = lane & (KEYS - 1), part = lane / KEYS;
     const int cpr = D * (int)sizeof(C) / 16;
 
-    int slot = 0;
+#pragma unroll 1
     while (walk.left > 0) {
         const Piece p = walk.piece(a);
+#pragma unroll 1
         for (int r = 0; r < p.rows; ++r) {
             const float *from = static_cast<const float *>(a.q) + q_at(a, p, r);
             for (int d = lane; d < DP; d += 32) qs[r * DP + d] = d < D ? from[d] * a.scale_log2 : 0.f;
@@ -81,15 +83,17 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlock
 #pragma unroll
             for (int j = 0; j < F::kCols; ++j) acc[r][j] = 0.f;
         }
-        for (int u = p.u0; u < p.u1; ++u) {
+#pragma unroll 1
+        for (uint32_t u = p.u0; u < p.u1; ++u) {
+            const int pos0 = (int)u * KEYS;
             st.ready();
-            const unsigned char *ks = own + slot * 2 * F::S::kHalf, *vs = ks + F::S::kHalf;
-            const uint8_t *sc = st.scales + slot * 2 * KEYS;
-            const int pos0 = u * KEYS;
             if (pos0 < p.last) {  // the same for the whole warp
+                const unsigned char *ks = own + st.slot * F::S::kSlot;
+                const uint8_t *sc = st.bytes();
                 float x[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) x[r] = 0.f;
+#pragma unroll 1
                 for (int c = part; c < cpr; c += F::kParts) {
                     float kf[F::kE];
                     unpack16<C>(kf, *reinterpret_cast<const uint4 *>(ks + key * F::S::kPitch + ((c ^ (key & 7)) << 4)));
@@ -141,6 +145,11 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlock
 #pragma unroll
                         for (int j = 0; j < F::kCols; ++j) acc[r][j] *= alpha[r];
                 }
+            }
+            st.template release<false>();
+            st.ready();
+            if (pos0 < p.last) {
+                const unsigned char *vs = own + st.slot * F::S::kSlot;
                 const bool edge = pos0 + KEYS > least;
 #pragma unroll 2
                 for (int k = 0; k < KEYS; ++k) {
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlock
                     }
                 }
             }
-            slot = st.next(slot);
+            st.template release<true>();
         }
         float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
 #pragma unroll
@@ -185,27 +194,27 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, STAGES>::kBlock
             }
         }
         __syncwarp();
-        walk.step(a, p);
+        walk.step(a, p.u1 - p.u0);
     }
     copies_wait<0>();
 }
 
-template <typename C, int DP, int RB, int KEYS, int STAGES>
+template <typename C, int DP, int RB, int KEYS, int SLOTS>
 struct Variant {
-    using F = Fma<C, DP, RB, KEYS, STAGES>;
+    using F = Fma<C, DP, RB, KEYS, SLOTS>;
     static cudaError_t launch(const Args &a, cudaStream_t stream) {
-        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, STAGES>, F::kSmem>(a, stream);
+        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, SLOTS>, F::kSmem>(a, stream);
     }
     static int blocks() { return F::kBlocks; }
     static int unit() { return KEYS; }
 };
-// Calls f with the variant for these sizes: rings that fill the shared memory of an SM, in one block or two.
+// Calls f with the variant for these sizes: rings that fill the shared memory of an SM, in one to three blocks.
 template <typename C, int RB, typename F>
 auto pick(const Args &a, F f) {
     constexpr bool k4 = sizeof(C) == 4;
-    if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16, 3>{});
-    if (a.cache.D <= 128) return f(Variant<C, 128, RB, k4 ? 8 : 16, k4 && RB == 16 ? 5 : 3>{});
-    return f(Variant<C, 256, RB == 16 ? 8 : RB, k4 ? 8 : 16, 3>{});
+    if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16, 6>{});
+    if (a.cache.D <= 128) return f(Variant<C, 128, RB, k4 ? 8 : 16, 5>{});
+    return f(Variant<C, 256, RB == 16 ? 8 : RB, k4 ? 8 : 16, 5>{});
 }
 template <typename F>
 auto pick(const Args &a, F f) {
@@ -216,8 +225,8 @@ auto pick(const Args &a, F f) {
 }  // namespace
 
 int fma_rows(int all, int D) { return all <= 4 ? 4 : D > 128 ? 8 : 16; }
-int fma_unit(const Args &a) {
-    return pick(a, [](auto v) { return decltype(v)::unit(); });
+int fma_unit_shift(const Args &a) {
+    return pick(a, [](auto v) { return decltype(v)::unit() == 16 ? 4 : 3; });
 }
 int fma_blocks(const Args &a) {
     return pick(a, [](auto v) { return decltype(v)::blocks(); });

@@ -12,7 +12,10 @@
 // (one conversion per two numbers; widening to bf16 takes four to five instructions). Q goes to fp16 times a power of two per
 // row that puts its largest entry at 2^14: entries down to 2^-28 of it stay exact. The power of two of a key multiplies
 // its scores, that of a value its probability: P' = 2^(score + sv - M) with a reference M of its own, between 2^-24 and
-// 2^14 in fp16 (11 bits), while the sum l keeps the plain 2^(score - m).
+// 2^14 in fp16 (11 bits), while the sum l keeps the plain 2^(score - m). Both references are watched by one
+// comparison per score, with min(m + 2^8, M's border - the largest sv so far).
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "attn_launch.h"
 
@@ -20,7 +23,8 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr float kGrow = 8.f;  // scores may pass their reference by 2^kGrow before it moves
+constexpr float kGrow = 8.f;  // a score may pass its reference by so much before it moves: exponentials up to 2^8
+constexpr float kMost = 14.f;  // 8-bit: P' up to 2^14, within fp16
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -58,73 +62,103 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return d;
 }
 
-template <typename C, int DP, int NT, int STAGES>
+template <typename C, int DP, int NT, int SLOTS>
 struct Mma {
     static constexpr bool kScaled = sizeof(C) == 1;
-    // blocks of 16 keys in a unit: two of 8-bit values, where the registers hold the scores of both beside O^T
-    static constexpr int kHalves = kScaled && DP * NT <= 256 ? 2 : 1;
-    static constexpr int kKeys = 16 * kHalves;
-    using S = Stream<C, DP, kKeys, STAGES>;
+    static constexpr int kJoint = kScaled ? 2 : 1;  // blocks of 16 keys in a unit
+    static constexpr int kKeys = 16 * kJoint;
+    using S = Stream<C, DP, kKeys, SLOTS>;
     static constexpr int kSteps = DP / 16;  // products of S^T, and blocks of 16 channels of O^T
-    // shared memory: rings, the plan, exponent bytes
-    static constexpr int kPlan = kWarps * S::kBytes;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kQBytes = NT * kSteps * 256;  // Q^T of a warp: [NT][kSteps][32 lanes] of 8 bytes
+    static constexpr int kStats = 4 * kRows;           // floats of a warp: what a score is multiplied with, m, M, a factor
+    // shared memory: rings, Q^T, statistics, the plan, exponent bytes
+    static constexpr int kQ = kWarps * S::kBytes;
+    static constexpr int kStat = kQ + kWarps * kQBytes;
+    static constexpr int kPlan = kStat + kWarps * kStats * 4;
     static constexpr int kSc = kPlan + kPlanBytes;
     static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
     static constexpr int kFit = (228 * 1024) / (kSmem + 1024);
-    // registers: O^T and Q^T alone are (4 + 2) kSteps NT of a lane's
-    static constexpr int kLive = 6 * kSteps * NT + 90;
+    // registers: O^T is 4 kSteps NT of a lane's, the scores 4 kJoint NT
+    static constexpr int kLive = 4 * kSteps * NT + 4 * kJoint * NT + 8 * NT + 72;
     static constexpr int kByRegs = 65536 / (kThreads * (kLive < 96 ? 96 : kLive > 255 ? 255 : kLive));
     static constexpr int kBlocks = kFit < kByRegs ? kFit : kByRegs;
 };
 
-template <typename C, int DP, int NT, int STAGES>
-__global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) attn_mma_kernel(const __grid_constant__ Args a) {
-    using M = Mma<C, DP, NT, STAGES>;
+// The largest of each of 2 NT values over the 8 lanes g: of value i it ends in the lanes with i in the upper bits of g (lane
+// bits 4, 3, 2). Half of the values go to the other lane in each step, while there are two or more.
+template <int N>
+__device__ __forceinline__ float spread_max(float (&v)[N], int lane) {
+    int n = N;
+#pragma unroll
+    for (int bit = 16; bit >= 4; bit >>= 1) {
+        const bool up = lane & bit;
+        if (n > 1) {
+            n /= 2;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+                }
+        } else {
+            v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+        }
+    }
+    return v[0];
+}
+
+// What is done once per piece is kept short (loops, statistics in shared memory while they change): code that runs once
+// is bound by fetching it, about 40 cycles for an instruction (16 sequences with four drafted tokens each: 119 us
+// with everything unrolled).
+template <typename C, int DP, int NT, int SLOTS>
+__global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn_mma_kernel(const __grid_constant__ Args a) {
+    using M = Mma<C, DP, NT, SLOTS>;
     using S = typename M::S;
-    constexpr int kSteps = M::kSteps, kHalves = M::kHalves, kKeys = M::kKeys;
+    constexpr int kSteps = M::kSteps, kJoint = M::kJoint, kKeys = M::kKeys, kRows = M::kRows;
     extern __shared__ __align__(1024) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     launch_dependents();
-    Walk walk = find_walk(a, reinterpret_cast<int64_t *>(mem + M::kPlan));
-    if (walk.left <= 0) return;
+    Walk walk = find_walk(a, reinterpret_cast<uint32_t *>(mem + M::kPlan));
+    if (walk.left == 0) return;
     unsigned char *own = mem + warp * S::kBytes;
     S st(a, own, mem + M::kSc + warp * S::kScaleBytes, lane, walk);
+    uint2 *qmem = reinterpret_cast<uint2 *>(mem + M::kQ + warp * M::kQBytes) + lane;  // [NT][kSteps], 32 apart
+    // of each row: what its scores are multiplied with, the references m and M, the factor of the last move
+    float *stats = reinterpret_cast<float *>(mem + M::kStat) + warp * M::kStats;
+    float *row_m = stats + kRows, *row_mv = row_m + kRows, *row_back = row_mv + kRows;
     const int D = a.cache.D;
+    // the row whose statistics this lane moves: of value i = 2 n + j, in the order of spread_max
+    const int my_i = g >> (NT == 4 ? 0 : NT == 2 ? 1 : 2), my_row = 8 * (my_i >> 1) + 2 * c + (my_i & 1);
 
-    int slot = 0;
+#pragma unroll 1
     while (walk.left > 0) {
         const Piece p = walk.piece(a);
         // Q^T: row 8 n + g, the lane's channels of each block of 16 in the order in which K's come out of the ring
-        uint32_t q[NT][kSteps][2];
-        float rowf[NT][2];  // what a score of rows 8 n + 2 c, + 1 is multiplied with
-#pragma unroll
+#pragma unroll 1
         for (int n = 0; n < NT; ++n) {
             const bool there = 8 * n + g < p.rows;
-            const bf16 *from = static_cast<const bf16 *>(a.q) + (there ? q_at(a, p, 8 * n + g) : 0);
-            float top = 0.f;
+            const bf16 *from = static_cast<const bf16 *>(a.q) + (there ? q_at(a, p, 8 * n + g) : 0) + (M::kScaled ? 4 * c : 2 * c);
+            uint2 x[kSteps];
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                q[n][k][0] = q[n][k][1] = 0u;
+                x[k] = make_uint2(0u, 0u);
                 if (there && 16 * k < D) {
-                    if constexpr (M::kScaled) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(from + 16 * k + 4 * c);
-                        q[n][k][0] = x.x;
-                        q[n][k][1] = x.y;
-                    } else {
-                        q[n][k][0] = *reinterpret_cast<const uint32_t *>(from + 16 * k + 2 * c);
-                        q[n][k][1] = *reinterpret_cast<const uint32_t *>(from + 16 * k + 2 * c + 8);
-                    }
+                    if constexpr (M::kScaled)
+                        x[k] = *reinterpret_cast<const uint2 *>(from + 16 * k);
+                    else
+                        x[k] = make_uint2(*reinterpret_cast<const uint32_t *>(from + 16 * k), *reinterpret_cast<const uint32_t *>(from + 16 * k + 8));
                 }
             }
+            float by = a.scale_log2;
             if constexpr (M::kScaled) {
+                float top = 0.f;
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        top = fmaxf(top, finite_abs(__uint_as_float(q[n][k][i] << 16)));
-                        top = fmaxf(top, finite_abs(__uint_as_float(q[n][k][i] & 0xffff0000u)));
-                    }
+                for (int k = 0; k < kSteps; ++k) {
+                    top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(x[k].x << 16)), finite_abs(__uint_as_float(x[k].x & 0xffff0000u))));
+                    top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(x[k].y << 16)), finite_abs(__uint_as_float(x[k].y & 0xffff0000u))));
+                }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // 2^e with the largest entry at 2^14 .. 2^15, within what fp32 holds
@@ -132,308 +166,378 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, STAGES>::kBlocks) att
                 e = e > 126 ? 126 : e;
                 const float up = pow2(e);
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        q[n][k][i] = pack_f16(__uint_as_float(q[n][k][i] << 16) * up, __uint_as_float(q[n][k][i] & 0xffff0000u) * up);
-                const float down = a.scale_log2 * pow2(-e);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) rowf[n][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
-            } else {
-                rowf[n][0] = rowf[n][1] = a.scale_log2;
+                for (int k = 0; k < kSteps; ++k) {
+                    x[k].x = pack_f16(__uint_as_float(x[k].x << 16) * up, __uint_as_float(x[k].x & 0xffff0000u) * up);
+                    x[k].y = pack_f16(__uint_as_float(x[k].y << 16) * up, __uint_as_float(x[k].y & 0xffff0000u) * up);
+                }
+                by *= pow2(-e);
             }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) qmem[(n * kSteps + k) * 32] = x[k];
+            if (c == 0) stats[8 * n + g] = by;
         }
         const int least = seen(a, p.len, p.row0);  // keys from here on are not seen by all rows
+        __syncwarp();
 
         float o[kSteps][NT][4];
-        float m[NT][2], l[NT][2], big[NT][2];  // reference of the exponentials, their sum, where the reference moves
-        float mv[NT][2], bigv[NT][2];          // 8-bit: the reference M of P', where it moves
-        float turn[NT][2];                     // 8-bit: 2^(m - M)
+        // of rows 8 n + 2 c, + 1: factor of the scores, -m, the sum of the exponentials, 8-bit: 2^(m - M); the score at which m
+        // or M moves (-infinity: nothing seen yet)
+        f2 rowf[NT], ref[NT], l[NT], turn[NT];
+        float lim[NT][2];
+        float sv_top = -127.f;      // 8-bit: the largest exponent of a value so far
+        bool nothing = true;        // of this lane's row my_row: nothing seen yet
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                m[n][j] = mv[n][j] = l[n][j] = 0.f;
-                turn[n][j] = 1.f;
-                big[n][j] = bigv[n][j] = -INFINITY;
-            }
+            const float2 by = *reinterpret_cast<const float2 *>(stats + 8 * n + 2 * c);
+            rowf[n] = pk(by.x, by.y);
+            ref[n] = l[n] = pk(0.f, 0.f);
+            turn[n] = pk(1.f, 1.f);
+            lim[n][0] = lim[n][1] = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[k][n][i] = 0.f;
         }
-
-        for (int u = p.u0; u < p.u1; ++u) {
-            st.ready();
-            const int pos0 = u * kKeys;
-            if (pos0 < p.last) {  // the same for the whole warp
-                const uint32_t ks = st.ring + slot * 2 * S::kHalf, vs = ks + S::kHalf;
-                // scores, base 2; element i of half h: key 16 h + g + 8 (i / 2), row 8 n + 2 c + i % 2
-                float x[kHalves][NT][4];
+        float my_m = 0.f, my_mv = 0.f;
+        // the borders of all rows from the references, after those or sv_top have moved
+        auto borders = [&](bool moved) {
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h)
+            for (int n = 0; n < NT; ++n) {
+                const float2 m2 = *reinterpret_cast<const float2 *>(row_m + 8 * n + 2 * c);
+                if (moved) ref[n] = pk(m2.x == -INFINITY ? 0.f : -m2.x, m2.y == -INFINITY ? 0.f : -m2.y);
+                lim[n][0] = m2.x + kGrow;
+                lim[n][1] = m2.y + kGrow;
+                if constexpr (M::kScaled) {
+                    const float2 v2 = *reinterpret_cast<const float2 *>(row_mv + 8 * n + 2 * c);
+                    lim[n][0] = fminf(lim[n][0], v2.x + kMost - sv_top);
+                    lim[n][1] = fminf(lim[n][1], v2.y + kMost - sv_top);
+                    if (moved) turn[n] = pk(m2.x == -INFINITY ? 1.f : tc5::ex2(m2.x - v2.x), m2.y == -INFINITY ? 1.f : tc5::ex2(m2.y - v2.y));
+                }
+            }
+        };
+        if (lane < kRows) {
+            row_m[lane] = -INFINITY;
+            row_mv[lane] = 0.f;
+        }
+
+#pragma unroll 1
+        for (uint32_t u = p.u0; u < p.u1; ++u) {
+            st.ready();
+            const int pos0 = (int)u * kKeys;
+            const bool count = pos0 < p.last;  // the same for the whole warp
+            float x[kJoint][NT][4];
+            if (count) {
+                const uint32_t krow = st.oldest() + (lane & 15) * S::kPitch;
+#pragma unroll
+                for (int h = 0; h < kJoint; ++h)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[h][n][i] = 0.f;
-                const uint32_t krow = ks + (lane & 15) * S::kPitch;
+                // few rows: sums of even and odd steps, so that half as many products wait for one another
+                constexpr bool kTwo = NT * kJoint == 1;
+                float x2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < kSteps; k += M::kScaled ? 2 : 1) {
+                    uint32_t f[kJoint][M::kScaled ? 2 : 1][4];
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        uint32_t r[4];
+                    for (int h = 0; h < kJoint; ++h) {
                         if constexpr (M::kScaled) {
                             // 16-byte chunks k and k + 1 are channels 16 k .. 16 k + 31: keys g and g + 8, channels 4 c .. 4 c + 3 of each
+                            uint32_t r[4];
                             ldsm(r, krow + 16 * h * S::kPitch + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
-                            uint32_t f[4];
-                            widen(r[0], f[0], f[2]);
-                            widen(r[1], f[1], f[3]);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(x[h][n], f, q[n][k][0], q[n][k][1]);
-                            widen(r[2], f[0], f[2]);
-                            widen(r[3], f[1], f[3]);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(x[h][n], f, q[n][k + 1][0], q[n][k + 1][1]);
+                            widen(r[0], f[h][0][0], f[h][0][2]);
+                            widen(r[1], f[h][0][1], f[h][0][3]);
+                            widen(r[2], f[h][1][0], f[h][1][2]);
+                            widen(r[3], f[h][1][1], f[h][1][3]);
                         } else {
-                            ldsm(r, krow + 16 * h * S::kPitch + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_bf16(x[h][n], r, q[n][k][0], q[n][k][1]);
-                        }
-                    }
-                }
-                float fv[kHalves][2], ev[kHalves][2];  // 8-bit: the values' powers of two and their exponents
-                const bool edge = pos0 + kKeys > least;
-                bool grows = false;
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    float fk[2] = {1.f, 1.f};
-                    if constexpr (M::kScaled) {
-                        const uint8_t *sc = st.scales + slot * 2 * kKeys + 16 * h;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            fk[i] = __uint_as_float((uint32_t)sc[g + 8 * i] << 23);
-                            const uint32_t e = sc[kKeys + g + 8 * i];
-                            fv[h][i] = __uint_as_float(e << 23);
-                            ev[h][i] = (float)((int)e - 127);
+                            ldsm(f[h][0], krow + 16 * h * S::kPitch + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
                         }
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float &y = x[h][n][i];
-                            y *= M::kScaled ? rowf[n][i & 1] * fk[i >> 1] : rowf[n][i & 1];
-                            if (edge && pos0 + 16 * h + g + 8 * (i >> 1) >= seen(a, p.len, p.row0 + 8 * n + 2 * c + (i & 1))) y = -INFINITY;
-                            grows |= y > big[n][i & 1];
-                            if constexpr (M::kScaled) grows |= y + ev[h][i >> 1] > bigv[n][i & 1];
+                        for (int t = 0; t < (M::kScaled ? 2 : 1); ++t) {
+                            const uint2 qv = qmem[(n * kSteps + k + t) * 32];
+#pragma unroll
+                            for (int h = 0; h < kJoint; ++h) {
+                                if constexpr (M::kScaled)
+                                    mma_f16(x[h][n], f[h][t], qv.x, qv.y);
+                                else
+                                    mma_bf16(kTwo && (k & 1) ? x2 : x[h][n], f[h][t], qv.x, qv.y);
+                            }
                         }
                 }
-                if (__any_sync(0xffffffffu, grows)) {
+                if constexpr (kTwo) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[0][0][i] += x2[i];
+                }
+            }
+            st.template release<false>();
+            uint32_t pb[kJoint][NT][2];
+            bool edge = false;
+            if (count) {
+                // scores, base 2; element i of block h: key 16 h + g + 8 (i / 2), row 8 n + 2 c + i % 2
+                float fv[kJoint][2];  // 8-bit: the values' powers of two
+                edge = pos0 + kKeys > least;
+                if constexpr (M::kScaled) {
+                    const uint8_t *sc = st.bytes();
+                    // an exponent above all others moves the borders; keys that no row sees have old bytes or none, which only lower them
+                    const float top = (float)((int)__reduce_max_sync(0xffffffffu, (uint32_t)sc[kKeys + lane]) - 127);
+                    if (top > sv_top) {
+                        sv_top = top;
+                        borders(false);
+                    }
+#pragma unroll
+                    for (int h = 0; h < kJoint; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float fk = __uint_as_float((uint32_t)sc[16 * h + g + 8 * i] << 23);
+                            fv[h][i] = __uint_as_float((uint32_t)sc[kKeys + 16 * h + g + 8 * i] << 23);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                upk(mul2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), mul2(rowf[n], pk(fk, fk))), x[h][n][2 * i], x[h][n][2 * i + 1]);
+                        }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) upk(mul2(pk(x[0][n][2 * i], x[0][n][2 * i + 1]), rowf[n]), x[0][n][2 * i], x[0][n][2 * i + 1]);
+                }
+                if (edge) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float top = -INFINITY, topv = -INFINITY;
+                            const int end = seen(a, p.len, p.row0 + 8 * n + 2 * c + j) - pos0 - g;
 #pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                                for (int i = j; i < 4; i += 2) {
-                                    top = fmaxf(top, x[h][n][i]);
-                                    if constexpr (M::kScaled) topv = fmaxf(topv, x[h][n][i] + ev[h][i >> 1]);
-                                }
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) {
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                                if constexpr (M::kScaled) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-                            }
-                            // each reference moves up alone, never down; nothing seen yet: l and O are 0
-                            float back = 1.f;
-                            if (top > big[n][j] - kGrow) {
-                                back = big[n][j] == -INFINITY ? 0.f : tc5::ex2(m[n][j] - top);
-                                l[n][j] *= back;
-                                m[n][j] = top;
-                                big[n][j] = top + kGrow;
-                            }
-                            if constexpr (M::kScaled) {
-                                // the largest P' at 2^6, so that none passes 2^14; rows of zeros (sv = -126) alone leave it lower,
-                                // or 2^(m - M) would pass what fp32 holds
-                                const float tv = fmaxf(topv, bigv[n][j] - kGrow);
-                                const float to = fmaxf(tv - 6.f, m[n][j] - 120.f);
-                                back = 1.f;
-                                if (tv > -INFINITY) {
-                                    back = bigv[n][j] == -INFINITY ? 0.f : tc5::ex2(mv[n][j] - to);
-                                    mv[n][j] = to;
-                                    bigv[n][j] = tv + kGrow;
-                                }
-                                turn[n][j] = tc5::ex2(m[n][j] - mv[n][j]);
-                            }
-                            if (back != 1.f) {
-#pragma unroll
-                                for (int k = 0; k < kSteps; ++k) {
-                                    o[k][n][j] *= back;
-                                    o[k][n][j + 2] *= back;
-                                }
+                            for (int h = 0; h < kJoint; ++h) {
+                                if (end <= 16 * h) x[h][n][j] = -INFINITY;
+                                if (end <= 16 * h + 8) x[h][n][j + 2] = -INFINITY;
                             }
                         }
                 }
-                uint32_t pb[kHalves][NT][2];
+                bool grows = false;
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h)
+                for (int h = 0; h < kJoint; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) grows |= x[h][n][i] > lim[n][i & 1];
+                if (__any_sync(0xffffffffu, grows)) {
+                    // each reference moves up alone, never down; with nothing seen yet l and O are 0
+                    float v[2 * NT];
+#pragma unroll
+                    for (int i = 0; i < 2 * NT; ++i) {
+                        v[i] = fmaxf(x[0][i / 2][i & 1], x[0][i / 2][(i & 1) + 2]);
+                        if constexpr (kJoint == 2) v[i] = fmaxf(v[i], fmaxf(x[1][i / 2][i & 1], x[1][i / 2][(i & 1) + 2]));
+                    }
+                    const float top = spread_max(v, lane);
+                    float back = 1.f, back_l = 1.f;
+                    const bool first = nothing;
+                    if (first ? top > -INFINITY : top > my_m) {
+                        back_l = first ? 0.f : tc5::ex2(my_m - top);
+                        my_m = top;
+                        nothing = false;
+                    }
+                    back = back_l;
+                    if constexpr (M::kScaled) {
+                        float ev[kJoint][2];
+#pragma unroll
+                        for (int h = 0; h < kJoint; ++h)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) ev[h][i] = (float)((int)(__float_as_uint(fv[h][i]) >> 23) - 127);
+#pragma unroll
+                        for (int i = 0; i < 2 * NT; ++i) {
+                            v[i] = fmaxf(x[0][i / 2][i & 1] + ev[0][0], x[0][i / 2][(i & 1) + 2] + ev[0][1]);
+                            if constexpr (kJoint == 2) v[i] = fmaxf(v[i], fmaxf(x[1][i / 2][i & 1] + ev[1][0], x[1][i / 2][(i & 1) + 2] + ev[1][1]));
+                        }
+                        // the largest P' at 2^6, so that none passes 2^kMost soon; rows of zeros (sv = -126) alone leave it lower, or
+                        // 2^(m - M) would pass what fp32 holds
+                        float to = fmaxf(spread_max(v, lane) - 6.f, my_m - 120.f);
+                        back = 1.f;
+                        if (!nothing) {
+                            if (!first) to = fmaxf(to, my_mv);
+                            back = first ? 0.f : tc5::ex2(my_mv - to);
+                            my_mv = to;
+                        }
+                        row_mv[my_row] = my_mv;
+                        stats[my_row] = back_l;
+                    }
+                    row_m[my_row] = nothing ? -INFINITY : my_m;
+                    row_back[my_row] = back;
+                    __syncwarp();
+                    borders(true);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float &y = x[h][n][i];
-                            y = tc5::ex2(y - m[n][i & 1]);
-                            l[n][i & 1] += y;
-                            if constexpr (M::kScaled) y *= fv[h][i >> 1] * turn[n][i & 1];
+                        const float2 b2 = *reinterpret_cast<const float2 *>(row_back + 8 * n + 2 * c);
+                        const f2 f = pk(b2.x, b2.y);
+                        if constexpr (M::kScaled) {
+                            const float2 l2 = *reinterpret_cast<const float2 *>(stats + 8 * n + 2 * c);
+                            l[n] = mul2(l[n], pk(l2.x, l2.y));
+                        } else {
+                            l[n] = mul2(l[n], f);
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float lo = x[h][n][2 * i], hi = x[h][n][2 * i + 1];
-                            pb[h][n][i] = transpose8(M::kScaled ? pack_f16(lo, hi) : pack_bf16(lo, hi));
-                        }
+                        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) upk(mul2(pk(o[k][n][2 * i], o[k][n][2 * i + 1]), f), o[k][n][2 * i], o[k][n][2 * i + 1]);
                     }
-                if (edge && a.T > 1) {
-                    // Values that are not finite would reach rows that do not see them, as 0 * NaN: such keys' shares are added one by
-                    // one to the rows that do, and their values then count as zeros.
-                    unsigned char *vals = own + slot * 2 * S::kHalf + S::kHalf;
-                    uint32_t odd = 0;
-                    for (int r = 0; r < kKeys; ++r) {
-                        bool bad = false;
-                        for (int w = lane; w < S::kPitch / 4; w += 32) {
-                            const uint32_t v = *reinterpret_cast<const uint32_t *>(vals + r * S::kPitch + 4 * w);
-                            if constexpr (M::kScaled)
-                                bad |= (v & 0x7fu) == 0x7fu || (v >> 8 & 0x7fu) == 0x7fu || (v >> 16 & 0x7fu) == 0x7fu || (v >> 24 & 0x7fu) == 0x7fu;
-                            else
-                                bad |= (v & 0x7f80u) == 0x7f80u || (v >> 16 & 0x7f80u) == 0x7f80u;
-                        }
-                        if (__any_sync(0xffffffffu, bad)) odd |= 1u << r;
-                    }
-                    if (odd != 0) {
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h)
-#pragma unroll 1
-                            for (int r = 0; r < 16; ++r) {
-                                if ((odd >> (16 * h + r) & 1) == 0) continue;
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        const float lo = __shfl_sync(0xffffffffu, x[h][n][j], 4 * (r & 7) + c);
-                                        const float hi = __shfl_sync(0xffffffffu, x[h][n][j + 2], 4 * (r & 7) + c);
-                                        const float w = r < 8 ? lo : hi;
-                                        if (pos0 + 16 * h + r >= seen(a, p.len, p.row0 + 8 * n + 2 * c + j)) continue;
-#pragma unroll
-                                        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                                            for (int t = 0; t < 2; ++t) {
-                                                const int byte = (16 * k + (M::kScaled ? 2 * g + t : g + 8 * t)) * (int)sizeof(C);
-                                                const unsigned char *e = vals + (16 * h + r) * S::kPitch + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-                                                float v, no;
-                                                if constexpr (M::kScaled)
-                                                    e4m3_to_f(*e, v, no);
-                                                else
-                                                    v = to_f(*reinterpret_cast<const bf16 *>(e));
-                                                o[k][n][j + 2 * t] = fmaf(w, v, o[k][n][j + 2 * t]);
-                                            }
-                                    }
-                            }
-                        __syncwarp();
-                        for (int r = 0; r < kKeys; ++r)
-                            if (odd >> r & 1)
-                                for (int w = lane; w < S::kPitch / 4; w += 32) *reinterpret_cast<uint32_t *>(vals + r * S::kPitch + 4 * w) = 0u;
-                        __syncwarp();
-                    }
+                    __syncwarp();
                 }
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    if constexpr (M::kScaled) {
-                        // 16 keys x 16-byte chunks k, k + 1, transposed in units of two bytes: channels 2 g, 2 g + 1 of keys 2 c, 2 c + 1
-                        const uint32_t vrow = vs + (16 * h + (lane & 15)) * S::kPitch;
+                for (int h = 0; h < kJoint; ++h)
 #pragma unroll
-                        for (int k = 0; k < kSteps; k += 2) {
-                            uint32_t r[4];
-                            ldsm_t(r, vrow + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int t = 0; t < 2; ++t) {
+                        for (int i = 0; i < 2; ++i) {
+                            f2 w = exp2_2(add2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), ref[n]));
+                            l[n] = add2(l[n], w);
+                            if constexpr (M::kScaled) w = mul2(w, mul2(turn[n], pk(fv[h][i], fv[h][i])));
+                            float lo, hi;
+                            upk(w, lo, hi);
+                            pb[h][n][i] = transpose8(M::kScaled ? pack_f16(lo, hi) : pack_bf16(lo, hi));
+                        }
+            }
+            st.ready();
+            if (count) {
+                const uint32_t vs = st.oldest();
+                // O^T += V^T P^T, for all rows or those of one token alone
+                auto values = [&](auto all, int token) {
+#pragma unroll
+                    for (int h = 0; h < kJoint; ++h) {
+                        const uint32_t vrow = vs + (16 * h + (M::kScaled ? lane & 15 : (lane & 7) + ((lane >> 4) << 3))) * S::kPitch;
+#pragma unroll
+                        for (int k = 0; k < kSteps; k += M::kScaled ? 2 : 1) {
+                            uint32_t r[4], f[2][4];
+                            if constexpr (M::kScaled) {
+                                // 16 keys x 16-byte chunks k, k + 1, transposed in units of two bytes: channels 2 g, 2 g + 1 of keys 2 c, 2 c + 1;
                                 // bytes (key 2c, channel 2g), (2c, 2g + 1), (2c + 1, 2g), (2c + 1, 2g + 1): pair the keys
-                                uint32_t f[4];
-                                widen(__byte_perm(r[2 * t], 0, 0x3120), f[0], f[1]);
-                                widen(__byte_perm(r[2 * t + 1], 0, 0x3120), f[2], f[3]);
+                                ldsm_t(r, vrow + (((k + (lane >> 4)) ^ (lane & 7)) << 4));
 #pragma unroll
-                                for (int n = 0; n < NT; ++n) mma_f16(o[k + t][n], f, pb[h][n][0], pb[h][n][1]);
+                                for (int t = 0; t < 2; ++t) {
+                                    widen(__byte_perm(r[2 * t], 0, 0x3120), f[t][0], f[t][1]);
+                                    widen(__byte_perm(r[2 * t + 1], 0, 0x3120), f[t][2], f[t][3]);
+                                }
+                            } else {
+                                ldsm_t(f[0], vrow + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
                             }
-                        }
-                    } else {
-                        const uint32_t vrow = vs + (16 * h + (lane & 7) + ((lane >> 4) << 3)) * S::kPitch;
 #pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            uint32_t r[4];
-                            ldsm_t(r, vrow + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+                            for (int t = 0; t < (M::kScaled ? 2 : 1); ++t)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_bf16(o[k][n], r, pb[h][n][0], pb[h][n][1]);
+                                for (int n = 0; n < NT; ++n) {
+                                    if constexpr (decltype(all)::value) {
+                                        if constexpr (M::kScaled)
+                                            mma_f16(o[k + t][n], f[t], pb[h][n][0], pb[h][n][1]);
+                                        else
+                                            mma_bf16(o[k + t][n], f[t], pb[h][n][0], pb[h][n][1]);
+                                    } else {
+                                        float add[4] = {0.f, 0.f, 0.f, 0.f};
+                                        if constexpr (M::kScaled)
+                                            mma_f16(add, f[t], pb[h][n][0], pb[h][n][1]);
+                                        else
+                                            mma_bf16(add, f[t], pb[h][n][0], pb[h][n][1]);
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            if (token_of(a, p.row0 + 8 * n + 2 * c + (i & 1)) == token) o[k + t][n][i] += add[i];
+                                    }
+                                }
                         }
+                    }
+                };
+                bool odd = false;
+                if (edge && a.T > 1) {  // is any value not finite?
+#pragma unroll 1
+                    for (uint32_t w = 16 * lane; w < (uint32_t)S::kSlot; w += 512) {
+                        const uint4 q4 = *reinterpret_cast<const uint4 *>(own + (vs - st.ring) + w);
+                        const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // all bits of an exponent (8-bit: of a number without its sign) set: adding the lowest of them carries out
+                            if constexpr (M::kScaled)
+                                odd |= (((q[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                            else
+                                odd |= (((q[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+                        }
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                }
+                if (!odd) {
+                    values(std::true_type{}, 0);
+                } else {
+                    // Such a value would reach rows that do not see its key, as 0 * NaN: one token's rows at a time, from the last token on,
+                    // with the values that it does not see set to zero.
+                    int from = kKeys;
+#pragma unroll 1
+                    for (int t = token_of(a, p.row0 + p.rows - 1); t >= token_of(a, p.row0); --t) {
+                        const int end = p.len - a.T + t + 1 - pos0;
+                        const int zero = end < 0 ? 0 : end < kKeys ? end : kKeys;
+                        __syncwarp();
+#pragma unroll 1
+                        for (int b = zero * S::kPitch + 4 * lane; b < from * S::kPitch; b += 128) *reinterpret_cast<uint32_t *>(own + (vs - st.ring) + b) = 0u;
+                        from = zero;
+                        __syncwarp();
+                        values(std::false_type{}, t);
                     }
                 }
             }
-            slot = st.next(slot);
+            st.template release<true>();
         }
+
         float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
         const bool whole = p.whole();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            float sum[2];
+            upk(l[n], sum[0], sum[1]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
+                for (int d = 4; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
                 const int r = 8 * n + 2 * c + j;
                 if (r >= p.rows) continue;
-                const float top = big[n][j] == -INFINITY ? -INFINITY : m[n][j];
-                float f = M::kScaled ? tc5::ex2(mv[n][j] - m[n][j]) : 1.f;
-                if (whole) {
-                    f = l[n][j] == 0.f ? 0.f : f / l[n][j];
-                    const int64_t row = out_row(a, p, r);
-                    bf16 *to = static_cast<bf16 *>(a.o) + row * D;
+                const float top = row_m[r];
+                float f = M::kScaled && top > -INFINITY ? tc5::ex2(row_mv[r] - top) : 1.f;
+                if (whole) f = sum[j] == 0.f ? 0.f : f / sum[j];
+                const int64_t row = out_row(a, p, r);
+                bf16 *to = static_cast<bf16 *>(a.o) + row * D;
+                float *part = piece + r * D;
+                if (g == 0) {
+                    if (!whole)
+                        reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(top, sum[j]);
+                    else if (a.lse != nullptr)
+                        a.lse[row] = lse_of(top, sum[j]);
+                }
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        if (16 * k >= D) break;
-                        const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
-                        if constexpr (M::kScaled) {
+                for (int k = 0; k < kSteps; ++k) {
+                    if (16 * k >= D) break;
+                    const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
+                    if constexpr (M::kScaled) {
+                        if (whole)
                             *reinterpret_cast<uint32_t *>(to + 16 * k + 2 * g) = pack_bf16(lo, hi);
-                        } else {
-                            to[16 * k + g] = from_f<bf16>(lo);
-                            to[16 * k + g + 8] = from_f<bf16>(hi);
-                        }
+                        else
+                            *reinterpret_cast<float2 *>(part + 16 * k + 2 * g) = make_float2(lo, hi);
+                    } else if (whole) {
+                        to[16 * k + g] = from_f<bf16>(lo);
+                        to[16 * k + g + 8] = from_f<bf16>(hi);
+                    } else {
+                        part[16 * k + g] = lo;
+                        part[16 * k + g + 8] = hi;
                     }
-                    if (g == 0 && a.lse != nullptr) a.lse[row] = lse_of(top, l[n][j]);
-                } else {
-                    float *to = piece + r * D;
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        if (16 * k >= D) break;
-                        const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
-                        if constexpr (M::kScaled) {
-                            *reinterpret_cast<float2 *>(to + 16 * k + 2 * g) = make_float2(lo, hi);
-                        } else {
-                            to[16 * k + g] = lo;
-                            to[16 * k + g + 8] = hi;
-                        }
-                    }
-                    if (g == 0) reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(top, l[n][j]);
                 }
             }
         }
-        walk.step(a, p);
+        __syncwarp();
+        walk.step(a, p.u1 - p.u0);
     }
     copies_wait<0>();
 }
 
-template <typename C, int DP, int NT, int STAGES>
+template <typename C, int DP, int NT, int SLOTS>
 struct Variant {
-    using M = Mma<C, DP, NT, STAGES>;
+    using M = Mma<C, DP, NT, SLOTS>;
     static cudaError_t launch(const Args &a, cudaStream_t stream) {
-        return launch_kernel<attn_mma_kernel<C, DP, NT, STAGES>, M::kSmem>(a, stream);
+        return launch_kernel<attn_mma_kernel<C, DP, NT, SLOTS>, M::kSmem>(a, stream);
     }
     static int blocks() { return M::kBlocks; }
     static int unit() { return M::kKeys; }
@@ -443,9 +547,9 @@ struct Variant {
 template <typename C, typename F>
 auto pick(const Args &a, F f) {
     if (a.cache.D <= 64)
-        return a.rows == 8 ? f(Variant<C, 64, 1, 4>{}) : a.rows == 16 ? f(Variant<C, 64, 2, 4>{}) : f(Variant<C, 64, 4, 4>{});
+        return a.rows == 8 ? f(Variant<C, 64, 1, 6>{}) : a.rows == 16 ? f(Variant<C, 64, 2, 6>{}) : f(Variant<C, 64, 4, 6>{});
     if (a.cache.D <= 128)
-        return a.rows == 8 ? f(Variant<C, 128, 1, 3>{}) : a.rows == 16 ? f(Variant<C, 128, 2, 3>{}) : f(Variant<C, 128, 4, sizeof(C) == 1 ? 6 : 3>{});
+        return a.rows == 8 ? f(Variant<C, 128, 1, 4>{}) : a.rows == 16 ? f(Variant<C, 128, 2, 4>{}) : f(Variant<C, 128, 4, 4>{});
     return a.rows == 8 ? f(Variant<C, 256, 1, 3>{}) : f(Variant<C, 256, 2, 3>{});
 }
 
@@ -453,8 +557,8 @@ auto pick(const Args &a, F f) {
 
 int mma_rows(int all, int D) { return all <= 8 ? 8 : (all <= 16 || D > 128) ? 16 : 32; }
 
-int mma_unit(const Args &a) {
-    auto f = [](auto v) { return decltype(v)::unit(); };
+int mma_unit_shift(const Args &a) {
+    auto f = [](auto v) { return decltype(v)::unit() == 32 ? 5 : 4; };
     return a.cache.ks != nullptr ? pick<uint8_t>(a, f) : pick<bf16>(a, f);
 }
 int mma_blocks(const Args &a) {

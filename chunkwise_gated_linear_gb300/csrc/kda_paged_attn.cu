@@ -5,74 +5,105 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kJoinWarps = 8;
-constexpr int kJoinThreads = 32 * kJoinWarps;
+constexpr int kJoinWarps = 8;  // of a block, at most
 
-// A query row of an item that was cut: the largest m of its pieces, then the sum of 2^(m - max) (l, O) over them. `split` warps
-// share a row's pieces, every split-th each, and their sums are added in order; lane i holds channels 4 i .. 4 i + 3
-// (and + 128). A block with nothing to join ends after the plan, which is made while the attention still runs.
+// A query row of an item that was cut: with the largest m of its pieces, the sum of 2^(m - max) (l, O) over them. `split` warps
+// share a row's pieces in order, each with a maximum of its own, and are then added up; lane i holds channels
+// 4 i .. 4 i + 3 (and + 128). A block with nothing to join ends after the plan, which is made while the attention
+// still runs. What it costs is waiting: each warp reads the statistics of all its pieces at once, then the pieces.
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ Args a, int split) {
-    __shared__ int64_t mem[kJoinWarps], mine;
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ Args a, int split) {
+    __shared__ uint32_t mem[kJoinWarps], mine;
     __shared__ float4 sums[kJoinWarps][64];
-    __shared__ float ls[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / a.per_seq, item = blockIdx.x - b * a.per_seq;
-    Scan<kJoinThreads> sc;
-    sc.run(a, mem);
-    if (b >= sc.first && b < sc.first + sc.each) {  // one thread's
-        int64_t before = sc.before;
-        for (int x = sc.first; x < b; ++x) before += (int64_t)units_of(cache_len(a.cache, x), a.unit) * a.per_seq;
+    __shared__ float2 stat[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    Walk walk;  // of the item
+    walk.b = blockIdx.x / a.per_seq;
+    const int item = blockIdx.x - walk.b * a.per_seq;
+    walk.rb = item / a.cache.heads;
+    walk.head = item - walk.rb * a.cache.heads;
+    walk.len = cache_len(a.cache, walk.b);
+    walk.u0 = 0;
+    walk.left = 0xffffffffu;
+    const Scan sc = scan_sequences(a, mem);
+    if (walk.b >= sc.first && walk.b < sc.first + sc.each) {  // one thread's
+        uint32_t before = sc.before;
+#pragma unroll 1
+        for (int x = sc.first; x < walk.b; ++x) before += units_of(a, cache_len(a.cache, x)) * a.per_seq;
         mine = before;
     }
     __syncthreads();
-    const int n = sharers(a, sc.total);
-    const int len = cache_len(a.cache, b), units = units_of(len, a.unit);
-    const int64_t begin = mine + (int64_t)item * units;
-    const int w0 = owner(sc.total, begin, n), w1 = owner(sc.total, begin + units - 1, n);
+    const Deal deal(a, sc.total);
+    const Piece p = walk.piece(a);
+    const uint32_t begin = mine + item * p.units;
+    const int w0 = deal.owner(begin), w1 = deal.owner(begin + p.units - 1);
     if (w0 == w1) return;
-    const Piece p = piece_of(a, b, len, item, 0, units);
     const int D = a.cache.D, part = warp % split;
-    const int r = blockIdx.y * (kJoinWarps / split) + warp / split;
+    const int r = blockIdx.y * (warps / split) + warp / split;
+    const int each = (w1 - w0 + split) / split;  // pieces of a warp
+    const int from = w0 + part * each, to = from + each < w1 + 1 ? from + each : w1 + 1;
     wait_for_previous();
     float m = -INFINITY, l = 0.f;
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    auto scale = [&](float f) {
+        l *= f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = make_float4(s[h].x * f, s[h].y * f, s[h].z * f, s[h].w * f);
+    };
     if (r < p.rows) {
-        // the piece of the first worker begins there, the others come from the one before
-        auto stats = [&](int w) { return reinterpret_cast<const float2 *>(piece_mem(a, w, w == w0) + (int64_t)a.rows * D)[r]; };
-        for (int w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, stats(w).x);
+#pragma unroll 1
+        for (int w = from; w < to; w += 32) {
+            // the piece of the first worker begins there, the others come from the one before
+            const int my = w + lane < to ? w + lane : w;
+            const float2 x = reinterpret_cast<const float2 *>(piece_mem(a, my, my == w0) + (int64_t)a.rows * D)[r];
+            float top = x.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m == -INFINITY ? 0.f : m;
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top > m) {
+                scale(tc5::ex2(m - top));
+                m = top;
+            }
+            const float f = tc5::ex2(x.x - (m == -INFINITY ? 0.f : m));
+            float ls = w + lane < to ? x.y * f : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            l += ls;
+            const int count = to - w < 32 ? to - w : 32;
 #pragma unroll 4
-        for (int w = w0 + part; w <= w1; w += split) {
-            const float2 x = stats(w);
-            const float f = tc5::ex2(x.x - ref);
-            l = fmaf(x.y, f, l);
-            const float *from = piece_mem(a, w, w == w0) + (int64_t)r * D + 4 * lane;
+            for (int i = 0; i < count; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float *o = piece_mem(a, w + i, w + i == w0) + (int64_t)r * D + 4 * lane;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (4 * lane + 128 * h < D) {
-                    const float4 v = *reinterpret_cast<const float4 *>(from + 128 * h);
-                    s[h].x = fmaf(v.x, f, s[h].x);
-                    s[h].y = fmaf(v.y, f, s[h].y);
-                    s[h].z = fmaf(v.z, f, s[h].z);
-                    s[h].w = fmaf(v.w, f, s[h].w);
-                }
+                for (int h = 0; h < 2; ++h)
+                    if (4 * lane + 128 * h < D) {
+                        const float4 v = *reinterpret_cast<const float4 *>(o + 128 * h);
+                        s[h].x = fmaf(v.x, fi, s[h].x);
+                        s[h].y = fmaf(v.y, fi, s[h].y);
+                        s[h].z = fmaf(v.z, fi, s[h].z);
+                        s[h].w = fmaf(v.w, fi, s[h].w);
+                    }
+            }
         }
     }
     if (split > 1) {
         sums[warp][lane] = s[0];
         sums[warp][32 + lane] = s[1];
-        if (lane == 0) ls[warp] = l;
+        if (lane == 0) stat[warp] = make_float2(m, l);
         __syncthreads();
         if (part != 0) return;
+#pragma unroll 1
         for (int v = warp + 1; v < warp + split; ++v) {
-            l += ls[v];
+            const float2 x = stat[v];
+            if (x.x > m) {
+                scale(tc5::ex2(m - x.x));
+                m = x.x;
+            }
+            const float f = tc5::ex2(x.x - (m == -INFINITY ? 0.f : m));
+            l = fmaf(x.y, f, l);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 x = sums[v][32 * h + lane];
-                s[h] = make_float4(s[h].x + x.x, s[h].y + x.y, s[h].z + x.z, s[h].w + x.w);
+                const float4 y = sums[v][32 * h + lane];
+                s[h] = make_float4(fmaf(y.x, f, s[h].x), fmaf(y.y, f, s[h].y), fmaf(y.z, f, s[h].z), fmaf(y.w, f, s[h].w));
             }
         }
     }
@@ -91,16 +122,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 template <typename T>
 cudaError_t launch_join(const Args &a, cudaStream_t stream) {
     const int64_t items = (int64_t)a.B * a.per_seq;
-    // about as many pieces as an item is cut into when all are of one length
+    const int rows = a.T * a.group < a.rows ? a.T * a.group : a.rows;
+    // warps for a row: so many that about 16 on every SM have something to do, but not below four pieces each when all items
+    // are of one length
     int split = 1;
-    while (split < kJoinWarps && split * 2 * items <= a.workers) split *= 2;
+    while (split < kJoinWarps && split * 8 * items <= a.workers && split * items * rows < 16 * (int64_t)sm_count()) split *= 2;
+    const int at_once = kJoinWarps / split < rows ? kJoinWarps / split : rows;  // rows of a block
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    const int rows = a.T * a.group < a.rows ? a.T * a.group : a.rows;
-    cfg.gridDim = dim3((unsigned)items, (unsigned)ceil_div(rows, kJoinWarps / split));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3((unsigned)items, (unsigned)ceil_div(rows, at_once));
+    cfg.blockDim = dim3((unsigned)(32 * split * at_once));
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -115,6 +148,7 @@ int check(const kda_attn_step_params &p) {
     const int st = cache_check(p.cache, p.dtype);
     if (st != KDA_OK) return st;
     if (p.q_heads % p.cache.heads != 0) return KDA_ERR_INVALID_ARG;
+    if (p.q_heads / p.cache.heads > 256) return KDA_ERR_UNSUPPORTED;
     if (p.T != 0 && (p.q == nullptr || p.o == nullptr)) return KDA_ERR_INVALID_ARG;
     const int64_t dense = (int64_t)p.q_heads * p.cache.D;
     if (p.q_stride != 0 && p.q_stride < dense) return KDA_ERR_INVALID_ARG;
@@ -140,8 +174,10 @@ Args make(const kda_attn_step_params &p, unsigned int *err) {
     const int all = a.T * a.group;
     const bool f32 = p.dtype == KDA_DTYPE_F32;
     a.rows = f32 ? fma_rows(all, a.cache.D) : mma_rows(all, a.cache.D);
-    a.per_seq = (int)ceil_div(all, a.rows) * a.cache.heads;
-    a.unit = f32 ? fma_unit(a) : mma_unit(a);
+    a.group_magic = (uint32_t)ceil_div((int64_t)1 << 32, a.group);  // not used for 1
+    a.row_blocks = (int)ceil_div(all, a.rows);
+    a.per_seq = a.row_blocks * a.cache.heads;
+    a.unit_shift = f32 ? fma_unit_shift(a) : mma_unit_shift(a);
     a.workers = sm_count() * (f32 ? fma_blocks(a) : mma_blocks(a)) * kWarps;
     return a;
 }
@@ -170,7 +206,8 @@ int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
     if (e != cudaSuccess) return status_of_cuda(e);
     Args a = attn::make(*p, err);
     if (a.workers == 0) return status_of_cuda(cudaErrorInvalidDevice);
-    if ((int64_t)a.B * a.per_seq >= (int64_t)1 << 31) return KDA_ERR_UNSUPPORTED;
+    // units of all sequences, were they as long as the table allows
+    if ((int64_t)a.B * a.per_seq * (((int64_t)a.cache.most >> a.unit_shift) + 1) >= (int64_t)1 << 32) return KDA_ERR_UNSUPPORTED;
     const size_t bytes = bytes_of(a);
     if (p->workspace != nullptr && p->workspace_bytes < bytes) return KDA_ERR_INVALID_ARG;
     if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;
