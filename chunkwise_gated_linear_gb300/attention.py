@@ -105,7 +105,7 @@ def kda_attn_step_workspace(params) -> int:
 
 # ---- checks -------------------------------------------------------------------------------
 
-def _place(lead, *others):
+def _place(lead, others):
     """Every tensor on the CUDA device of ``lead``."""
     device = lead.get_device()  # -1 on the host
     good = device >= 0
@@ -120,19 +120,31 @@ def _place(lead, *others):
     raise ValueError("every tensor must be a CUDA tensor")
 
 
-def _dense(**tensors):
-    for name, t in tensors.items():
+def _dense(names, *tensors):
+    for t in tensors:
         if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+            bad = [n for n, x in zip(names.split(), tensors) if x is not None and not x.is_contiguous()]
+            raise ValueError(f"{bad[0]} must be contiguous")
 
 
-def _heads(t, name, B, T, D, like):
-    """The heads of a tensor [B, T, heads, D] beside another one, and its token stride."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != D or t.shape[2] < 1:
-        raise ValueError(f"{name} must be [{B}, {T}, heads, {D}], not {list(t.shape)}")
-    if t.dtype != like.dtype:
+def _heads(t, name, B, T, D, dtype):
+    """The heads of a tensor [B, T, heads, D] and its token stride."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != D or shape[2] < 1:
+        raise ValueError(f"{name} must be [{B}, {T}, heads, {D}], not {list(shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must have the dtype of the other data tensors")
-    return t.shape[2], _token_stride(t, name)
+    return shape[2], _tokens(t, name, B, T, shape[2], D)
+
+
+def _tokens(t, name, B, T, H, D):
+    """Elements between consecutive tokens: :func:`mixer._token_stride`, its usual cases first."""
+    s = t.stride()
+    if s[3] == 1 and s[2] == D:
+        step = s[1] if T > 1 else s[0] if B > 1 else H * D
+        if step >= H * D and (B == 1 or T == 1 or s[0] == T * step):
+            return step
+    return _token_stride(t, name)
 
 
 # ---- the cache ------------------------------------------------------------------------------
@@ -181,68 +193,75 @@ def _page_stride(t, name):
 
 
 def _cache(cache, block_table, lens, N, data):
-    """The C struct of a cache that N sequences of tensors like ``data`` use, and its tensors."""
+    """The C struct of a cache that N sequences of tensors of type ``data`` use."""
     torch = sys.modules["torch"]
 
     k, v, ks, vs = cache
-    if k.dim() != 4 or min(k.shape) < 1 or k.shape[3] % 16 != 0 or k.shape[3] > 256:
+    shape, kind = k.shape, k.dtype
+    if len(shape) != 4 or min(shape) < 1 or shape[3] % 16 != 0 or shape[3] > 256:
         raise ValueError("the cache must be [pages, heads, page_size, D], D a multiple of 16 up to 256")
-    pages, heads, page, D = k.shape
-    if k.dtype == torch.float8_e4m3fn:
-        kind = KDA_DTYPE_E4M3
+    pages, heads, page, D = shape
+    scale_stride = 0
+    if kind is torch.float8_e4m3fn:
+        code = KDA_DTYPE_E4M3
         if ks is None or vs is None:
             raise ValueError("a float8_e4m3fn cache has k_scale and v_scale")
-        _want(ks, "k_scale", k.shape[:3], torch.float8_e8m0fnu)
-        _want(vs, "v_scale", k.shape[:3], torch.float8_e8m0fnu)
-        scale_stride = _page_stride(ks, "k_scale")
-        if _page_stride(vs, "v_scale") != scale_stride:
-            raise ValueError("k_scale and v_scale must have the same strides")
+        _want(ks, "k_scale", shape[:3], torch.float8_e8m0fnu)
+        _want(vs, "v_scale", shape[:3], torch.float8_e8m0fnu)
+        if not (ks.is_contiguous() and vs.is_contiguous()):
+            scale_stride = _page_stride(ks, "k_scale")
+            if _page_stride(vs, "v_scale") != scale_stride:
+                raise ValueError("k_scale and v_scale must have the same strides")
     else:
-        if k.dtype != data:
+        if kind is not data:
             raise TypeError("the cache must have the dtype of the data or float8_e4m3fn")
         if ks is not None or vs is not None:
             raise ValueError("only a float8_e4m3fn cache has scales")
-        kind = KDA_DTYPE_BF16 if data == torch.bfloat16 else KDA_DTYPE_F32
-        scale_stride = 0
-    _want(v, "v of the cache", k.shape, k.dtype)
-    page_stride = _page_stride(k, "k of the cache")
-    if _page_stride(v, "v of the cache") != page_stride:
-        raise ValueError("k and v of the cache must have the same strides")
-    if page_stride % D != 0:
-        raise ValueError("the pages of the cache must lie a multiple of D elements apart")
-    if block_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        code = KDA_DTYPE_BF16 if data is torch.bfloat16 else KDA_DTYPE_F32
+    _want(v, "v of the cache", shape, kind)
+    page_stride = 0
+    if not (k.is_contiguous() and v.is_contiguous()):
+        page_stride = _page_stride(k, "k of the cache")
+        if _page_stride(v, "v of the cache") != page_stride:
+            raise ValueError("k and v of the cache must have the same strides")
+        if page_stride % D != 0:
+            raise ValueError("the pages of the cache must lie a multiple of D elements apart")
+    if block_table.dtype is not torch.int32 or lens.dtype is not torch.int32:
         raise TypeError("block_table and lens must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != N or block_table.shape[1] < 1:
-        raise ValueError(f"block_table must be [{N}, pages per sequence], not {list(block_table.shape)}")
+    table = block_table.shape
+    if len(table) != 2 or table[0] != N or table[1] < 1:
+        raise ValueError(f"block_table must be [{N}, pages per sequence], not {list(table)}")
     if lens.shape != (N,):
         raise ValueError(f"lens must be [{N}], not {list(lens.shape)}")
-    _dense(lens=lens)
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1 or N > 1 and block_table.stride(0) < block_table.shape[1]:
-        raise ValueError("block_table: the entries of a sequence must be contiguous")
-    width = block_table.shape[1]
-    c = kda_kv_cache(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), page_stride, scale_stride, pages, heads, page, D, kind,
-                     _ptr(block_table), width, block_table.stride(0) if N > 1 else 0, _ptr(lens))
-    return c, (k, v, ks, vs, block_table, lens)
+    width = table[1]
+    row = width
+    if not block_table.is_contiguous():
+        row = block_table.stride(0) if N > 1 else width
+        if width > 1 and block_table.stride(1) != 1 or row < width:
+            raise ValueError("block_table: the entries of a sequence must be contiguous")
+    if not lens.is_contiguous():
+        raise ValueError("lens must be contiguous")
+    return kda_kv_cache(k.data_ptr(), v.data_ptr(), _ptr(ks), _ptr(vs), page_stride, scale_stride, pages, heads, page, D, code,
+                        block_table.data_ptr(), width, row, lens.data_ptr())
 
 
 def kv_cache_write(k, v, cache, block_table, lens, *, cu_seqlens=None, stream=None):
     """The new tokens k, v [B, T, heads, D] (bf16 or fp32) into the cache, each at its position; other places
     stay as they are. A float8_e4m3fn cache takes each row with the least power of two that leaves its
     largest entry at 448 or below, rounded to nearest. No two tokens of a call may have one place."""
-    torch = sys.modules["torch"]
-
-    if k.dim() != 4:
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("k must be [B, T, heads, D]")
-    B, T, H, D = k.shape
+    B, T, H, D = shape
     dtype = _dtype(k, "k")
     N = _sequences(cu_seqlens, B)
-    Hv, v_stride = _heads(v, "v", B, T, D, k)
-    k_stride = _token_stride(k, "k")
-    c, tensors = _cache(cache, block_table, lens, N, k.dtype)
+    Hv, v_stride = _heads(v, "v", B, T, D, k.dtype)
+    k_stride = _tokens(k, "k", B, T, H, D)
+    c = _cache(cache, block_table, lens, N, k.dtype)
     if Hv != H or c.heads != H or c.D != D:
         raise ValueError("k, v and the cache must have the same heads and channels")
-    _dense(cu_seqlens=cu_seqlens)
-    _place(k, v, cu_seqlens, *tensors)
+    _dense("cu_seqlens", cu_seqlens)
+    _place(k, (v, cu_seqlens, *cache, block_table, lens))
     p = kda_kv_cache_write_params(_ptr(k), _ptr(v), k_stride, v_stride, N, T, _ptr(cu_seqlens), dtype, c)
     _call("kda_kv_cache_write", p, k, stream)
 
@@ -261,12 +280,12 @@ def kv_cache_read(cache, block_table, lens, tokens, *, cu_seqlens=None, dtype=No
     N = _sequences(cu_seqlens, B)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    c, tensors = _cache(cache, block_table, lens, N, dtype)
+    c = _cache(cache, block_table, lens, N, dtype)
     shape = (B, tokens, c.heads, c.D)
     _want(k, "k", shape, dtype)
     _want(v, "v", shape, dtype)
-    _dense(k=k, v=v, cu_seqlens=cu_seqlens)
-    _place(*tensors, k, v, cu_seqlens)
+    _dense("k v cu_seqlens", k, v, cu_seqlens)
+    _place(cache.k, (*cache, block_table, lens, k, v, cu_seqlens))
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.k.device)
     if v is None:
@@ -300,30 +319,34 @@ def rope_frequencies(R, theta=10000.0, *, inv_freq=None, device="cuda"):
 def _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, q_out, k_out):
     torch = sys.modules["torch"]
 
-    if q.dim() != 4:
+    shape, kind = q.shape, q.dtype
+    if len(shape) != 4:
         raise ValueError("q must be [B, T, heads, D]")
-    B, T, Hq, D = q.shape
+    B, T, Hq, D = shape
     if not 1 <= D <= 256 or Hq < 1:
         raise ValueError("q must be [B, T, heads, D] with 1 <= D <= 256")
     dtype = _dtype(q, "q")
     N = _sequences(cu_seqlens, B)
-    Hk, k_stride = _heads(k, "k", B, T, D, q)
-    q_stride = _token_stride(q, "q")
+    Hk, k_stride = _heads(k, "k", B, T, D, kind)
+    q_stride = _tokens(q, "q", B, T, Hq, D)
     _want(q_weight, "q_weight", (D,), torch.float32)
     _want(k_weight, "k_weight", (D,), torch.float32)
     R = 0
     if freq is not None:
-        if freq.dtype != torch.int64:
+        if freq.dtype is not torch.int64:
             raise TypeError("freq must be int64 (rope_frequencies)")
-        if freq.dim() != 1 or 2 * freq.shape[0] > D:
+        R = 2 * freq.numel()
+        if freq.dim() != 1 or R > D:
             raise ValueError("freq must be [R / 2] with R <= D")
-        R = 2 * freq.shape[0]
-    _want(positions, "positions", (B, T), torch.int32)
-    _want(q_out, "q_out", q.shape, q.dtype)
-    _want(k_out, "k_out", k.shape, q.dtype)
-    _dense(q_weight=q_weight, k_weight=k_weight, freq=freq, positions=positions, cu_seqlens=cu_seqlens, q_out=q_out, k_out=k_out)
-    return kda_qk_norm_params(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freq) if R else None, _ptr(positions), _ptr(q_out),
-                              _ptr(k_out), q_stride, k_stride, N, T, Hq, Hk, D, R, _ptr(cu_seqlens), eps, dtype,
+    if positions is not None:
+        _want(positions, "positions", (B, T), torch.int32)
+    if q_out is not None:
+        _want(q_out, "q_out", shape, kind)
+    if k_out is not None:
+        _want(k_out, "k_out", k.shape, kind)
+    _dense("q_weight k_weight freq positions cu_seqlens q_out k_out", q_weight, k_weight, freq, positions, cu_seqlens, q_out, k_out)
+    return kda_qk_norm_params(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(freq) if R else None, _ptr(positions),
+                              _ptr(q_out), _ptr(k_out), q_stride, k_stride, N, T, Hq, Hk, D, R, _ptr(cu_seqlens), eps, dtype,
                               1 if interleaved else 0)
 
 
@@ -340,7 +363,7 @@ def qk_norm_fwd(q, k, q_weight=None, k_weight=None, freq=None, *, positions=None
     torch = sys.modules["torch"]
 
     p = _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, q_out, k_out)
-    _place(q, k, q_weight, k_weight, freq, positions, cu_seqlens, q_out, k_out)
+    _place(q, (k, q_weight, k_weight, freq, positions, cu_seqlens, q_out, k_out))
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
@@ -359,8 +382,8 @@ def qk_norm_bwd(q, k, q_weight, k_weight, freq, dq_out, dk_out, *, positions=Non
     f = _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, None, None)
     _want(dq_out, "dq_out", q.shape, q.dtype)
     _want(dk_out, "dk_out", k.shape, q.dtype)
-    _dense(dq_out=dq_out, dk_out=dk_out)
-    _place(q, k, q_weight, k_weight, freq, positions, cu_seqlens, dq_out, dk_out)
+    _dense("dq_out dk_out", dq_out, dk_out)
+    _place(q, (k, q_weight, k_weight, freq, positions, cu_seqlens, dq_out, dk_out))
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
@@ -377,14 +400,15 @@ def qk_norm_step(q, k, v, cache, block_table, lens, q_weight=None, k_weight=None
     torch = sys.modules["torch"]
 
     f = _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, q_out, None)
-    Hv, v_stride = _heads(v, "v", *q.shape[:2], q.shape[3], q)
-    c, tensors = _cache(cache, block_table, lens, f.B, q.dtype)
+    shape = q.shape
+    Hv, v_stride = _heads(v, "v", shape[0], shape[1], shape[3], q.dtype)
+    c = _cache(cache, block_table, lens, f.B, q.dtype)
     if Hv != f.k_heads or c.heads != f.k_heads or c.D != f.D:
         raise ValueError("k, v and the cache must have the same heads and channels")
-    _place(q, k, v, q_weight, k_weight, freq, positions, cu_seqlens, q_out, *tensors)
+    _place(q, (k, v, q_weight, k_weight, freq, positions, cu_seqlens, q_out, *cache, block_table, lens))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    f.q_out = _ptr(q_out)
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        f.q_out = q_out.data_ptr()
     p = kda_qk_norm_step_params(f, _ptr(v), v_stride, c)
     _call("kda_qk_norm_step", p, q, stream)
     return q_out
@@ -403,22 +427,25 @@ def paged_attn_step(q, cache, block_table, lens, *, scale=None, want_lse=False, 
     """
     torch = sys.modules["torch"]
 
-    if q.dim() != 4:
+    shape, kind = q.shape, q.dtype
+    if len(shape) != 4:
         raise ValueError("q must be [B, T, heads, D]")
-    B, T, Hq, D = q.shape
+    B, T, Hq, D = shape
     dtype = _dtype(q, "q")
-    stride = _token_stride(q, "q")
-    c, tensors = _cache(cache, block_table, lens, B, q.dtype)
+    stride = _tokens(q, "q", B, T, Hq, D)
+    c = _cache(cache, block_table, lens, B, kind)
     if c.D != D or Hq < 1 or Hq % c.heads != 0:
         raise ValueError("q must have the cache's channels and a multiple of its heads")
     if scale is None:
         scale = D ** -0.5
-    _want(o, "o", q.shape, q.dtype)
-    _want(lse, "lse", (B, T, Hq), torch.float32)
-    _dense(o=o, lse=lse)
-    _place(q, o, lse, *tensors)
+    if o is not None:
+        _want(o, "o", shape, kind)
+    if lse is not None:
+        _want(lse, "lse", (B, T, Hq), torch.float32)
+    _dense("o lse", o, lse)
+    _place(q, (o, lse, *cache, block_table, lens))
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        o = torch.empty(shape, dtype=kind, device=q.device)
     if want_lse and lse is None:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
     p = kda_attn_step_params(_ptr(q), _ptr(o), _ptr(lse) if want_lse else None, stride, B, T, Hq, scale, dtype, c, None, 0)
