@@ -8,6 +8,10 @@
 
 #include "cache_common.cuh"
 
+#ifndef FWD_U
+#define FWD_U 2
+#define FWD_BLOCKS 2
+#endif
 namespace kda {
 namespace {
 
@@ -258,35 +262,88 @@ __global__ void __launch_bounds__(32 * kWarps) any_read_kernel(HeadArgs a) {
 
 // ---- rows of whole vectors -------------------------------------------------------------------
 // LPR lanes share a row, 16 channels each as two chunks of 8; a warp holds 32 / LPR rows (heads of one token) at a time
-// and U such groups, of queries, keys or values alone, for one token after another: what belongs to the
-// channels (weights, frequencies) is loaded once, the angles once per token, and each group's rows of the
-// next token are on their way as soon as the current ones are unpacked.
+// and U such groups, of queries, keys or values alone (a slice). A block takes some tokens: first the place and the
+// angles of each are worked out once and left in shared memory, then its warps go through the tokens' slices in turn, the
+// next slice's rows on their way while the ones before are worked on. Arithmetic goes in pairs of fp32.
 constexpr int kVecWarps = 8;
+constexpr int kVecThreads = 32 * kVecWarps;
+constexpr int kVecTokens = 32;  // of a block at a time, at most
 
-struct Share {
-    int part;   // 0 queries, 1 keys, 2 values
-    int head0;  // first head
+struct VecArgs {
+    HeadArgs h;
+    int tokens;   // of a block at a time
+    int batches;  // ceil(rows / tokens)
 };
+
+// A token's place, in shared memory.
+struct Place {
+    int pos, page, slot;  // for the rotation; in the cache (page < 0: not there)
+};
+
+// What a block works out for its tokens `row0 ..` before their rows: places, cosines and sines. `count`: tokens that exist.
+__device__ __forceinline__ void vec_places(const HeadArgs &a, int64_t row0, int count, Place *place) {
+    // the sequence of the first token: how many offsets are not after it, counted by all threads at once
+    int s0 = 0;
+    if (a.seqs.cu != nullptr) {
+        int n = 0;
+        for (int i = threadIdx.x; i - (int)threadIdx.x < a.seqs.N; i += kVecThreads)  // the same number of turns for all
+            n += __syncthreads_count(i < a.seqs.N && a.seqs.cu[i] <= row0);
+        s0 = n < 1 ? 0 : n - 1;
+    }
+    if ((int)threadIdx.x >= count) return;
+    const int64_t row = row0 + threadIdx.x;
+    SeqAt at;
+    if (a.seqs.cu == nullptr) {
+        at = seq_find(a.seqs, row);
+    } else {
+        at.s = s0;
+        while (at.s < a.seqs.N - 1 && a.seqs.cu[at.s + 1] <= row) ++at.s;
+        seq_fill(a.seqs, row, at);
+    }
+    Place p;
+    p.page = -1;
+    p.slot = 0;
+    p.pos = (int)(row - at.start);
+    if (a.cached) {
+        p.pos += cache_len(a.cache, at.s) - (int)(at.end - at.start);
+        if (p.pos >= 0) p.page = cache_page(a.cache, at.s, p.pos, p.slot);
+    }
+    if (a.pos != nullptr) p.pos = a.pos[row];
+    place[threadIdx.x] = p;
+}
+// `table`: of each token R / 2 cosines, sines and negative sines.
+__device__ __forceinline__ void vec_angles(const HeadArgs &a, int count, const Place *place, float *table) {
+    const int half = a.R / 2;
+    for (int i = threadIdx.x; i < count * half; i += kVecThreads) {
+        const int t = i / half, e = i - t * half;
+        float c, s;
+        turn(a.freq[e], place[t].pos, c, s);
+        float *to = table + t * 3 * half + e;
+        to[0] = c;
+        to[half] = s;
+        to[2 * half] = -s;
+    }
+}
+// The two weights [D] (ones where there is none).
+__device__ __forceinline__ void vec_weights(const HeadArgs &a, float *w) {
+    for (int i = threadIdx.x; i < 2 * a.D; i += kVecThreads) {
+        const float *from = i < a.D ? a.qw : a.kw;
+        w[i] = from != nullptr ? from[i < a.D ? i : i - a.D] : 1.f;
+    }
+}
+
 // The slices of heads of a token, `each` heads apiece: of queries, then keys, then values.
 __host__ __device__ __forceinline__ int slices_of(int heads, int each) { return (heads + each - 1) / each; }
-__device__ __forceinline__ Share share_of(const HeadArgs &a, int slice, int each) {
-    const int nq = slices_of(a.Hq, each), nk = slices_of(a.Hk, each);
-    if (slice < nq) return Share{0, slice * each};
-    slice -= nq;
-    if (slice < nk) return Share{1, slice * each};
-    return Share{2, (slice - nk) * each};
-}
 
 // The lane's place in a row.
 struct LaneAt {
     int o0, o1;      // first channels of its two chunks
-    bool in, turns;  // within the row; its channels are turned (pair e: freq[8 j + e])
+    bool in, turns;  // within the row; its channels are turned (pair e: 8 j + e)
 };
-template <int LPR>
-__device__ __forceinline__ LaneAt lane_at(const HeadArgs &a, int part, int j) {
+__device__ __forceinline__ LaneAt lane_at(const HeadArgs &a, bool turned, int j) {
     LaneAt l;
     l.in = 16 * j < a.D;
-    l.turns = part < 2 && 16 * j < a.R;
+    l.turns = turned && 16 * j < a.R;
     l.o0 = 16 * j;
     l.o1 = 16 * j + 8;
     if (l.turns && !a.pairs) {  // channels i and i + R / 2
@@ -295,6 +352,22 @@ __device__ __forceinline__ LaneAt lane_at(const HeadArgs &a, int part, int j) {
     }
     return l;
 }
+
+// A warp's way through the (token, slice) items of a block: every kVecWarps-th.
+struct Item {
+    int token, slice;
+    __device__ __forceinline__ Item(int warp, int slices) {
+        token = warp / slices;
+        slice = warp - token * slices;
+    }
+    __device__ __forceinline__ void step(int slices) {
+        slice += kVecWarps;
+        while (slice >= slices) {
+            slice -= slices;
+            ++token;
+        }
+    }
+};
 
 template <typename T>
 struct Two {
@@ -308,23 +381,34 @@ struct Two {
             b.zero();
         }
     }
-    __device__ __forceinline__ void unpack(float (&f)[16]) const {
+    __device__ __forceinline__ void unpack(f2 (&x)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] = a.get(i);
-            f[8 + i] = b.get(i);
+        for (int i = 0; i < 4; ++i) {
+            x[i] = a.pair(i);
+            x[4 + i] = b.pair(i);
         }
     }
-    static __device__ __forceinline__ void store(void *base, int64_t at, const LaneAt &l, const float (&f)[16]) {
+    static __device__ __forceinline__ void store(void *base, int64_t at, const LaneAt &l, const f2 (&x)[8]) {
         float t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = f[i];
+        for (int i = 0; i < 4; ++i) upk(x[i], t[2 * i], t[2 * i + 1]);
         store_vec<T, 8>(static_cast<T *>(base) + at + l.o0, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = f[8 + i];
+        for (int i = 0; i < 4; ++i) upk(x[4 + i], t[2 * i], t[2 * i + 1]);
         store_vec<T, 8>(static_cast<T *>(base) + at + l.o1, t);
     }
 };
+// 16 floats of shared memory at the lane's chunks (16-byte aligned).
+__device__ __forceinline__ void lane_floats(f2 (&x)[8], const float *a, const float *b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 p = reinterpret_cast<const float4 *>(a)[i], q = reinterpret_cast<const float4 *>(b)[i];
+        x[2 * i] = pk(p.x, p.y);
+        x[2 * i + 1] = pk(p.z, p.w);
+        x[4 + 2 * i] = pk(q.x, q.y);
+        x[5 + 2 * i] = pk(q.z, q.w);
+    }
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -333,274 +417,333 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The lane's 8 pairs by their angles; `sign` -1: back.
-__device__ __forceinline__ void turn_pairs(float (&f)[16], const float (&c)[8], const float (&s)[8], bool pairs, float sign) {
+// The lane's 8 pairs by their angles: cosines, sines and negative sines of pairs 2 i, 2 i + 1 in c[i], s[i], n[i].
+__device__ __forceinline__ void turn_pairs(f2 (&x)[8], const f2 (&c)[4], const f2 (&s)[4], const f2 (&n)[4], bool pairs) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float sn = s[e] * sign;
-        if (pairs) {
-            const float x = f[2 * e], y = f[2 * e + 1];
-            f[2 * e] = x * c[e] - y * sn;
-            f[2 * e + 1] = y * c[e] + x * sn;
+    for (int i = 0; i < 4; ++i) {
+        if (pairs) {  // both numbers of a pair in one register
+            float c0, c1, s0, s1, n0, n1, a, b;
+            upk(c[i], c0, c1);
+            upk(s[i], s0, s1);
+            upk(n[i], n0, n1);
+            upk(x[2 * i], a, b);
+            x[2 * i] = fma2(pk(b, a), pk(n0, s0), mul2(x[2 * i], pk(c0, c0)));
+            upk(x[2 * i + 1], a, b);
+            x[2 * i + 1] = fma2(pk(b, a), pk(n1, s1), mul2(x[2 * i + 1], pk(c1, c1)));
         } else {
-            const float x = f[e], y = f[8 + e];
-            f[e] = x * c[e] - y * sn;
-            f[8 + e] = y * c[e] + x * sn;
+            const f2 a = x[i], b = x[4 + i];
+            x[i] = fma2(b, n[i], mul2(a, c[i]));
+            x[4 + i] = fma2(a, s[i], mul2(b, c[i]));
         }
     }
 }
-
-// A token's sequence as a warp goes from one token to a later one.
-struct TokenAt {
-    SeqAt at{0, 0, 0};
-    int len = 0;  // in the cache
-    __device__ __forceinline__ RowAt row(const HeadArgs &a, int64_t row, bool places) {
-        if (row >= at.end) {
-            at = seq_find(a.seqs, row);
-            if (a.cached) len = cache_len(a.cache, at.s);
-        }
-        RowAt r;
-        r.page = -1;
-        r.slot = 0;
-        r.pos = (int)(row - at.start);
-        if (a.cached) {
-            r.pos += len - (int)(at.end - at.start);
-            if (places && r.pos >= 0) r.page = cache_page(a.cache, at.s, r.pos, r.slot);
-        }
-        if (a.pos != nullptr) r.pos = a.pos[row];
-        return r;
-    }
-};
+__device__ __forceinline__ void lane_angles(f2 (&x)[4], const float *from) {
+    const float4 p = reinterpret_cast<const float4 *>(from)[0], q = reinterpret_cast<const float4 *>(from)[1];
+    x[0] = pk(p.x, p.y);
+    x[1] = pk(p.z, p.w);
+    x[2] = pk(q.x, q.y);
+    x[3] = pk(q.z, q.w);
+}
 
 template <int LPR>
-__device__ __forceinline__ void vec_put_e4m3(const Cache &c, bool value, const float (&f)[16], const LaneAt &l, bool ok, int page, int head, int slot,
-                                             int j) {
-    float top = 0.f;
-    bool inf = false;
+__device__ __forceinline__ void vec_put_e4m3(const Cache &c, bool value, const f2 (&x)[8], const LaneAt &l, bool ok, const Place &p, int head, int j) {
+    float top = 0.f;  // an infinity's exponent is 120 by the same rule; NaN is passed over
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, finite_abs(f[i]));
-        inf |= fabsf(f[i]) == INFINITY;
+    for (int i = 0; i < 8; ++i) {
+        float lo, hi;
+        upk(x[i], lo, hi);
+        top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
     }
-    if (inf) top = INFINITY;
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = row_exponent(top);  // 120 for an infinity
-    const float unit = pow2(-e);
+    const int e = row_exponent(top);
+    const f2 unit = pk(pow2(-e), pow2(-e));
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3_pair(f[4 * i] * unit, f[4 * i + 1] * unit) | e4m3_pair(f[4 * i + 2] * unit, f[4 * i + 3] * unit) << 16;
-    if (!ok || page < 0) return;
-    const int64_t row = cache_row(c, page, head, slot);
+    for (int i = 0; i < 4; ++i) {
+        float f[4];
+        upk(mul2(x[2 * i], unit), f[0], f[1]);
+        upk(mul2(x[2 * i + 1], unit), f[2], f[3]);
+        w[i] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
+    }
+    if (!ok || p.page < 0) return;
+    const int64_t row = cache_row(c, p.page, head, p.slot);
     uint8_t *to = static_cast<uint8_t *>(value ? c.v : c.k) + row * c.D;
     *reinterpret_cast<uint2 *>(to + l.o0) = make_uint2(w[0], w[1]);
     *reinterpret_cast<uint2 *>(to + l.o1) = make_uint2(w[2], w[3]);
-    if (j == 0) (value ? c.vs : c.ks)[cache_scale(c, page, head, slot)] = (uint8_t)(e + 127);
+    if (j == 0) (value ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)] = (uint8_t)(e + 127);
 }
 
 template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(32 * kVecWarps, 2) vec_rows_kernel(const __grid_constant__ HeadArgs a, int slices, int tokens) {
-    constexpr int kAtOnce = 32 / LPR;
+__global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const __grid_constant__ VecArgs v) {
+    constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
+    __shared__ Place place[kVecTokens];
+    extern __shared__ __align__(16) float mem[];
+    const HeadArgs &a = v.h;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / LPR, j = lane % LPR;
-    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, 32 * kVecWarps);
-    const Share sh = share_of(a, blockIdx.x % slices, U * kAtOnce);
-    const LaneAt l = lane_at<LPR>(a, sh.part, j);
-    const int64_t first = (int64_t)(blockIdx.x / slices) * tokens + warp;
-    int64_t stop = (int64_t)(blockIdx.x / slices + 1) * tokens;
-    if (stop > a.seqs.rows) stop = a.seqs.rows;
-    if (first >= stop) return;
-    const bool isq = sh.part == 0, isv = sh.part == 2;
-    const int heads = isq ? a.Hq : isv ? a.Hv : a.Hk;
-    const void *in = isq ? a.q : isv ? a.v : a.k;
-    void *out = isq ? a.q_out : isv ? nullptr : a.k_out;
-    const int64_t stride = isq ? a.q_stride : isv ? a.v_stride : a.k_stride;
-    const float *w = isq ? a.qw : isv ? nullptr : a.kw;
+    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, kVecThreads);
+    const int64_t row0 = (int64_t)blockIdx.x * v.tokens;
+    const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
+    float *weights = mem, *table = mem + 2 * a.D;
+    const int nq = slices_of(a.Hq, kHeads), nk = slices_of(a.Hk, kHeads), slices = nq + nk + slices_of(a.Hv, kHeads);
+    const LaneAt lt = lane_at(a, true, j);
+
+    // of the slice whose rows are on their way: queries, keys or values (0, 1, 2), the row's first head and what is left of them
+    Item it(warp, slices);
     Two<T> raw[U];
-    auto ok = [&](int u) { return l.in && sh.head0 + u * kAtOnce + sub < heads; };
-    const int64_t lane_in = (int64_t)(sh.head0 + sub) * a.D;
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u].load(in, first * stride + lane_in + u * kAtOnce * a.D, l, ok(u));
-    float wt[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) wt[i] = 1.f;
-    if (w != nullptr && l.in) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // parameters may be aligned to 4 bytes alone
-            wt[i] = w[l.o0 + i];
-            wt[8 + i] = w[l.o1 + i];
+    int part = 0, head = 0, left = 0;
+    const T *in = nullptr;
+    LaneAt l = lt;
+    auto aim = [&] {
+        part = it.slice < nq ? 0 : it.slice < nq + nk ? 1 : 2;
+        head = (it.slice - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * kHeads + sub;
+        left = it.token < count && lt.in ? (part == 0 ? a.Hq : part == 1 ? a.Hk : a.Hv) - head : 0;
+        if (part == 2) {
+            l.o0 = 16 * j;
+            l.o1 = 16 * j + 8;
+        } else {
+            l = lt;
         }
-    }
-    int64_t freq[8];
+        in = static_cast<const T *>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
+             (row0 + it.token) * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (int64_t)head * a.D;
+    };
+    auto fetch = [&](int u) { raw[u].load(in, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left); };
+    aim();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) freq[e] = l.turns ? a.freq[8 * j + e] : 0;
-    TokenAt at;
+    for (int u = 0; u < U; ++u) fetch(u);
+    vec_places(a, row0, count, place);
+    vec_weights(a, weights);
+    __syncthreads();
+    if (a.R > 0) {
+        vec_angles(a, count, place, table);
+        __syncthreads();
+    }
     const float inv_d = 1.f / (float)a.D;
 #pragma unroll 1
-    for (int64_t row = first; row < stop; row += kVecWarps) {
-        RowAt r{0, -1, 0};
-        if (a.R > 0 || a.cached) r = at.row(a, row, !isq);
-        float c[8], s[8];
-        if (l.turns) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) turn(freq[e], r.pos, c[e], s[e]);
+    while (it.token < count) {
+        const int now_part = part, now_head = head, now_left = left;
+        const LaneAt now = l;
+        const bool isq = part == 0, isv = part == 2, turns = !isv && l.turns;
+        const int heads = isq ? a.Hq : a.Hk;
+        const bool normed = !isv && (isq ? a.qw : a.kw) != nullptr;
+        T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
+        const bool to_out = !isv && out != nullptr;
+        out += ((row0 + it.token) * heads + now_head) * a.D;
+        const Place p = place[it.token];
+        f2 wt[8], c[4], s[4], n[4];
+        if (normed && now.in) lane_floats(wt, weights + (isq ? 0 : a.D) + now.o0, weights + (isq ? 0 : a.D) + now.o1);
+        if (turns) {
+            const float *from = table + it.token * (a.R / 2) * 3 + 8 * j;
+            lane_angles(c, from);
+            lane_angles(s, from + a.R / 2);
+            lane_angles(n, from + a.R);
         }
+        it.step(slices);
+        aim();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int head = sh.head0 + u * kAtOnce + sub;
-            float f[16];
-            raw[u].unpack(f);
-            if (row + kVecWarps < stop) raw[u].load(in, (row + kVecWarps) * stride + lane_in + u * kAtOnce * a.D, l, ok(u));
-            if (w != nullptr) {
-                float q = 0.f;
+            const bool ok = u * kAtOnce < now_left;
+            f2 x[8];
+            raw[u].unpack(x);
+            fetch(u);
+            if (normed) {
+                f2 q = mul2(x[0], x[0]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) q = fmaf(f[i], f[i], q);
-                const float inv = rsqrtf(row_sum<LPR>(q) * inv_d + a.eps);
+                for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
+                const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
+                const f2 by = pk(inv, inv);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] *= inv * wt[i];
+                for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(wt[i], by));
             }
-            if (l.turns) turn_pairs(f, c, s, a.pairs, 1.f);
-            if (out != nullptr && ok(u)) Two<T>::store(out, (row * heads + head) * a.D, l, f);
-            if (a.cached && !isq) {
+            if (turns) turn_pairs(x, c, s, n, a.pairs);
+            if (to_out && ok) Two<T>::store(out, (int64_t)u * kAtOnce * a.D, now, x);
+            if (a.cached && now_part != 0) {
+                const int h = now_head + u * kAtOnce;
                 if (a.cache.ks != nullptr)
-                    vec_put_e4m3<LPR>(a.cache, isv, f, l, ok(u), r.page, head, r.slot, j);
-                else if (ok(u) && r.page >= 0)
-                    Two<T>::store(isv ? a.cache.v : a.cache.k, cache_row(a.cache, r.page, head, r.slot) * a.D, l, f);
+                    vec_put_e4m3<LPR>(a.cache, isv, x, now, ok, p, h, j);
+                else if (ok && p.page >= 0)
+                    Two<T>::store(isv ? a.cache.v : a.cache.k, cache_row(a.cache, p.page, h, p.slot) * a.D, now, x);
             }
         }
     }
 }
 
+// The gradient: blocks go through batches of tokens, each lane adds up the weights' gradients at its channels.
 template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(32 * kVecWarps, 2) vec_rows_bwd_kernel(const __grid_constant__ HeadArgs a, int slices, int tokens) {
-    constexpr int kAtOnce = 32 / LPR;
-    __shared__ float red[kVecWarps][kMaxD];
+__global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __grid_constant__ VecArgs v) {
+    constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
+    __shared__ Place place[kVecTokens];
+    extern __shared__ __align__(16) float mem[];
+    const HeadArgs &a = v.h;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / LPR, j = lane % LPR;
-    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, 32 * kVecWarps);
-    const Share sh = share_of(a, blockIdx.x % slices, U * kAtOnce);
-    const LaneAt l = lane_at<LPR>(a, sh.part, j);
-    const int64_t first = (int64_t)(blockIdx.x / slices) * tokens + warp;
-    int64_t stop = (int64_t)(blockIdx.x / slices + 1) * tokens;
-    if (stop > a.seqs.rows) stop = a.seqs.rows;
-    const bool isq = sh.part == 0;
-    const int heads = isq ? a.Hq : a.Hk;
-    const void *in = isq ? a.q : a.k, *dout = isq ? a.dq_out : a.dk_out;
-    void *out = isq ? a.q_out : a.k_out;
-    const int64_t stride = isq ? a.q_stride : a.k_stride;
-    const float *w = isq ? a.qw : a.kw;
-    Two<T> raw[U], raw_g[U];
-    auto ok = [&](int u) { return l.in && sh.head0 + u * kAtOnce + sub < heads; };
-    auto fetch = [&](int u, int64_t row) {
-        const int head = sh.head0 + u * kAtOnce + sub;
-        raw_g[u].load(dout, (row * heads + head) * a.D, l, ok(u));
-        if (w != nullptr) raw[u].load(in, row * stride + (int64_t)head * a.D, l, ok(u));
-    };
-    if (first < stop) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) fetch(u, first);
-    }
-    float wt[16], sum[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        wt[i] = w != nullptr && l.in ? w[(i < 8 ? l.o0 : l.o1 - 8) + i] : 0.f;
-        sum[i] = 0.f;
-    }
-    int64_t freq[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) freq[e] = l.turns ? a.freq[8 * j + e] : 0;
-    TokenAt at;
+    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, kVecThreads);
+    // shared floats: weights, the lanes' sums of the weights' gradients ([2][4] of four channels, a thread's 16 bytes beside its
+    // neighbours'), angles (at the end a row of sums for each warp)
+    float *weights = mem, *table = mem + 2 * a.D + 32 * kVecThreads;
+    float4 *sums = reinterpret_cast<float4 *>(mem + 2 * a.D) + threadIdx.x;
+    const LaneAt l = lane_at(a, true, j);
+    const int nq = slices_of(a.Hq, kHeads), slices = nq + slices_of(a.Hk, kHeads);
     const float inv_d = 1.f / (float)a.D;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[i * kVecThreads] = make_float4(0.f, 0.f, 0.f, 0.f);
+    vec_weights(a, weights);
+
 #pragma unroll 1
-    for (int64_t row = first; row < stop; row += kVecWarps) {
-        int pos = 0;
-        if (a.R > 0) pos = at.row(a, row, false).pos;
-        float c[8], s[8];
-        if (l.turns) {
+    for (int batch = blockIdx.x; batch < v.batches; batch += gridDim.x) {
+        const int64_t row0 = (int64_t)batch * v.tokens;
+        const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
+        Item it(warp, slices);
+        Two<T> raw[U], raw_g[U];
+        bool isq = true;
+        int left = 0;
+        int64_t dense = 0;
+        const T *in = nullptr, *dout = nullptr;
+        auto aim = [&] {
+            isq = it.slice < nq;
+            const int head = (isq ? it.slice : it.slice - nq) * kHeads + sub, heads = isq ? a.Hq : a.Hk;
+            left = it.token < count && l.in ? heads - head : 0;
+            dense = ((row0 + it.token) * heads + head) * a.D;
+            dout = static_cast<const T *>(isq ? a.dq_out : a.dk_out) + dense;
+            in = static_cast<const T *>(isq ? a.q : a.k) + (row0 + it.token) * (isq ? a.q_stride : a.k_stride) + (int64_t)head * a.D;
+        };
+        auto fetch = [&](int u) {
+            raw_g[u].load(dout, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left);
+            raw[u].load(in, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left && (isq ? a.qw : a.kw) != nullptr);
+        };
+        aim();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) turn(freq[e], pos, c[e], s[e]);
+        for (int u = 0; u < U; ++u) fetch(u);
+        if (a.R > 0) vec_places(a, row0, count, place);
+        __syncthreads();
+        if (a.R > 0) {
+            vec_angles(a, count, place, table);
+            __syncthreads();
         }
+#pragma unroll 1
+        while (it.token < count) {
+            const bool now_q = isq, normed = (isq ? a.qw : a.kw) != nullptr;
+            const int now_left = left;
+            T *out = static_cast<T *>(isq ? a.q_out : a.k_out) + dense;
+            f2 wt[8], c[4], s[4], n[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float g[16], x[16];
-            raw_g[u].unpack(g);
-            if (w != nullptr) raw[u].unpack(x);
-            if (row + kVecWarps < stop) fetch(u, row + kVecWarps);
-            if (l.turns) turn_pairs(g, c, s, a.pairs, -1.f);
-            if (w != nullptr) {
-                float q = 0.f, m = 0.f;
+            for (int i = 0; i < 8; ++i) wt[i] = pk(0.f, 0.f);
+            if (l.in) lane_floats(wt, weights + (isq ? 0 : a.D) + l.o0, weights + (isq ? 0 : a.D) + l.o1);
+            if (l.turns) {
+                const float *from = table + it.token * (a.R / 2) * 3 + 8 * j;
+                lane_angles(c, from);
+                lane_angles(s, from + a.R / 2);
+                lane_angles(n, from + a.R);
+            }
+            it.step(slices);
+            aim();
+            f2 total[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    q = fmaf(x[i], x[i], q);
-                    m = fmaf(g[i] * x[i], wt[i], m);
+            for (int i = 0; i < 8; ++i) total[i] = pk(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                f2 g[8], x[8];
+                raw_g[u].unpack(g);
+                raw[u].unpack(x);
+                fetch(u);
+                if (l.turns) turn_pairs(g, c, n, s, a.pairs);  // back
+                if (normed) {
+                    f2 q = mul2(x[0], x[0]), m = pk(0.f, 0.f);
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
+                    const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
+                    const f2 by = pk(inv, inv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const f2 gx = mul2(g[i], x[i]);
+                        m = fma2(gx, wt[i], m);
+                        total[i] = fma2(gx, by, total[i]);
+                        g[i] = mul2(g[i], mul2(wt[i], by));
+                    }
+                    const float k = row_sum<LPR>(hsum2(m)) * inv_d * inv * inv * inv;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = fma2(x[i], pk(-k, -k), g[i]);
                 }
-                q = row_sum<LPR>(q);
-                m = row_sum<LPR>(m);
-                const float inv = rsqrtf(q * inv_d + a.eps);
-                m *= inv_d * inv * inv;
+                if (u * kAtOnce < now_left) Two<T>::store(out, (int64_t)u * kAtOnce * a.D, l, g);
+            }
+            if (normed) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    sum[i] = fmaf(g[i] * x[i], inv, sum[i]);
-                    g[i] = inv * (g[i] * wt[i] - x[i] * m);
+                for (int i = 0; i < 4; ++i) {
+                    float4 &to = sums[((now_q ? 0 : 4) + i) * kVecThreads];
+                    float t[4];
+                    upk(total[2 * i], t[0], t[1]);
+                    upk(total[2 * i + 1], t[2], t[3]);
+                    to = make_float4(to.x + t[0], to.y + t[1], to.z + t[2], to.w + t[3]);
                 }
             }
-            if (ok(u)) Two<T>::store(out, (row * heads + sh.head0 + u * kAtOnce + sub) * a.D, l, g);
         }
+        __syncthreads();  // the angles of the next batch go where these are
     }
     if (a.partial == nullptr) return;
-    // the weight's gradient of this block: over the rows of a warp, then its warps in order; zeros for the other weight
+    // over the rows of a warp, then the block's warps in order
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const float4 t4 = sums[(4 * part + i) * kVecThreads];
+            float t[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+            for (int h = 0; h < 4; ++h) {
 #pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        if (sub == 0 && l.in) red[warp][(i < 8 ? l.o0 : l.o1 - 8) + i] = sum[i];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kVecWarps) {
-        float t = 0.f;
-        if ((i < a.D) == isq) {
-#pragma unroll
-            for (int v = 0; v < kVecWarps; ++v) t += red[v][i < a.D ? i : i - a.D];
+                for (int o = LPR; o < 32; o <<= 1) t[h] += __shfl_xor_sync(0xffffffffu, t[h], o);
+                if (sub == 0 && l.in) table[warp * a.D + (i < 2 ? l.o0 : l.o1 - 8) + 4 * i + h] = t[h];
+            }
         }
-        a.partial[(int64_t)blockIdx.x * 2 * a.D + i] = t;
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.D; i += kVecThreads) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < kVecWarps; ++w) t += table[w * a.D + i];
+            a.partial[((int64_t)blockIdx.x * 2 + part) * a.D + i] = t;
+        }
+        __syncthreads();
     }
 }
 
-// Rows of the cache into contiguous ones: a lane has 16 channels of a row.
+// Rows of the cache into contiguous ones: a lane has 16 channels of a row, and U rows on their way at a time. A block takes
+// some tokens; their rows in the order (token, keys or values, head).
 template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(32 * kVecWarps) vec_read_kernel(const __grid_constant__ HeadArgs a, int slices, int tokens) {
+__global__ void __launch_bounds__(kVecThreads) vec_read_kernel(const __grid_constant__ VecArgs v) {
     constexpr int kAtOnce = 32 / LPR;
+    __shared__ Place place[kVecThreads];
+    const HeadArgs &a = v.h;
+    const Cache &c = a.cache;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / LPR, j = lane % LPR;
-    const Cache &c = a.cache;
-    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, 32 * kVecWarps);
-    const int half = slices / 2, slice = blockIdx.x % slices;
-    const bool isv = slice >= half;
-    const int head0 = (isv ? slice - half : slice) * U * kAtOnce;
-    const int64_t first = (int64_t)(blockIdx.x / slices) * tokens + warp;
-    int64_t stop = (int64_t)(blockIdx.x / slices + 1) * tokens;
-    if (stop > a.seqs.rows) stop = a.seqs.rows;
+    if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, kVecThreads);
+    const int64_t row0 = (int64_t)blockIdx.x * v.tokens;
+    const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
+    vec_places(a, row0, count, place);
+    __syncthreads();
     const LaneAt l{16 * j, 16 * j + 8, 16 * j < c.D, false};
-    void *out = isv ? a.q_out : a.k_out;
-    const void *base = isv ? c.v : c.k;
-    TokenAt at;
+    const int each = 2 * a.Hk, all = count * each;
 #pragma unroll 1
-    for (int64_t row = first; row < stop; row += kVecWarps) {
-        const RowAt r = at.row(a, row, true);
+    for (int first = warp * U * kAtOnce; first < all; first += kVecWarps * U * kAtOnce) {
         uint4 q[U];
         uint32_t e[U];
         Two<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int head = head0 + u * kAtOnce + sub;
-            const bool ok = l.in && head < a.Hk && r.page >= 0;
-            const int64_t from = ok ? cache_row(c, r.page, head, r.slot) : 0;
+            const int i = first + u * kAtOnce + sub, token = i / each, h = i - token * each;
+            const bool isv = h >= a.Hk;
+            const int head = isv ? h - a.Hk : h;
+            Place p{0, -1, 0};
+            if (i < all) p = place[token];
+            const bool ok = l.in && p.page >= 0;
+            const int64_t from = ok ? cache_row(c, p.page, head, p.slot) : 0;
+            const void *base = isv ? c.v : c.k;
             if (c.ks != nullptr) {
                 q[u] = make_uint4(0u, 0u, 0u, 0u);
                 e[u] = 0u;
                 if (ok) {
                     q[u] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + from * c.D + l.o0);
-                    e[u] = (isv ? c.vs : c.ks)[cache_scale(c, r.page, head, r.slot)];
+                    e[u] = (isv ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)];
                 }
             } else {
                 raw[u].load(base, from * c.D, l, ok);
@@ -608,21 +751,24 @@ __global__ void __launch_bounds__(32 * kVecWarps) vec_read_kernel(const __grid_c
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int head = head0 + u * kAtOnce + sub;
-            if (!l.in || head >= a.Hk) continue;
-            const int64_t to = (row * a.Hk + head) * c.D;
+            const int i = first + u * kAtOnce + sub, token = i / each, h = i - token * each;
+            if (!l.in || i >= all) continue;
+            const bool isv = h >= a.Hk;
+            void *out = isv ? a.q_out : a.k_out;
+            const int64_t to = ((row0 + token) * a.Hk + (isv ? h - a.Hk : h)) * c.D;
             if (c.ks != nullptr) {
-                const float unit = __uint_as_float(e[u] << 23);
+                const f2 unit = pk(__uint_as_float(e[u] << 23), __uint_as_float(e[u] << 23));
                 const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-                float f[16];
+                f2 x[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e4m3_to_f(w[i] & 0xffffu, f[4 * i], f[4 * i + 1]);
-                    e4m3_to_f(w[i] >> 16, f[4 * i + 2], f[4 * i + 3]);
+                for (int k = 0; k < 4; ++k) {
+                    float f[4];
+                    e4m3_to_f(w[k] & 0xffffu, f[0], f[1]);
+                    e4m3_to_f(w[k] >> 16, f[2], f[3]);
+                    x[2 * k] = mul2(pk(f[0], f[1]), unit);
+                    x[2 * k + 1] = mul2(pk(f[2], f[3]), unit);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] *= unit;
-                Two<T>::store(out, to, l, f);
+                Two<T>::store(out, to, l, x);
             } else {
                 raw[u].a.store(static_cast<T *>(out) + to + l.o0);
                 raw[u].b.store(static_cast<T *>(out) + to + l.o1);
@@ -700,55 +846,60 @@ bool vec_ok(const HeadArgs &a, bool f32, const void *const *ptrs, int n) {
     return ok;
 }
 
-// How rows are shared out: `u` groups of heads to a warp, `tokens` tokens to a block.
+// How tokens are shared out: `u` groups of rows to a warp.
 struct VecPlan {
-    int lpr, u, slices, tokens;
+    VecArgs v;
+    int lpr, u;
     unsigned blocks;
+    size_t smem;
 };
-VecPlan vec_plan(const HeadArgs &a, int u, int blocks_per_sm) {
+VecPlan vec_plan(const HeadArgs &a, int u) {
     VecPlan p;
+    p.v.h = a;
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
-    const int at_once = 32 / p.lpr;
-    auto slices = [&](int n) { return slices_of(a.Hq, n * at_once) + slices_of(a.Hk, n * at_once) + slices_of(a.Hv, n * at_once); };
-    const int64_t most = (int64_t)sm_count() * blocks_per_sm;
-    // few tokens: a warp for each group of heads
     p.u = u;
-    if (ceil_div(a.seqs.rows, kVecWarps) * slices(u) < most) p.u = 1;
-    p.slices = slices(p.u);
-    // the tokens of a block: a multiple of its warps, so that `most` blocks or fewer cover all
-    const int64_t chunks = most / p.slices < 1 ? 1 : most / p.slices;
-    p.tokens = (int)(ceil_div(ceil_div(a.seqs.rows, chunks), kVecWarps) * kVecWarps);
-    if (p.tokens < kVecWarps) p.tokens = kVecWarps;
-    p.blocks = (unsigned)(ceil_div(a.seqs.rows, p.tokens) * p.slices);
+    p.v.tokens = 16;
+    // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy
+    const int64_t sms = sm_count();
+    if (a.seqs.rows < 2 * sms * p.v.tokens) {
+        const int groups = slices_of(a.Hq + a.Hk + a.Hv, 32 / p.lpr);
+        p.v.tokens = groups >= kVecWarps ? 1 : kVecWarps / groups;
+        while (p.v.tokens < 16 && ceil_div(a.seqs.rows, p.v.tokens) > 2 * sms) p.v.tokens *= 2;
+        if (a.seqs.rows * groups < 2 * sms * kVecWarps * u) p.u = 1;
+    }
+    p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
+    p.blocks = (unsigned)p.v.batches;
+    p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 2 * a.D) * sizeof(float);  // at most 26 KB
     return p;
 }
 
-#define KDA_VEC_LAUNCH(kernel, T, U)                                                                                \
-    switch (p.lpr) {                                                                                                \
-        case 4: kernel<T, 4, U><<<p.blocks, 32 * kVecWarps, 0, stream>>>(a, p.slices, p.tokens); break;             \
-        case 8: kernel<T, 8, U><<<p.blocks, 32 * kVecWarps, 0, stream>>>(a, p.slices, p.tokens); break;             \
-        default: kernel<T, 16, U><<<p.blocks, 32 * kVecWarps, 0, stream>>>(a, p.slices, p.tokens); break;           \
+#define KDA_VEC_LAUNCH(kernel, T, U)                                                           \
+    switch (p.lpr) {                                                                           \
+        case 4: kernel<T, 4, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
+        case 8: kernel<T, 8, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
+        default: kernel<T, 16, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;      \
     }
-#define KDA_VEC(kernel, U)                                                                                          \
-    if (f32) {                                                                                                      \
-        if (p.u == 1) {                                                                                             \
-            KDA_VEC_LAUNCH(kernel, float, 1)                                                                        \
-        } else {                                                                                                    \
-            KDA_VEC_LAUNCH(kernel, float, U / 2)                                                                    \
-        }                                                                                                           \
-    } else if (p.u == 1) {                                                                                          \
-        KDA_VEC_LAUNCH(kernel, bf16, 1)                                                                             \
-    } else {                                                                                                        \
-        KDA_VEC_LAUNCH(kernel, bf16, U)                                                                             \
-    }                                                                                                               \
+// U: groups of a warp for bf16, half as many for fp32, or one
+#define KDA_VEC(kernel, U)                             \
+    if (f32) {                                         \
+        if (p.u == 1) {                                \
+            KDA_VEC_LAUNCH(kernel, float, 1)           \
+        } else {                                       \
+            KDA_VEC_LAUNCH(kernel, float, (U) / 2)     \
+        }                                              \
+    } else if (p.u == 1) {                             \
+        KDA_VEC_LAUNCH(kernel, bf16, 1)                \
+    } else {                                           \
+        KDA_VEC_LAUNCH(kernel, bf16, U)                \
+    }                                                  \
     return cudaGetLastError();
 
 cudaError_t launch_rows(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     const void *ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 5)) {
-        const VecPlan p = vec_plan(a, f32 ? 2 : 4, 3);
-        KDA_VEC(vec_rows_kernel, 4)
+        const VecPlan p = vec_plan(a, f32 ? FWD_U / 2 : FWD_U);
+        KDA_VEC(vec_rows_kernel, FWD_U)
     }
     const unsigned blocks = any_blocks(a.seqs.rows * (a.Hq + a.Hk + a.Hv));
     if (f32)
@@ -762,10 +913,20 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     const void *ptrs[] = {a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 2)) {
-        HeadArgs b = a;  // slices of keys, then of values
-        b.Hv = b.Hk;
-        const VecPlan p = vec_plan(b, f32 ? 2 : 4, 4);
-        KDA_VEC(vec_read_kernel, 4)
+        VecPlan p = vec_plan(a, 2);
+        // as many tokens as a block's warps have rows on their way
+        const int rows = kVecWarps * (f32 ? 4 : 8) * 32 / p.lpr;
+        int tokens = rows / (2 * a.Hk);
+        p.u = 2;
+        if (ceil_div(a.seqs.rows, tokens < 1 ? 1 : tokens) < 2 * sm_count()) {
+            p.u = 1;
+            tokens = kVecWarps * 32 / p.lpr / (2 * a.Hk);
+        }
+        p.v.tokens = tokens < 1 ? 1 : tokens > kVecThreads ? kVecThreads : tokens;
+        p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
+        p.blocks = (unsigned)p.v.batches;
+        p.smem = 0;
+        KDA_VEC(vec_read_kernel, 8)
     }
     const unsigned blocks = any_blocks(a.seqs.rows * 2 * a.Hk);
     if (f32)
@@ -805,8 +966,20 @@ BwdPlan bwd_plan(const kda_qk_norm_bwd_params &p, int64_t rows, unsigned int *er
     const void *ptrs[] = {p.f.q, p.f.k, p.dq_out, p.dk_out, p.dq, p.dk};
     q.vec = rows != 0 && vec_ok(q.a, f32, ptrs, 6);
     if (q.vec) {
-        q.p = vec_plan(q.a, f32 ? 1 : 2, 2);
+        q.p = vec_plan(q.a, f32 ? 1 : 2);
+        const unsigned most = (unsigned)sm_count() * 2;
+        // at most as many tokens at a time as there is room for the angles of (46 KB in all)
+        int cap = (46 * 1024 / 4 - 2 * p.f.D - 32 * kVecThreads) / (p.f.R / 2 * 3 + 1);
+        cap = cap > kVecTokens ? kVecTokens : cap;
+        if (q.p.blocks > most || q.p.v.tokens > cap) {
+            const int64_t times = ceil_div(rows, (int64_t)most * cap);  // the same for every block
+            q.p.v.tokens = (int)ceil_div(rows, most * times);
+            q.p.v.batches = (int)ceil_div(rows, q.p.v.tokens);
+            q.p.blocks = q.p.v.batches < (int)most ? (unsigned)q.p.v.batches : most;
+        }
         q.blocks = q.p.blocks;
+        const int table = q.p.v.tokens * (p.f.R / 2) * 3;
+        q.p.smem = (size_t)(2 * p.f.D + 32 * kVecThreads + (table > kVecWarps * p.f.D ? table : kVecWarps * p.f.D)) * sizeof(float);
     } else {
         const int64_t most = (int64_t)sm_count() * 4, need = ceil_div(rows * (p.f.q_heads + p.f.k_heads), kWarps);
         q.blocks = (unsigned)(need < 1 ? 1 : need < most ? need : most);
@@ -819,7 +992,8 @@ cudaError_t launch_bwd(const BwdPlan &q, bool f32, cudaStream_t stream) {
     const HeadArgs &a = q.a;
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     if (q.vec) {
-        const VecPlan &p = q.p;
+        VecPlan p = q.p;
+        p.v.h = a;
         KDA_VEC(vec_rows_bwd_kernel, 2)
     }
     if (f32)
