@@ -8,9 +8,10 @@
 
 #include "cache_common.cuh"
 
-#ifndef FWD_U
+#ifndef FWD_BLOCKS
+#define FWD_BLOCKS 3
+#define BWD_BLOCKS 2
 #define FWD_U 2
-#define FWD_BLOCKS 2
 #endif
 namespace kda {
 namespace {
@@ -398,16 +399,19 @@ struct Two {
         store_vec<T, 8>(static_cast<T *>(base) + at + l.o1, t);
     }
 };
-// 16 floats of shared memory at the lane's chunks (16-byte aligned).
-__device__ __forceinline__ void lane_floats(f2 (&x)[8], const float *a, const float *b) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 p = reinterpret_cast<const float4 *>(a)[i], q = reinterpret_cast<const float4 *>(b)[i];
-        x[2 * i] = pk(p.x, p.y);
-        x[2 * i + 1] = pk(p.z, p.w);
-        x[4 + 2 * i] = pk(q.x, q.y);
-        x[5 + 2 * i] = pk(q.z, q.w);
-    }
+// Floats of shared memory as pairs, loaded where they are used (a copy in registers for all rows of a slice would cost a block
+// on each SM).
+__device__ __forceinline__ void lds4(f2 &x, f2 &y, uint32_t at) { asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at)); }
+// eight of them, and 16 at the lane's chunks
+__device__ __forceinline__ void lds8(f2 (&x)[4], uint32_t at) {
+    lds4(x[0], x[1], at);
+    lds4(x[2], x[3], at + 16);
+}
+__device__ __forceinline__ void lds16(f2 (&x)[8], uint32_t row, const LaneAt &l) {
+    lds4(x[0], x[1], row + 4 * l.o0);
+    lds4(x[2], x[3], row + 4 * l.o0 + 16);
+    lds4(x[4], x[5], row + 4 * l.o1);
+    lds4(x[6], x[7], row + 4 * l.o1 + 16);
 }
 
 template <int LPR>
@@ -417,32 +421,33 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The lane's 8 pairs by their angles: cosines, sines and negative sines of pairs 2 i, 2 i + 1 in c[i], s[i], n[i].
-__device__ __forceinline__ void turn_pairs(f2 (&x)[8], const f2 (&c)[4], const f2 (&s)[4], const f2 (&n)[4], bool pairs) {
+// The lane's 8 pairs by their angles: cosines, sines and negative sines of its pairs at shared addresses c, s, n.
+__device__ __forceinline__ void turn_pairs(f2 (&x)[8], uint32_t c_at, uint32_t s_at, uint32_t n_at, bool pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (pairs) {  // both numbers of a pair in one register
-            float c0, c1, s0, s1, n0, n1, a, b;
-            upk(c[i], c0, c1);
-            upk(s[i], s0, s1);
-            upk(n[i], n0, n1);
-            upk(x[2 * i], a, b);
-            x[2 * i] = fma2(pk(b, a), pk(n0, s0), mul2(x[2 * i], pk(c0, c0)));
-            upk(x[2 * i + 1], a, b);
-            x[2 * i + 1] = fma2(pk(b, a), pk(n1, s1), mul2(x[2 * i + 1], pk(c1, c1)));
-        } else {
-            const f2 a = x[i], b = x[4 + i];
-            x[i] = fma2(b, n[i], mul2(a, c[i]));
-            x[4 + i] = fma2(a, s[i], mul2(b, c[i]));
+    for (int h = 0; h < 2; ++h) {
+        f2 c[2], s[2], n[2];
+        lds4(c[0], c[1], c_at + 16 * h);
+        lds4(s[0], s[1], s_at + 16 * h);
+        lds4(n[0], n[1], n_at + 16 * h);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = 2 * h + k;
+            if (pairs) {  // both numbers of a pair in one register
+                float c0, c1, s0, s1, n0, n1, a, b;
+                upk(c[k], c0, c1);
+                upk(s[k], s0, s1);
+                upk(n[k], n0, n1);
+                upk(x[2 * i], a, b);
+                x[2 * i] = fma2(pk(b, a), pk(n0, s0), mul2(x[2 * i], pk(c0, c0)));
+                upk(x[2 * i + 1], a, b);
+                x[2 * i + 1] = fma2(pk(b, a), pk(n1, s1), mul2(x[2 * i + 1], pk(c1, c1)));
+            } else {
+                const f2 a = x[i], b = x[4 + i];
+                x[i] = fma2(b, n[k], mul2(a, c[k]));
+                x[4 + i] = fma2(a, s[k], mul2(b, c[k]));
+            }
         }
     }
-}
-__device__ __forceinline__ void lane_angles(f2 (&x)[4], const float *from) {
-    const float4 p = reinterpret_cast<const float4 *>(from)[0], q = reinterpret_cast<const float4 *>(from)[1];
-    x[0] = pk(p.x, p.y);
-    x[1] = pk(p.z, p.w);
-    x[2] = pk(q.x, q.y);
-    x[3] = pk(q.z, q.w);
 }
 
 template <int LPR>
@@ -474,8 +479,11 @@ __device__ __forceinline__ void vec_put_e4m3(const Cache &c, bool value, const f
     if (j == 0) (value ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)] = (uint8_t)(e + 127);
 }
 
-template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const __grid_constant__ VecArgs v) {
+// Queries and keys normed and turned (kNorm), that with keys and values into the cache (kStep), or the latter alone (kWrite).
+enum Mode { kNorm, kStep, kWrite };
+
+template <typename T, int LPR, int U, int MODE>
+__global__ void __launch_bounds__(kVecThreads, MODE == kWrite ? 4 : FWD_BLOCKS) vec_rows_kernel(const __grid_constant__ VecArgs v) {
     constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
     __shared__ Place place[kVecTokens];
     extern __shared__ __align__(16) float mem[];
@@ -513,9 +521,9 @@ __global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const
 #pragma unroll
     for (int u = 0; u < U; ++u) fetch(u);
     vec_places(a, row0, count, place);
-    vec_weights(a, weights);
+    if constexpr (MODE != kWrite) vec_weights(a, weights);
     __syncthreads();
-    if (a.R > 0) {
+    if (MODE != kWrite && a.R > 0) {
         vec_angles(a, count, place, table);
         __syncthreads();
     }
@@ -524,21 +532,16 @@ __global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const
     while (it.token < count) {
         const int now_part = part, now_head = head, now_left = left;
         const LaneAt now = l;
-        const bool isq = part == 0, isv = part == 2, turns = !isv && l.turns;
+        const bool isq = part == 0, isv = part == 2, turns = MODE != kWrite && !isv && l.turns;
         const int heads = isq ? a.Hq : a.Hk;
-        const bool normed = !isv && (isq ? a.qw : a.kw) != nullptr;
+        const bool normed = MODE != kWrite && !isv && (isq ? a.qw : a.kw) != nullptr;
         T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
-        const bool to_out = !isv && out != nullptr;
-        out += ((row0 + it.token) * heads + now_head) * a.D;
-        const Place p = place[it.token];
-        f2 wt[8], c[4], s[4], n[4];
-        if (normed && now.in) lane_floats(wt, weights + (isq ? 0 : a.D) + now.o0, weights + (isq ? 0 : a.D) + now.o1);
-        if (turns) {
-            const float *from = table + it.token * (a.R / 2) * 3 + 8 * j;
-            lane_angles(c, from);
-            lane_angles(s, from + a.R / 2);
-            lane_angles(n, from + a.R);
-        }
+        const bool to_out = MODE != kWrite && !isv && out != nullptr;
+        if (MODE != kWrite) out += ((row0 + it.token) * heads + now_head) * a.D;
+        Place p{0, -1, 0};
+        if constexpr (MODE != kNorm) p = place[it.token];
+        const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 4 * a.D);
+        const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 8 * j);
         it.step(slices);
         aim();
 #pragma unroll
@@ -553,12 +556,16 @@ __global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const
                 for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
                 const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
                 const f2 by = pk(inv, inv);
+                if (now.in) {
+                    f2 wt[8];
+                    lds16(wt, wt_at, now);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(wt[i], by));
+                    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(wt[i], by));
+                }
             }
-            if (turns) turn_pairs(x, c, s, n, a.pairs);
+            if (turns) turn_pairs(x, angles, angles + 2 * a.R, angles + 4 * a.R, a.pairs);
             if (to_out && ok) Two<T>::store(out, (int64_t)u * kAtOnce * a.D, now, x);
-            if (a.cached && now_part != 0) {
+            if (MODE != kNorm && now_part != 0) {
                 const int h = now_head + u * kAtOnce;
                 if (a.cache.ks != nullptr)
                     vec_put_e4m3<LPR>(a.cache, isv, x, now, ok, p, h, j);
@@ -571,7 +578,7 @@ __global__ void __launch_bounds__(kVecThreads, FWD_BLOCKS) vec_rows_kernel(const
 
 // The gradient: blocks go through batches of tokens, each lane adds up the weights' gradients at its channels.
 template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __grid_constant__ VecArgs v) {
+__global__ void __launch_bounds__(kVecThreads, BWD_BLOCKS) vec_rows_bwd_kernel(const __grid_constant__ VecArgs v) {
     constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
     __shared__ Place place[kVecTokens];
     extern __shared__ __align__(16) float mem[];
@@ -626,16 +633,8 @@ __global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __gr
             const bool now_q = isq, normed = (isq ? a.qw : a.kw) != nullptr;
             const int now_left = left;
             T *out = static_cast<T *>(isq ? a.q_out : a.k_out) + dense;
-            f2 wt[8], c[4], s[4], n[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) wt[i] = pk(0.f, 0.f);
-            if (l.in) lane_floats(wt, weights + (isq ? 0 : a.D) + l.o0, weights + (isq ? 0 : a.D) + l.o1);
-            if (l.turns) {
-                const float *from = table + it.token * (a.R / 2) * 3 + 8 * j;
-                lane_angles(c, from);
-                lane_angles(s, from + a.R / 2);
-                lane_angles(n, from + a.R);
-            }
+            const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 4 * a.D);
+            const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 8 * j);
             it.step(slices);
             aim();
             f2 total[8];
@@ -647,8 +646,12 @@ __global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __gr
                 raw_g[u].unpack(g);
                 raw[u].unpack(x);
                 fetch(u);
-                if (l.turns) turn_pairs(g, c, n, s, a.pairs);  // back
+                if (l.turns) turn_pairs(g, angles, angles + 4 * a.R, angles + 2 * a.R, a.pairs);  // back
                 if (normed) {
+                    f2 wt[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) wt[i] = pk(0.f, 0.f);
+                    if (l.in) lds16(wt, wt_at, l);
                     f2 q = mul2(x[0], x[0]), m = pk(0.f, 0.f);
 #pragma unroll
                     for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
@@ -708,8 +711,8 @@ __global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __gr
 
 // Rows of the cache into contiguous ones: a lane has 16 channels of a row, and U rows on their way at a time. A block takes
 // some tokens; their rows in the order (token, keys or values, head).
-template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(kVecThreads) vec_read_kernel(const __grid_constant__ VecArgs v) {
+template <typename T, int LPR, int U, int SCALED>
+__global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(const __grid_constant__ VecArgs v) {
     constexpr int kAtOnce = 32 / LPR;
     __shared__ Place place[kVecThreads];
     const HeadArgs &a = v.h;
@@ -725,20 +728,29 @@ __global__ void __launch_bounds__(kVecThreads) vec_read_kernel(const __grid_cons
     const int each = 2 * a.Hk, all = count * each;
 #pragma unroll 1
     for (int first = warp * U * kAtOnce; first < all; first += kVecWarps * U * kAtOnce) {
-        uint4 q[U];
-        uint32_t e[U];
-        Two<T> raw[U];
+        uint4 q[SCALED ? U : 1];
+        uint32_t e[SCALED ? U : 1];
+        Two<T> raw[SCALED ? 1 : U];
+        // row `first + sub` and those kAtOnce further on: head h of the token's keys and values
+        int token = (first + sub) / each, h = first + sub - token * each;
+        const int token0 = token, h0 = h;
+        auto next = [&] {
+            h += kAtOnce;
+            while (h >= each) {
+                h -= each;
+                ++token;
+            }
+        };
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = first + u * kAtOnce + sub, token = i / each, h = i - token * each;
             const bool isv = h >= a.Hk;
-            const int head = isv ? h - a.Hk : h;
             Place p{0, -1, 0};
-            if (i < all) p = place[token];
+            if (token < count) p = place[token];
             const bool ok = l.in && p.page >= 0;
+            const int head = isv ? h - a.Hk : h;
             const int64_t from = ok ? cache_row(c, p.page, head, p.slot) : 0;
             const void *base = isv ? c.v : c.k;
-            if (c.ks != nullptr) {
+            if constexpr (SCALED) {
                 q[u] = make_uint4(0u, 0u, 0u, 0u);
                 e[u] = 0u;
                 if (ok) {
@@ -748,31 +760,35 @@ __global__ void __launch_bounds__(kVecThreads) vec_read_kernel(const __grid_cons
             } else {
                 raw[u].load(base, from * c.D, l, ok);
             }
+            next();
         }
+        token = token0;
+        h = h0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = first + u * kAtOnce + sub, token = i / each, h = i - token * each;
-            if (!l.in || i >= all) continue;
-            const bool isv = h >= a.Hk;
-            void *out = isv ? a.q_out : a.k_out;
-            const int64_t to = ((row0 + token) * a.Hk + (isv ? h - a.Hk : h)) * c.D;
-            if (c.ks != nullptr) {
-                const f2 unit = pk(__uint_as_float(e[u] << 23), __uint_as_float(e[u] << 23));
-                const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-                f2 x[8];
+            if (l.in && token < count) {
+                const bool isv = h >= a.Hk;
+                T *out = static_cast<T *>(isv ? a.q_out : a.k_out) + ((row0 + token) * a.Hk + (isv ? h - a.Hk : h)) * c.D;
+                if constexpr (SCALED) {
+                    // a scale of 2^-127 (byte 0), which no row written here has, is below fp32's normal numbers: 0
+                    const f2 unit = pk(__uint_as_float(e[u] << 23), __uint_as_float(e[u] << 23));
+                    const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                    f2 x[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f[4];
-                    e4m3_to_f(w[k] & 0xffffu, f[0], f[1]);
-                    e4m3_to_f(w[k] >> 16, f[2], f[3]);
-                    x[2 * k] = mul2(pk(f[0], f[1]), unit);
-                    x[2 * k + 1] = mul2(pk(f[2], f[3]), unit);
+                    for (int k = 0; k < 4; ++k) {
+                        float f[4];
+                        e4m3_to_f(w[k] & 0xffffu, f[0], f[1]);
+                        e4m3_to_f(w[k] >> 16, f[2], f[3]);
+                        x[2 * k] = mul2(pk(f[0], f[1]), unit);
+                        x[2 * k + 1] = mul2(pk(f[2], f[3]), unit);
+                    }
+                    Two<T>::store(out, 0, l, x);
+                } else {
+                    raw[u].a.store(out + l.o0);
+                    raw[u].b.store(out + l.o1);
                 }
-                Two<T>::store(out, to, l, x);
-            } else {
-                raw[u].a.store(static_cast<T *>(out) + to + l.o0);
-                raw[u].b.store(static_cast<T *>(out) + to + l.o1);
             }
+            next();
         }
     }
 }
@@ -873,33 +889,40 @@ VecPlan vec_plan(const HeadArgs &a, int u) {
     return p;
 }
 
-#define KDA_VEC_LAUNCH(kernel, T, U)                                                           \
-    switch (p.lpr) {                                                                           \
-        case 4: kernel<T, 4, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
-        case 8: kernel<T, 8, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
-        default: kernel<T, 16, U><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;      \
+#define KDA_VEC_LAUNCH(kernel, ...)                                                                     \
+    switch (p.lpr) {                                                                                    \
+        case 4: kernel(4, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;          \
+        case 8: kernel(8, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;          \
+        default: kernel(16, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
     }
+#define KDA_VEC_ROWS(LPR, T, U, M) vec_rows_kernel<T, LPR, U, M>
+#define KDA_VEC_BWD(LPR, T, U, M) vec_rows_bwd_kernel<T, LPR, U>
+#define KDA_VEC_READ(LPR, T, U, M) vec_read_kernel<T, LPR, U, M>
 // U: groups of a warp for bf16, half as many for fp32, or one
-#define KDA_VEC(kernel, U)                             \
-    if (f32) {                                         \
-        if (p.u == 1) {                                \
-            KDA_VEC_LAUNCH(kernel, float, 1)           \
-        } else {                                       \
-            KDA_VEC_LAUNCH(kernel, float, (U) / 2)     \
-        }                                              \
-    } else if (p.u == 1) {                             \
-        KDA_VEC_LAUNCH(kernel, bf16, 1)                \
-    } else {                                           \
-        KDA_VEC_LAUNCH(kernel, bf16, U)                \
-    }                                                  \
-    return cudaGetLastError();
+#define KDA_VEC(kernel, U, M)                                     \
+    {                                                             \
+        if (f32) {                                                \
+            if (p.u == 1) {                                       \
+                KDA_VEC_LAUNCH(kernel, float, 1, M)               \
+            } else {                                              \
+                KDA_VEC_LAUNCH(kernel, float, (U) / 2, M)         \
+            }                                                     \
+        } else if (p.u == 1) {                                    \
+            KDA_VEC_LAUNCH(kernel, bf16, 1, M)                    \
+        } else {                                                  \
+            KDA_VEC_LAUNCH(kernel, bf16, U, M)                    \
+        }                                                         \
+        return cudaGetLastError();                                \
+    }
 
 cudaError_t launch_rows(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     const void *ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 5)) {
         const VecPlan p = vec_plan(a, f32 ? FWD_U / 2 : FWD_U);
-        KDA_VEC(vec_rows_kernel, FWD_U)
+        if (!a.cached) KDA_VEC(KDA_VEC_ROWS, FWD_U, kNorm)
+        if (a.q != nullptr) KDA_VEC(KDA_VEC_ROWS, FWD_U, kStep)
+        KDA_VEC(KDA_VEC_ROWS, FWD_U, kWrite)
     }
     const unsigned blocks = any_blocks(a.seqs.rows * (a.Hq + a.Hk + a.Hv));
     if (f32)
@@ -915,7 +938,7 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (vec_ok(a, f32, ptrs, 2)) {
         VecPlan p = vec_plan(a, 2);
         // as many tokens as a block's warps have rows on their way
-        const int rows = kVecWarps * (f32 ? 4 : 8) * 32 / p.lpr;
+        const int rows = kVecWarps * (a.cache.ks != nullptr ? 8 : 4) / (f32 ? 2 : 1) * 32 / p.lpr;
         int tokens = rows / (2 * a.Hk);
         p.u = 2;
         if (ceil_div(a.seqs.rows, tokens < 1 ? 1 : tokens) < 2 * sm_count()) {
@@ -926,7 +949,8 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
         p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
         p.blocks = (unsigned)p.v.batches;
         p.smem = 0;
-        KDA_VEC(vec_read_kernel, 8)
+        if (a.cache.ks != nullptr) KDA_VEC(KDA_VEC_READ, 8, 1)
+        KDA_VEC(KDA_VEC_READ, 4, 0)
     }
     const unsigned blocks = any_blocks(a.seqs.rows * 2 * a.Hk);
     if (f32)
@@ -994,7 +1018,7 @@ cudaError_t launch_bwd(const BwdPlan &q, bool f32, cudaStream_t stream) {
     if (q.vec) {
         VecPlan p = q.p;
         p.v.h = a;
-        KDA_VEC(vec_rows_bwd_kernel, 2)
+        KDA_VEC(KDA_VEC_BWD, 2, 0)
     }
     if (f32)
         any_rows_bwd_kernel<float><<<q.blocks, 32 * kWarps, 0, stream>>>(a);
