@@ -8,11 +8,6 @@
 
 #include "cache_common.cuh"
 
-#ifndef FWD_BLOCKS
-#define FWD_BLOCKS 3
-#define BWD_BLOCKS 2
-#define FWD_U 2
-#endif
 namespace kda {
 namespace {
 
@@ -262,10 +257,11 @@ __global__ void __launch_bounds__(32 * kWarps) any_read_kernel(HeadArgs a) {
 }
 
 // ---- rows of whole vectors -------------------------------------------------------------------
-// LPR lanes share a row, 16 channels each as two chunks of 8; a warp holds 32 / LPR rows (heads of one token) at a time
-// and U such groups, of queries, keys or values alone (a slice). A block takes some tokens: first the place and the
-// angles of each are worked out once and left in shared memory, then its warps go through the tokens' slices in turn, the
-// next slice's rows on their way while the ones before are worked on. Arithmetic goes in pairs of fp32.
+// LPR lanes share a row, 16 channels each as two chunks of 8; a warp holds a group of 32 / LPR rows (heads of one token) at
+// a time. A block takes some tokens: first the place and the angles of each are worked out once and left in shared
+// memory, then its warps go through the tokens' slices (a few groups of queries, keys or values), the
+// next rows on their way while some are worked on. Arithmetic goes in pairs of fp32. What bounds it is the
+// instructions: about 130 for a group of 1 KB in and out, with what belongs to a slice worked out once.
 constexpr int kVecWarps = 8;
 constexpr int kVecThreads = 32 * kVecWarps;
 constexpr int kVecTokens = 32;  // of a block at a time, at most
@@ -274,6 +270,7 @@ struct VecArgs {
     HeadArgs h;
     int tokens;   // of a block at a time
     int batches;  // ceil(rows / tokens)
+    int each;     // backward: groups of a slice, at most
 };
 
 // A token's place, in shared memory.
@@ -312,28 +309,26 @@ __device__ __forceinline__ void vec_places(const HeadArgs &a, int64_t row0, int 
     if (a.pos != nullptr) p.pos = a.pos[row];
     place[threadIdx.x] = p;
 }
-// `table`: of each token R / 2 cosines, sines and negative sines.
+// `table`: of each token R / 2 cosines, sines and negative sines; the lane's two quads of each (pairs 8 j .. 8 j + 3 and the four
+// after them) lie beside its neighbours': as they lie in the row, lanes would meet in the same banks.
 __device__ __forceinline__ void vec_angles(const HeadArgs &a, int count, const Place *place, float *table) {
     const int half = a.R / 2;
     for (int i = threadIdx.x; i < count * half; i += kVecThreads) {
         const int t = i / half, e = i - t * half;
         float c, s;
         turn(a.freq[e], place[t].pos, c, s);
-        float *to = table + t * 3 * half + e;
+        float *to = table + t * 3 * half + ((e >> 2 & 1) * (half / 8) + (e >> 3)) * 4 + (e & 3);
         to[0] = c;
         to[half] = s;
         to[2 * half] = -s;
     }
 }
-// The two weights [D] (ones where there is none).
-__device__ __forceinline__ void vec_weights(const HeadArgs &a, float *w) {
-    for (int i = threadIdx.x; i < 2 * a.D; i += kVecThreads) {
-        const float *from = i < a.D ? a.qw : a.kw;
-        w[i] = from != nullptr ? from[i < a.D ? i : i - a.D] : 1.f;
-    }
+// Where a block's share of all tokens begins.
+__device__ __forceinline__ int64_t share_of(int64_t rows, int block) {
+    const int64_t base = rows / gridDim.x, more = rows - base * gridDim.x;
+    return block * base + (block < more ? block : more);
 }
-
-// The slices of heads of a token, `each` heads apiece: of queries, then keys, then values.
+// The slices of heads of a token, `each` heads apiece.
 __host__ __device__ __forceinline__ int slices_of(int heads, int each) { return (heads + each - 1) / each; }
 
 // The lane's place in a row.
@@ -354,14 +349,17 @@ __device__ __forceinline__ LaneAt lane_at(const HeadArgs &a, bool turned, int j)
     return l;
 }
 
-// A warp's way through the (token, slice) items of a block: every kVecWarps-th.
-struct Item {
-    int token, slice;
-    __device__ __forceinline__ Item(int warp, int slices) {
+// A warp's way through a block's (token, slice) items, every kVecWarps-th of them: the warps of a block read neighbouring rows
+// at a time (a run of items for each warp, so that it has whole tokens, is slower: memory pages change more often).
+struct Items {
+    int token, slice, left;
+    __device__ __forceinline__ Items(int warp, int tokens, int slices) {
+        left = (tokens * slices - warp + kVecWarps - 1) / kVecWarps;
         token = warp / slices;
         slice = warp - token * slices;
     }
     __device__ __forceinline__ void step(int slices) {
+        --left;
         slice += kVecWarps;
         while (slice >= slices) {
             slice -= slices;
@@ -370,13 +368,25 @@ struct Item {
     }
 };
 
+// The two weights (ones where there is none), [2][4][LPR] quads: of lane j its first chunk's two and its second chunk's two.
+template <int LPR>
+__device__ __forceinline__ void vec_weights(const HeadArgs &a, float *w) {
+    for (int i = threadIdx.x; i < 2 * 16 * LPR; i += kVecThreads) {
+        const float *from = i < 16 * LPR ? a.qw : a.kw;
+        const int k = i % (16 * LPR), quad = k / (4 * LPR), j = k / 4 % LPR;
+        const LaneAt l = lane_at(a, true, j);
+        w[i] = from != nullptr && l.in ? from[(quad < 2 ? l.o0 : l.o1 - 8) + 4 * quad + (k & 3)] : 1.f;
+    }
+}
+
 template <typename T>
 struct Two {
     Raw<T, 8> a, b;
-    __device__ __forceinline__ void load(const void *base, int64_t at, const LaneAt &l, bool ok) {
+    // of the row at `row`
+    __device__ __forceinline__ void load(const T *row, const LaneAt &l, bool ok) {
         if (ok) {
-            a.load(static_cast<const T *>(base) + at + l.o0);
-            b.load(static_cast<const T *>(base) + at + l.o1);
+            a.load(row + l.o0);
+            b.load(row + l.o1);
         } else {
             a.zero();
             b.zero();
@@ -389,29 +399,24 @@ struct Two {
             x[4 + i] = b.pair(i);
         }
     }
-    static __device__ __forceinline__ void store(void *base, int64_t at, const LaneAt &l, const f2 (&x)[8]) {
+    static __device__ __forceinline__ void store(T *row, const LaneAt &l, const f2 (&x)[8]) {
         float t[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) upk(x[i], t[2 * i], t[2 * i + 1]);
-        store_vec<T, 8>(static_cast<T *>(base) + at + l.o0, t);
+        store_vec<T, 8>(row + l.o0, t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) upk(x[4 + i], t[2 * i], t[2 * i + 1]);
-        store_vec<T, 8>(static_cast<T *>(base) + at + l.o1, t);
+        store_vec<T, 8>(row + l.o1, t);
     }
 };
 // Floats of shared memory as pairs, loaded where they are used (a copy in registers for all rows of a slice would cost a block
 // on each SM).
 __device__ __forceinline__ void lds4(f2 &x, f2 &y, uint32_t at) { asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at)); }
-// eight of them, and 16 at the lane's chunks
-__device__ __forceinline__ void lds8(f2 (&x)[4], uint32_t at) {
-    lds4(x[0], x[1], at);
-    lds4(x[2], x[3], at + 16);
-}
-__device__ __forceinline__ void lds16(f2 (&x)[8], uint32_t row, const LaneAt &l) {
-    lds4(x[0], x[1], row + 4 * l.o0);
-    lds4(x[2], x[3], row + 4 * l.o0 + 16);
-    lds4(x[4], x[5], row + 4 * l.o1);
-    lds4(x[6], x[7], row + 4 * l.o1 + 16);
+// the lane's 16 weights
+template <int LPR>
+__device__ __forceinline__ void lds16(f2 (&x)[8], uint32_t at) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds4(x[2 * i], x[2 * i + 1], at + i * LPR * 16);
 }
 
 template <int LPR>
@@ -421,14 +426,15 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The lane's 8 pairs by their angles: cosines, sines and negative sines of its pairs at shared addresses c, s, n.
-__device__ __forceinline__ void turn_pairs(f2 (&x)[8], uint32_t c_at, uint32_t s_at, uint32_t n_at, bool pairs) {
+// The lane's 8 pairs by their angles: cosines, sines and negative sines of its pairs at shared addresses c, s, n, the second four
+// `hop` bytes on.
+__device__ __forceinline__ void turn_pairs(f2 (&x)[8], uint32_t c_at, uint32_t s_at, uint32_t n_at, int hop, bool pairs) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         f2 c[2], s[2], n[2];
-        lds4(c[0], c[1], c_at + 16 * h);
-        lds4(s[0], s[1], s_at + 16 * h);
-        lds4(n[0], n[1], n_at + 16 * h);
+        lds4(c[0], c[1], c_at + hop * h);
+        lds4(s[0], s[1], s_at + hop * h);
+        lds4(n[0], n[1], n_at + hop * h);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int i = 2 * h + k;
@@ -450,8 +456,9 @@ __device__ __forceinline__ void turn_pairs(f2 (&x)[8], uint32_t c_at, uint32_t s
     }
 }
 
+// A row in 8 bits at `to`, its exponent byte at `scale`.
 template <int LPR>
-__device__ __forceinline__ void vec_put_e4m3(const Cache &c, bool value, const f2 (&x)[8], const LaneAt &l, bool ok, const Place &p, int head, int j) {
+__device__ __forceinline__ void vec_put_e4m3(uint8_t *to, uint8_t *scale, const f2 (&x)[8], const LaneAt &l, bool ok, int j) {
     float top = 0.f;  // an infinity's exponent is 120 by the same rule; NaN is passed over
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -471,115 +478,123 @@ __device__ __forceinline__ void vec_put_e4m3(const Cache &c, bool value, const f
         upk(mul2(x[2 * i + 1], unit), f[2], f[3]);
         w[i] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
     }
-    if (!ok || p.page < 0) return;
-    const int64_t row = cache_row(c, p.page, head, p.slot);
-    uint8_t *to = static_cast<uint8_t *>(value ? c.v : c.k) + row * c.D;
+    if (!ok) return;
     *reinterpret_cast<uint2 *>(to + l.o0) = make_uint2(w[0], w[1]);
     *reinterpret_cast<uint2 *>(to + l.o1) = make_uint2(w[2], w[3]);
-    if (j == 0) (value ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)] = (uint8_t)(e + 127);
+    if (j == 0) *scale = (uint8_t)(e + 127);
 }
 
 // Queries and keys normed and turned (kNorm), that with keys and values into the cache (kStep), or the latter alone (kWrite).
 enum Mode { kNorm, kStep, kWrite };
 
 template <typename T, int LPR, int U, int MODE>
-__global__ void __launch_bounds__(kVecThreads, MODE == kWrite ? 4 : FWD_BLOCKS) vec_rows_kernel(const __grid_constant__ VecArgs v) {
-    constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
+__global__ void __launch_bounds__(kVecThreads, MODE == kWrite ? 4 : 3) vec_rows_kernel(const __grid_constant__ VecArgs v) {
+    constexpr int kAtOnce = 32 / LPR;
     __shared__ Place place[kVecTokens];
     extern __shared__ __align__(16) float mem[];
     const HeadArgs &a = v.h;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / LPR, j = lane % LPR;
     if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, kVecThreads);
-    const int64_t row0 = (int64_t)blockIdx.x * v.tokens;
-    const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
-    float *weights = mem, *table = mem + 2 * a.D;
-    const int nq = slices_of(a.Hq, kHeads), nk = slices_of(a.Hk, kHeads), slices = nq + nk + slices_of(a.Hv, kHeads);
-    const LaneAt lt = lane_at(a, true, j);
-
-    // of the slice whose rows are on their way: queries, keys or values (0, 1, 2), the row's first head and what is left of them
-    Item it(warp, slices);
-    Two<T> raw[U];
-    int part = 0, head = 0, left = 0;
-    const T *in = nullptr;
-    LaneAt l = lt;
-    auto aim = [&] {
-        part = it.slice < nq ? 0 : it.slice < nq + nk ? 1 : 2;
-        head = (it.slice - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * kHeads + sub;
-        left = it.token < count && lt.in ? (part == 0 ? a.Hq : part == 1 ? a.Hk : a.Hv) - head : 0;
-        if (part == 2) {
-            l.o0 = 16 * j;
-            l.o1 = 16 * j + 8;
-        } else {
-            l = lt;
-        }
-        in = static_cast<const T *>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
-             (row0 + it.token) * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (int64_t)head * a.D;
-    };
-    auto fetch = [&](int u) { raw[u].load(in, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left); };
-    aim();
-#pragma unroll
-    for (int u = 0; u < U; ++u) fetch(u);
-    vec_places(a, row0, count, place);
-    if constexpr (MODE != kWrite) vec_weights(a, weights);
-    __syncthreads();
-    if (MODE != kWrite && a.R > 0) {
-        vec_angles(a, count, place, table);
-        __syncthreads();
-    }
+    float *weights = mem, *table = mem + 32 * LPR;
+    constexpr int per = U * kAtOnce;  // heads of a slice
+    const int hop = kAtOnce * a.D;    // channels between groups
+    const int nq = slices_of(a.Hq, per), nk = slices_of(a.Hk, per), slices = nq + nk + slices_of(a.Hv, per);
+    const LaneAt lt = lane_at(a, true, j), lv{16 * j, 16 * j + 8, lt.in, false};
     const float inv_d = 1.f / (float)a.D;
+    if constexpr (MODE != kWrite) vec_weights<LPR>(a, weights);
+
+    // the block's tokens, v.tokens at a time
+    const int64_t end = share_of(a.seqs.rows, blockIdx.x + 1);
 #pragma unroll 1
-    while (it.token < count) {
-        const int now_part = part, now_head = head, now_left = left;
-        const LaneAt now = l;
-        const bool isq = part == 0, isv = part == 2, turns = MODE != kWrite && !isv && l.turns;
-        const int heads = isq ? a.Hq : a.Hk;
-        const bool normed = MODE != kWrite && !isv && (isq ? a.qw : a.kw) != nullptr;
-        T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
-        const bool to_out = MODE != kWrite && !isv && out != nullptr;
-        if (MODE != kWrite) out += ((row0 + it.token) * heads + now_head) * a.D;
-        Place p{0, -1, 0};
-        if constexpr (MODE != kNorm) p = place[it.token];
-        const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 4 * a.D);
-        const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 8 * j);
-        it.step(slices);
+    for (int64_t row0 = share_of(a.seqs.rows, blockIdx.x); row0 < end; row0 += v.tokens) {
+        const int count = end - row0 < v.tokens ? (int)(end - row0) : v.tokens;
+        Items it(warp, count, slices);
+        // of the slice ahead: queries, keys or values (0, 1, 2), the lane's first head, heads from there on, and its row
+        int part = 0, head = 0, left = 0;
+        const T *in = nullptr;
+        auto aim = [&] {
+            part = it.slice < nq ? 0 : it.slice < nq + nk ? 1 : 2;
+            const int first = (it.slice - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * per;
+            const int heads = part == 0 ? a.Hq : part == 1 ? a.Hk : a.Hv;
+            head = first + sub;
+            left = it.left > 0 ? (first + per < heads ? first + per : heads) - head : 0;
+            in = static_cast<const T *>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
+                 (row0 + it.token) * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (int64_t)head * a.D;
+        };
+        Two<T> raw[U];
         aim();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool ok = u * kAtOnce < now_left;
-            f2 x[8];
-            raw[u].unpack(x);
-            fetch(u);
-            if (normed) {
-                f2 q = mul2(x[0], x[0]);
-#pragma unroll
-                for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
-                const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
-                const f2 by = pk(inv, inv);
-                if (now.in) {
-                    f2 wt[8];
-                    lds16(wt, wt_at, now);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(wt[i], by));
+        for (int u = 0; u < U; ++u) raw[u].load(in + u * hop, part == 2 ? lv : lt, left > u * kAtOnce && lt.in);
+        __syncthreads();  // the places and angles of the tokens before are done with
+        vec_places(a, row0, count, place);
+        __syncthreads();
+        if (MODE != kWrite && a.R > 0) {
+            vec_angles(a, count, place, table);
+            __syncthreads();
+        }
+#pragma unroll 1
+        while (it.left > 0) {
+            const bool isq = part == 0, isv = part == 2, turns = MODE != kWrite && !isv && lt.turns;
+            const LaneAt l = isv ? lv : lt;
+            const bool normed = MODE != kWrite && !isv && (isq ? a.qw : a.kw) != nullptr;
+            T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
+            const bool to_out = MODE != kWrite && !isv && out != nullptr;
+            if constexpr (MODE != kWrite) out += ((row0 + it.token) * (isq ? a.Hq : a.Hk) + head) * a.D;
+            const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 64 * LPR) + 16 * j;
+            const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 4 * j);
+            // the row's place in the cache
+            bool put = false;
+            uint8_t *to = nullptr, *scale = nullptr;
+            if constexpr (MODE != kNorm) {
+                const Place p = place[it.token];
+                if (!isq && p.page >= 0) {
+                    put = true;
+                    to = static_cast<uint8_t *>(isv ? a.cache.v : a.cache.k) +
+                         cache_row(a.cache, p.page, head, p.slot) * a.D * (a.cache.ks != nullptr ? 1 : (int)sizeof(T));
+                    scale = (isv ? a.cache.vs : a.cache.ks) + cache_scale(a.cache, p.page, head, p.slot);
                 }
             }
-            if (turns) turn_pairs(x, angles, angles + 2 * a.R, angles + 4 * a.R, a.pairs);
-            if (to_out && ok) Two<T>::store(out, (int64_t)u * kAtOnce * a.D, now, x);
-            if (MODE != kNorm && now_part != 0) {
-                const int h = now_head + u * kAtOnce;
-                if (a.cache.ks != nullptr)
-                    vec_put_e4m3<LPR>(a.cache, isv, x, now, ok, p, h, j);
-                else if (ok && p.page >= 0)
-                    Two<T>::store(isv ? a.cache.v : a.cache.k, cache_row(a.cache, p.page, h, p.slot) * a.D, now, x);
+            const int live = lt.in ? left : 0;
+            it.step(slices);
+            aim();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool ok = live > u * kAtOnce;
+                f2 x[8];
+                raw[u].unpack(x);
+                raw[u].load(in + u * hop, part == 2 ? lv : lt, lt.in && left > u * kAtOnce);
+                if (normed) {
+                    f2 q = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
+                    const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
+                    const f2 by = pk(inv, inv);
+                    if (lt.in) {
+                        f2 wt[8];
+                        lds16<LPR>(wt, wt_at);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(wt[i], by));
+                    }
+                }
+                if (turns) turn_pairs(x, angles, angles + 2 * a.R, angles + 4 * a.R, a.R, a.pairs);
+                if (to_out && ok) Two<T>::store(out + u * hop, l, x);
+                if (MODE != kNorm && put) {
+                    const int64_t at = (int64_t)u * hop * a.cache.page;
+                    if (a.cache.ks != nullptr)
+                        vec_put_e4m3<LPR>(to + at, scale + u * kAtOnce * a.cache.page, x, l, ok, j);
+                    else if (ok)
+                        Two<T>::store(reinterpret_cast<T *>(to) + at, l, x);
+                }
             }
         }
     }
 }
 
 // The gradient: blocks go through batches of tokens, each lane adds up the weights' gradients at its channels.
-template <typename T, int LPR, int U>
-__global__ void __launch_bounds__(kVecThreads, BWD_BLOCKS) vec_rows_bwd_kernel(const __grid_constant__ VecArgs v) {
-    constexpr int kAtOnce = 32 / LPR, kHeads = U * kAtOnce;
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __grid_constant__ VecArgs v) {
+    constexpr int kAtOnce = 32 / LPR;
     __shared__ Place place[kVecTokens];
     extern __shared__ __align__(16) float mem[];
     const HeadArgs &a = v.h;
@@ -588,40 +603,40 @@ __global__ void __launch_bounds__(kVecThreads, BWD_BLOCKS) vec_rows_bwd_kernel(c
     if (blockIdx.x == 0) seq_check(a.seqs, a.err, threadIdx.x, kVecThreads);
     // shared floats: weights, the lanes' sums of the weights' gradients ([2][4] of four channels, a thread's 16 bytes beside its
     // neighbours'), angles (at the end a row of sums for each warp)
-    float *weights = mem, *table = mem + 2 * a.D + 32 * kVecThreads;
-    float4 *sums = reinterpret_cast<float4 *>(mem + 2 * a.D) + threadIdx.x;
+    float *weights = mem, *table = mem + 32 * LPR + 32 * kVecThreads;
+    float4 *sums = reinterpret_cast<float4 *>(mem + 32 * LPR) + threadIdx.x;
     const LaneAt l = lane_at(a, true, j);
-    const int nq = slices_of(a.Hq, kHeads), slices = nq + slices_of(a.Hk, kHeads);
+    const int per = v.each * kAtOnce, hop = kAtOnce * a.D;
+    const int nq = slices_of(a.Hq, per), slices = nq + slices_of(a.Hk, per);
     const float inv_d = 1.f / (float)a.D;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[i * kVecThreads] = make_float4(0.f, 0.f, 0.f, 0.f);
-    vec_weights(a, weights);
+    vec_weights<LPR>(a, weights);
 
 #pragma unroll 1
     for (int batch = blockIdx.x; batch < v.batches; batch += gridDim.x) {
         const int64_t row0 = (int64_t)batch * v.tokens;
         const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
-        Item it(warp, slices);
-        Two<T> raw[U], raw_g[U];
+        Items it(warp, count, slices);
+        Two<T> raw, raw_g;
         bool isq = true;
         int left = 0;
         int64_t dense = 0;
         const T *in = nullptr, *dout = nullptr;
         auto aim = [&] {
             isq = it.slice < nq;
-            const int head = (isq ? it.slice : it.slice - nq) * kHeads + sub, heads = isq ? a.Hq : a.Hk;
-            left = it.token < count && l.in ? heads - head : 0;
+            const int first = (isq ? it.slice : it.slice - nq) * per, heads = isq ? a.Hq : a.Hk, head = first + sub;
+            left = it.left > 0 ? (first + per < heads ? first + per : heads) - head : 0;
             dense = ((row0 + it.token) * heads + head) * a.D;
             dout = static_cast<const T *>(isq ? a.dq_out : a.dk_out) + dense;
             in = static_cast<const T *>(isq ? a.q : a.k) + (row0 + it.token) * (isq ? a.q_stride : a.k_stride) + (int64_t)head * a.D;
         };
-        auto fetch = [&](int u) {
-            raw_g[u].load(dout, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left);
-            raw[u].load(in, (int64_t)u * kAtOnce * a.D, l, u * kAtOnce < left && (isq ? a.qw : a.kw) != nullptr);
+        auto fetch = [&](bool ok) {
+            raw_g.load(dout, l, ok);
+            raw.load(in, l, ok && (isq ? a.qw : a.kw) != nullptr);
         };
         aim();
-#pragma unroll
-        for (int u = 0; u < U; ++u) fetch(u);
+        fetch(left > 0 && l.in);
         if (a.R > 0) vec_places(a, row0, count, place);
         __syncthreads();
         if (a.R > 0) {
@@ -629,29 +644,39 @@ __global__ void __launch_bounds__(kVecThreads, BWD_BLOCKS) vec_rows_bwd_kernel(c
             __syncthreads();
         }
 #pragma unroll 1
-        while (it.token < count) {
-            const bool now_q = isq, normed = (isq ? a.qw : a.kw) != nullptr;
-            const int now_left = left;
+        while (it.left > 0) {
+            const bool normed = (isq ? a.qw : a.kw) != nullptr;
             T *out = static_cast<T *>(isq ? a.q_out : a.k_out) + dense;
-            const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 4 * a.D);
-            const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 8 * j);
-            it.step(slices);
-            aim();
+            const uint32_t wt_at = smem_u32(weights) + (isq ? 0 : 64 * LPR) + 16 * j;
+            const uint32_t angles = smem_u32(table) + 4 * (it.token * (a.R / 2) * 3 + 4 * j);
+            float4 *to = sums + (isq ? 0 : 4) * kVecThreads;
             f2 total[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) total[i] = pk(0.f, 0.f);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            int now_left = left, n = v.each;
+            bool last;
+#pragma unroll 1
+            do {
+                const bool ok = now_left > 0 && l.in;
                 f2 g[8], x[8];
-                raw_g[u].unpack(g);
-                raw[u].unpack(x);
-                fetch(u);
-                if (l.turns) turn_pairs(g, angles, angles + 4 * a.R, angles + 2 * a.R, a.pairs);  // back
+                raw_g.unpack(g);
+                raw.unpack(x);
+                now_left -= kAtOnce;
+                last = --n == 0 || __all_sync(0xffffffffu, now_left <= 0);
+                if (last) {
+                    it.step(slices);
+                    aim();
+                } else {
+                    in += hop;
+                    dout += hop;
+                }
+                fetch((last ? left : now_left) > 0 && l.in);
+                if (l.turns) turn_pairs(g, angles, angles + 4 * a.R, angles + 2 * a.R, a.R, a.pairs);  // back
                 if (normed) {
                     f2 wt[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) wt[i] = pk(0.f, 0.f);
-                    if (l.in) lds16(wt, wt_at, l);
+                    if (l.in) lds16<LPR>(wt, wt_at);
                     f2 q = mul2(x[0], x[0]), m = pk(0.f, 0.f);
 #pragma unroll
                     for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
@@ -668,16 +693,17 @@ __global__ void __launch_bounds__(kVecThreads, BWD_BLOCKS) vec_rows_bwd_kernel(c
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] = fma2(x[i], pk(-k, -k), g[i]);
                 }
-                if (u * kAtOnce < now_left) Two<T>::store(out, (int64_t)u * kAtOnce * a.D, l, g);
-            }
+                if (ok) Two<T>::store(out, l, g);
+                out += hop;
+            } while (!last);
             if (normed) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float4 &to = sums[((now_q ? 0 : 4) + i) * kVecThreads];
+                    const float4 old = to[i * kVecThreads];
                     float t[4];
                     upk(total[2 * i], t[0], t[1]);
                     upk(total[2 * i + 1], t[2], t[3]);
-                    to = make_float4(to.x + t[0], to.y + t[1], to.z + t[2], to.w + t[3]);
+                    to[i * kVecThreads] = make_float4(old.x + t[0], old.y + t[1], old.z + t[2], old.w + t[3]);
                 }
             }
         }
@@ -758,7 +784,7 @@ __global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(c
                     e[u] = (isv ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)];
                 }
             } else {
-                raw[u].load(base, from * c.D, l, ok);
+                raw[u].load(static_cast<const T *>(base) + from * c.D, l, ok);
             }
             next();
         }
@@ -782,7 +808,7 @@ __global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(c
                         x[2 * k] = mul2(pk(f[0], f[1]), unit);
                         x[2 * k + 1] = mul2(pk(f[2], f[3]), unit);
                     }
-                    Two<T>::store(out, 0, l, x);
+                    Two<T>::store(out, l, x);
                 } else {
                     raw[u].a.store(out + l.o0);
                     raw[u].b.store(out + l.o1);
@@ -862,67 +888,80 @@ bool vec_ok(const HeadArgs &a, bool f32, const void *const *ptrs, int n) {
     return ok;
 }
 
-// How tokens are shared out: `u` groups of rows to a warp.
+// How tokens are shared out.
 struct VecPlan {
     VecArgs v;
     int lpr, u;
     unsigned blocks;
     size_t smem;
 };
-VecPlan vec_plan(const HeadArgs &a, int u) {
+VecPlan vec_plan(const HeadArgs &a, bool f32) {
     VecPlan p;
     p.v.h = a;
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
-    p.u = u;
-    p.v.tokens = 16;
+    p.v.tokens = a.q != nullptr ? 12 : 16;
+    p.v.each = 4;
+    p.u = f32 ? 1 : 2;
     // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy
     const int64_t sms = sm_count();
-    if (a.seqs.rows < 2 * sms * p.v.tokens) {
+    if (a.seqs.rows < 4 * sms * p.v.tokens) {
         const int groups = slices_of(a.Hq + a.Hk + a.Hv, 32 / p.lpr);
         p.v.tokens = groups >= kVecWarps ? 1 : kVecWarps / groups;
-        while (p.v.tokens < 16 && ceil_div(a.seqs.rows, p.v.tokens) > 2 * sms) p.v.tokens *= 2;
-        if (a.seqs.rows * groups < 2 * sms * kVecWarps * u) p.u = 1;
+        while (p.v.tokens < 16 && ceil_div(a.seqs.rows, p.v.tokens) > 4 * sms) p.v.tokens *= 2;
+        if (a.seqs.rows * groups < 4 * sms * kVecWarps * 4) p.v.each = p.u = 1;
     }
     p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
-    p.blocks = (unsigned)p.v.batches;
-    p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 2 * a.D) * sizeof(float);  // at most 26 KB
+    // with norms and angles, blocks that stay and go through shares of all tokens; rows that are only written, 16 tokens a block
+    p.blocks = (unsigned)(a.q == nullptr || p.v.batches < 3 * sms ? p.v.batches : 3 * sms);
+    p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 32 * p.lpr) * sizeof(float);  // at most 26 KB
     return p;
 }
 
-#define KDA_VEC_LAUNCH(kernel, ...)                                                                     \
-    switch (p.lpr) {                                                                                    \
-        case 4: kernel(4, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;          \
-        case 8: kernel(8, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;          \
-        default: kernel(16, __VA_ARGS__)<<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;        \
+#define KDA_VEC(kernel, T, ...)                                                                              \
+    switch (p.lpr) {                                                                                         \
+        case 4: kernel<T, 4 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;             \
+        case 8: kernel<T, 8 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;             \
+        default: kernel<T, 16 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;           \
     }
-#define KDA_VEC_ROWS(LPR, T, U, M) vec_rows_kernel<T, LPR, U, M>
-#define KDA_VEC_BWD(LPR, T, U, M) vec_rows_bwd_kernel<T, LPR, U>
-#define KDA_VEC_READ(LPR, T, U, M) vec_read_kernel<T, LPR, U, M>
-// U: groups of a warp for bf16, half as many for fp32, or one
-#define KDA_VEC(kernel, U, M)                                     \
-    {                                                             \
-        if (f32) {                                                \
-            if (p.u == 1) {                                       \
-                KDA_VEC_LAUNCH(kernel, float, 1, M)               \
-            } else {                                              \
-                KDA_VEC_LAUNCH(kernel, float, (U) / 2, M)         \
-            }                                                     \
-        } else if (p.u == 1) {                                    \
-            KDA_VEC_LAUNCH(kernel, bf16, 1, M)                    \
-        } else {                                                  \
-            KDA_VEC_LAUNCH(kernel, bf16, U, M)                    \
-        }                                                         \
-        return cudaGetLastError();                                \
+
+template <typename T>
+cudaError_t vec_rows(const VecPlan &p, cudaStream_t stream) {
+#define KDA_COMMA ,
+#define KDA_MODES(U)                                                        \
+    if (!p.v.h.cached)                                                      \
+        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kNorm)            \
+    else if (p.v.h.q != nullptr)                                            \
+        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kStep)            \
+    else                                                                    \
+        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kWrite)
+    if (p.u == 1) {
+        KDA_MODES(1)
+    } else {
+        KDA_MODES(2)
     }
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t vec_bwd(const VecPlan &p, cudaStream_t stream) {
+    KDA_VEC(vec_rows_bwd_kernel, T)
+    return cudaGetLastError();
+}
+// U: rows of a lane on their way
+template <typename T, int U, int SCALED>
+cudaError_t vec_read(const VecPlan &p, cudaStream_t stream) {
+    if (p.u == 1)
+        KDA_VEC(vec_read_kernel, T, KDA_COMMA 1 KDA_COMMA SCALED)
+    else
+        KDA_VEC(vec_read_kernel, T, KDA_COMMA U KDA_COMMA SCALED)
+    return cudaGetLastError();
+}
 
 cudaError_t launch_rows(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     const void *ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 5)) {
-        const VecPlan p = vec_plan(a, f32 ? FWD_U / 2 : FWD_U);
-        if (!a.cached) KDA_VEC(KDA_VEC_ROWS, FWD_U, kNorm)
-        if (a.q != nullptr) KDA_VEC(KDA_VEC_ROWS, FWD_U, kStep)
-        KDA_VEC(KDA_VEC_ROWS, FWD_U, kWrite)
+        const VecPlan p = vec_plan(a, f32);
+        return f32 ? vec_rows<float>(p, stream) : vec_rows<bf16>(p, stream);
     }
     const unsigned blocks = any_blocks(a.seqs.rows * (a.Hq + a.Hk + a.Hv));
     if (f32)
@@ -936,11 +975,11 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
     if (sm_count() == 0) return cudaErrorInvalidDevice;
     const void *ptrs[] = {a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 2)) {
-        VecPlan p = vec_plan(a, 2);
+        VecPlan p = vec_plan(a, f32);
         // as many tokens as a block's warps have rows on their way
-        const int rows = kVecWarps * (a.cache.ks != nullptr ? 8 : 4) / (f32 ? 2 : 1) * 32 / p.lpr;
-        int tokens = rows / (2 * a.Hk);
-        p.u = 2;
+        const bool scaled = a.cache.ks != nullptr;
+        p.u = (scaled ? 8 : 4) / (f32 ? 2 : 1);
+        int tokens = kVecWarps * p.u * 32 / p.lpr / (2 * a.Hk);
         if (ceil_div(a.seqs.rows, tokens < 1 ? 1 : tokens) < 2 * sm_count()) {
             p.u = 1;
             tokens = kVecWarps * 32 / p.lpr / (2 * a.Hk);
@@ -949,8 +988,8 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
         p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
         p.blocks = (unsigned)p.v.batches;
         p.smem = 0;
-        if (a.cache.ks != nullptr) KDA_VEC(KDA_VEC_READ, 8, 1)
-        KDA_VEC(KDA_VEC_READ, 4, 0)
+        if (f32) return scaled ? vec_read<float, 4, 1>(p, stream) : vec_read<float, 2, 0>(p, stream);
+        return scaled ? vec_read<bf16, 8, 1>(p, stream) : vec_read<bf16, 4, 0>(p, stream);
     }
     const unsigned blocks = any_blocks(a.seqs.rows * 2 * a.Hk);
     if (f32)
@@ -990,10 +1029,11 @@ BwdPlan bwd_plan(const kda_qk_norm_bwd_params &p, int64_t rows, unsigned int *er
     const void *ptrs[] = {p.f.q, p.f.k, p.dq_out, p.dk_out, p.dq, p.dk};
     q.vec = rows != 0 && vec_ok(q.a, f32, ptrs, 6);
     if (q.vec) {
-        q.p = vec_plan(q.a, f32 ? 1 : 2);
+        q.p = vec_plan(q.a, f32);
+        q.p.blocks = (unsigned)q.p.v.batches;
         const unsigned most = (unsigned)sm_count() * 2;
         // at most as many tokens at a time as there is room for the angles of (46 KB in all)
-        int cap = (46 * 1024 / 4 - 2 * p.f.D - 32 * kVecThreads) / (p.f.R / 2 * 3 + 1);
+        int cap = (46 * 1024 / 4 - 32 * q.p.lpr - 32 * kVecThreads) / (p.f.R / 2 * 3 + 1);
         cap = cap > kVecTokens ? kVecTokens : cap;
         if (q.p.blocks > most || q.p.v.tokens > cap) {
             const int64_t times = ceil_div(rows, (int64_t)most * cap);  // the same for every block
@@ -1003,7 +1043,7 @@ BwdPlan bwd_plan(const kda_qk_norm_bwd_params &p, int64_t rows, unsigned int *er
         }
         q.blocks = q.p.blocks;
         const int table = q.p.v.tokens * (p.f.R / 2) * 3;
-        q.p.smem = (size_t)(2 * p.f.D + 32 * kVecThreads + (table > kVecWarps * p.f.D ? table : kVecWarps * p.f.D)) * sizeof(float);
+        q.p.smem = (size_t)(32 * q.p.lpr + 32 * kVecThreads + (table > kVecWarps * p.f.D ? table : kVecWarps * p.f.D)) * sizeof(float);
     } else {
         const int64_t most = (int64_t)sm_count() * 4, need = ceil_div(rows * (p.f.q_heads + p.f.k_heads), kWarps);
         q.blocks = (unsigned)(need < 1 ? 1 : need < most ? need : most);
@@ -1018,7 +1058,7 @@ cudaError_t launch_bwd(const BwdPlan &q, bool f32, cudaStream_t stream) {
     if (q.vec) {
         VecPlan p = q.p;
         p.v.h = a;
-        KDA_VEC(KDA_VEC_BWD, 2, 0)
+        return f32 ? vec_bwd<float>(p, stream) : vec_bwd<bf16>(p, stream);
     }
     if (f32)
         any_rows_bwd_kernel<float><<<q.blocks, 32 * kWarps, 0, stream>>>(a);
