@@ -2,9 +2,9 @@
 // stream in, and how the pieces of one result are joined.
 //
 // An item is one (sequence, block of query rows, key head); its keys are cut into units of UNIT (16 or 32, by the kernel).
-// All items' units, one after another, are dealt out in equal shares to the warps of the grid: a warp is a worker of its
-// own, with its own ring of shared memory and no barrier with the others. It has at most one item that began in the
-// share before and one that goes on in the next; such pieces leave (m, l, O) in scratch: the reference m of their
+// All items' units, one after another, are dealt out in equal shares to the workers of the grid: warps, each with its own
+// ring of shared memory and no barrier with the others, or, where there are many query rows, teams of warps that
+// share a ring and take some of the rows each. A worker has at most one item that began in the share before and one that goes on in the next; such pieces leave (m, l, O) in scratch: the reference m of their
 // exponentials 2^(s - m), the sum l of those, and O = sum 2^(s - m) v. A second kernel joins them in the order of
 // the workers. Which items are cut follows from the lengths and sizes alone, so results repeat bit for bit.
 // (Blocks of four warps that shared each item's keys and joined them in shared memory: 4 to 7 us for every piece
@@ -103,10 +103,18 @@ struct Piece {
     uint32_t u0, u1, units;
     int last;  // keys that the last of its rows sees: no key at or after this one counts
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+    // The piece for `most` of its rows from row `from` on (none: `last` 0).
+    __device__ __forceinline__ void mine(const Args &a, int from, int most);
 };
 __device__ __forceinline__ int seen(const Args &a, int len, int row) {
     const int n = len - a.T + token_of(a, row) + 1;
     return n < 0 ? 0 : n;
+}
+
+__device__ __forceinline__ void Piece::mine(const Args &a, int from, int most) {
+    row0 += from;
+    rows = rows - from < most ? rows - from : most;
+    last = rows > 0 ? seen(a, len, row0 + rows - 1) : 0;
 }
 
 // A worker's way through its share, piece by piece: items in the order (sequence, block of rows, key head).
@@ -141,14 +149,15 @@ struct Walk {
         read_ahead(a);
     }
 };
-// The start of every warp's share; `mem`: 3 kWarps ints. Ends with a barrier; `left` 0: no share.
+// The start of the share of every warp's worker (of TEAM warps); `mem`: 3 kWarps ints. Ends with a barrier; `left` 0: no share.
+template <int TEAM>
 __device__ __forceinline__ Walk find_walk(const Args &a, uint32_t *mem) {
     const Scan sc = scan_sequences(a, mem);
     const Deal deal(a, sc.total);
-    const uint32_t w0 = blockIdx.x * kWarps;
+    const uint32_t w0 = blockIdx.x * (kWarps / TEAM);
     uint32_t *found = mem + kWarps, *rest = found + kWarps;
 #pragma unroll 1
-    for (uint32_t v = 0; v < kWarps && w0 + v < deal.n; ++v) {
+    for (uint32_t v = 0; v < kWarps / TEAM && w0 + v < deal.n; ++v) {
         const uint32_t at = deal.start(w0 + v);
         if (at - sc.before < sc.sum) {  // one thread's
             int b = sc.first;
@@ -165,7 +174,7 @@ __device__ __forceinline__ Walk find_walk(const Args &a, uint32_t *mem) {
         }
     }
     __syncthreads();
-    const uint32_t v = threadIdx.x >> 5;
+    const uint32_t v = (threadIdx.x >> 5) / TEAM;
     Walk k;
     k.left = 0;
     k.b = k.len = k.rb = k.head = k.u0 = k.next_len = 0;
@@ -220,7 +229,9 @@ __device__ __forceinline__ void copies_wait() {
 // Rows that no query of the piece sees, or without a page, are zeros. The stream runs ahead of the computation over the
 // borders of pieces. The page of a row is read from the table two units before its copies are issued, and the rows'
 // exponent bytes one unit before, so that neither is waited for.
-template <typename C, int DP, int KEYS, int SLOTS>
+// Of a team, each warp copies its part of every unit's rows, and a barrier of the team in front of each slot both shows its
+// rows to all and says that the slot before is free.
+template <typename C, int DP, int KEYS, int SLOTS, int TEAM = 1>
 struct Stream {
     static constexpr int kPitch = DP * (int)sizeof(C) < 128 ? 128 : DP * (int)sizeof(C);
     static constexpr int kSlot = KEYS * kPitch;
@@ -228,7 +239,9 @@ struct Stream {
     static constexpr int kUnits = SLOTS / 2 + 2;  // whose exponent bytes may be held at a time
     static constexpr int kScaleBytes = sizeof(C) == 1 ? kUnits * 2 * KEYS : 0;
     static constexpr int kChunks = kPitch / 16;         // of a row
-    static constexpr int kTurns = KEYS * kChunks / 32;  // copies of a lane for KEYS rows
+    static constexpr int kMine = KEYS / TEAM;           // rows that a warp copies
+    static constexpr int kTurns = kMine * kChunks / 32;
+    static_assert(kTurns >= 1 && (TEAM == 1 || kMine % 4 == 0), "whole turns");
     static constexpr bool kScaled = sizeof(C) == 1;
 
     const Args &a;
@@ -238,13 +251,16 @@ struct Stream {
     Walk walk;               // of the unit that is looked up next
     uint32_t u, u1;          // that unit, and where its piece ends
     int last;                // keys of its piece that count
-    int entry, place;        // of this lane's row (lane % KEYS), looked up: the table's entry, the row within the page and head (-1: none)
+    int entry, place;        // of this lane's row (first + lane % kMine), looked up: the table's entry, the row within the page and head (-1: none)
     int row;                 // and of the unit that is copied next: the row of the cache (-1: zeros)
     uint32_t sk, sv;         // its exponent bytes
     int slot, unit_in, unit_out;  // the oldest slot, and where exponent bytes are written and read
+    int first, barrier;           // team: the first row that this warp copies, the team's barrier
+    bool begun;
 
-    __device__ __forceinline__ Stream(const Args &a_, unsigned char *mem, uint8_t *sc, int lane_, const Walk &w)
-        : a(a_), ring(smem_u32(mem)), scales(sc), lane(lane_), walk(w), sk(0), sv(0), slot(0), unit_in(0), unit_out(0) {
+    __device__ __forceinline__ Stream(const Args &a_, unsigned char *mem, uint8_t *sc, int lane_, int warp, const Walk &w)
+        : a(a_), ring(smem_u32(mem)), scales(sc), lane(lane_), walk(w), sk(0), sv(0), slot(0), unit_in(0), unit_out(0),
+          first(warp % TEAM * kMine), barrier(1 + warp / TEAM), begun(false) {
         enter();
         place = -1;
         // one unit looked up, then one resolved and the next looked up; then the slots in order
@@ -269,7 +285,7 @@ struct Stream {
     __device__ __forceinline__ void look() {
         place = -1;
         if (walk.left == 0) return;
-        const int pos = (int)u * KEYS + (lane & (KEYS - 1));
+        const int pos = (int)u * KEYS + first + (lane & (kMine - 1));
         if (pos < last) {
             int at, s;
             cache_split(a.cache, pos, at, s);
@@ -296,7 +312,7 @@ struct Stream {
         }
     }
     __device__ __forceinline__ void copy_rows(const void *base, int to_slot) {
-        const uint32_t to = ring + to_slot * kSlot;
+        const uint32_t to = ring + to_slot * kSlot + first * kPitch;
         const uint32_t width = a.cache.D * (uint32_t)sizeof(C);
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
@@ -304,7 +320,7 @@ struct Stream {
             const int c = kChunks <= 32 ? lane % kChunks : (i % (kChunks / 32)) * 32 + lane;
             const int from = __shfl_sync(0xffffffffu, row, r);
             const bool ok = from >= 0 && c * 16u < width;
-            copy16(to + r * kPitch + ((c ^ (r & 7)) << 4), static_cast<const char *>(base) + (uint64_t)(uint32_t)(ok ? from : 0) * width + (ok ? c * 16u : 0u), ok);
+            copy16(to + r * kPitch + ((c ^ ((first + r) & 7)) << 4), static_cast<const char *>(base) + (uint64_t)(uint32_t)(ok ? from : 0) * width + (ok ? c * 16u : 0u), ok);
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
@@ -312,9 +328,9 @@ struct Stream {
         copy_rows(a.cache.k, to_slot);
         if constexpr (kScaled) {
             uint8_t *x = scales + unit_in * 2 * KEYS;
-            if (lane < KEYS) {
-                x[lane] = (uint8_t)sk;
-                x[KEYS + lane] = (uint8_t)sv;
+            if (lane < kMine) {
+                x[first + lane] = (uint8_t)sk;
+                x[KEYS + first + lane] = (uint8_t)sv;
             }
             unit_in = unit_in == kUnits - 1 ? 0 : unit_in + 1;
         }
@@ -324,22 +340,37 @@ struct Stream {
         resolve();
         look();
     }
-    // The oldest slot is complete and seen by the warp.
+    // What comes SLOTS slots after slot `at`, which held K or V (`V`), goes into it.
+    template <bool V>
+    __device__ __forceinline__ void refill(int at) {
+        if constexpr (V == (SLOTS % 2 == 0))
+            fetch_v(at);
+        else
+            fetch_k(at);
+    }
+    // The oldest slot, K or V, is complete and seen by the worker. A team is then done with the slot before.
+    template <bool V>
     __device__ __forceinline__ void ready() {
-        copies_wait<SLOTS - 1>();
-        __syncwarp();
+        if constexpr (TEAM == 1) {
+            copies_wait<SLOTS - 1>();
+            __syncwarp();
+        } else {
+            copies_wait<SLOTS - 2>();
+            tcu::bar_named(barrier, 32 * TEAM);
+            if (begun) refill<!V>(slot == 0 ? SLOTS - 1 : slot - 1);
+            begun = true;
+        }
     }
     // Shared address of the oldest slot; the exponent bytes of the oldest unit.
     __device__ __forceinline__ uint32_t oldest() const { return ring + slot * kSlot; }
     __device__ __forceinline__ const uint8_t *bytes() const { return scales + unit_out * 2 * KEYS; }
-    // The warp is done with the oldest slot, K or V (`V`): what comes SLOTS slots later goes into it.
+    // The warp is done with the oldest slot, K or V.
     template <bool V>
     __device__ __forceinline__ void release() {
-        __syncwarp();
-        if constexpr (V == (SLOTS % 2 == 0))
-            fetch_v(slot);
-        else
-            fetch_k(slot);
+        if constexpr (TEAM == 1) {
+            __syncwarp();
+            refill<V>(slot);
+        }
         slot = slot == SLOTS - 1 ? 0 : slot + 1;
         if constexpr (V) unit_out = unit_out == kUnits - 1 ? 0 : unit_out + 1;
     }

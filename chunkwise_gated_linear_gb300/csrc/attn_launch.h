@@ -8,19 +8,19 @@
 namespace kda {
 namespace attn {
 
-// Query rows of an item for `all` rows of a sequence and key head, keys of a unit (its power of two), blocks on an SM, and the launch, of the
-// kernel for fp32 data and of that for bf16.
+// Query rows of an item for `all` rows of a sequence and key head, keys of a unit (its power of two), workers on an SM, and the
+// launch, of the kernel for fp32 data and of that for bf16.
 int fma_rows(int all, int D);
 int fma_unit_shift(const Args &a);
-int fma_blocks(const Args &a);
+int fma_workers(const Args &a);
 cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream);
 int mma_rows(int all, int D);
 int mma_unit_shift(const Args &a);
-int mma_blocks(const Args &a);
+int mma_workers(const Args &a);
 cudaError_t launch_attn_mma(const Args &a, cudaStream_t stream);
 
-// Launches a kernel of kSmem bytes of shared memory with a warp for each worker.
-template <auto kernel, int kSmem>
+// Launches a kernel of kSmem bytes of shared memory with TEAM warps for each worker.
+template <auto kernel, int kSmem, int TEAM>
 cudaError_t launch_kernel(const Args &a, cudaStream_t stream) {
     static std::atomic<bool> ready[64];  // per device, of this kernel
     int dev = 0;
@@ -31,7 +31,7 @@ cudaError_t launch_kernel(const Args &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
     }
-    kernel<<<a.workers / kWarps, kThreads, kSmem, stream>>>(a);
+    kernel<<<a.workers / (kWarps / TEAM), kThreads, kSmem, stream>>>(a);
     return cudaGetLastError();
 }
 

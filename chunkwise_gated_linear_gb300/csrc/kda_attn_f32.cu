@@ -54,13 +54,13 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
     extern __shared__ __align__(128) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     launch_dependents();
-    Walk walk = find_walk(a, reinterpret_cast<uint32_t *>(mem + F::kPlan));
+    Walk walk = find_walk<1>(a, reinterpret_cast<uint32_t *>(mem + F::kPlan));
     if (walk.left == 0) return;
     float *qs = reinterpret_cast<float *>(mem + F::kQ) + warp * RB * DP;
     float *pw = reinterpret_cast<float *>(mem + F::kP) + warp * KEYS * RB;
     int *lim = reinterpret_cast<int *>(mem + F::kLim) + warp * RB;
     unsigned char *own = mem + warp * F::S::kBytes;
-    typename F::S st(a, own, mem + F::kSc + warp * F::S::kScaleBytes, lane, walk);
+    typename F::S st(a, own, mem + F::kSc + warp * F::S::kScaleBytes, lane, warp, walk);
     const int D = a.cache.D, key = lane & (KEYS - 1), part = lane / KEYS;
     const int cpr = D * (int)sizeof(C) / 16;
 
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
 #pragma unroll 1
         for (uint32_t u = p.u0; u < p.u1; ++u) {
             const int pos0 = (int)u * KEYS;
-            st.ready();
+            st.template ready<false>();
             if (pos0 < p.last) {  // the same for the whole warp
                 const unsigned char *ks = own + st.slot * F::S::kSlot;
                 const uint8_t *sc = st.bytes();
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
                 }
             }
             st.template release<false>();
-            st.ready();
+            st.template ready<true>();
             if (pos0 < p.last) {
                 const unsigned char *vs = own + st.slot * F::S::kSlot;
                 const bool edge = pos0 + KEYS > least;
@@ -203,9 +203,9 @@ template <typename C, int DP, int RB, int KEYS, int SLOTS>
 struct Variant {
     using F = Fma<C, DP, RB, KEYS, SLOTS>;
     static cudaError_t launch(const Args &a, cudaStream_t stream) {
-        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, SLOTS>, F::kSmem>(a, stream);
+        return launch_kernel<attn_fma_kernel<C, DP, RB, KEYS, SLOTS>, F::kSmem, 1>(a, stream);
     }
-    static int blocks() { return F::kBlocks; }
+    static int workers() { return F::kBlocks * kWarps; }
     static int unit() { return KEYS; }
 };
 // Calls f with the variant for these sizes: rings that fill the shared memory of an SM, in one to three blocks.
@@ -228,8 +228,8 @@ int fma_rows(int all, int D) { return all <= 4 ? 4 : D > 128 ? 8 : 16; }
 int fma_unit_shift(const Args &a) {
     return pick(a, [](auto v) { return decltype(v)::unit() == 16 ? 4 : 3; });
 }
-int fma_blocks(const Args &a) {
-    return pick(a, [](auto v) { return decltype(v)::blocks(); });
+int fma_workers(const Args &a) {
+    return pick(a, [](auto v) { return decltype(v)::workers(); });
 }
 cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream) {
     return pick(a, [&](auto v) { return decltype(v)::launch(a, stream); });

@@ -62,22 +62,23 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return d;
 }
 
-template <typename C, int DP, int NT, int SLOTS>
+template <typename C, int DP, int NT, int SLOTS, int TEAM>
 struct Mma {
     static constexpr bool kScaled = sizeof(C) == 1;
-    static constexpr int kJoint = kScaled ? 2 : 1;  // blocks of 16 keys in a unit
+    static constexpr int kJoint = kScaled || TEAM > 1 ? 2 : 1;  // blocks of 16 keys in a unit
     static constexpr int kKeys = 16 * kJoint;
-    using S = Stream<C, DP, kKeys, SLOTS>;
+    using S = Stream<C, DP, kKeys, SLOTS, TEAM>;
     static constexpr int kSteps = DP / 16;  // products of S^T, and blocks of 16 channels of O^T
-    static constexpr int kRows = 8 * NT;
+    static constexpr int kRows = 8 * NT;  // of a warp
     static constexpr int kQBytes = NT * kSteps * 256;  // Q^T of a warp: [NT][kSteps][32 lanes] of 8 bytes
     static constexpr int kStats = 4 * kRows;           // floats of a warp: what a score is multiplied with, m, M, a factor
     // shared memory: rings, Q^T, statistics, the plan, exponent bytes
-    static constexpr int kQ = kWarps * S::kBytes;
+    static constexpr int kWorkers = kWarps / TEAM;
+    static constexpr int kQ = kWorkers * S::kBytes;
     static constexpr int kStat = kQ + kWarps * kQBytes;
     static constexpr int kPlan = kStat + kWarps * kStats * 4;
     static constexpr int kSc = kPlan + kPlanBytes;
-    static constexpr int kSmem = kSc + kWarps * S::kScaleBytes;
+    static constexpr int kSmem = kSc + kWorkers * S::kScaleBytes;
     static constexpr int kFit = (228 * 1024) / (kSmem + 1024);
     // registers: O^T is 4 kSteps NT of a lane's, the scores 4 kJoint NT
     static constexpr int kLive = 4 * kSteps * NT + 4 * kJoint * NT + 8 * NT + 72;
@@ -111,19 +112,20 @@ __device__ __forceinline__ float spread_max(float (&v)[N], int lane) {
 // What is done once per piece is kept short (loops, statistics in shared memory while they change): code that runs once
 // is bound by fetching it, about 40 cycles for an instruction (16 sequences with four drafted tokens each: 119 us
 // with everything unrolled).
-template <typename C, int DP, int NT, int SLOTS>
-__global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn_mma_kernel(const __grid_constant__ Args a) {
-    using M = Mma<C, DP, NT, SLOTS>;
+template <typename C, int DP, int NT, int SLOTS, int TEAM>
+__global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks) attn_mma_kernel(const __grid_constant__ Args a) {
+    using M = Mma<C, DP, NT, SLOTS, TEAM>;
     using S = typename M::S;
     constexpr int kSteps = M::kSteps, kJoint = M::kJoint, kKeys = M::kKeys, kRows = M::kRows;
     extern __shared__ __align__(1024) unsigned char mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     launch_dependents();
-    Walk walk = find_walk(a, reinterpret_cast<uint32_t *>(mem + M::kPlan));
-    if (walk.left == 0) return;
-    unsigned char *own = mem + warp * S::kBytes;
-    S st(a, own, mem + M::kSc + warp * S::kScaleBytes, lane, walk);
+    Walk walk = find_walk<TEAM>(a, reinterpret_cast<uint32_t *>(mem + M::kPlan));
+    if (walk.left == 0) return;  // the whole team
+    const int worker = warp / TEAM;
+    unsigned char *own = mem + worker * S::kBytes;
+    S st(a, own, mem + M::kSc + worker * S::kScaleBytes, lane, warp, walk);
     uint2 *qmem = reinterpret_cast<uint2 *>(mem + M::kQ + warp * M::kQBytes) + lane;  // [NT][kSteps], 32 apart
     // of each row: what its scores are multiplied with, the references m and M, the factor of the last move
     float *stats = reinterpret_cast<float *>(mem + M::kStat) + warp * M::kStats;
@@ -134,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
 
 #pragma unroll 1
     while (walk.left > 0) {
-        const Piece p = walk.piece(a);
+        Piece p = walk.piece(a);
+        if constexpr (TEAM > 1) p.mine(a, warp % TEAM * kRows, kRows);
         // Q^T: row 8 n + g, the lane's channels of each block of 16 in the order in which K's come out of the ring
 #pragma unroll 1
         for (int n = 0; n < NT; ++n) {
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
 
 #pragma unroll 1
         for (uint32_t u = p.u0; u < p.u1; ++u) {
-            st.ready();
+            st.template ready<false>();
             const int pos0 = (int)u * kKeys;
             const bool count = pos0 < p.last;  // the same for the whole warp
             float x[kJoint][NT][4];
@@ -300,9 +303,11 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
                         }
                 } else {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int h = 0; h < kJoint; ++h)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) upk(mul2(pk(x[0][n][2 * i], x[0][n][2 * i + 1]), rowf[n]), x[0][n][2 * i], x[0][n][2 * i + 1]);
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) upk(mul2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), rowf[n]), x[h][n][2 * i], x[h][n][2 * i + 1]);
                 }
                 if (edge) {
 #pragma unroll
@@ -399,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
                             pb[h][n][i] = transpose8(M::kScaled ? pack_f16(lo, hi) : pack_bf16(lo, hi));
                         }
             }
-            st.ready();
+            st.template ready<true>();
             if (count) {
                 const uint32_t vs = st.oldest();
-                // O^T += V^T P^T, for all rows or those of one token alone
-                auto values = [&](auto all, int token) {
+                // O^T += V^T P^T, for all rows, or those of one token alone, from the values at its first `end` keys
+                auto values = [&](auto all, int token, int end) {
 #pragma unroll
                     for (int h = 0; h < kJoint; ++h) {
                         const uint32_t vrow = vs + (16 * h + (M::kScaled ? lane & 15 : (lane & 7) + ((lane >> 4) << 3))) * S::kPitch;
@@ -421,6 +426,15 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
                                 }
                             } else {
                                 ldsm_t(f[0], vrow + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+                            }
+                            if constexpr (!decltype(all)::value) {
+                                // registers 0, 1: keys 2 c, 2 c + 1; 2, 3: eight further on
+                                const int e = end - 16 * h - 2 * c;
+                                const uint32_t near = e <= 0 ? 0u : e == 1 ? 0xffffu : ~0u, far = e <= 8 ? 0u : e == 9 ? 0xffffu : ~0u;
+#pragma unroll
+                                for (int t = 0; t < (M::kScaled ? 2 : 1); ++t)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) f[t][i] &= i < 2 ? near : far;
                             }
 #pragma unroll
                             for (int t = 0; t < (M::kScaled ? 2 : 1); ++t)
@@ -463,28 +477,20 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
                     odd = __any_sync(0xffffffffu, odd);
                 }
                 if (!odd) {
-                    values(std::true_type{}, 0);
+                    values(std::true_type{}, 0, 0);
                 } else {
-                    // Such a value would reach rows that do not see its key, as 0 * NaN: one token's rows at a time, from the last token on,
-                    // with the values that it does not see set to zero.
-                    int from = kKeys;
+                    // Such a value would reach rows that do not see its key, as 0 * NaN: one token's rows at a time, the values that it
+                    // does not see taken as zeros.
 #pragma unroll 1
-                    for (int t = token_of(a, p.row0 + p.rows - 1); t >= token_of(a, p.row0); --t) {
-                        const int end = p.len - a.T + t + 1 - pos0;
-                        const int zero = end < 0 ? 0 : end < kKeys ? end : kKeys;
-                        __syncwarp();
-#pragma unroll 1
-                        for (int b = zero * S::kPitch + 4 * lane; b < from * S::kPitch; b += 128) *reinterpret_cast<uint32_t *>(own + (vs - st.ring) + b) = 0u;
-                        from = zero;
-                        __syncwarp();
-                        values(std::false_type{}, t);
-                    }
+                    for (int t = token_of(a, p.row0); t <= token_of(a, p.row0 + p.rows - 1); ++t) values(std::false_type{}, t, p.len - a.T + t + 1 - pos0);
                 }
             }
             st.template release<true>();
         }
 
-        float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
+        // of the worker's rows, this warp's begin at `base`
+        const int base = TEAM > 1 ? warp % TEAM * kRows : 0;
+        float *piece = piece_mem(a, blockIdx.x * M::kWorkers + worker, p.u0 == 0);
         const bool whole = p.whole();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -501,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
                 if (whole) f = sum[j] == 0.f ? 0.f : f / sum[j];
                 const int64_t row = out_row(a, p, r);
                 bf16 *to = static_cast<bf16 *>(a.o) + row * D;
-                float *part = piece + r * D;
+                float *part = piece + (base + r) * D;
                 if (g == 0) {
                     if (!whole)
-                        reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(top, sum[j]);
+                        reinterpret_cast<float2 *>(piece + a.rows * D)[base + r] = make_float2(top, sum[j]);
                     else if (a.lse != nullptr)
                         a.lse[row] = lse_of(top, sum[j]);
                 }
@@ -533,36 +539,45 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS>::kBlocks) attn
     copies_wait<0>();
 }
 
-template <typename C, int DP, int NT, int SLOTS>
+template <typename C, int DP, int NT, int SLOTS, int TEAM>
 struct Variant {
-    using M = Mma<C, DP, NT, SLOTS>;
+    using M = Mma<C, DP, NT, SLOTS, TEAM>;
     static cudaError_t launch(const Args &a, cudaStream_t stream) {
-        return launch_kernel<attn_mma_kernel<C, DP, NT, SLOTS>, M::kSmem>(a, stream);
+        return launch_kernel<attn_mma_kernel<C, DP, NT, SLOTS, TEAM>, M::kSmem, TEAM>(a, stream);
     }
-    static int blocks() { return M::kBlocks; }
+    static int workers() { return M::kBlocks * M::kWorkers; }
     static int unit() { return M::kKeys; }
 };
 
-// Calls f with the variant for these sizes. Query rows: 8, 16 or 32 (16 where O^T of wide heads fills the registers).
+// Calls f with the variant for these sizes. Query rows: 8 or 16 of a warp, 32 or 64 of a team of four.
+template <typename C, int DP, int SLOTS, int SLOTS_TEAM, typename F>
+auto pick_rows(const Args &a, F f) {
+    if (a.rows == 8) return f(Variant<C, DP, 1, SLOTS, 1>{});
+    if constexpr (DP <= 128) {
+        if (a.rows == 16) return f(Variant<C, DP, 2, SLOTS, 1>{});
+        if (a.rows == 64) return f(Variant<C, DP, 2, SLOTS_TEAM, 4>{});
+    } else {
+        if (a.rows == 16) return f(Variant<C, DP, 1, SLOTS_TEAM, 2>{});
+    }
+    return f(Variant<C, DP, 1, SLOTS_TEAM, 4>{});
+}
 template <typename C, typename F>
 auto pick(const Args &a, F f) {
-    if (a.cache.D <= 64)
-        return a.rows == 8 ? f(Variant<C, 64, 1, 6>{}) : a.rows == 16 ? f(Variant<C, 64, 2, 6>{}) : f(Variant<C, 64, 4, 6>{});
-    if (a.cache.D <= 128)
-        return a.rows == 8 ? f(Variant<C, 128, 1, 4>{}) : a.rows == 16 ? f(Variant<C, 128, 2, 4>{}) : f(Variant<C, 128, 4, 4>{});
-    return a.rows == 8 ? f(Variant<C, 256, 1, 3>{}) : f(Variant<C, 256, 2, 3>{});
+    if (a.cache.D <= 64) return pick_rows<C, 64, 6, 7>(a, f);
+    if (a.cache.D <= 128) return pick_rows<C, 128, 4, sizeof(C) == 1 ? 7 : 5>(a, f);
+    return pick_rows<C, 256, 3, 5>(a, f);
 }
 
 }  // namespace
 
-int mma_rows(int all, int D) { return all <= 8 ? 8 : (all <= 16 || D > 128) ? 16 : 32; }
+int mma_rows(int all, int D) { return all <= 8 ? 8 : all <= 16 ? 16 : all <= 32 || D > 128 ? 32 : 64; }
 
 int mma_unit_shift(const Args &a) {
     auto f = [](auto v) { return decltype(v)::unit() == 32 ? 5 : 4; };
     return a.cache.ks != nullptr ? pick<uint8_t>(a, f) : pick<bf16>(a, f);
 }
-int mma_blocks(const Args &a) {
-    auto f = [](auto v) { return decltype(v)::blocks(); };
+int mma_workers(const Args &a) {
+    auto f = [](auto v) { return decltype(v)::workers(); };
     return a.cache.ks != nullptr ? pick<uint8_t>(a, f) : pick<bf16>(a, f);
 }
 cudaError_t launch_attn_mma(const Args &a, cudaStream_t stream) {

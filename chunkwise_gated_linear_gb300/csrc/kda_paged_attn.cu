@@ -178,7 +178,7 @@ Args make(const kda_attn_step_params &p, unsigned int *err) {
     a.row_blocks = (int)ceil_div(all, a.rows);
     a.per_seq = a.row_blocks * a.cache.heads;
     a.unit_shift = f32 ? fma_unit_shift(a) : mma_unit_shift(a);
-    a.workers = sm_count() * (f32 ? fma_blocks(a) : mma_blocks(a)) * kWarps;
+    a.workers = sm_count() * (f32 ? fma_workers(a) : mma_workers(a));
     return a;
 }
 size_t bytes_of(const Args &a) { return (size_t)2 * a.workers * a.rows * (a.cache.D + 2) * sizeof(float); }
