@@ -22,6 +22,10 @@ namespace attn {
 using namespace mix;
 
 constexpr int kWarps = 4;  // of a block
+// What an item costs beside its units, in units, when the work is dealt out: its queries in, its result out and the waits in
+// between. (16 sequences of up to 8192 tokens, among them one of 4 and one at rest: 29 us without it, the
+// short ones' items one after another in two shares.)
+constexpr uint32_t kItemCost = 2;
 constexpr int kThreads = 32 * kWarps;
 
 struct Args {
@@ -48,8 +52,12 @@ __device__ __forceinline__ uint32_t units_of(const Args &a, int len) {
     return n == 0 ? 1 : n;
 }
 
-// The units of all items (below 2^32, checked on the host for the longest sequences) dealt out: how many workers have a
-// share (each then has a unit at least), where share w begins, and whose share unit x is in.
+// The units and costs of an item.
+__device__ __forceinline__ uint32_t weight_of(const Args &a, int len) { return units_of(a, len) + kItemCost; }
+
+// The weights of all items (below 2^32, checked on the host for the longest sequences) dealt out: how many workers have a
+// share (each then has some), where share w begins, and whose share
+// weight x is in.
 struct Deal {
     uint32_t n, base, more;  // the first `more` shares have base + 1 units
     __device__ __forceinline__ Deal(const Args &a, uint32_t total) {
@@ -67,7 +75,7 @@ struct Deal {
 // A scan over the sequences by the threads of a block: thread i adds up the sequences i * each .. i * each + each - 1.
 struct Scan {
     int each, first;
-    uint32_t sum, before, total;  // units of the thread's sequences, of those before, of all
+    uint32_t sum, before, total;  // weights of the thread's sequences, of those before, of all
 };
 // `mem`: an int for each warp.
 __device__ __forceinline__ Scan scan_sequences(const Args &a, uint32_t *mem) {
@@ -77,7 +85,7 @@ __device__ __forceinline__ Scan scan_sequences(const Args &a, uint32_t *mem) {
     s.first = threadIdx.x * s.each;
     s.sum = 0;
 #pragma unroll 1
-    for (int b = s.first; b < s.first + s.each && b < a.B; ++b) s.sum += units_of(a, cache_len(a.cache, b));
+    for (int b = s.first; b < s.first + s.each && b < a.B; ++b) s.sum += weight_of(a, cache_len(a.cache, b));
     s.sum *= a.per_seq;
     uint32_t scan = s.sum;
 #pragma unroll
@@ -97,10 +105,12 @@ __device__ __forceinline__ Scan scan_sequences(const Args &a, uint32_t *mem) {
     return s;
 }
 
-// One piece of work: units u0 .. u1 - 1 of an item's `units`.
+// One piece of work: units u0 .. u1 - 1 of an item's `units` (none where the share's border falls into the item's cost, which
+// stands before its units), and what they weigh.
 struct Piece {
     int b, len, head, row0, rows;  // first query row of the item and how many it has
-    uint32_t u0, u1, units;
+    uint32_t u0, u1, units, weight;
+    __device__ __forceinline__ bool none() const { return u0 == u1; }
     int last;  // keys that the last of its rows sees: no key at or after this one counts
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
     // The piece for `most` of its rows from row `from` on (none: `last` 0).
@@ -120,7 +130,7 @@ __device__ __forceinline__ void Piece::mine(const Args &a, int from, int most) {
 // A worker's way through its share, piece by piece: items in the order (sequence, block of rows, key head).
 struct Walk {
     int b, len, rb, head;
-    uint32_t u0, left;
+    uint32_t w0, left;  // weight of the item that is done, and of the share that is left
     int next_len;  // of sequence b + 1, read ahead
     __device__ __forceinline__ void read_ahead(const Args &a) { next_len = b + 1 < a.B ? cache_len(a.cache, b + 1) : 0; }
     __device__ __forceinline__ Piece piece(const Args &a) const {
@@ -128,8 +138,11 @@ struct Walk {
         p.b = b;
         p.len = len;
         p.units = units_of(a, len);
-        p.u0 = u0;
-        p.u1 = left < p.units - u0 ? u0 + left : p.units;
+        p.weight = p.units + kItemCost - w0;
+        p.weight = left < p.weight ? left : p.weight;
+        const uint32_t w1 = w0 + p.weight;
+        p.u0 = w0 < kItemCost ? 0 : w0 - kItemCost;
+        p.u1 = w1 < kItemCost ? 0 : w1 - kItemCost;
         p.head = head;
         p.row0 = rb * a.rows;
         const int all = a.T * a.group;
@@ -137,9 +150,10 @@ struct Walk {
         p.last = seen(a, len, p.row0 + p.rows - 1);
         return p;
     }
-    __device__ __forceinline__ void step(const Args &a, uint32_t done) {
-        left -= done;
-        u0 = 0;
+    // On past a piece.
+    __device__ __forceinline__ void step(const Args &a, uint32_t weight) {
+        left -= weight;
+        w0 = 0;
         if (++head < a.cache.heads) return;
         head = 0;
         if (++rb < a.row_blocks) return;
@@ -164,7 +178,7 @@ __device__ __forceinline__ Walk find_walk(const Args &a, uint32_t *mem) {
             uint32_t before = sc.before;
 #pragma unroll 1
             for (;;) {
-                const uint32_t x = units_of(a, cache_len(a.cache, b)) * a.per_seq;
+                const uint32_t x = weight_of(a, cache_len(a.cache, b)) * a.per_seq;
                 if (at - before < x) break;
                 before += x;
                 ++b;
@@ -177,15 +191,15 @@ __device__ __forceinline__ Walk find_walk(const Args &a, uint32_t *mem) {
     const uint32_t v = (threadIdx.x >> 5) / TEAM;
     Walk k;
     k.left = 0;
-    k.b = k.len = k.rb = k.head = k.u0 = k.next_len = 0;
+    k.b = k.len = k.rb = k.head = k.w0 = k.next_len = 0;
     if (w0 + v < deal.n) {
         k.left = deal.start(w0 + v + 1) - deal.start(w0 + v);
         k.b = (int)found[v];
         k.len = cache_len(a.cache, k.b);
-        const uint32_t units = units_of(a, k.len), item = rest[v] / units;
+        const uint32_t weight = weight_of(a, k.len), item = rest[v] / weight;
         k.rb = (int)(item / a.cache.heads);
         k.head = (int)item - k.rb * a.cache.heads;
-        k.u0 = rest[v] - item * units;
+        k.w0 = rest[v] - item * weight;
         k.read_ahead(a);
     }
     return k;
@@ -249,7 +263,7 @@ struct Stream {
     uint8_t *scales;         // [kUnits][2][KEYS] exponent bytes
     int lane;
     Walk walk;               // of the unit that is looked up next
-    uint32_t u, u1;          // that unit, and where its piece ends
+    uint32_t u, u1, weight;  // that unit, where its piece ends, what the piece weighs
     int last;                // keys of its piece that count
     int entry, place;        // of this lane's row (first + lane % kMine), looked up: the table's entry, the row within the page and head (-1: none)
     int row;                 // and of the unit that is copied next: the row of the cache (-1: zeros)
@@ -276,11 +290,15 @@ struct Stream {
         }
     }
     __device__ __forceinline__ void enter() {
-        if (walk.left == 0) return;
-        const Piece p = walk.piece(a);
-        u = p.u0;
-        u1 = p.u1;
-        last = p.last;
+        while (walk.left != 0) {
+            const Piece p = walk.piece(a);
+            u = p.u0;
+            u1 = p.u1;
+            last = p.last;
+            weight = p.weight;
+            if (!p.none()) break;
+            walk.step(a, weight);
+        }
     }
     __device__ __forceinline__ void look() {
         place = -1;
@@ -293,7 +311,7 @@ struct Stream {
             place = walk.head * a.cache.page + s;
         }
         if (++u == u1) {
-            walk.step(a, u1 - walk.u0);
+            walk.step(a, weight);
             enter();
         }
     }

@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
 #pragma unroll 1
     while (walk.left > 0) {
         const Piece p = walk.piece(a);
+        if (p.none()) {
+            walk.step(a, p.weight);
+            continue;
+        }
 #pragma unroll 1
         for (int r = 0; r < p.rows; ++r) {
             const float *from = static_cast<const float *>(a.q) + q_at(a, p, r);
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             }
         }
         __syncwarp();
-        walk.step(a, p.u1 - p.u0);
+        walk.step(a, p.weight);
     }
     copies_wait<0>();
 }

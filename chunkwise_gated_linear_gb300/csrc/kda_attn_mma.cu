@@ -137,6 +137,10 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
 #pragma unroll 1
     while (walk.left > 0) {
         Piece p = walk.piece(a);
+        if (p.none()) {
+            walk.step(a, p.weight);
+            continue;
+        }
         if constexpr (TEAM > 1) p.mine(a, warp % TEAM * kRows, kRows);
         // Q^T: row 8 n + g, the lane's channels of each block of 16 in the order in which K's come out of the ring
 #pragma unroll 1
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
             }
         }
         __syncwarp();
-        walk.step(a, p.u1 - p.u0);
+        walk.step(a, p.weight);
     }
     copies_wait<0>();
 }

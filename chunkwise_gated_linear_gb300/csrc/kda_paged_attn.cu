@@ -5,7 +5,7 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kJoinWarps = 8;  // of a block, at most
+constexpr int kJoinWarps = 16;  // of a block, at most
 
 // A query row of an item that was cut: with the largest m of its pieces, the sum of 2^(m - max) (l, O) over them. `split` warps
 // share a row's pieces in order, each with a maximum of its own, and are then added up; lane i holds channels
@@ -23,20 +23,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     walk.rb = item / a.cache.heads;
     walk.head = item - walk.rb * a.cache.heads;
     walk.len = cache_len(a.cache, walk.b);
-    walk.u0 = 0;
+    walk.w0 = 0;
     walk.left = 0xffffffffu;
     const Scan sc = scan_sequences(a, mem);
     if (walk.b >= sc.first && walk.b < sc.first + sc.each) {  // one thread's
         uint32_t before = sc.before;
 #pragma unroll 1
-        for (int x = sc.first; x < walk.b; ++x) before += units_of(a, cache_len(a.cache, x)) * a.per_seq;
+        for (int x = sc.first; x < walk.b; ++x) before += weight_of(a, cache_len(a.cache, x)) * a.per_seq;
         mine = before;
     }
     __syncthreads();
     const Deal deal(a, sc.total);
     const Piece p = walk.piece(a);
-    const uint32_t begin = mine + item * p.units;
-    const int w0 = deal.owner(begin), w1 = deal.owner(begin + p.units - 1);
+    const uint32_t end = mine + (item + 1) * (p.units + kItemCost);
+    const int w0 = deal.owner(end - p.units), w1 = deal.owner(end - 1);
     if (w0 == w1) return;
     const int D = a.cache.D, part = warp % split;
     const int r = blockIdx.y * (warps / split) + warp / split;
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
             for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
             l += ls;
             const int count = to - w < 32 ? to - w : 32;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < count; ++i) {
                 const float fi = __shfl_sync(0xffffffffu, f, i);
                 const float *o = piece_mem(a, w + i, w + i == w0) + (int64_t)r * D + 4 * lane;
@@ -207,7 +207,7 @@ int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
     Args a = attn::make(*p, err);
     if (a.workers == 0) return status_of_cuda(cudaErrorInvalidDevice);
     // units of all sequences, were they as long as the table allows
-    if ((int64_t)a.B * a.per_seq * (((int64_t)a.cache.most >> a.unit_shift) + 1) >= (int64_t)1 << 32) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)a.B * a.per_seq * (((int64_t)a.cache.most >> a.unit_shift) + 1 + kItemCost) >= (int64_t)1 << 32) return KDA_ERR_UNSUPPORTED;
     const size_t bytes = bytes_of(a);
     if (p->workspace != nullptr && p->workspace_bytes < bytes) return KDA_ERR_INVALID_ARG;
     if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;
