@@ -2,7 +2,8 @@
 // for how the work is cut.
 //
 // A unit is KEYS keys: lane (key, part) takes every (32 / KEYS)-th 16-byte chunk of its key against all query rows, the
-// parts are added across lanes; then a lane owns columns lane + 32 j of O and goes through the keys.
+// parts are added across lanes; then a lane owns DP / 32 neighbouring columns of O and goes through the keys. Arithmetic
+// goes in pairs of fp32.
 #include "attn_common.cuh"
 #include "attn_launch.h"
 
@@ -10,24 +11,25 @@ namespace kda {
 namespace attn {
 namespace {
 
-template <typename C>
-__device__ __forceinline__ void unpack16(float (&f)[16 / sizeof(C)], const uint4 &v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// N consecutive values of a row as pairs.
+template <typename C, int N>
+__device__ __forceinline__ void values(f2 (&x)[N / 2], const unsigned char *at) {
+    if constexpr (sizeof(C) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(C) == 4) {
-            f[i] = __uint_as_float(w[i]);
-        } else {
-            e4m3_to_f(w[i] & 0xffffu, f[4 * i], f[4 * i + 1]);
-            e4m3_to_f(w[i] >> 16, f[4 * i + 2], f[4 * i + 3]);
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 v = reinterpret_cast<const float2 *>(at)[i];
+            x[i] = pk(v.x, v.y);
+        }
+    } else {
+        Raw<uint16_t, N / 2> r;  // two values in each
+        r.load(reinterpret_cast<const uint16_t *>(at));
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            float lo, hi;
+            e4m3_to_f(r.w[i / 2] >> (16 * (i & 1)) & 0xffffu, lo, hi);
+            x[i] = pk(lo, hi);
         }
     }
-}
-__device__ __forceinline__ float elem(const float *p) { return *p; }
-__device__ __forceinline__ float elem(const uint8_t *p) {
-    float lo, hi;
-    e4m3_to_f(*p, lo, hi);
-    return lo;
 }
 
 template <typename C, int DP, int RB, int KEYS, int SLOTS>
@@ -35,7 +37,7 @@ struct Fma {
     using S = Stream<C, DP, KEYS, SLOTS>;
     static constexpr int kParts = 32 / KEYS;
     static constexpr int kE = 16 / (int)sizeof(C);
-    static constexpr int kCols = DP / 32;
+    static constexpr int kCols = DP / 32;  // of a lane, side by side
     // shared memory: rings, q [warps][RB][DP], p [warps][KEYS][RB], rows' limits [warps][RB], the plan, exponent bytes
     static constexpr int kQ = kWarps * S::kBytes;
     static constexpr int kP = kQ + kWarps * RB * DP * 4;
@@ -79,13 +81,14 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
         if (lane < RB) lim[lane] = lane < p.rows ? seen(a, p.len, p.row0 + lane) : 0;
         __syncwarp();
         const int least = lim[0];  // keys from here on are not seen by all rows
-        float m[RB], l[RB], acc[RB][F::kCols];
+        float m[RB], l[RB];
+        f2 acc[RB][F::kCols / 2];
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
 #pragma unroll
-            for (int j = 0; j < F::kCols; ++j) acc[r][j] = 0.f;
+            for (int j = 0; j < F::kCols / 2; ++j) acc[r][j] = pk(0.f, 0.f);
         }
 #pragma unroll 1
         for (uint32_t u = p.u0; u < p.u1; ++u) {
@@ -94,26 +97,27 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             if (pos0 < p.last) {  // the same for the whole warp
                 const unsigned char *ks = own + st.slot * F::S::kSlot;
                 const uint8_t *sc = st.bytes();
-                float x[RB];
+                f2 dots[RB];
 #pragma unroll
-                for (int r = 0; r < RB; ++r) x[r] = 0.f;
+                for (int r = 0; r < RB; ++r) dots[r] = pk(0.f, 0.f);
 #pragma unroll 1
                 for (int c = part; c < cpr; c += F::kParts) {
-                    float kf[F::kE];
-                    unpack16<C>(kf, *reinterpret_cast<const uint4 *>(ks + key * F::S::kPitch + ((c ^ (key & 7)) << 4)));
+                    f2 kf[F::kE / 2];
+                    values<C, F::kE>(kf, ks + key * F::S::kPitch + ((c ^ (key & 7)) << 4));
 #pragma unroll
                     for (int r = 0; r < RB; ++r) {
                         if (r >= p.rows) break;
 #pragma unroll
                         for (int e = 0; e < F::kE; e += 4) {
                             const float4 qv = *reinterpret_cast<const float4 *>(qs + r * DP + c * F::kE + e);
-                            x[r] = fmaf(kf[e], qv.x, x[r]);
-                            x[r] = fmaf(kf[e + 1], qv.y, x[r]);
-                            x[r] = fmaf(kf[e + 2], qv.z, x[r]);
-                            x[r] = fmaf(kf[e + 3], qv.w, x[r]);
+                            dots[r] = fma2(kf[e / 2], pk(qv.x, qv.y), dots[r]);
+                            dots[r] = fma2(kf[e / 2 + 1], pk(qv.z, qv.w), dots[r]);
                         }
                     }
                 }
+                float x[RB];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) x[r] = hsum2(dots[r]);
                 float kscale = 1.f, vscale = 1.f;
                 if constexpr (F::S::kScaled) {
                     kscale = __uint_as_float((uint32_t)sc[key] << 23);
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
 #pragma unroll
                     for (int r = 0; r < RB; ++r)
 #pragma unroll
-                        for (int j = 0; j < F::kCols; ++j) acc[r][j] *= alpha[r];
+                        for (int j = 0; j < F::kCols / 2; ++j) acc[r][j] = mul2(acc[r][j], pk(alpha[r], alpha[r]));
                 }
             }
             st.template release<false>();
@@ -157,20 +161,25 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
                 const bool edge = pos0 + KEYS > least;
 #pragma unroll 2
                 for (int k = 0; k < KEYS; ++k) {
-                    float v[F::kCols];
+                    f2 v[F::kCols / 2];
+                    constexpr int kBytes = F::kCols * (int)sizeof(C), kStep = kBytes < 16 ? kBytes : 16, kN = kStep / (int)sizeof(C);
 #pragma unroll
-                    for (int j = 0; j < F::kCols; ++j) {
-                        const int byte = (lane + 32 * j) * (int)sizeof(C);
-                        v[j] = elem(reinterpret_cast<const C *>(vs + k * F::S::kPitch + ((((byte >> 4) ^ (k & 7)) << 4) | (byte & 15))));
+                    for (int h = 0; h < kBytes / kStep; ++h) {
+                        const int byte = lane * kBytes + h * kStep;
+                        f2 t[kN / 2];
+                        values<C, kN>(t, vs + k * F::S::kPitch + ((((byte >> 4) ^ (k & 7)) << 4) | (byte & 15)));
+#pragma unroll
+                        for (int i = 0; i < kN / 2; ++i) v[h * kN / 2 + i] = t[i];
                     }
+                    float w[RB];
+                    load_vec<float, RB>(w, pw + k * RB);
 #pragma unroll
                     for (int r = 0; r < RB; ++r) {
                         if (r >= p.rows) break;
                         // a value that this row does not see must not reach it, not even times zero
                         if (edge && pos0 + k >= lim[r]) continue;
-                        const float w = pw[k * RB + r];
 #pragma unroll
-                        for (int j = 0; j < F::kCols; ++j) acc[r][j] = fmaf(w, v[j], acc[r][j]);
+                        for (int j = 0; j < F::kCols / 2; ++j) acc[r][j] = fma2(pk(w[r], w[r]), v[j], acc[r][j]);
                     }
                 }
             }
@@ -188,8 +197,12 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             const float f = whole ? (t == 0.f ? 0.f : 1.f / t) : 1.f;
             float *to = whole ? static_cast<float *>(a.o) + row * D : piece + r * D;
 #pragma unroll
-            for (int j = 0; j < F::kCols; ++j)
-                if (lane + 32 * j < D) to[lane + 32 * j] = acc[r][j] * f;
+            for (int j = 0; j < F::kCols / 2; ++j) {
+                const int d = lane * F::kCols + 2 * j;
+                float lo, hi;
+                upk(mul2(acc[r][j], pk(f, f)), lo, hi);
+                if (d < D) *reinterpret_cast<float2 *>(to + d) = make_float2(lo, hi);
+            }
             if (lane == 0) {
                 if (!whole)
                     reinterpret_cast<float2 *>(piece + a.rows * D)[r] = make_float2(m[r], t);
@@ -217,7 +230,7 @@ template <typename C, int RB, typename F>
 auto pick(const Args &a, F f) {
     constexpr bool k4 = sizeof(C) == 4;
     if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16, 6>{});
-    if (a.cache.D <= 128) return f(Variant<C, 128, RB, k4 ? 8 : 16, 5>{});
+    if (a.cache.D <= 128) return f(Variant<C, 128, RB, (k4 && RB > 4) ? 8 : 16, (k4 && RB == 4) ? 3 : 5>{});
     return f(Variant<C, 256, RB == 16 ? 8 : RB, k4 ? 8 : 16, 5>{});
 }
 template <typename F>

@@ -51,11 +51,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
         for (int h = 0; h < 2; ++h) s[h] = make_float4(s[h].x * f, s[h].y * f, s[h].z * f, s[h].w * f);
     };
     if (r < p.rows) {
+        // pieces 2 w, and of the first worker, where the item begins, 2 w + 1
+        const int64_t size = (int64_t)a.rows * (D + 2);
 #pragma unroll 1
         for (int w = from; w < to; w += 32) {
-            // the piece of the first worker begins there, the others come from the one before
             const int my = w + lane < to ? w + lane : w;
-            const float2 x = reinterpret_cast<const float2 *>(piece_mem(a, my, my == w0) + (int64_t)a.rows * D)[r];
+            const float2 x = reinterpret_cast<const float2 *>(a.pieces + (2 * my + (my == w0)) * size + (int64_t)a.rows * D)[r];
             float top = x.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -69,19 +70,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
             for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
             l += ls;
             const int count = to - w < 32 ? to - w : 32;
-#pragma unroll 8
-            for (int i = 0; i < count; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float *o = piece_mem(a, w + i, w + i == w0) + (int64_t)r * D + 4 * lane;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (4 * lane + 128 * h < D) {
-                        const float4 v = *reinterpret_cast<const float4 *>(o + 128 * h);
-                        s[h].x = fmaf(v.x, fi, s[h].x);
-                        s[h].y = fmaf(v.y, fi, s[h].y);
-                        s[h].z = fmaf(v.z, fi, s[h].z);
-                        s[h].w = fmaf(v.w, fi, s[h].w);
-                    }
+            const float *o = a.pieces + 2 * w * size + (int64_t)r * D + 4 * lane;
+#pragma unroll 1
+            for (int h = 0; h < 2 && 128 * h < D; ++h) {
+                const bool in = 4 * lane + 128 * h < D;
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int i = 0; i < count; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in) v = *reinterpret_cast<const float4 *>(o + (2 * i + (w + i == w0)) * size + 128 * h);
+                    t = make_float4(fmaf(v.x, fi, t.x), fmaf(v.y, fi, t.y), fmaf(v.z, fi, t.z), fmaf(v.w, fi, t.w));
+                }
+                float4 &to_sum = h == 0 ? s[0] : s[1];
+                to_sum = make_float4(to_sum.x + t.x, to_sum.y + t.y, to_sum.z + t.z, to_sum.w + t.w);
             }
         }
     }
