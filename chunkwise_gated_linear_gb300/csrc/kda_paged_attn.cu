@@ -8,13 +8,16 @@ namespace {
 constexpr int kJoinWarps = 16;  // of a block, at most
 
 // A query row of an item that was cut: with the largest m of its pieces, the sum of 2^(m - max) (l, O) over them. `split` warps
-// share a row's pieces in order, each with a maximum of its own, and are then added up; lane i holds channels
-// 4 i .. 4 i + 3 (and + 128). A block with nothing to join ends after the plan, which is made while the attention
-// still runs. What it costs is waiting: each warp reads the statistics of all its pieces at once, then the pieces.
-template <typename T>
+// share a row's pieces in order, each with a maximum of its own, and are then added up. Of a warp, LC lanes hold four
+// channels each and the others take other pieces: 32 for many rows, 8 (and a block for every 32 channels) for few. A
+// block with nothing to join ends after the plan, which is made while the attention still runs. What it costs is waiting:
+// each warp reads the statistics of all its pieces at once, then the pieces. (One sequence of 131071 tokens, 228
+// pieces a row: 13 us with 16 warps for a row.)
+template <typename T, int LC>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ Args a, int split) {
     __shared__ uint32_t mem[kJoinWarps], mine;
-    __shared__ float4 sums[kJoinWarps][64];
+    constexpr int kAtOnce = 32 / LC, kPasses = LC == 8 ? 1 : 2;  // pieces of a warp at a time; turns over its channels
+    __shared__ float4 sums[kJoinWarps][kPasses * LC];
     __shared__ float2 stat[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     Walk walk;  // of the item
@@ -44,11 +47,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     const int from = w0 + part * each, to = from + each < w1 + 1 ? from + each : w1 + 1;
     wait_for_previous();
     float m = -INFINITY, l = 0.f;
-    float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float4 s[kPasses];
+#pragma unroll
+    for (int h = 0; h < kPasses; ++h) s[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int mine_of = lane / LC, d0 = (LC == 8 ? 32 * (int)blockIdx.z : 0) + 4 * (lane % LC);
     auto scale = [&](float f) {
         l *= f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[h] = make_float4(s[h].x * f, s[h].y * f, s[h].z * f, s[h].w * f);
+        for (int h = 0; h < kPasses; ++h) s[h] = make_float4(s[h].x * f, s[h].y * f, s[h].z * f, s[h].w * f);
     };
     if (r < p.rows) {
         // pieces 2 w, and of the first worker, where the item begins, 2 w + 1
@@ -70,26 +76,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
             for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
             l += ls;
             const int count = to - w < 32 ? to - w : 32;
-            const float *o = a.pieces + 2 * w * size + (int64_t)r * D + 4 * lane;
-#pragma unroll 1
-            for (int h = 0; h < 2 && 128 * h < D; ++h) {
-                const bool in = 4 * lane + 128 * h < D;
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *o = a.pieces + 2 * w * size + (int64_t)r * D + d0;
+#pragma unroll
+            for (int h = 0; h < kPasses; ++h) {
+                if (128 * h >= D) break;
+                const bool in = d0 + 128 * h < D;
 #pragma unroll 4
-                for (int i = 0; i < count; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i);
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (in) v = *reinterpret_cast<const float4 *>(o + (2 * i + (w + i == w0)) * size + 128 * h);
-                    t = make_float4(fmaf(v.x, fi, t.x), fmaf(v.y, fi, t.y), fmaf(v.z, fi, t.z), fmaf(v.w, fi, t.w));
+                for (int i = mine_of; i - mine_of < count; i += kAtOnce) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i & 31);
+                    if (in && i < count) {
+                        const float4 v = *reinterpret_cast<const float4 *>(o + (2 * i + (w + i == w0)) * size + 128 * h);
+                        s[h] = make_float4(fmaf(v.x, fi, s[h].x), fmaf(v.y, fi, s[h].y), fmaf(v.z, fi, s[h].z), fmaf(v.w, fi, s[h].w));
+                    }
                 }
-                float4 &to_sum = h == 0 ? s[0] : s[1];
-                to_sum = make_float4(to_sum.x + t.x, to_sum.y + t.y, to_sum.z + t.z, to_sum.w + t.w);
+            }
+        }
+        if constexpr (LC < 32) {
+#pragma unroll
+            for (int off = LC; off < 32; off <<= 1) {
+                s[0].x += __shfl_xor_sync(0xffffffffu, s[0].x, off);
+                s[0].y += __shfl_xor_sync(0xffffffffu, s[0].y, off);
+                s[0].z += __shfl_xor_sync(0xffffffffu, s[0].z, off);
+                s[0].w += __shfl_xor_sync(0xffffffffu, s[0].w, off);
             }
         }
     }
     if (split > 1) {
-        sums[warp][lane] = s[0];
-        sums[warp][32 + lane] = s[1];
+        if (lane < LC) {
+#pragma unroll
+            for (int h = 0; h < kPasses; ++h) sums[warp][h * LC + lane] = s[h];
+        }
         if (lane == 0) stat[warp] = make_float2(m, l);
         __syncthreads();
         if (part != 0) return;
@@ -103,22 +119,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
             const float f = tc5::ex2(x.x - (m == -INFINITY ? 0.f : m));
             l = fmaf(x.y, f, l);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 y = sums[v][32 * h + lane];
+            for (int h = 0; h < kPasses; ++h) {
+                const float4 y = sums[v][h * LC + lane % LC];
                 s[h] = make_float4(fmaf(y.x, f, s[h].x), fmaf(y.y, f, s[h].y), fmaf(y.z, f, s[h].z), fmaf(y.w, f, s[h].w));
             }
         }
     }
-    if (r >= p.rows) return;
+    if (r >= p.rows || lane >= LC) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t row = out_row(a, p, r);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (4 * lane + 128 * h < D) {
+    for (int h = 0; h < kPasses; ++h)
+        if (d0 + 128 * h < D) {
             const float y[4] = {s[h].x * inv, s[h].y * inv, s[h].z * inv, s[h].w * inv};
-            store_vec<T, 4>(static_cast<T *>(a.o) + row * D + 4 * lane + 128 * h, y);
+            store_vec<T, 4>(static_cast<T *>(a.o) + row * D + d0 + 128 * h, y);
         }
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = lse_of(m, l);
+    if (d0 == 0 && a.lse != nullptr) a.lse[row] = lse_of(m, l);
 }
 
 template <typename T>
@@ -134,12 +150,13 @@ cudaError_t launch_join(const Args &a, cudaStream_t stream) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)items, (unsigned)ceil_div(rows, at_once));
+    const bool few = split == kJoinWarps;
+    cfg.gridDim = dim3((unsigned)items, (unsigned)ceil_div(rows, at_once), few ? (unsigned)ceil_div(a.cache.D, 32) : 1u);
     cfg.blockDim = dim3((unsigned)(32 * split * at_once));
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T>, a, split);
+    return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 8>, a, split) : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 32>, a, split);
 }
 
 int elem_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
