@@ -1031,7 +1031,8 @@ BwdPlan bwd_plan(const kda_qk_norm_bwd_params &p, int64_t rows, unsigned int *er
     if (q.vec) {
         q.p = vec_plan(q.a, f32);
         q.p.blocks = (unsigned)q.p.v.batches;
-        const unsigned most = (unsigned)sm_count() * 2;
+        const int sms = sm_count();  // 0 without a device: the call itself reports that
+        const unsigned most = sms > 0 ? 2 * sms : 1;
         // at most as many tokens at a time as there is room for the angles of (46 KB in all)
         int cap = (46 * 1024 / 4 - 32 * q.p.lpr - 32 * kVecThreads) / (p.f.R / 2 * 3 + 1);
         cap = cap > kVecTokens ? kVecTokens : cap;

@@ -141,6 +141,16 @@ def test_workspace_sizes_of_rejected_calls_are_zero():
     assert attention.kda_attn_step_workspace(_attn(T=0)) == 0
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a host without a device")
+def test_well_formed_calls_report_a_missing_device():
+    for fn, make in (("qk_norm_fwd", _fwd), ("qk_norm_bwd", _bwd), ("qk_norm_step", _step), ("kv_cache_write", _write), ("kv_cache_read", _read),
+                     ("attn_step", _attn)):
+        for over in (dict(), dict(D=24, R=24)) if fn.startswith("qk_norm") and fn != "qk_norm_step" else (dict(),):
+            assert getattr(attention, "kda_" + fn)(make(**over), 0) == kda.KDA_ERR_CUDA, (fn, over)
+    attention.kda_qk_norm_bwd_workspace(_bwd())
+    attention.kda_attn_step_workspace(_attn())
+
+
 def _t(*shape, dtype=BF):
     return torch.zeros(*shape, dtype=torch.uint8).view(dtype) if dtype in (E4M3, E8M0) else torch.zeros(*shape, dtype=dtype)
 
