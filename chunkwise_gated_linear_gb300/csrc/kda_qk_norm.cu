@@ -822,18 +822,19 @@ __global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(c
 // ---- host side -------------------------------------------------------------------------------
 int elem_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
-int sizes_check(int B, int T, const int32_t *cu, int dtype, int heads, int64_t *rows) {
+int sizes_check(int B, int T, const int32_t *cu, int dtype, int64_t heads, int64_t *rows) {
     if (B < 1 || T < 0 || heads < 1) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
     *rows = cu != nullptr ? T : (int64_t)B * T;
-    if (*rows * heads >= (int64_t)1 << 31) return KDA_ERR_UNSUPPORTED;
+    // counts of heads of tokens go a block's stride beyond their number
+    if (*rows != 0 && heads > (INT32_MAX - (1 << 16)) / *rows) return KDA_ERR_UNSUPPORTED;
     return aligned(cu, 4) ? KDA_OK : KDA_ERR_ALIGNMENT;
 }
 int stride_check(int64_t given, int64_t dense) { return given != 0 && given < dense ? KDA_ERR_INVALID_ARG : KDA_OK; }
 
 int norm_check(const kda_qk_norm_params &p, bool q_out, bool k_out, int64_t *rows) {
     if (p.q_heads < 1 || p.k_heads < 1 || p.D < 1 || p.R < 0 || p.R % 2 != 0 || p.R > p.D || !(p.eps >= 0.f)) return KDA_ERR_INVALID_ARG;
-    const int st = sizes_check(p.B, p.T, p.cu_seqlens, p.dtype, p.q_heads + 2 * p.k_heads, rows);
+    const int st = sizes_check(p.B, p.T, p.cu_seqlens, p.dtype, p.q_heads + 2 * (int64_t)p.k_heads, rows);
     if (st != KDA_OK) return st;
     if (p.D > kMaxD) return KDA_ERR_UNSUPPORTED;
     if (stride_check(p.q_stride, (int64_t)p.q_heads * p.D) != KDA_OK || stride_check(p.k_stride, (int64_t)p.k_heads * p.D) != KDA_OK)
@@ -1113,7 +1114,7 @@ int kda_kv_cache_write(const kda_kv_cache_write_params *p, cudaStream_t stream) 
     using namespace kda;
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     int64_t rows = 0;
-    int st = sizes_check(p->B, p->T, p->cu_seqlens, p->dtype, 2 * p->cache.heads, &rows);
+    int st = sizes_check(p->B, p->T, p->cu_seqlens, p->dtype, 2 * (int64_t)p->cache.heads, &rows);
     if (st == KDA_OK) st = cache_check(p->cache, p->dtype);
     if (st != KDA_OK) return st;
     const int64_t dense = (int64_t)p->cache.heads * p->cache.D;
@@ -1142,7 +1143,7 @@ int kda_kv_cache_read(const kda_kv_cache_read_params *p, cudaStream_t stream) {
     using namespace kda;
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     int64_t rows = 0;
-    int st = sizes_check(p->B, p->T, p->cu_seqlens, p->dtype, 2 * p->cache.heads, &rows);
+    int st = sizes_check(p->B, p->T, p->cu_seqlens, p->dtype, 2 * (int64_t)p->cache.heads, &rows);
     if (st == KDA_OK) st = cache_check(p->cache, p->dtype);
     if (st != KDA_OK) return st;
     if (rows != 0 && (p->k == nullptr || p->v == nullptr)) return KDA_ERR_INVALID_ARG;

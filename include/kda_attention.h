@@ -87,7 +87,7 @@ typedef struct kda_kv_cache {
  *   q, q_out [B, T, q_heads, D], k, k_out [B, T, k_heads, D] `dtype`; q_weight, k_weight [D]
  *   fp32 or NULL; freq [R / 2] (NULL with R == 0); positions [B, T] int32, or NULL: the token's index in
  *   its sequence. 1 <= D <= 256, R even, R <= D. q_out may be q and k_out may be k when they are
- *   contiguous. B times T (packed: T) times the heads is below 2^31.
+ *   contiguous. B times T (packed: T) times (q_heads + 2 k_heads) is below 2^31 - 2^16.
  */
 typedef struct kda_qk_norm_params {
     const void *q, *k;

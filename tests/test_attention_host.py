@@ -101,7 +101,9 @@ CACHE = [(dict(c_k=None), INV), (dict(c_v=None), INV), (dict(c_block_table=None)
     ("qk_norm_fwd", _fwd, dict(q_stride=255), INV), ("qk_norm_fwd", _fwd, dict(k_stride=-128), INV), ("qk_norm_fwd", _fwd, dict(q=A + 1), ALI),
     ("qk_norm_fwd", _fwd, dict(q_weight=A + 2), ALI), ("qk_norm_fwd", _fwd, dict(freq=A + 4), ALI),
     ("qk_norm_fwd", _fwd, dict(positions=A + 1), ALI), ("qk_norm_fwd", _fwd, dict(cu_seqlens=A + 2), ALI),
-    ("qk_norm_fwd", _fwd, dict(B=1 << 15, T=1 << 15), UNS),
+    ("qk_norm_fwd", _fwd, dict(B=1 << 15, T=1 << 15), UNS), ("qk_norm_fwd", _fwd, dict(q_heads=4, k_heads=(1 << 31) - 1), UNS),
+    ("qk_norm_fwd", _fwd, dict(B=1, T=1 << 28, q_heads=4, k_heads=2), UNS), ("qk_norm_bwd", _bwd, dict(k_heads=(1 << 31) - 1), UNS),
+    ("kv_cache_write", _write, dict(c_heads=(1 << 30) + 2), UNS), ("kv_cache_read", _read, dict(c_heads=(1 << 31) - 1), UNS),
     ("qk_norm_fwd", _fwd, dict(q_out=A, q_stride=512), INV), ("qk_norm_fwd", _fwd, dict(k_out=A, k_stride=512), INV),  # in place: contiguous
     ("qk_norm_bwd", _bwd, dict(dq_out=None), INV), ("qk_norm_bwd", _bwd, dict(dk=None), INV), ("qk_norm_bwd", _bwd, dict(q_weight=None), INV),
     ("qk_norm_bwd", _bwd, dict(k_weight=None), INV), ("qk_norm_bwd", _bwd, dict(dq=A + 1), ALI), ("qk_norm_bwd", _bwd, dict(dk_weight=A + 1), ALI),
