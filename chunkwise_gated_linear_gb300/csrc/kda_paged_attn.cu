@@ -10,7 +10,7 @@ constexpr int kJoinWarps = 16;  // of a block, at most
 // A query row of an item that was cut: with the largest m of its pieces, the sum of 2^(m - max) (l, O) over them. `split` warps
 // share a row's pieces in order, each with a maximum of its own, and are then added up. Of a warp, LC lanes hold four
 // channels each and the others take other pieces: 32 for many rows, 8 (and a block for every 32 channels) for few. A
-// block with nothing to join ends after the plan, which is made while the attention still runs. What it costs is waiting:
+// block with nothing to join ends after the plan, which is made while the attention still runs (but for the first). What it costs is waiting:
 // each warp reads the statistics of all its pieces at once, then the pieces. (One sequence of 131071 tokens, 228
 // pieces a row: 13 us with 16 warps for a row.)
 template <typename T, int LC>
@@ -40,7 +40,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     const Piece p = walk.piece(a);
     const uint32_t end = mine + (item + 1) * (p.units + kItemCost);
     const int w0 = deal.owner(end - p.units), w1 = deal.owner(end - 1);
-    if (w0 == w1) return;
+    if (w0 == w1) {
+        // the first block stays, or this kernel could be over, and the stream go on, while the attention still runs
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) wait_for_previous();
+        return;
+    }
     const int D = a.cache.D, part = warp % split;
     const int r = blockIdx.y * (warps / split) + warp / split;
     const int each = (w1 - w0 + split) / split;  // pieces of a warp
