@@ -317,6 +317,7 @@ struct Stream {
     }
     __device__ __forceinline__ void resolve() {
         row = -1;
+        sk = sv = 0;  // not those of another sequence's row, which may be no number
         if (place < 0) return;
         if ((unsigned)entry < (unsigned)a.cache.pages) {
             row = entry * (int)a.cache.page_rows + place;

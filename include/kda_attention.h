@@ -53,7 +53,8 @@ extern "C" {
  *               block_table[b][p / page_size]. `dtype`: the type of the data, or KDA_DTYPE_E4M3.
  *               16-byte aligned, D a multiple of 16, at most 256; page_size of any size.
  *   k_scale,    [pages, heads, page_size] bytes, KDA_DTYPE_E4M3 only: a row holds the values
- *   v_scale     e4m3 * 2^(byte - 127).
+ *   v_scale     e4m3 * 2^(byte - 127), byte 1 to 254 (another one leaves results of its own
+ *               sequence undefined, not those of others).
  *   page_stride, scale_stride  elements between consecutive pages of k and v, and of the
  *               scales (k and v alike; 0: contiguous). page_stride is a multiple of D.
  *   block_table [B, max_pages] int32, rows table_stride apart (0: max_pages). Entries beyond a

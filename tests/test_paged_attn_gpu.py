@@ -345,3 +345,20 @@ def test_tiny_values_in_an_8_bit_cache(dtype):
         pos = torch.arange(n)
         index(cache.v_scale)[table[b].long()[pos // 16], :, pos % 16] = (5 + 20 * (pos % 2))[:, None].to(torch.uint8)
     _check(_q(g, 2, 1, 8, 64, dtype, E4M3), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 3])
+def test_power_of_two_that_is_no_number_stays_in_its_sequence(dtype, T):
+    """The byte 255 (NaN) in one sequence's scales: the sequences beside it, worked on after it by the same warps, are as they
+    are without it."""
+    g = torch.Generator().manual_seed(15)
+    lens = [37, 5] * 1000
+    cache, table = filled(g, lens, 16, 8, 64, E4M3)
+    q = _q(g, len(lens), T, 32, 64, dtype, E4M3)
+    call = lambda: paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens))  # noqa: E731
+    want = call()
+    for b in range(0, len(lens), 2):
+        pos = torch.arange(lens[b])
+        index(cache.v_scale)[table[b].long()[pos // 16], :, pos % 16] = 0xFF
+    assert bool(torch.isfinite(want).all()) and torch.equal(call()[1::2], want[1::2])
