@@ -182,7 +182,7 @@ int check(const kda_attn_step_params &p) {
     return KDA_OK;
 }
 
-Args make(const kda_attn_step_params &p, unsigned int *err) {
+Args make(const kda_attn_step_params &p) {
     Args a{};
     a.q = p.q;
     a.o = p.o;
@@ -193,7 +193,7 @@ Args make(const kda_attn_step_params &p, unsigned int *err) {
     a.Hq = p.q_heads;
     a.group = p.q_heads / p.cache.heads;
     a.scale_log2 = p.scale * kLog2e;
-    a.cache = cache_args(p.cache, err);
+    a.cache = cache_args(p.cache, nullptr);
     const int all = a.T * a.group;
     const bool f32 = p.dtype == KDA_DTYPE_F32;
     a.rows = f32 ? fma_rows(all, a.cache.D) : mma_rows(all, a.cache.D);
@@ -203,6 +203,11 @@ Args make(const kda_attn_step_params &p, unsigned int *err) {
     a.unit_shift = f32 ? fma_unit_shift(a) : mma_unit_shift(a);
     a.workers = sm_count() * (f32 ? fma_workers(a) : mma_workers(a));
     return a;
+}
+// Whether the units and costs of all items, were all sequences as long as the table allows, are counted in 32 bits.
+bool in_range(const Args &a) {
+    const int64_t weight = ((int64_t)a.cache.most >> a.unit_shift) + 1 + kItemCost;
+    return (int64_t)a.B * a.per_seq <= (int64_t)UINT32_MAX / weight;
 }
 size_t bytes_of(const Args &a) { return (size_t)2 * a.workers * a.rows * (a.cache.D + 2) * sizeof(float); }
 
@@ -215,7 +220,8 @@ extern "C" {
 size_t kda_attn_step_workspace(const kda_attn_step_params *p) {
     using namespace kda;
     if (p == nullptr || attn::check(*p) != KDA_OK || p->T == 0) return 0;
-    return attn::bytes_of(attn::make(*p, nullptr));
+    const attn::Args a = attn::make(*p);
+    return attn::in_range(a) ? attn::bytes_of(a) : 0;
 }
 
 int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
@@ -224,13 +230,11 @@ int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     const int st = attn::check(*p);
     if (st != KDA_OK || p->T == 0) return st;
-    unsigned int *err = nullptr;
-    cudaError_t e = device_error_word(&err);
+    Args a = attn::make(*p);
+    if (!in_range(a)) return KDA_ERR_UNSUPPORTED;
+    cudaError_t e = device_error_word(&a.cache.err);
     if (e != cudaSuccess) return status_of_cuda(e);
-    Args a = attn::make(*p, err);
     if (a.workers == 0) return status_of_cuda(cudaErrorInvalidDevice);
-    // units of all sequences, were they as long as the table allows
-    if ((int64_t)a.B * a.per_seq * (((int64_t)a.cache.most >> a.unit_shift) + 1 + kItemCost) >= (int64_t)1 << 32) return KDA_ERR_UNSUPPORTED;
     const size_t bytes = bytes_of(a);
     if (p->workspace != nullptr && p->workspace_bytes < bytes) return KDA_ERR_INVALID_ARG;
     if (!aligned(p->workspace, 16)) return KDA_ERR_ALIGNMENT;

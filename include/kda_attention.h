@@ -62,7 +62,7 @@ extern "C" {
  *   lens        [B] int32: the length of each sequence WITH the new tokens of the call: of n new
  *               tokens, token i stands at position lens[b] - n + i. A token at a negative
  *               position is not there (a sequence at rest in a batch has length 0).
- * Rows of a cache number less than 2^31 (page_stride / D times pages).
+ * Rows of a cache number at most 2^31 (page_stride / D times pages). Sequences longer than 2^31 - 65 are taken as long as that.
  */
 typedef struct kda_kv_cache {
     void *k, *v;
@@ -144,7 +144,8 @@ int kda_qk_norm_step(const kda_qk_norm_step_params *p, cudaStream_t stream);
  * power of two costs an 8-bit floating-point value no precision, and every product with it is
  * exact.) NaN is kept; a row with an infinity keeps it and has e = 120. Otherwise the cache has the type
  * of the data and holds it unchanged. No two tokens of a call may lie in the same place; other
- * places of the cache are left as they were.
+ * places of the cache are left as they were. 2 B T heads (packed: 2 T heads) is below 2^31 - 2^16, here and in
+ * kda_kv_cache_read.
  */
 typedef struct kda_kv_cache_write_params {
     const void *k, *v;
@@ -185,8 +186,10 @@ int kda_kv_cache_read(const kda_kv_cache_read_params *p, cudaStream_t stream);
  *   data: fp32 throughout.
  * The sequences' lengths are cut into equal shares for the GPU's SMs, and results of sequences that were
  * cut are joined in the order of their shares: which are cut follows from the lengths and sizes alone.
- * One call reads the cache ceil(T q_heads / heads / 32) times or less (16 for wide heads and fp32):
- * T in the hundreds works but is not what it is made for.
+ * One call reads the cache ceil(T q_heads / heads / 64) times (bf16, D up to 128; 32 for wider heads; fp32 16, and 8
+ * for wider ones): T in the hundreds works but is not what it is made for.
+ * Limits: q_heads / heads at most 256, T times that below 2^24, B T q_heads below 2^31; the sequences' units of 16 or 32 keys
+ * (8 for wide heads in fp32), were all as long as the table allows, times the key heads and reads of the cache, below 2^32.
  * Scratch: kda_attn_step_workspace bytes (a function of the sizes, not of the lengths).
  */
 typedef struct kda_attn_step_params {

@@ -119,6 +119,8 @@ CACHE = [(dict(c_k=None), INV), (dict(c_v=None), INV), (dict(c_block_table=None)
     ("attn_step", _attn, dict(scale=float("inf")), INV), ("attn_step", _attn, dict(scale=float("nan")), INV), ("attn_step", _attn, dict(dtype=2), UNS),
     ("attn_step", _attn, dict(q_stride=500), INV), ("attn_step", _attn, dict(q_stride=513), ALI), ("attn_step", _attn, dict(q=A + 8), ALI),
     ("attn_step", _attn, dict(o=A + 2), ALI), ("attn_step", _attn, dict(lse=A + 2), ALI), ("attn_step", _attn, dict(T=1 << 28), UNS),
+    ("attn_step", _attn, dict(q_heads=514), UNS), ("attn_step", _attn, dict(B=4, T=1 << 20, c_max_pages=1 << 20), UNS),  # counts of units
+    ("attn_step", _attn, dict(B=1 << 20, T=1, c_max_pages=1 << 20, dtype=1, c_dtype=1), UNS),
 ] + [(fn, make, over, want) for over, want in CACHE
      for fn, make in (("qk_norm_step", _step), ("kv_cache_write", _write), ("kv_cache_read", _read), ("attn_step", _attn))])
 def test_bad_arguments_are_rejected(fn, make, over, want):
@@ -141,6 +143,7 @@ def test_workspace_sizes_of_rejected_calls_are_zero():
     assert attention.kda_qk_norm_bwd_workspace(_bwd(D=0)) == 0
     assert attention.kda_attn_step_workspace(_attn(c_D=8)) == 0
     assert attention.kda_attn_step_workspace(_attn(T=0)) == 0
+    assert attention.kda_attn_step_workspace(_attn(B=4, T=1 << 20, c_max_pages=1 << 20)) == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a host without a device")
