@@ -422,7 +422,7 @@ def paged_attn_step(q, cache, block_table, lens, *, scale=None, want_lse=False, 
     q [B, T, q_heads, D] bf16 or fp32, T typically 1, q_heads a multiple of the cache's heads (query head h
     reads key head h // (q_heads // heads)): token t of a sequence attends to the positions below
     lens - T + t + 1, with softmax(scale q . k), ``scale`` D ** -0.5 by default. A token that sees nothing gives
-    zeros. Returns o like q, or ``(o, lse)`` with ``want_lse``: lse fp32 [B, T, q_heads], the logarithm of the
+    zeros. Returns o like q, or ``(o, lse)`` with ``want_lse`` or a given ``lse``: lse fp32 [B, T, q_heads], the logarithm of the
     sum of e^score (-inf where nothing is seen), with which results over several caches can be joined.
     """
     torch = sys.modules["torch"]
@@ -448,6 +448,6 @@ def paged_attn_step(q, cache, block_table, lens, *, scale=None, want_lse=False, 
         o = torch.empty(shape, dtype=kind, device=q.device)
     if want_lse and lse is None:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-    p = kda_attn_step_params(_ptr(q), _ptr(o), _ptr(lse) if want_lse else None, stride, B, T, Hq, scale, dtype, c, None, 0)
+    p = kda_attn_step_params(_ptr(q), _ptr(o), _ptr(lse), stride, B, T, Hq, scale, dtype, c, None, 0)
     _call("kda_attn_step", p, q, stream, workspace=True)
-    return (o, lse) if want_lse else o
+    return o if lse is None else (o, lse)

@@ -129,12 +129,13 @@ def test_sharp_and_flat_scores(dtype, kind, size):
 
 
 @pytest.mark.parametrize("dtype,kind", KINDS)
-def test_values_without_a_meaning_stay_where_no_row_sees_them(dtype, kind):
+@pytest.mark.parametrize("D,group", [(64, 2), (64, 1), (128, 5), (64, 8), (256, 3), (256, 6)])
+def test_values_without_a_meaning_stay_where_no_row_sees_them(dtype, kind, D, group):
     """NaN and infinities at positions that only later tokens of the call see do not reach earlier ones."""
     lens, T = [70, 9, 200], 5
     g = torch.Generator().manual_seed(3)
-    cache, table = filled(g, lens, 16, 2, 64, kind)
-    q = _q(g, 3, T, 4, 64, dtype, kind)
+    cache, table = filled(g, lens, 16, 2, D, kind)
+    q = _q(g, 3, T, 2 * group, D, dtype, kind)
     clean = _check(q, cache, table, lens, dtype)
     bad = KVCache(*(None if t is None else t.clone() for t in cache))
     for b, n in enumerate(lens):
@@ -145,8 +146,8 @@ def test_values_without_a_meaning_stay_where_no_row_sees_them(dtype, kind):
                 t[table[b, (pos + 1) // 16].long(), 0, (pos + 1) % 16, at] = float("inf")
     o = paged_attn_step(q.to(dev), to_gpu(bad), table.to(dev), _int32(lens))
     assert torch.equal(o[:, :T - 2], clean[:, :T - 2])
-    assert torch.equal(o[:, :, 2:], clean[:, :, 2:])  # the other key head
-    assert bool(torch.isnan(o[:, T - 2:, :2]).all())
+    assert torch.equal(o[:, :, group:], clean[:, :, group:])  # the other key head
+    assert bool(torch.isnan(o[:, T - 2:, :group]).all())
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -317,6 +318,10 @@ def test_no_tokens_and_given_outputs():
     o, lse = torch.empty_like(q), torch.empty(1, 1, 4, device=dev)
     got = paged_attn_step(q, c, t, lens, want_lse=True, o=o, lse=lse)
     assert got[0] is o and got[1] is lse and math.isfinite(float(lse.sum()))
+    kept = lse.clone()
+    lse.zero_()
+    got = paged_attn_step(q, c, t, lens, lse=lse)  # given is wanted
+    assert got[1] is lse and torch.equal(lse, kept)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
