@@ -4,6 +4,8 @@
 // A unit is KEYS keys: lane (key, part) takes every (32 / KEYS)-th 16-byte chunk of its key against all query rows, the
 // parts are added across lanes; then a lane owns DP / 32 neighbouring columns of O and goes through the keys. Arithmetic
 // goes in pairs of fp32.
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "attn_launch.h"
 
@@ -74,13 +76,13 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             continue;
         }
 #pragma unroll 1
-        for (int r = 0; r < p.rows; ++r) {
-            const float *from = static_cast<const float *>(a.q) + q_at(a, p, r);
-            for (int d = lane; d < DP; d += 32) qs[r * DP + d] = d < D ? from[d] * a.scale_log2 : 0.f;
+        for (int r = 0; r < RB; ++r) {  // rows that are not there: zeros, which see nothing
+            const float *from = static_cast<const float *>(a.q) + q_at(a, p, r < p.rows ? r : 0);
+            for (int d = lane; d < DP; d += 32) qs[r * DP + d] = r < p.rows && d < D ? from[d] * a.scale_log2 : 0.f;
         }
         if (lane < RB) lim[lane] = lane < p.rows ? seen(a, p.len, p.row0 + lane) : 0;
         __syncwarp();
-        const int least = lim[0];  // keys from here on are not seen by all rows
+        const int least = lim[0];  // keys from here on are not seen by all its rows
         float m[RB], l[RB];
         f2 acc[RB][F::kCols / 2];
 #pragma unroll
@@ -100,13 +102,12 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
                 f2 dots[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) dots[r] = pk(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll (RB > 8 ? 2 : 4)
                 for (int c = part; c < cpr; c += F::kParts) {
                     f2 kf[F::kE / 2];
                     values<C, F::kE>(kf, ks + key * F::S::kPitch + ((c ^ (key & 7)) << 4));
 #pragma unroll
                     for (int r = 0; r < RB; ++r) {
-                        if (r >= p.rows) break;
 #pragma unroll
                         for (int e = 0; e < F::kE; e += 4) {
                             const float4 qv = *reinterpret_cast<const float4 *>(qs + r * DP + c * F::kE + e);
@@ -129,7 +130,6 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
                     alpha[r] = 1.f;
-                    if (r >= p.rows) continue;
 #pragma unroll
                     for (int o = KEYS; o < 32; o <<= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], o);
                     x[r] = pos < lim[r] ? x[r] * kscale : -INFINITY;
@@ -158,9 +158,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             st.template ready<true>();
             if (pos0 < p.last) {
                 const unsigned char *vs = own + st.slot * F::S::kSlot;
-                const bool edge = pos0 + KEYS > least;
-#pragma unroll 2
-                for (int k = 0; k < KEYS; ++k) {
+                auto add = [&](int k, auto all) {
                     f2 v[F::kCols / 2];
                     constexpr int kBytes = F::kCols * (int)sizeof(C), kStep = kBytes < 16 ? kBytes : 16, kN = kStep / (int)sizeof(C);
 #pragma unroll
@@ -175,12 +173,18 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
                     load_vec<float, RB>(w, pw + k * RB);
 #pragma unroll
                     for (int r = 0; r < RB; ++r) {
-                        if (r >= p.rows) break;
                         // a value that this row does not see must not reach it, not even times zero
-                        if (edge && pos0 + k >= lim[r]) continue;
+                        if (!decltype(all)::value && pos0 + k >= lim[r]) continue;
 #pragma unroll
                         for (int j = 0; j < F::kCols / 2; ++j) acc[r][j] = fma2(pk(w[r], w[r]), v[j], acc[r][j]);
                     }
+                };
+                if (pos0 + KEYS <= least) {
+#pragma unroll 4
+                    for (int k = 0; k < KEYS; ++k) add(k, std::true_type{});
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < KEYS; ++k) add(k, std::false_type{});
                 }
             }
             st.template release<true>();
