@@ -952,6 +952,8 @@ template <typename T, int U, int SCALED>
 cudaError_t vec_read(const VecPlan &p, cudaStream_t stream) {
     if (p.u == 1)
         KDA_VEC(vec_read_kernel, T, KDA_COMMA 1 KDA_COMMA SCALED)
+    else if (p.u == 2)
+        KDA_VEC(vec_read_kernel, T, KDA_COMMA 2 KDA_COMMA SCALED)
     else
         KDA_VEC(vec_read_kernel, T, KDA_COMMA U KDA_COMMA SCALED)
     return cudaGetLastError();
@@ -977,15 +979,20 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
     const void *ptrs[] = {a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 2)) {
         VecPlan p = vec_plan(a, f32);
-        // as many tokens as a block's warps have rows on their way
+        // As many tokens in a block as its warps have rows on their way: eight (four in the data's type; half in fp32) where that
+        // leaves 32 blocks for each SM, or two, or one where even then there would not be two blocks. (8-bit to bf16, 131072
+        // tokens of 8 heads of 128: 146 us with eight, 155 with two; 32768 tokens: 45 and 42; 8000: 14 and 11; 800:
+        // 5.9 and, with one, 3.4.)
         const bool scaled = a.cache.ks != nullptr;
+        const int64_t sms = sm_count();
+        auto tokens = [&](int u) {
+            const int n = kVecWarps * u * 32 / p.lpr / (2 * a.Hk);
+            return n < 1 ? 1 : n > kVecThreads ? kVecThreads : n;
+        };
         p.u = (scaled ? 8 : 4) / (f32 ? 2 : 1);
-        int tokens = kVecWarps * p.u * 32 / p.lpr / (2 * a.Hk);
-        if (ceil_div(a.seqs.rows, tokens < 1 ? 1 : tokens) < 2 * sm_count()) {
-            p.u = 1;
-            tokens = kVecWarps * 32 / p.lpr / (2 * a.Hk);
-        }
-        p.v.tokens = tokens < 1 ? 1 : tokens > kVecThreads ? kVecThreads : tokens;
+        if (ceil_div(a.seqs.rows, tokens(p.u)) < 32 * sms) p.u = 2;
+        if (ceil_div(a.seqs.rows, tokens(p.u)) < 2 * sms) p.u = 1;
+        p.v.tokens = tokens(p.u);
         p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
         p.blocks = (unsigned)p.v.batches;
         p.smem = 0;
