@@ -4,7 +4,7 @@
 //   n = x r w, r = (mean x^2 + eps)^(-1/2);  pairs (a, b) of n -> (a cos - b sin, b cos + a sin)
 //
 // Gradient: g is dy with its pairs turned back, gw = g w, dx = r (gw - x r^2 mean(gw x)), dw = sum g x r.
-#include <cuda_fp16.h>
+#include <type_traits>
 
 #include "cache_common.cuh"
 
@@ -260,8 +260,11 @@ __global__ void __launch_bounds__(32 * kWarps) any_read_kernel(HeadArgs a) {
 // LPR lanes share a row, 16 channels each as two chunks of 8; a warp holds a group of 32 / LPR rows (heads of one token) at
 // a time. A block takes some tokens: first the place and the angles of each are worked out once and left in shared
 // memory, then its warps go through the tokens' slices (a few groups of queries, keys or values), the
-// next rows on their way while some are worked on. Arithmetic goes in pairs of fp32. What bounds it is the
-// instructions: about 130 for a group of 1 KB in and out, with what belongs to a slice worked out once.
+// next rows on their way while some are worked on. Arithmetic goes in pairs of fp32. The norms move 86 % of what a plain copy does
+// (2 x 8192 tokens of 40 heads of 128, bf16: 59 us); what holds them is the instructions, about 240 for a group of 1 KB in
+// and out (2.3 per clock and SM, waiting for shared memory, reciprocal roots and one another), with what belongs to a slice
+// worked out once. The gradient (8191 tokens of 18 heads of 256: 48 us, 69 % of a copy) has 128 registers a thread,
+// so only 16 warps on an SM. 8-bit writes: 38 us for 32768 tokens of 16 rows of 128, 76 %.
 constexpr int kVecWarps = 8;
 constexpr int kVecThreads = 32 * kVecWarps;
 constexpr int kVecTokens = 32;  // of a block at a time, at most
@@ -331,7 +334,8 @@ __device__ __forceinline__ int64_t share_of(int64_t rows, int block) {
 // The slices of heads of a token, `each` heads apiece.
 __host__ __device__ __forceinline__ int slices_of(int heads, int each) { return (heads + each - 1) / each; }
 
-// The lane's place in a row.
+// The lane's place in a row: two chunks of 8 channels, each beside its neighbours' (16 channels in one piece would leave every
+// other 16 bytes to a second access).
 struct LaneAt {
     int o0, o1;      // first channels of its two chunks
     bool in, turns;  // within the row; its channels are turned (pair e: 8 j + e)
@@ -340,11 +344,13 @@ __device__ __forceinline__ LaneAt lane_at(const HeadArgs &a, bool turned, int j)
     LaneAt l;
     l.in = 16 * j < a.D;
     l.turns = turned && 16 * j < a.R;
-    l.o0 = 16 * j;
-    l.o1 = 16 * j + 8;
-    if (l.turns && !a.pairs) {  // channels i and i + R / 2
-        l.o0 = 8 * j;
-        l.o1 = a.R / 2 + 8 * j;
+    if (l.turns) {
+        l.o0 = a.pairs ? 16 * j : 8 * j;
+        l.o1 = a.pairs ? 16 * j + 8 : a.R / 2 + 8 * j;  // channels i and i + R / 2
+    } else {
+        const int from = turned ? a.R : 0;
+        l.o0 = from / 2 + 8 * j;
+        l.o1 = a.D / 2 + 8 * j;
     }
     return l;
 }
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kVecThreads, MODE == kWrite ? 4 : 3) vec_rows_
     constexpr int per = U * kAtOnce;  // heads of a slice
     const int hop = kAtOnce * a.D;    // channels between groups
     const int nq = slices_of(a.Hq, per), nk = slices_of(a.Hk, per), slices = nq + nk + slices_of(a.Hv, per);
-    const LaneAt lt = lane_at(a, true, j), lv{16 * j, 16 * j + 8, lt.in, false};
+    const LaneAt lt = lane_at(a, true, j), lv = lane_at(a, false, j);
     const float inv_d = 1.f / (float)a.D;
     if constexpr (MODE != kWrite) vec_weights<LPR>(a, weights);
 
@@ -750,7 +756,7 @@ __global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(c
     const int count = a.seqs.rows - row0 < v.tokens ? (int)(a.seqs.rows - row0) : v.tokens;
     vec_places(a, row0, count, place);
     __syncthreads();
-    const LaneAt l{16 * j, 16 * j + 8, 16 * j < c.D, false};
+    const LaneAt l = lane_at(a, false, j);
     const int each = 2 * a.Hk, all = count * each;
 #pragma unroll 1
     for (int first = warp * U * kAtOnce; first < all; first += kVecWarps * U * kAtOnce) {
@@ -780,7 +786,9 @@ __global__ void __launch_bounds__(kVecThreads, SCALED ? 4 : 3) vec_read_kernel(c
                 q[u] = make_uint4(0u, 0u, 0u, 0u);
                 e[u] = 0u;
                 if (ok) {
-                    q[u] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + from * c.D + l.o0);
+                    const uint8_t *row = static_cast<const uint8_t *>(base) + from * c.D;
+                    const uint2 lo = *reinterpret_cast<const uint2 *>(row + l.o0), hi = *reinterpret_cast<const uint2 *>(row + l.o1);
+                    q[u] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     e[u] = (isv ? c.vs : c.ks)[cache_scale(c, p.page, head, p.slot)];
                 }
             } else {
@@ -881,7 +889,7 @@ unsigned any_blocks(int64_t items) {
 }
 
 // Whole vectors: the widths, all rows and all pointers allow 16 bytes at a time. (Norms of 2 x 8192 tokens, 40 heads of 128:
-// 438 us a warp per row and channel by channel.)
+// 59 us, and 438 a warp per row and channel by channel.)
 bool vec_ok(const HeadArgs &a, bool f32, const void *const *ptrs, int n) {
     const int v = f32 ? 4 : 8;
     bool ok = a.D % 16 == 0 && a.R % 16 == 0 && a.q_stride % v == 0 && a.k_stride % v == 0 && a.v_stride % v == 0;
@@ -902,8 +910,9 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
     p.v.tokens = a.q != nullptr ? 12 : 16;
     p.v.each = 4;
-    p.u = f32 ? 1 : 2;
-    // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy
+    p.u = f32 ? 1 : 2;  // groups of a warp on their way: 16 registers each (bf16 norms as above 59 us with two, 62 with one; 8-bit writes 39, 42)
+    // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy (8 single tokens into the
+    // cache: 4.4 us, and 11 with twelve tokens in a block)
     const int64_t sms = sm_count();
     if (a.seqs.rows < 4 * sms * p.v.tokens) {
         const int groups = slices_of(a.Hq + a.Hk + a.Hv, 32 / p.lpr);
@@ -912,51 +921,49 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
         if (a.seqs.rows * groups < 4 * sms * kVecWarps * 4) p.v.each = p.u = 1;
     }
     p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
-    // with norms and angles, blocks that stay and go through shares of all tokens; rows that are only written, 16 tokens a block
+    // With norms and angles, blocks that stay and go through shares of all tokens (norms as above 59 us, and 64 with a block for
+    // each 12 tokens); rows that are only written, 16 tokens a block (39 us, and 41 with blocks that stay).
     p.blocks = (unsigned)(a.q == nullptr || p.v.batches < 3 * sms ? p.v.batches : 3 * sms);
     p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 32 * p.lpr) * sizeof(float);  // at most 26 KB
     return p;
 }
 
-#define KDA_VEC(kernel, T, ...)                                                                              \
-    switch (p.lpr) {                                                                                         \
-        case 4: kernel<T, 4 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;             \
-        case 8: kernel<T, 8 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;             \
-        default: kernel<T, 16 __VA_ARGS__><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); break;           \
-    }
-
+template <int N>
+using Int = std::integral_constant<int, N>;
+// Calls f with the lanes of a row as a constant.
+template <typename F>
+cudaError_t with_lpr(const VecPlan &p, F f) {
+    if (p.lpr == 4)
+        f(Int<4>{});
+    else if (p.lpr == 8)
+        f(Int<8>{});
+    else
+        f(Int<16>{});
+    return cudaGetLastError();
+}
+template <typename T, int U, int MODE>
+cudaError_t vec_mode(const VecPlan &p, cudaStream_t stream) {
+    return with_lpr(p, [&](auto lpr) { vec_rows_kernel<T, decltype(lpr)::value, U, MODE><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); });
+}
 template <typename T>
 cudaError_t vec_rows(const VecPlan &p, cudaStream_t stream) {
-#define KDA_COMMA ,
-#define KDA_MODES(U)                                                        \
-    if (!p.v.h.cached)                                                      \
-        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kNorm)            \
-    else if (p.v.h.q != nullptr)                                            \
-        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kStep)            \
-    else                                                                    \
-        KDA_VEC(vec_rows_kernel, T, KDA_COMMA U KDA_COMMA kWrite)
-    if (p.u == 1) {
-        KDA_MODES(1)
-    } else {
-        KDA_MODES(2)
-    }
-    return cudaGetLastError();
+    if (!p.v.h.cached) return p.u == 1 ? vec_mode<T, 1, kNorm>(p, stream) : vec_mode<T, 2, kNorm>(p, stream);
+    if (p.v.h.q != nullptr) return p.u == 1 ? vec_mode<T, 1, kStep>(p, stream) : vec_mode<T, 2, kStep>(p, stream);
+    return p.u == 1 ? vec_mode<T, 1, kWrite>(p, stream) : vec_mode<T, 2, kWrite>(p, stream);
 }
 template <typename T>
 cudaError_t vec_bwd(const VecPlan &p, cudaStream_t stream) {
-    KDA_VEC(vec_rows_bwd_kernel, T)
-    return cudaGetLastError();
+    return with_lpr(p, [&](auto lpr) { vec_rows_bwd_kernel<T, decltype(lpr)::value><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); });
 }
-// U: rows of a lane on their way
-template <typename T, int U, int SCALED>
+// MOST: rows of a lane on their way where there are enough
+template <typename T, int MOST, int SCALED>
 cudaError_t vec_read(const VecPlan &p, cudaStream_t stream) {
-    if (p.u == 1)
-        KDA_VEC(vec_read_kernel, T, KDA_COMMA 1 KDA_COMMA SCALED)
-    else if (p.u == 2)
-        KDA_VEC(vec_read_kernel, T, KDA_COMMA 2 KDA_COMMA SCALED)
-    else
-        KDA_VEC(vec_read_kernel, T, KDA_COMMA U KDA_COMMA SCALED)
-    return cudaGetLastError();
+    auto rows = [&](auto u) {
+        return with_lpr(p, [&](auto lpr) {
+            vec_read_kernel<T, decltype(lpr)::value, decltype(u)::value, SCALED><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v);
+        });
+    };
+    return p.u == 1 ? rows(Int<1>{}) : rows(Int<MOST>{});
 }
 
 cudaError_t launch_rows(const HeadArgs &a, bool f32, cudaStream_t stream) {
@@ -979,24 +986,22 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
     const void *ptrs[] = {a.q_out, a.k_out};
     if (vec_ok(a, f32, ptrs, 2)) {
         VecPlan p = vec_plan(a, f32);
-        // As many tokens in a block as its warps have rows on their way: eight (four in the data's type; half in fp32) where that
-        // leaves 32 blocks for each SM, or two, or one where even then there would not be two blocks. (8-bit to bf16, 131072
-        // tokens of 8 heads of 128: 146 us with eight, 155 with two; 32768 tokens: 45 and 42; 8000: 14 and 11; 800:
-        // 5.9 and, with one, 3.4.)
+        // As many tokens in a block as its warps have rows on their way: eight of a lane, four in the data's type, two in fp32 (8-bit to
+        // bf16, 32768 tokens of 8 heads of 128: 38 us with eight, 43 with four; to fp32 71 with two, 76 with four), or one where there
+        // would not be two blocks for each SM (800 tokens: 3.0 us, and 5.9).
         const bool scaled = a.cache.ks != nullptr;
         const int64_t sms = sm_count();
         auto tokens = [&](int u) {
             const int n = kVecWarps * u * 32 / p.lpr / (2 * a.Hk);
             return n < 1 ? 1 : n > kVecThreads ? kVecThreads : n;
         };
-        p.u = (scaled ? 8 : 4) / (f32 ? 2 : 1);
-        if (ceil_div(a.seqs.rows, tokens(p.u)) < 32 * sms) p.u = 2;
+        p.u = f32 ? 2 : scaled ? 8 : 4;
         if (ceil_div(a.seqs.rows, tokens(p.u)) < 2 * sms) p.u = 1;
         p.v.tokens = tokens(p.u);
         p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
         p.blocks = (unsigned)p.v.batches;
         p.smem = 0;
-        if (f32) return scaled ? vec_read<float, 4, 1>(p, stream) : vec_read<float, 2, 0>(p, stream);
+        if (f32) return scaled ? vec_read<float, 2, 1>(p, stream) : vec_read<float, 2, 0>(p, stream);
         return scaled ? vec_read<bf16, 8, 1>(p, stream) : vec_read<bf16, 4, 0>(p, stream);
     }
     const unsigned blocks = any_blocks(a.seqs.rows * 2 * a.Hk);
