@@ -1,12 +1,13 @@
 // Attention over a paged cache (kda_attention.h), what its kernels share: how the work is cut, how keys and values
 // stream in, and how the pieces of one result are joined.
 //
-// An item is one (sequence, block of query rows, key head); its keys are cut into units of UNIT (16 or 32, by the kernel).
+// An item is one (sequence, block of query rows, key head); its keys are cut into units of 8, 16 or 32 (by the kernel).
 // All items' units, one after another, are dealt out in equal shares to the workers of the grid: warps, each with its own
 // ring of shared memory and no barrier with the others, or, where there are many query rows, teams of warps that
-// share a ring and take some of the rows each. A worker has at most one item that began in the share before and one that goes on in the next; such pieces leave (m, l, O) in scratch: the reference m of their
-// exponentials 2^(s - m), the sum l of those, and O = sum 2^(s - m) v. A second kernel joins them in the order of
-// the workers. Which items are cut follows from the lengths and sizes alone, so results repeat bit for bit.
+// share a ring and take some of the rows each. A worker has at most one item that began in the share before and one that
+// goes on in the next; such pieces leave (m, l, O) in scratch: the reference m of their exponentials 2^(s - m), the
+// sum l of those, and O = sum 2^(s - m) v. A second kernel joins them in the order of the workers. Which items are cut follows
+// from the lengths and sizes alone, so results repeat bit for bit.
 // (Blocks of four warps that shared each item's keys and joined them in shared memory: 4 to 7 us for every piece
 // of an item, most of it waiting; 2048 items of 450 keys took 74 us.)
 //
@@ -23,8 +24,8 @@ using namespace mix;
 
 constexpr int kWarps = 4;  // of a block
 // What an item costs beside its units, in units, when the work is dealt out: its queries in, its result out and the waits in
-// between. (16 sequences of up to 8192 tokens, among them one of 4 and one at rest: 29 us without it, the
-// short ones' items one after another in two shares.)
+// between. (16 sequences of up to 8192 tokens, among them one of 4 and one at rest, four new tokens each: 51 us without it, the
+// short ones' items one after another in two shares, and 44 with it; 256 sequences of up to 900 tokens 56 and 50.)
 constexpr uint32_t kItemCost = 2;
 constexpr int kThreads = 32 * kWarps;
 
@@ -56,8 +57,7 @@ __device__ __forceinline__ uint32_t units_of(const Args &a, int len) {
 __device__ __forceinline__ uint32_t weight_of(const Args &a, int len) { return units_of(a, len) + kItemCost; }
 
 // The weights of all items (below 2^32, checked on the host for the longest sequences) dealt out: how many workers have a
-// share (each then has some), where share w begins, and whose share
-// weight x is in.
+// share (each then has some), where share w begins, and whose share weight x is in.
 struct Deal {
     uint32_t n, base, more;  // the first `more` shares have base + 1 units
     __device__ __forceinline__ Deal(const Args &a, uint32_t total) {

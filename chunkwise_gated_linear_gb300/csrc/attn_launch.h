@@ -10,7 +10,7 @@ namespace attn {
 
 // Query rows of an item for `all` rows of a sequence and key head, keys of a unit (its power of two), workers on an SM, and the
 // launch, of the kernel for fp32 data and of that for bf16.
-int fma_rows(int all, int D);
+int fma_rows(int all);
 int fma_unit_shift(const Args &a);
 int fma_workers(const Args &a);
 cudaError_t launch_attn_fma(const Args &a, cudaStream_t stream);

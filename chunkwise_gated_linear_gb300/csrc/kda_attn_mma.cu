@@ -8,6 +8,12 @@
 // lane and the reference m of the exponentials moves only when some score passes it by 2^8 or more, so that
 // most steps exchange nothing between lanes.
 //
+// What bounds it is the stream of keys and values where they are many: 64 sequences of up to 16384 tokens, 8 key heads of 128 in
+// 8 bits, 188 us, 95 % of what a copy moves (three blocks of four warps on an SM, each warp 24 KB ahead; tensor pipes 18 % busy,
+// so larger matrix instructions would change nothing); one sequence of 131071 in bf16 93 us, 85 % with the start and
+// the join. With many rows it is the instructions, about 650 for a warp's 32 keys and 8 rows in 8 bits: 4 new tokens
+// of 8 heads a key head, 16 sequences of up to 8192: 42 us, 23 %.
+//
 // 8-bit cache: e4m3 numbers are exact in fp16, so K and V are widened in registers and the products run in fp16
 // (one conversion per two numbers; widening to bf16 takes four to five instructions). Q goes to fp16 times a power of two per
 // row that puts its largest entry at 2^14: entries down to 2^-28 of it stay exact. The power of two of a key multiplies
@@ -553,15 +559,22 @@ struct Variant {
     static int unit() { return M::kKeys; }
 };
 
-// Calls f with the variant for these sizes. Query rows: 8 or 16 of a warp, 32 or 64 of a team of four.
+// Calls f with the variant for these sizes. 8 query rows of a warp, 16 of a team of two (8-bit values, which each warp of a team would
+// widen for itself, of one warp while the registers allow it), 32 and 64 of a team of four. (16 sequences of up to 8192
+// tokens, 4 key heads of 128: 16 rows over bf16 33 us with two warps and 40 with one, over 8 bits 31 and 29; 32 rows
+// as two blocks of 16 instead of a team's 63 and 41, 43 and 42; 64 rows as two of 32 68 and 56, 68 and 65. Few rows in an
+// item of 16: 64 sequences over an 8-bit cache 212 us, and 188 in items of 8.)
 template <typename C, int DP, int SLOTS, int SLOTS_TEAM, typename F>
 auto pick_rows(const Args &a, F f) {
     if (a.rows == 8) return f(Variant<C, DP, 1, SLOTS, 1>{});
     if constexpr (DP <= 128) {
-        if (a.rows == 16) return f(Variant<C, DP, 2, SLOTS, 1>{});
         if (a.rows == 64) return f(Variant<C, DP, 2, SLOTS_TEAM, 4>{});
-    } else {
-        if (a.rows == 16) return f(Variant<C, DP, 1, SLOTS_TEAM, 2>{});
+    }
+    if (a.rows == 16) {
+        if constexpr (DP <= 128 && sizeof(C) == 1)
+            return f(Variant<C, DP, 2, SLOTS, 1>{});
+        else
+            return f(Variant<C, DP, 1, SLOTS_TEAM, 2>{});
     }
     return f(Variant<C, DP, 1, SLOTS_TEAM, 4>{});
 }

@@ -186,10 +186,10 @@ int kda_kv_cache_read(const kda_kv_cache_read_params *p, cudaStream_t stream);
  *   data: fp32 throughout.
  * The sequences' lengths are cut into equal shares for the GPU's SMs, and results of sequences that were
  * cut are joined in the order of their shares: which are cut follows from the lengths and sizes alone.
- * One call reads the cache ceil(T q_heads / heads / 64) times (bf16, D up to 128; 32 for wider heads; fp32 16, and 8
- * for wider ones): T in the hundreds works but is not what it is made for.
+ * One call reads the cache ceil(T q_heads / heads / 64) times (bf16, D up to 128; 32 for wider heads; fp32
+ * 8): T in the hundreds works but is not what it is made for.
  * Limits: q_heads / heads at most 256, T times that below 2^24, B T q_heads below 2^31; the sequences' units of 16 or 32 keys
- * (8 for wide heads in fp32), were all as long as the table allows, times the key heads and reads of the cache, below 2^32.
+ * (8 in fp32 above 64 channels), were all as long as the table allows, times the key heads and reads of the cache, below 2^32.
  * Scratch: kda_attn_step_workspace bytes (a function of the sizes, not of the lengths).
  */
 typedef struct kda_attn_step_params {
