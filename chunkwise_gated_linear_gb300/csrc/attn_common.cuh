@@ -43,6 +43,7 @@ struct Args {
     float scale_log2;      // scale * log2 e
     Cache cache;
     float *pieces;         // [2 workers][rows * (D + 2)]: O [rows][D], then (m, l) [rows]
+    int2 *ends;            // of each item (in the order of the deal): the workers that have its first and its last piece
 };
 
 __device__ __forceinline__ int token_of(const Args &a, int row) {
@@ -57,7 +58,7 @@ __device__ __forceinline__ uint32_t units_of(const Args &a, int len) {
 __device__ __forceinline__ uint32_t weight_of(const Args &a, int len) { return units_of(a, len) + kItemCost; }
 
 // The weights of all items (below 2^32, checked on the host for the longest sequences) dealt out: how many workers have a
-// share (each then has some), where share w begins, and whose share weight x is in.
+// share (each then has some), and where share w begins.
 struct Deal {
     uint32_t n, base, more;  // the first `more` shares have base + 1 units
     __device__ __forceinline__ Deal(const Args &a, uint32_t total) {
@@ -66,10 +67,6 @@ struct Deal {
         more = total - base * n;
     }
     __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * base + (w < more ? w : more); }
-    __device__ __forceinline__ int owner(uint32_t x) const {
-        const uint32_t big = more * (base + 1);
-        return (int)(x < big ? x / (base + 1) : more + (x - big) / base);
-    }
 };
 
 // A scan over the sequences by the threads of a block: thread i adds up the sequences i * each .. i * each + each - 1.
@@ -218,6 +215,13 @@ __device__ __forceinline__ int64_t out_row(const Args &a, const Piece &p, int r)
 // A worker's scratch for a piece: the first when the item began before, the second when it goes on (or both).
 __device__ __forceinline__ float *piece_mem(const Args &a, int worker, bool begins) {
     return a.pieces + (int64_t)(2 * worker + (begins ? 1 : 0)) * a.rows * (a.cache.D + 2);
+}
+
+// The workers of the item's ends, one thread's to say.
+__device__ __forceinline__ void tell_ends(const Args &a, const Piece &p, int worker) {
+    int2 *at = a.ends + (int64_t)p.b * a.per_seq + p.row0 / a.rows * a.cache.heads + p.head;
+    if (p.u0 == 0) at->x = worker;
+    if (p.u1 == p.units) at->y = worker;
 }
 
 constexpr float kLn2 = 0.6931471805599453f;

@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             st.template release<true>();
         }
         float *piece = piece_mem(a, blockIdx.x * kWarps + warp, p.u0 == 0);
+        if (lane == 0) tell_ends(a, p, blockIdx.x * kWarps + warp);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             if (r >= p.rows) break;

@@ -502,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
         const int base = TEAM > 1 ? warp % TEAM * kRows : 0;
         float *piece = piece_mem(a, blockIdx.x * M::kWorkers + worker, p.u0 == 0);
         const bool whole = p.whole();
+        if (warp % TEAM == 0 && lane == 0) tell_ends(a, p, blockIdx.x * M::kWorkers + worker);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float sum[2];

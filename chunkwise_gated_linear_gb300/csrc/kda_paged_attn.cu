@@ -5,52 +5,37 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kJoinWarps = 16;  // of a block, at most
+constexpr int kSplit = 16;  // warps for a row, at most
+constexpr int join_warps(int lc) { return lc == 8 ? kSplit : 8; }  // of a block, at most
 
 // A query row of an item that was cut: with the largest m of its pieces, the sum of 2^(m - max) (l, O) over them. `split` warps
 // share a row's pieces in order, each with a maximum of its own, and are then added up. Of a warp, LC lanes hold four
-// channels each and the others take other pieces: 32 for many rows, 8 (and a block for every 32 channels) for few. A
-// block with nothing to join ends after the plan, which is made while the attention still runs (but for the first). What it costs is waiting:
-// each warp reads the statistics of all its pieces at once, then the pieces; about 8 us behind the attention. (One sequence of
-// 131071 tokens, 228 pieces a row, both kernels: 102 us with 8 warps for a row, 96 with 16, 94 with a block for every 32
-// channels.)
+// channels each and the others take other pieces: 32 for many rows, 8 (and a block for every 32 channels) for few. The
+// workers of the attention have left word where the pieces of an item begin and end. What it costs is waiting, for the
+// attention's end, for that word and for the pieces, of which a warp reads all statistics and the first few at once: 4 to 6
+// us behind the attention. It is launched early, which saves 1 to 4 of them. (One sequence of 131071 tokens, 228 pieces a
+// row, both kernels: 102 us with 8 warps for a row, 96 with 16, 94 with a block for every 32 channels; 91 since the ends
+// are told, as a plan of its own, with the registers that the attention takes, did not run before its end.)
 template <typename T, int LC>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ Args a, int split) {
-    __shared__ uint32_t mem[kJoinWarps], mine;
+__global__ void __launch_bounds__(32 * join_warps(LC), 2) attn_join_kernel(const __grid_constant__ Args a, int split) {
     constexpr int kAtOnce = 32 / LC, kPasses = LC == 8 ? 1 : 2;  // pieces of a warp at a time; turns over its channels
-    __shared__ float4 sums[kJoinWarps][kPasses * LC];
-    __shared__ float2 stat[kJoinWarps];
+    constexpr int kAhead = LC == 8 ? 4 : 2;  // pieces read before the statistics are here
+    __shared__ float4 sums[join_warps(LC)][kPasses * LC];
+    __shared__ float2 stat[join_warps(LC)];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    Walk walk;  // of the item
-    walk.b = blockIdx.x / a.per_seq;
-    const int item = blockIdx.x - walk.b * a.per_seq;
-    walk.rb = item / a.cache.heads;
-    walk.head = item - walk.rb * a.cache.heads;
-    walk.len = cache_len(a.cache, walk.b);
-    walk.w0 = 0;
-    walk.left = 0xffffffffu;
-    const Scan sc = scan_sequences(a, mem);
-    if (walk.b >= sc.first && walk.b < sc.first + sc.each) {  // one thread's
-        uint32_t before = sc.before;
-#pragma unroll 1
-        for (int x = sc.first; x < walk.b; ++x) before += weight_of(a, cache_len(a.cache, x)) * a.per_seq;
-        mine = before;
-    }
-    __syncthreads();
-    const Deal deal(a, sc.total);
-    const Piece p = walk.piece(a);
-    const uint32_t end = mine + (item + 1) * (p.units + kItemCost);
-    const int w0 = deal.owner(end - p.units), w1 = deal.owner(end - 1);
-    if (w0 == w1) {
-        // the first block stays, or this kernel could be over, and the stream go on, while the attention still runs
-        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) wait_for_previous();
-        return;
-    }
+    Piece p;  // the item
+    p.b = blockIdx.x / a.per_seq;
+    const int item = blockIdx.x - p.b * a.per_seq, rb = item / a.cache.heads;
+    p.head = item - rb * a.cache.heads;
+    p.row0 = rb * a.rows;
+    p.rows = a.T * a.group - p.row0 < a.rows ? a.T * a.group - p.row0 : a.rows;
+    wait_for_previous();
+    const int w0 = a.ends[blockIdx.x].x, w1 = a.ends[blockIdx.x].y;
+    if (w0 == w1) return;
     const int D = a.cache.D, part = warp % split;
     const int r = blockIdx.y * (warps / split) + warp / split;
     const int each = (w1 - w0 + split) / split;  // pieces of a warp
     const int from = w0 + part * each, to = from + each < w1 + 1 ? from + each : w1 + 1;
-    wait_for_previous();
     float m = -INFINITY, l = 0.f;
     float4 s[kPasses];
 #pragma unroll
@@ -66,8 +51,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
         const int64_t size = (int64_t)a.rows * (D + 2);
 #pragma unroll 1
         for (int w = from; w < to; w += 32) {
-            const int my = w + lane < to ? w + lane : w;
+            const int my = w + lane < to ? w + lane : w, count = to - w < 32 ? to - w : 32;
             const float2 x = reinterpret_cast<const float2 *>(a.pieces + (2 * my + (my == w0)) * size + (int64_t)a.rows * D)[r];
+            const float *o = a.pieces + 2 * w * size + (int64_t)r * D + d0;
+            auto load = [&](int i, int h) {
+                return i < count && d0 + 128 * h < D ? *reinterpret_cast<const float4 *>(o + (2 * i + (w + i == w0)) * size + 128 * h)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            float4 first[kAhead][kPasses];
+#pragma unroll
+            for (int t = 0; t < kAhead; ++t)
+#pragma unroll
+                for (int h = 0; h < kPasses; ++h) first[t][h] = load(mine_of + t * kAtOnce, h);
             float top = x.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -75,26 +70,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
                 scale(tc5::ex2(m - top));
                 m = top;
             }
-            const float f = tc5::ex2(x.x - (m == -INFINITY ? 0.f : m));
+            float f = tc5::ex2(x.x - (m == -INFINITY ? 0.f : m));
             float ls = w + lane < to ? x.y * f : 0.f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
             l += ls;
-            const int count = to - w < 32 ? to - w : 32;
-            const float *o = a.pieces + 2 * w * size + (int64_t)r * D + d0;
+            auto add = [&](int i, int h, const float4 &v) {
+                const float fi = __shfl_sync(0xffffffffu, f, i & 31);
+                if (i < count) s[h] = make_float4(fmaf(v.x, fi, s[h].x), fmaf(v.y, fi, s[h].y), fmaf(v.z, fi, s[h].z), fmaf(v.w, fi, s[h].w));
+            };
 #pragma unroll
-            for (int h = 0; h < kPasses; ++h) {
-                if (128 * h >= D) break;
-                const bool in = d0 + 128 * h < D;
-#pragma unroll 4
-                for (int i = mine_of; i - mine_of < count; i += kAtOnce) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i & 31);
-                    if (in && i < count) {
-                        const float4 v = *reinterpret_cast<const float4 *>(o + (2 * i + (w + i == w0)) * size + 128 * h);
-                        s[h] = make_float4(fmaf(v.x, fi, s[h].x), fmaf(v.y, fi, s[h].y), fmaf(v.z, fi, s[h].z), fmaf(v.w, fi, s[h].w));
-                    }
-                }
-            }
+            for (int t = 0; t < kAhead; ++t)
+#pragma unroll
+                for (int h = 0; h < kPasses; ++h) add(mine_of + t * kAtOnce, h, first[t][h]);
+#pragma unroll 2
+            for (int i = mine_of + kAhead * kAtOnce; i - mine_of < count; i += kAtOnce)
+#pragma unroll
+                for (int h = 0; h < kPasses; ++h) add(i, h, load(i, h));
         }
         if constexpr (LC < 32) {
 #pragma unroll
@@ -142,20 +134,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     if (d0 == 0 && a.lse != nullptr) a.lse[row] = lse_of(m, l);
 }
 
+int64_t items_of(const Args &a) { return (int64_t)a.B * a.per_seq; }
+
 template <typename T>
 cudaError_t launch_join(const Args &a, cudaStream_t stream) {
-    const int64_t items = (int64_t)a.B * a.per_seq;
+    const int64_t items = items_of(a);
     const int rows = a.T * a.group < a.rows ? a.T * a.group : a.rows;
-    // warps for a row: so many that about 16 on every SM have something to do, but not below four pieces each when all items
-    // are of one length
+    // Warps for a row: so many that about 16 on every SM have something to do, but not below four pieces each when all items are of one
+    // length. (Blocks of 8 warps instead of 16 where rows share them: 8 sequences of up to 700 tokens 13.3 -> 12.6 us, wide
+    // heads 58 -> 57 us.)
     int split = 1;
-    while (split < kJoinWarps && split * 8 * items <= a.workers && split * items * rows < 16 * (int64_t)sm_count()) split *= 2;
-    const int at_once = kJoinWarps / split < rows ? kJoinWarps / split : rows;  // rows of a block
+    while (split < kSplit && split * 8 * items <= a.workers && split * items * rows < 16 * (int64_t)sm_count()) split *= 2;
+    const bool few = split == kSplit;
+    const int most = join_warps(few ? 8 : 32) / split, at_once = most < rows ? most : rows;  // rows of a block
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    const bool few = split == kJoinWarps;
     cfg.gridDim = dim3((unsigned)items, (unsigned)ceil_div(rows, at_once), few ? (unsigned)ceil_div(a.cache.D, 32) : 1u);
     cfg.blockDim = dim3((unsigned)(32 * split * at_once));
     cfg.stream = stream;
@@ -208,9 +203,10 @@ Args make(const kda_attn_step_params &p) {
 // Whether the units and costs of all items, were all sequences as long as the table allows, are counted in 32 bits.
 bool in_range(const Args &a) {
     const int64_t weight = ((int64_t)a.cache.most >> a.unit_shift) + 1 + kItemCost;
-    return (int64_t)a.B * a.per_seq <= (int64_t)UINT32_MAX / weight;
+    return items_of(a) <= (int64_t)UINT32_MAX / weight;
 }
-size_t bytes_of(const Args &a) { return (size_t)2 * a.workers * a.rows * (a.cache.D + 2) * sizeof(float); }
+size_t pieces_of(const Args &a) { return (size_t)2 * a.workers * a.rows * (a.cache.D + 2); }
+size_t bytes_of(const Args &a) { return pieces_of(a) * sizeof(float) + (size_t)items_of(a) * sizeof(int2); }
 
 }  // namespace
 }  // namespace attn
@@ -243,6 +239,7 @@ int kda_attn_step(const kda_attn_step_params *p, cudaStream_t stream) {
     e = ws.get(p->workspace, bytes, stream);
     if (e != cudaSuccess) return status_of_cuda(e);
     a.pieces = static_cast<float *>(ws.ptr);
+    a.ends = reinterpret_cast<int2 *>(a.pieces + pieces_of(a));
     const bool f32 = p->dtype == KDA_DTYPE_F32;
     e = f32 ? launch_attn_fma(a, stream) : launch_attn_mma(a, stream);
     if (e == cudaSuccess) e = f32 ? launch_join<float>(a, stream) : launch_join<bf16>(a, stream);
