@@ -9,8 +9,8 @@
 // most steps exchange nothing between lanes.
 //
 // What bounds it is the stream of keys and values where they are many: 64 sequences of up to 16384 tokens, 8 key heads of 128 in
-// 8 bits, 188 us, 95 % of what a copy moves (three blocks of four warps on an SM, each warp 24 KB ahead; tensor pipes 18 % busy,
-// so larger matrix instructions would change nothing); one sequence of 131071 in bf16 93 us, 85 % with the start and
+// 8 bits, 186 us, 95 % of what a copy moves (three blocks of four warps on an SM, each warp 24 KB ahead; tensor pipes 18 % busy,
+// so larger matrix instructions would change nothing); one sequence of 131071 in bf16 91 us, 87 % with the start and
 // the join. With many rows it is the instructions, about 650 for a warp's 32 keys and 8 rows in 8 bits: 4 new tokens
 // of 8 heads a key head, 16 sequences of up to 8192: 42 us, 23 %.
 //

@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(32 * kWarps) any_read_kernel(HeadArgs a) {
 // LPR lanes share a row, 16 channels each as two chunks of 8; a warp holds a group of 32 / LPR rows (heads of one token) at
 // a time. A block takes some tokens: first the place and the angles of each are worked out once and left in shared
 // memory, then its warps go through the tokens' slices (a few groups of queries, keys or values), the
-// next rows on their way while some are worked on. Arithmetic goes in pairs of fp32. The norms move 86 % of what a plain copy does
-// (2 x 8192 tokens of 40 heads of 128, bf16: 59 us); what holds them is the instructions, about 240 for a group of 1 KB in
+// next rows on their way while some are worked on. Arithmetic goes in pairs of fp32. The norms move 82 % of what a plain copy does
+// (2 x 8192 tokens of 40 heads of 128, bf16: 60 us); what holds them is the instructions, about 240 for a group of 1 KB in
 // and out (2.3 per clock and SM, waiting for shared memory, reciprocal roots and one another), with what belongs to a slice
-// worked out once. The gradient (8191 tokens of 18 heads of 256: 48 us, 69 % of a copy) has 128 registers a thread,
-// so only 16 warps on an SM. 8-bit writes: 38 us for 32768 tokens of 16 rows of 128, 76 %.
+// worked out once. The gradient (8191 tokens of 18 heads of 256: 49 us, 68 % of a copy) has 128 registers a thread,
+// so only 16 warps on an SM. 8-bit writes: 39 us for 32761 tokens of 16 rows of 128, 77 %.
 constexpr int kVecWarps = 8;
 constexpr int kVecThreads = 32 * kVecWarps;
 constexpr int kVecTokens = 32;  // of a block at a time, at most
@@ -909,7 +909,7 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
     p.v.h = a;
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
     p.v.tokens = a.q != nullptr ? 12 : 16;
-    p.v.each = 4;
+    p.v.each = 4;  // gradient: groups of a slice (8191 tokens of 18 heads of 256: 49 us with two or four, 62 with eight, which 18 heads do not fill)
     p.u = f32 ? 1 : 2;  // groups of a warp on their way: 16 registers each (bf16 norms as above 59 us with two, 62 with one; 8-bit writes 39, 42)
     // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy (8 single tokens into the
     // cache: 4.4 us, and 11 with twelve tokens in a block)
