@@ -43,13 +43,8 @@ def _expect(x, kind):
     return val, unit
 
 
-@pytest.mark.parametrize("dtype,kind", [(BF, BF), (BF, E4M3), (F32, F32), (F32, E4M3)])
-@pytest.mark.parametrize("page", [1, 7, 16, 64])
-@pytest.mark.parametrize("cached,news,packed", LENS)
-@pytest.mark.parametrize("D", [16, 80, 128, 256])
-def test_write_and_read(dtype, kind, page, cached, news, packed, D):
+def _check_write_and_read(dtype, kind, page, cached, news, packed, D, heads):
     g = torch.Generator().manual_seed(D + page)
-    heads = 3
     k, v, cu = _data(g, cached, news, packed, heads, D, dtype)
     table, count = tables(g, cached, page)
     cache = KVCache.empty(count, heads, page, D, kind)
@@ -79,6 +74,22 @@ def test_write_and_read(dtype, kind, page, cached, news, packed, D):
             assert torch.equal(now[pages, :, slots].view(E8M0).double(), unit)
             now[pages, :, slots] = index(old[2 + i])[pages, :, slots]
             assert torch.equal(now, index(old[2 + i]))
+
+
+@pytest.mark.parametrize("dtype,kind", [(BF, BF), (BF, E4M3), (F32, F32), (F32, E4M3)])
+@pytest.mark.parametrize("page", [1, 7, 16, 64])
+@pytest.mark.parametrize("cached,news,packed", LENS)
+@pytest.mark.parametrize("D", [16, 80, 128, 256])
+def test_write_and_read(dtype, kind, page, cached, news, packed, D):
+    _check_write_and_read(dtype, kind, page, cached, news, packed, D, 3)
+
+
+@pytest.mark.parametrize("dtype,kind", [(BF, BF), (BF, E4M3), (F32, F32), (F32, E4M3)])
+@pytest.mark.parametrize("D,heads", [(128, 4), (64, 9), (256, 2)])
+def test_more_tokens_than_blocks_take_at_once(dtype, kind, D, heads):
+    """Several rows of a lane on their way, and more sequences than threads that look for a token's."""
+    news = [(7 * i) % 29 for i in range(720)]
+    _check_write_and_read(dtype, kind, 16, [n + i % 3 for i, n in enumerate(news)], news, True, D, heads)
 
 
 def test_rounding_of_every_border():

@@ -19,7 +19,7 @@ import torch
 import attention_reference as aref
 import mixer_reference as ref
 from attention_cases import BF, E4M3, F32, filled, index, to_gpu
-from chunkwise_gated_linear_gb300 import KVCache, attention, kda, paged_attn_step
+from chunkwise_gated_linear_gb300 import KVCache, attention, kda, paged_attn_step, qk_norm_step, rope_frequencies
 
 pytestmark = pytest.mark.gpu
 dev = "cuda"
@@ -287,6 +287,34 @@ def test_graphs_streams_and_growing_lengths(dtype, kind):
             assert torch.equal(o, paged_attn_step(q, c, t, lens))
             want, _ = aref.attention(q.cpu(), cache, table, now, 64 ** -0.5)
             ref.check("replayed", o, want, dtype, WORK[dtype])
+
+
+def test_a_captured_serving_step():
+    """Norms with the write, attention and the count of the new tokens in one graph, replayed as the sequences grow: the same bits as
+    the calls one by one."""
+    g = torch.Generator().manual_seed(16)
+    B, Hq, H, D, page, start = 3, 8, 2, 64, 16, [0, 15, 300]
+    table = torch.arange(B * 21, dtype=torch.int32, device=dev).view(B, 21)
+    freq, w = rope_frequencies(D), torch.ones(D, device=dev)
+    tokens = [[torch.randn(B, 1, h, D, generator=g).to(BF).to(dev) for h in (Hq, H, H)] for _ in range(20)]
+    caches, counts = [KVCache.empty(B * 21, H, page, D, E4M3) for _ in range(2)], [_int32(start) for _ in range(2)]
+
+    def step(q, k, v, cache, lens):
+        lens.add_(1)
+        return paged_attn_step(qk_norm_step(q, k, v, cache, table, lens, w, w, freq), cache, table, lens)
+
+    want = [step(*x, caches[0], counts[0]) for x in tokens]
+    side = [x.clone() for x in tokens[0]]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(*side, caches[1], counts[1])
+    for x, o in zip(tokens, want):
+        for a, b in zip(side, x):
+            a.copy_(b)
+        graph.replay()
+        assert torch.equal(got, o)
+    assert all(torch.equal(index(a), index(b)) for a, b in zip(*caches)) and counts[1].tolist() == [n + 20 for n in start]
 
 
 def test_calls_on_two_streams_at_once():

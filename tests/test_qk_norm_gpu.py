@@ -82,6 +82,16 @@ def test_sequences_and_parts(dtype, parts, lens, Hq, Hk):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R,interleaved", [(64, False), (32, False), (64, True), (0, False)])
+def test_more_tokens_than_blocks_take_at_once(dtype, R, interleaved):
+    """Blocks go through several shares of the tokens, and look for their first one among more sequences than threads."""
+    lens = [(7 * i) % 29 for i in range(720)]
+    assert 9728 < sum(lens) < 12000
+    args = _case(torch.Generator().manual_seed(11), lens, True, 1, 1, 64, dtype, "qk")
+    _check_all(*args, R, dtype, interleaved)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_far_and_negative_positions(dtype):
     """Angles stay exact at positions where a product in 32 bits would have lost them."""
     g = torch.Generator().manual_seed(1)
