@@ -120,6 +120,12 @@ def _place(lead, others):
     raise ValueError("every tensor must be a CUDA tensor")
 
 
+def _like(t):
+    """An empty contiguous tensor like ``t``."""
+    torch = sys.modules["torch"]
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _dense(names, *tensors):
     for t in tensors:
         if t is not None and not t.is_contiguous():
@@ -206,8 +212,10 @@ def _cache(cache, block_table, lens, N, data):
         code = KDA_DTYPE_E4M3
         if ks is None or vs is None:
             raise ValueError("a float8_e4m3fn cache has k_scale and v_scale")
-        _want(ks, "k_scale", shape[:3], torch.float8_e8m0fnu)
-        _want(vs, "v_scale", shape[:3], torch.float8_e8m0fnu)
+        rows, bits = shape[:3], torch.float8_e8m0fnu
+        if not (ks.dtype is bits and vs.dtype is bits and ks.shape == rows and vs.shape == rows):
+            _want(ks, "k_scale", rows, bits)
+            _want(vs, "v_scale", rows, bits)
         if not (ks.is_contiguous() and vs.is_contiguous()):
             scale_stride = _page_stride(ks, "k_scale")
             if _page_stride(vs, "v_scale") != scale_stride:
@@ -218,7 +226,8 @@ def _cache(cache, block_table, lens, N, data):
         if ks is not None or vs is not None:
             raise ValueError("only a float8_e4m3fn cache has scales")
         code = KDA_DTYPE_BF16 if data is torch.bfloat16 else KDA_DTYPE_F32
-    _want(v, "v of the cache", shape, kind)
+    if not (v.dtype is kind and v.shape == shape):
+        _want(v, "v of the cache", shape, kind)
     page_stride = 0
     if not (k.is_contiguous() and v.is_contiguous()):
         page_stride = _page_stride(k, "k of the cache")
@@ -360,14 +369,12 @@ def qk_norm_fwd(q, k, q_weight=None, k_weight=None, freq=None, *, positions=None
     (i, i + R / 2), or (2 i, 2 i + 1) with ``interleaved``. ``positions`` int32 [B, T]; None: the token's index in
     its sequence. ``q_out`` may be q and ``k_out`` may be k where those are contiguous.
     """
-    torch = sys.modules["torch"]
-
     p = _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, q_out, k_out)
     _place(q, (k, q_weight, k_weight, freq, positions, cu_seqlens, q_out, k_out))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _like(q)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _like(k)
     p.q_out, p.k_out = _ptr(q_out), _ptr(k_out)
     _call("kda_qk_norm_fwd", p, q, stream)
     return q_out, k_out
@@ -384,8 +391,7 @@ def qk_norm_bwd(q, k, q_weight, k_weight, freq, dq_out, dk_out, *, positions=Non
     _want(dk_out, "dk_out", k.shape, q.dtype)
     _dense("dq_out dk_out", dq_out, dk_out)
     _place(q, (k, q_weight, k_weight, freq, positions, cu_seqlens, dq_out, dk_out))
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dq, dk = _like(q), _like(k)
     dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
     p = kda_qk_norm_bwd_params(f, _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), None, 0)
     _call("kda_qk_norm_bwd", p, q, stream, workspace=True)
@@ -397,8 +403,6 @@ def qk_norm_step(q, k, v, cache, block_table, lens, q_weight=None, k_weight=None
     """:func:`qk_norm_fwd` on the new tokens of the cache's sequences, k after norm and rotation and v
     [B, T, k_heads, D] as it is going straight into the cache (:func:`kv_cache_write`). Positions are those in the
     cache unless ``positions`` gives others for the rotation. Returns q_out."""
-    torch = sys.modules["torch"]
-
     f = _norm_check(q, k, q_weight, k_weight, freq, positions, cu_seqlens, eps, interleaved, q_out, None)
     shape = q.shape
     Hv, v_stride = _heads(v, "v", shape[0], shape[1], shape[3], q.dtype)
@@ -407,7 +411,7 @@ def qk_norm_step(q, k, v, cache, block_table, lens, q_weight=None, k_weight=None
         raise ValueError("k, v and the cache must have the same heads and channels")
     _place(q, (k, v, q_weight, k_weight, freq, positions, cu_seqlens, q_out, *cache, block_table, lens))
     if q_out is None:
-        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        q_out = _like(q)
         f.q_out = q_out.data_ptr()
     p = kda_qk_norm_step_params(f, _ptr(v), v_stride, c)
     _call("kda_qk_norm_step", p, q, stream)
@@ -445,7 +449,7 @@ def paged_attn_step(q, cache, block_table, lens, *, scale=None, want_lse=False, 
     _dense("o lse", o, lse)
     _place(q, (o, lse, *cache, block_table, lens))
     if o is None:
-        o = torch.empty(shape, dtype=kind, device=q.device)
+        o = _like(q)
     if want_lse and lse is None:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
     p = kda_attn_step_params(_ptr(q), _ptr(o), _ptr(lse), stride, B, T, Hq, scale, dtype, c, None, 0)
