@@ -908,6 +908,7 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
     VecPlan p;
     p.v.h = a;
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
+    // 8-bit writes of 32761 tokens 40 us with 8 tokens, 38 with 16, 37 with 32; norms alike from 9 to 16
     p.v.tokens = a.q != nullptr ? 12 : 16;
     p.v.each = 4;  // gradient: groups of a slice (8191 tokens of 18 heads of 256: 49 us with two or four, 62 with eight, which 18 heads do not fill)
     p.u = f32 ? 1 : 2;  // groups of a warp on their way: 16 registers each (bf16 norms as above 59 us with two, 62 with one; 8-bit writes 39, 42)
