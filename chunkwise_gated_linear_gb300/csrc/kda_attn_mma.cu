@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                             if constexpr (kJoint == 2) v[i] = fmaxf(v[i], fmaxf(x[1][i / 2][i & 1] + ev[1][0], x[1][i / 2][(i & 1) + 2] + ev[1][1]));
                         }
                         // the largest P' at 2^6, so that none passes 2^kMost soon; rows of zeros (sv = -126) alone leave it lower, or
-                        // 2^(m - M) would pass what fp32 holds
-                        float to = fmaxf(spread_max(v, lane) - 6.f, my_m - 120.f);
+                        // 2^(score - M), with a score of up to m + 8, would pass what fp32 holds
+                        float to = fmaxf(spread_max(v, lane) - 6.f, my_m - 119.f);
                         back = 1.f;
                         if (!nothing) {
                             if (!first) to = fmaxf(to, my_mv);
@@ -408,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                         for (int i = 0; i < 2; ++i) {
                             f2 w = exp2_2(add2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), ref[n]));
                             l[n] = add2(l[n], w);
-                            if constexpr (M::kScaled) w = mul2(w, mul2(turn[n], pk(fv[h][i], fv[h][i])));
+                            // in this order: w turn is P' without the value's power of two, at most 2^127 and 0 for a key that is not seen; turn fv
+                            // alone passes what fp32 holds where the powers of two lie far apart (2^120 beside an infinity)
+                            if constexpr (M::kScaled) w = mul2(mul2(w, turn[n]), pk(fv[h][i], fv[h][i]));
                             float lo, hi;
                             upk(w, lo, hi);
                             pb[h][n][i] = transpose8(M::kScaled ? pack_f16(lo, hi) : pack_bf16(lo, hi));

@@ -395,3 +395,66 @@ def test_power_of_two_that_is_no_number_stays_in_its_sequence(dtype, T):
         pos = torch.arange(lens[b])
         index(cache.v_scale)[table[b].long()[pos // 16], :, pos % 16] = 0xFF
     assert bool(torch.isfinite(want).all()) and torch.equal(call()[1::2], want[1::2])
+
+
+def _places(table, b, pos, page=16):
+    """Page, key head 0 and row of a position, as an index."""
+    return table[b, pos // page].long(), 0, pos % page
+
+
+def _infinite_row(t, scale, at, channel):
+    """The row of an 8-bit cache at `at` as kv_cache_write leaves it when one channel is infinite: 448 2^120, and zeros."""
+    row = torch.zeros(t.shape[3], dtype=torch.uint8)
+    row[channel] = 0x7E
+    index(t)[at] = row
+    index(scale)[at] = 120 + 127
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("part", ["k", "v", "kv"])
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 2), (128, 5), (64, 8), (256, 3), (256, 6), (128, 13)])
+def test_infinities_of_an_8_bit_cache_stay_where_no_row_sees_them(dtype, part, D, group):
+    """The last new token's key or value has an infinity: the tokens before it, and the other key head, are as defined."""
+    lens, T = [70, 9, 200, 5], 5
+    g = torch.Generator().manual_seed(17)
+    cache, table = filled(g, lens, 16, 2, D, E4M3)
+    q = _q(g, len(lens), T, 2 * group, D, dtype, E4M3)
+    for b, n in enumerate(lens):
+        at = _places(table, b, n - 1)
+        if "k" in part:
+            _infinite_row(cache.k, cache.k_scale, at, 3)
+        if "v" in part:
+            _infinite_row(cache.v, cache.v_scale, at, 5)
+    want, _ = aref.attention(q, cache, table, lens, D ** -0.5)
+    o = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens))
+    ref.check("before", o[:, :T - 1], want[:, :T - 1], dtype, WORK[dtype])
+    ref.check("other head", o[:, :, group:], want[:, :, group:], dtype, WORK[dtype])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("score,byte", [(-208.0, 143), (-28.0, 143), (-208.0, 200)])
+def test_large_values_of_little_weight_after_rows_of_zeros(dtype, T, score, byte):
+    """Powers of two 2^142 and more apart: the rows of zeros have nearly all of the weight, the others e^-28 of it or, at
+    e^-208, none that 32 bits hold (such a result is 0)."""
+    g = torch.Generator().manual_seed(18)
+    lens = [100, 41]
+    cache, table = filled(g, lens, 16, 1, 64, E4M3)
+    q = torch.zeros(2, T, 4, 64)
+    q[..., 0] = 8.0  # times 64^-1/2: a key's channel 0 is its score
+    index(cache.k_scale)[:] = 127
+    for b, n in enumerate(lens):
+        for pos in range(n):
+            at = _places(table, b, pos)
+            row = torch.zeros(64)
+            row[0] = score if pos >= 38 else 0.0
+            index(cache.k)[at] = row.to(E4M3).view(torch.uint8)
+            index(cache.v_scale)[at] = byte if pos >= 38 else 1
+            if pos < 38:
+                index(cache.v)[at] = 0
+    want, _ = aref.attention(q, cache, table, lens, 0.125)
+    o = paged_attn_step(q.to(dtype).to(dev), to_gpu(cache), table.to(dev), _int32(lens))
+    if score < -200:
+        assert not o.any()
+    else:
+        ref.check("o", o, want, dtype, WORK[dtype])
