@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
 #pragma unroll
                         for (int i = 0; i < 4; ++i) grows |= x[h][n][i] > lim[n][i & 1];
                 if (__any_sync(0xffffffffu, grows)) {
-                    // each reference moves up alone, never down; with nothing seen yet l and O are 0
+                    // A reference moves up, never down, and by what its own row sees alone, so that a row's result does not follow, not
+                    // even in its roundings, from the others of the warp. With nothing seen yet l and O are 0.
                     float v[2 * NT];
 #pragma unroll
                     for (int i = 0; i < 2 * NT; ++i) {
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                     const float top = spread_max(v, lane);
                     float back = 1.f, back_l = 1.f;
                     const bool first = nothing;
-                    if (first ? top > -INFINITY : top > my_m) {
+                    if (top > (first ? -INFINITY : my_m + kGrow)) {
                         back_l = first ? 0.f : tc5::ex2(my_m - top);
                         my_m = top;
                         nothing = false;
@@ -369,10 +370,10 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                         }
                         // the largest P' at 2^6, so that none passes 2^kMost soon; rows of zeros (sv = -126) alone leave it lower, or
                         // 2^(score - M), with a score of up to m + 8, would pass what fp32 holds
-                        float to = fmaxf(spread_max(v, lane) - 6.f, my_m - 119.f);
+                        const float top_v = spread_max(v, lane);
                         back = 1.f;
                         if (!nothing) {
-                            if (!first) to = fmaxf(to, my_mv);
+                            const float to = fmaxf(first || top_v > my_mv + kMost ? top_v - 6.f : my_mv, my_m - 119.f);
                             back = first ? 0.f : tc5::ex2(my_mv - to);
                             my_mv = to;
                         }
@@ -458,14 +459,15 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                                         else
                                             mma_bf16(o[k + t][n], f[t], pb[h][n][0], pb[h][n][1]);
                                     } else {
-                                        float add[4] = {0.f, 0.f, 0.f, 0.f};
+                                        // added up as above, so that such a value changes no rounding either
+                                        float sum[4] = {o[k + t][n][0], o[k + t][n][1], o[k + t][n][2], o[k + t][n][3]};
                                         if constexpr (M::kScaled)
-                                            mma_f16(add, f[t], pb[h][n][0], pb[h][n][1]);
+                                            mma_f16(sum, f[t], pb[h][n][0], pb[h][n][1]);
                                         else
-                                            mma_bf16(add, f[t], pb[h][n][0], pb[h][n][1]);
+                                            mma_bf16(sum, f[t], pb[h][n][0], pb[h][n][1]);
 #pragma unroll
                                         for (int i = 0; i < 4; ++i)
-                                            if (token_of(a, p.row0 + 8 * n + 2 * c + (i & 1)) == token) o[k + t][n][i] += add[i];
+                                            if (token_of(a, p.row0 + 8 * n + 2 * c + (i & 1)) == token) o[k + t][n][i] = sum[i];
                                     }
                                 }
                         }

@@ -458,3 +458,33 @@ def test_large_values_of_little_weight_after_rows_of_zeros(dtype, T, score, byte
         assert not o.any()
     else:
         ref.check("o", o, want, dtype, WORK[dtype])
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 2), (128, 4), (64, 8), (256, 3), (256, 6), (128, 13)])
+@pytest.mark.parametrize("what", ["key", "value", "nan", "infinity"])
+def test_results_do_not_depend_on_what_a_row_does_not_see(dtype, kind, D, group, what):
+    """With another key or value at the last position the tokens before are the same bit for bit: no rounding of theirs
+    follows from what other rows see."""
+    lens, T = [25, 40, 70, 9, 200, 6] * 60, 5  # so many that a warp goes through several units of a sequence
+    g = torch.Generator().manual_seed(19)
+    cache, table = filled(g, lens, 16, 2, D, kind)
+    q = _q(g, len(lens), T, 2 * group, D, dtype, kind)
+    bad = KVCache(*(None if t is None else t.clone() for t in cache))
+    for b, n in enumerate(lens):
+        at = _places(table, b, n - 1)
+        for t, scale, times in ((bad.k, bad.k_scale, 5 if what == "key" else 0), (bad.v, bad.v_scale, 14 if what == "value" else 0)):
+            if what == "nan":
+                index(t)[at] = 0x7F if kind == E4M3 else float("nan")
+            elif what == "infinity" and kind == E4M3:
+                _infinite_row(t, scale, at, 5)
+            elif what == "infinity":
+                t[(*at, 5)] = float("inf")
+            elif kind == E4M3:
+                index(scale)[at] += times
+            else:
+                t[at] *= 2.0 ** times
+    call = lambda c: paged_attn_step(q.to(dev), to_gpu(c), table.to(dev), _int32(lens), want_lse=True)  # noqa: E731
+    for x, y in zip(call(bad), call(cache)):
+        assert torch.equal(x[:, :T - 1], y[:, :T - 1])
+        assert torch.equal(x[:, :, group:], y[:, :, group:])  # the other key head
