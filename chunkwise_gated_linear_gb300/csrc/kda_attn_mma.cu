@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                             const float fk = __uint_as_float((uint32_t)sc[16 * h + g + 8 * i] << 23);
                             fv[h][i] = __uint_as_float((uint32_t)sc[kKeys + 16 * h + g + 8 * i] << 23);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                upk(mul2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), mul2(rowf[n], pk(fk, fk))), x[h][n][2 * i], x[h][n][2 * i + 1]);
+                            for (int n = 0; n < NT; ++n)  // the row's factor first: times a large power of two it could pass fp32 where the sum is 0
+                                upk(mul2(mul2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), rowf[n]), pk(fk, fk)), x[h][n][2 * i], x[h][n][2 * i + 1]);
                         }
                 } else {
 #pragma unroll

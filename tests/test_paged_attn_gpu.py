@@ -488,3 +488,20 @@ def test_results_do_not_depend_on_what_a_row_does_not_see(dtype, kind, D, group,
     for x, y in zip(call(bad), call(cache)):
         assert torch.equal(x[:, :T - 1], y[:, :T - 1])
         assert torch.equal(x[:, :, group:], y[:, :, group:])  # the other key head
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scores_of_zero_from_keys_and_queries_of_far_sizes(dtype):
+    """Keys with the largest power of two, 2^127, meet entries of 2^20 of a query only in zeros: their scores are 0."""
+    g = torch.Generator().manual_seed(20)
+    lens = [70, 5]
+    cache, table = filled(g, lens, 16, 1, 64, E4M3)
+    q = torch.zeros(2, 1, 4, 64)
+    q[..., 0] = 2.0 ** 20
+    for b, n in enumerate(lens):
+        for pos in range(n):
+            at = _places(table, b, pos)
+            index(cache.k)[(*at, 0)] = 0
+            if pos % 2:
+                index(cache.k_scale)[at] = 254
+    _check(q.to(dtype), cache, table, lens, dtype)
