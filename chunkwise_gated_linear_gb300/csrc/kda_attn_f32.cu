@@ -201,14 +201,15 @@ __global__ void __launch_bounds__(kThreads, Fma<C, DP, RB, KEYS, SLOTS>::kBlocks
             for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
             const bool whole = p.whole();
             const int64_t row = out_row(a, p, r);
-            const float f = whole ? (t == 0.f ? 0.f : 1.f / t) : 1.f;
+            const bool empty = whole && t == 0.f;  // zeros, whatever the values are
+            const float f = whole ? 1.f / t : 1.f;
             float *to = whole ? static_cast<float *>(a.o) + row * D : piece + r * D;
 #pragma unroll
             for (int j = 0; j < F::kCols / 2; ++j) {
                 const int d = lane * F::kCols + 2 * j;
                 float lo, hi;
                 upk(mul2(acc[r][j], pk(f, f)), lo, hi);
-                if (d < D) *reinterpret_cast<float2 *>(to + d) = make_float2(lo, hi);
+                if (d < D) *reinterpret_cast<float2 *>(to + d) = empty ? make_float2(0.f, 0.f) : make_float2(lo, hi);
             }
             if (lane == 0) {
                 if (!whole)

@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                 if (r >= p.rows) continue;
                 const float top = row_m[r];
                 float f = M::kScaled && top > -INFINITY ? tc5::ex2(row_mv[r] - top) : 1.f;
-                if (whole) f = sum[j] == 0.f ? 0.f : f / sum[j];
+                const bool empty = whole && sum[j] == 0.f;  // zeros, whatever the values are
+                if (whole) f = f / sum[j];
                 const int64_t row = out_row(a, p, r);
                 bf16 *to = static_cast<bf16 *>(a.o) + row * D;
                 float *part = piece + (base + r) * D;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
                     if (16 * k >= D) break;
-                    const float lo = o[k][n][j] * f, hi = o[k][n][j + 2] * f;
+                    const float lo = empty ? 0.f : o[k][n][j] * f, hi = empty ? 0.f : o[k][n][j + 2] * f;
                     if constexpr (M::kScaled) {
                         if (whole)
                             *reinterpret_cast<uint32_t *>(to + 16 * k + 2 * g) = pack_bf16(lo, hi);

@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(32 * join_warps(LC), 2) attn_join_kernel(const
         }
     }
     if (r >= p.rows || lane >= LC) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool empty = l == 0.f;  // zeros, whatever the values are
+    const float inv = 1.f / l;
     const int64_t row = out_row(a, p, r);
 #pragma unroll
     for (int h = 0; h < kPasses; ++h)
         if (d0 + 128 * h < D) {
-            const float y[4] = {s[h].x * inv, s[h].y * inv, s[h].z * inv, s[h].w * inv};
+            const float y[4] = {empty ? 0.f : s[h].x * inv, empty ? 0.f : s[h].y * inv, empty ? 0.f : s[h].z * inv, empty ? 0.f : s[h].w * inv};
             store_vec<T, 4>(static_cast<T *>(a.o) + row * D + d0 + 128 * h, y);
         }
     if (d0 == 0 && a.lse != nullptr) a.lse[row] = lse_of(m, l);

@@ -505,3 +505,22 @@ def test_scores_of_zero_from_keys_and_queries_of_far_sizes(dtype):
             if pos % 2:
                 index(cache.k_scale)[at] = 254
     _check(q.to(dtype), cache, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [1, 4, 16])
+def test_scores_that_are_all_minus_infinity(dtype, group):
+    """Such a row is empty whatever its values are, in one piece or in many."""
+    g = torch.Generator().manual_seed(21)
+    lens = [5, 300, 20000, 0]
+    cache, table = filled(g, lens, 16, 1, 64, dtype)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        at = table[b].long()[pos // 16], 0, pos % 16
+        cache.k[(*at, 0)] = -float("inf")
+        cache.v[(*at, 7)] = float("nan")
+        cache.v[(*at, 9)] = float("inf")
+    q = _q(g, len(lens), 2, group, 64, dtype, dtype)
+    q[..., 0] = 1.0
+    o, lse = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens), want_lse=True)
+    assert torch.equal(o, torch.zeros_like(o)) and torch.equal(lse, torch.full_like(lse, -math.inf))
