@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __gr
             bool last;
 #pragma unroll 1
             do {
-                const bool ok = now_left > 0 && l.in;
+                const bool there = now_left > 0, ok = there && l.in;
                 f2 g[8], x[8];
                 raw_g.unpack(g);
                 raw.unpack(x);
@@ -686,7 +686,9 @@ __global__ void __launch_bounds__(kVecThreads, 2) vec_rows_bwd_kernel(const __gr
                     f2 q = mul2(x[0], x[0]), m = pk(0.f, 0.f);
 #pragma unroll
                     for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
-                    const float inv = rsqrtf(row_sum<LPR>(hsum2(q)) * inv_d + a.eps);
+                    // a row of the last group that is not there adds zeros to the weights' gradients, with eps = 0 too
+                    const float mean = row_sum<LPR>(hsum2(q)) * inv_d;
+                    const float inv = there ? rsqrtf(mean + a.eps) : 0.f;
                     const f2 by = pk(inv, inv);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {

@@ -250,3 +250,23 @@ def test_step_is_forward_and_write(kind):
     assert torch.equal(qa, qb) and torch.equal(index(a.v), index(b.v))
     if kind == BF:
         assert torch.equal(a.k, b.k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hk", [(5, 1), (3, 2), (8, 4)])
+@pytest.mark.parametrize("D", [16, 64, 128, 256, 37])
+def test_gradient_without_eps(dtype, D, Hq, Hk):
+    """eps 0, with heads that do and do not fill a warp's groups of rows."""
+    g = torch.Generator().manual_seed(12)
+    q, k, qw, kw, _, pos = _case(g, [7, 7, 7], False, Hq, Hk, D, dtype, "qk")
+    R = D // 4 * 2
+    v = ref.leaves(dict(q=q, k=k, qw=qw, kw=kw))
+    y = [aref.norm_rope(v[x].flatten(0, 1), v[x + "w"], pos, aref.inv_freq(R), 0.0, False) for x in "qk"]
+    for name, o, w in zip("qk", qk_norm_fwd(q, k, qw, kw, rope_frequencies(R), eps=0.0), y):
+        ref.check(name, o, w.reshape(o.shape), dtype, WORK)
+    dq, dk = _r(g, *q.shape, dt=dtype), _r(g, *k.shape, dt=dtype)
+    want = ref.grads(y, (dq.flatten(0, 1), dk.flatten(0, 1)), v)
+    got = qk_norm_bwd(q, k, qw, kw, rope_frequencies(R), dq, dk, eps=0.0)
+    for name, o, key, dt, tol in zip(("dq", "dk", "dqw", "dkw"), got, ("q", "k", "qw", "kw"), (dtype, dtype, F32, F32),
+                                     (WORK, WORK, SUMS, SUMS)):
+        ref.check(name, o, want[key], dt, tol)
