@@ -842,7 +842,11 @@ int sizes_check(int B, int T, const int32_t *cu, int dtype, int64_t heads, int64
 }
 int stride_check(int64_t given, int64_t dense) { return given != 0 && given < dense ? KDA_ERR_INVALID_ARG : KDA_OK; }
 
-int norm_check(const kda_qk_norm_params &p, bool q_out, bool k_out, int64_t *rows) {
+// Which outputs a call writes: q_out and k_out (the forward pass), k_out only if it is given (single tokens), or neither (gradient).
+enum Outs { kBoth, kKeysIfGiven, kNeither };
+
+int norm_check(const kda_qk_norm_params &p, Outs outs, int64_t *rows) {
+    const bool q_out = outs != kNeither, k_out = outs == kBoth || (outs == kKeysIfGiven && p.k_out != nullptr);
     if (p.q_heads < 1 || p.k_heads < 1 || p.D < 1 || p.R < 0 || p.R % 2 != 0 || p.R > p.D || !(p.eps >= 0.f)) return KDA_ERR_INVALID_ARG;
     const int st = sizes_check(p.B, p.T, p.cu_seqlens, p.dtype, p.q_heads + 2 * (int64_t)p.k_heads, rows);
     if (st != KDA_OK) return st;
@@ -1016,7 +1020,7 @@ cudaError_t launch_read(const HeadArgs &a, bool f32, cudaStream_t stream) {
 }
 
 int bwd_check(const kda_qk_norm_bwd_params &p, int64_t *rows) {
-    const int st = norm_check(p.f, false, false, rows);
+    const int st = norm_check(p.f, kNeither, rows);
     if (st != KDA_OK) return st;
     if (*rows != 0 && (p.dq_out == nullptr || p.dk_out == nullptr || p.dq == nullptr || p.dk == nullptr)) return KDA_ERR_INVALID_ARG;
     if ((p.dq_weight != nullptr && p.f.q_weight == nullptr) || (p.dk_weight != nullptr && p.f.k_weight == nullptr))
@@ -1093,7 +1097,7 @@ int kda_qk_norm_fwd(const kda_qk_norm_params *p, cudaStream_t stream) {
     using namespace kda;
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     int64_t rows = 0;
-    const int st = norm_check(*p, true, true, &rows);
+    const int st = norm_check(*p, kBoth, &rows);
     if (st != KDA_OK || rows == 0) return st;
     unsigned int *err = nullptr;
     const cudaError_t e = device_error_word(&err);
@@ -1105,7 +1109,7 @@ int kda_qk_norm_step(const kda_qk_norm_step_params *p, cudaStream_t stream) {
     using namespace kda;
     if (p == nullptr) return KDA_ERR_INVALID_ARG;
     int64_t rows = 0;
-    int st = norm_check(p->f, true, false, &rows);
+    int st = norm_check(p->f, kKeysIfGiven, &rows);
     if (st == KDA_OK) st = cache_check(p->cache, p->f.dtype);
     if (st != KDA_OK) return st;
     if (p->cache.heads != p->f.k_heads || p->cache.D != p->f.D || stride_check(p->v_stride, (int64_t)p->f.k_heads * p->f.D) != KDA_OK)

@@ -124,7 +124,7 @@ size_t kda_qk_norm_bwd_workspace(const kda_qk_norm_bwd_params *p);
 /*
  * kda_qk_norm_step — kda_qk_norm_fwd on the new tokens of the cache's sequences, with k after norm and
  * rotation and v [B, T, k_heads, D] as it is written into the cache as by kda_kv_cache_write
- * (an 8-bit cache takes them from fp32). f.k_out may be NULL. Positions are those in the cache unless
+ * (an 8-bit cache takes them from fp32). f.k_out may be NULL (or k, as in kda_qk_norm_fwd). Positions are those in the cache unless
  * f.positions says otherwise (for the rotation alone). Rows of q whose token is not there are
  * computed like the others.
  */

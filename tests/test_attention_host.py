@@ -127,6 +127,12 @@ def test_bad_arguments_are_rejected(fn, make, over, want):
     assert getattr(attention, "kda_" + fn)(make(**over), 0) == want
 
 
+def test_step_with_keys_in_place():
+    """Keys that are also written beside the cache may be written in place only where they are contiguous, as in the forward call."""
+    assert attention.kda_qk_norm_step(_step(k_out=A, k_stride=512), 0) == INV
+    assert attention.kda_qk_norm_step(_step(q_out=A, q_stride=512), 0) == INV
+
+
 @pytest.mark.parametrize("D", [8, 24, 272])
 def test_widths_that_a_cache_does_not_hold(D):
     assert attention.kda_kv_cache_write(_write(c_D=D), 0) == UNS
