@@ -100,6 +100,7 @@ inline int cache_check(const kda_kv_cache &c, int dtype) {
     const bool e4m3 = c.dtype == KDA_DTYPE_E4M3;
     if (e4m3 != (c.k_scale != nullptr) || e4m3 != (c.v_scale != nullptr)) return KDA_ERR_INVALID_ARG;
     const int64_t dense = (int64_t)c.heads * c.page_size;
+    if (dense > ((int64_t)1 << 31) / c.pages) return KDA_ERR_UNSUPPORTED;  // so that its products below stay in 64 bits
     const int64_t stride = c.page_stride == 0 ? dense * c.D : c.page_stride;
     if (stride < dense * c.D || stride % c.D != 0) return KDA_ERR_INVALID_ARG;
     if (c.scale_stride != 0 && c.scale_stride < dense) return KDA_ERR_INVALID_ARG;

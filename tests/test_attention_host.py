@@ -133,6 +133,15 @@ def test_step_with_keys_in_place():
     assert attention.kda_qk_norm_step(_step(q_out=A, q_stride=512), 0) == INV
 
 
+@pytest.mark.parametrize("over", [dict(c_heads=1 << 29, c_page_size=1 << 30, c_D=32), dict(c_heads=(1 << 30) - (1 << 16), c_page_size=(1 << 31) - 1, c_D=256),
+                                  dict(c_heads=1 << 20, c_page_size=1 << 20, c_D=64), dict(c_heads=1, c_page_size=(1 << 31) - 1, c_pages=3)])
+def test_caches_of_more_rows_than_are_counted(over):
+    """Sizes whose products pass 63 bits are refused like all that pass the limit of rows."""
+    sizes = {"B": 1, "T": 1, "c_pages": 1, **over}
+    assert attention.kda_kv_cache_write(_write(**sizes), 0) == UNS
+    assert attention.kda_kv_cache_read(_read(**sizes), 0) == UNS
+
+
 @pytest.mark.parametrize("D", [8, 24, 272])
 def test_widths_that_a_cache_does_not_hold(D):
     assert attention.kda_kv_cache_write(_write(c_D=D), 0) == UNS
