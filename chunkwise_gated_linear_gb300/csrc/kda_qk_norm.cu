@@ -952,11 +952,16 @@ template <typename T, int U, int MODE>
 cudaError_t vec_mode(const VecPlan &p, cudaStream_t stream) {
     return with_lpr(p, [&](auto lpr) { vec_rows_kernel<T, decltype(lpr)::value, U, MODE><<<p.blocks, kVecThreads, p.smem, stream>>>(p.v); });
 }
+template <typename T, int MODE>
+cudaError_t vec_groups(const VecPlan &p, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2)  // fp32 has one on its way
+        if (p.u == 2) return vec_mode<T, 2, MODE>(p, stream);
+    return vec_mode<T, 1, MODE>(p, stream);
+}
 template <typename T>
 cudaError_t vec_rows(const VecPlan &p, cudaStream_t stream) {
-    if (!p.v.h.cached) return p.u == 1 ? vec_mode<T, 1, kNorm>(p, stream) : vec_mode<T, 2, kNorm>(p, stream);
-    if (p.v.h.q != nullptr) return p.u == 1 ? vec_mode<T, 1, kStep>(p, stream) : vec_mode<T, 2, kStep>(p, stream);
-    return p.u == 1 ? vec_mode<T, 1, kWrite>(p, stream) : vec_mode<T, 2, kWrite>(p, stream);
+    if (!p.v.h.cached) return vec_groups<T, kNorm>(p, stream);
+    return p.v.h.q != nullptr ? vec_groups<T, kStep>(p, stream) : vec_groups<T, kWrite>(p, stream);
 }
 template <typename T>
 cudaError_t vec_bwd(const VecPlan &p, cudaStream_t stream) {
