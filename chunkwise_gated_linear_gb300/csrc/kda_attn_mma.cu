@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                                             mma_bf16(sum, f[t], pb[h][n][0], pb[h][n][1]);
 #pragma unroll
                                         for (int i = 0; i < 4; ++i)
-                                            if (token_of(a, p.row0 + 8 * n + 2 * c + (i & 1)) == token) o[k + t][n][i] = sum[i];
+                                            if ((unsigned)(p.row0 + 8 * n + 2 * c + (i & 1) - token * a.group) < (unsigned)a.group) o[k + t][n][i] = sum[i];
                                     }
                                 }
                         }
