@@ -5,7 +5,8 @@
 // parts are added across lanes; then a lane owns DP / 32 neighbouring columns of O and goes through the keys. Arithmetic
 // goes in pairs of fp32, without branches per row: rows that are not there are zeros (with a branch for each row the
 // compiler keeps the rows' loads apart: 32768 tokens of 3 sequences, 4 key heads of 128, 135 us instead of 85, 70 % of what a
-// copy moves). Two blocks of four warps on an SM, as their rings fill its shared memory.
+// copy moves). The rings fill the shared memory of an SM: two blocks of four warps, in fp32 above 128 channels one, over 8 bits with 4 rows up to
+// 128 channels three.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -233,13 +234,17 @@ struct Variant {
     static int workers() { return F::kBlocks * kWarps; }
     static int unit() { return KEYS; }
 };
-// Calls f with the variant for these sizes: rings that fill the shared memory of an SM, in one to three blocks.
+// Calls f with the variant for these sizes. Keys of a unit: 16, or 8 where an fp32 ring of such units would leave one block. Slots of a ring: in
+// fp32 as many as leave room for two blocks on an SM up to 128 channels, and five in one block above; over 8 bits, which leave room
+// for two blocks or more, five or six, and four above 128 channels. (us, with one slot less and one more; 3 sequences of 32768, 16384 or 8192
+// tokens for 64, 128 and 256 channels, 4 key heads, 4 rows and 8 rows: fp32 50 (50, 71), 74 (74, 105); 52 (54, 57), 84 (83, 107);
+// 54 (53, 55), 79 (78, 82); 8 bits 43 (43, 43), 71 (71, 71); 38 (38, 38), 62 (62, 63); 34 and, with five, 35; 55 and, with five, 60.)
 template <typename C, int RB, typename F>
 auto pick(const Args &a, F f) {
     constexpr bool k4 = sizeof(C) == 4;
     if (a.cache.D <= 64) return f(Variant<C, 64, RB, 16, 6>{});
     if (a.cache.D <= 128) return f(Variant<C, 128, RB, (k4 && RB > 4) ? 8 : 16, (k4 && RB == 4) ? 3 : 5>{});
-    return f(Variant<C, 256, RB, k4 ? 8 : 16, 5>{});
+    return f(Variant<C, 256, RB, k4 ? 8 : 16, k4 ? 5 : 4>{});
 }
 template <typename F>
 auto pick(const Args &a, F f) {

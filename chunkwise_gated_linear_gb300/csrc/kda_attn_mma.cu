@@ -570,6 +570,12 @@ struct Variant {
 // tokens, 4 key heads of 128: 16 rows over bf16 33 us with two warps and 40 with one, over 8 bits 31 and 29; 32 rows
 // as two blocks of 16 instead of a team's 63 and 41, 43 and 42; 64 rows as two of 32 68 and 56, 68 and 65. Few rows in an
 // item of 16: 64 sequences over an 8-bit cache 212 us, and 188 in items of 8.)
+// Slots of the rings, with one less and one more (us; one token of 16 sequences of 16384, 32768 or 8192 tokens for 128, 64 and 256 channels,
+// new tokens over up to 8192, 4 key heads): one less leaves a worker waiting, one more can cost a block of the SM.
+//   64 channels:  8 rows bf16 95 (121, 95), 8 bits 73 (70, 107); 16 rows 24 (25, 24), 24 (24, 28); 32 and 64 rows within 2 %
+//   128 channels: 8 rows 92 (92, 92), 55 (54, 55); 16 rows 33 (35, 34), 29 (35, 29); 32 rows 42 (39, 41), 41 (41, 42); 64 rows 52 (52, 56), 56 (59, 60)
+//   256 channels: 8 rows 92 (91, 92), 57 (54, 59), but one long sequence over 8 bits 36 (37); 16 rows 55 (53, 56), 39 (-, 41); 32 rows 65 (65, 66),
+//                 59 (-, 61); 64 rows 109 (111, 113), 100 (-, 102)
 template <typename C, int DP, int SLOTS, int SLOTS_TEAM, typename F>
 auto pick_rows(const Args &a, F f) {
     if (a.rows == 8) return f(Variant<C, DP, 1, SLOTS, 1>{});
@@ -588,7 +594,7 @@ template <typename C, typename F>
 auto pick(const Args &a, F f) {
     if (a.cache.D <= 64) return pick_rows<C, 64, 6, 7>(a, f);
     if (a.cache.D <= 128) return pick_rows<C, 128, 4, sizeof(C) == 1 ? 7 : 5>(a, f);
-    return pick_rows<C, 256, 3, 5>(a, f);
+    return pick_rows<C, 256, 3, sizeof(C) == 1 ? 4 : 5>(a, f);
 }
 
 }  // namespace
