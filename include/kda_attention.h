@@ -142,7 +142,9 @@ int kda_qk_norm_step(const kda_qk_norm_step_params *p, cudaStream_t stream);
  * position. An 8-bit cache holds, of a row x, the values e4m3(x 2^-e) (round to nearest even) with the
  * least e >= -126 that leaves the largest finite |x| at 448 or below, and the byte e + 127. (A
  * power of two costs an 8-bit floating-point value no precision, and every product with it is
- * exact.) NaN is kept; a row with an infinity keeps it and has e = 120. Otherwise the cache has the type
+ * exact.) NaN is kept; a row with an infinity has e = 120 and holds it as 448 * 2^120, beside which numbers below 2^110
+ * are zeros. kda_kv_cache_read gives infinity for that, as for all that passes its type (from 248 * 2^120 on); the attention
+ * counts it as the number that it is. Otherwise the cache has the type
  * of the data and holds it unchanged. No two tokens of a call may lie in the same place; other
  * places of the cache are left as they were. 2 B T heads (packed: 2 T heads) is below 2^31 - 2^16, here and in
  * kda_kv_cache_read.
@@ -160,7 +162,7 @@ int kda_kv_cache_write(const kda_kv_cache_write_params *p, cudaStream_t stream);
 
 /* kda_kv_cache_read — the reverse: the last T tokens of each sequence (packed: as many as
  * cu_seqlens says) into k, v [B, T, heads, D] `dtype`; zeros for a token that is not there. An
- * 8-bit cache is read into bf16 or fp32 (both exact), another one into its own type. */
+ * 8-bit cache is read into bf16 or fp32 (exactly, within the type's range), another one into its own type. */
 typedef struct kda_kv_cache_read_params {
     void *k, *v;
     int B, T;
@@ -179,11 +181,15 @@ int kda_kv_cache_read(const kda_kv_cache_read_params *p, cudaStream_t stream);
  *     o = sum_j softmax_j(scale q . k_j) v_j,    lse = log sum_j exp(scale q . k_j)
  *
  * n <= 0 (or scores that are all -infinity): o = 0, lse = -infinity. What lies in the cache at other
- * positions, NaN and infinities too, has no part in the result.
+ * positions, NaN and infinities too, has no part in the result: with something else there it is the same bit for bit.
  *   q, o [B, T, q_heads, D] `dtype`, q 16-byte aligned with q_stride a multiple of 16 bytes; lse
- *   [B, T, q_heads] fp32 or NULL. The cache has the type of the data or is 8-bit. bf16 data: products of
- *   bf16 (8-bit values are exact in it; the probabilities are rounded to it) summed in fp32; fp32
- *   data: fp32 throughout.
+ *   [B, T, q_heads] fp32 or NULL. The cache has the type of the data or is 8-bit.
+ * bf16 data: products of bf16 (the probabilities are rounded to it) summed in fp32; over an 8-bit cache products of fp16, in
+ * which its values are exact: a probability times its value's power of two has 11 bits, fewer below 2^-20 of the row's
+ * largest and none below 2^-31. fp32 data: fp32 throughout. The values are summed before the division: results are finite for
+ * values below 2^89. An infinity in an 8-bit cache that a token sees counts as 1.75 * 2^128: as a value it makes its channel
+ * infinite or that large times its probability, and beside it the other channels lose, for bf16 data, what lies 2^31 below; as a
+ * key it has all of the weight or none, or makes the row NaN.
  * The sequences' lengths are cut into equal shares for the GPU's SMs, and results of sequences that were
  * cut are joined in the order of their shares: which are cut follows from the lengths and sizes alone.
  * One call reads the cache ceil(T q_heads / heads / 64) times (bf16, D up to 128; 32 for wider heads; fp32

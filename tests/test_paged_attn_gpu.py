@@ -524,3 +524,27 @@ def test_scores_that_are_all_minus_infinity(dtype, group):
     q[..., 0] = 1.0
     o, lse = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens), want_lse=True)
     assert torch.equal(o, torch.zeros_like(o)) and torch.equal(lse, torch.full_like(lse, -math.inf))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("part,q0", [("v", 24.0), ("k", 0.01), ("k", -0.01)])
+def test_an_infinity_of_an_8_bit_cache_counts_as_the_number_it_is_held_as(dtype, part, q0):
+    """448 2^120, of a value with weight e^-3 beside ones of weight 1, and of a key, which then has all of the weight or none."""
+    g = torch.Generator().manual_seed(22)
+    lens = [70, 200]
+    cache, table = filled(g, lens, 16, 1, 64, E4M3)
+    q = torch.zeros(2, 1, 4, 64)
+    q[..., 0] = q0
+    for b, n in enumerate(lens):
+        for pos in range(n):
+            at = _places(table, b, pos)
+            index(cache.k)[(*at, 0)] = torch.tensor(1.0 if pos != 37 else 0.0).to(E4M3).view(torch.uint8)
+            index(cache.k_scale)[at] = 127
+        if part == "v":
+            _infinite_row(cache.v, cache.v_scale, _places(table, b, 37), 5)
+        else:
+            _infinite_row(cache.k, cache.k_scale, _places(table, b, 37), 0)
+    q = q.to(dtype)
+    want, _ = aref.attention(q, cache, table, lens, 0.125)
+    o = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens))
+    ref.check("o", o, want, dtype, WORK[dtype])
