@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(32 * kWarps) any_read_kernel(HeadArgs a) {
 // (2 x 8192 tokens of 40 heads of 128, bf16: 60 us); what holds them is the instructions, about 240 for a group of 1 KB in
 // and out (2.3 per clock and SM, waiting for shared memory, reciprocal roots and one another), with what belongs to a slice
 // worked out once. The gradient (8191 tokens of 18 heads of 256: 49 us, 68 % of a copy) has 128 registers a thread,
-// so only 16 warps on an SM. 8-bit writes: 39 us for 32761 tokens of 16 rows of 128, 77 %.
+// so only 16 warps on an SM. 8-bit writes: 38 us for 32761 tokens of 16 rows of 128, 77 %.
 constexpr int kVecWarps = 8;
 constexpr int kVecThreads = 32 * kVecWarps;
 constexpr int kVecTokens = 32;  // of a block at a time, at most
@@ -895,7 +895,7 @@ unsigned any_blocks(int64_t items) {
 }
 
 // Whole vectors: the widths, all rows and all pointers allow 16 bytes at a time. (Norms of 2 x 8192 tokens, 40 heads of 128:
-// 59 us, and 438 a warp per row and channel by channel.)
+// 60 us, and 439 a warp per row and channel by channel; gradient of 8191 tokens 49 and 292, 8-bit writes 38 and 324.)
 bool vec_ok(const HeadArgs &a, bool f32, const void *const *ptrs, int n) {
     const int v = f32 ? 4 : 8;
     bool ok = a.D % 16 == 0 && a.R % 16 == 0 && a.q_stride % v == 0 && a.k_stride % v == 0 && a.v_stride % v == 0;
@@ -914,10 +914,11 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
     VecPlan p;
     p.v.h = a;
     p.lpr = a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
-    // 8-bit writes of 32761 tokens 40 us with 8 tokens, 38 with 16, 37 with 32; norms alike from 9 to 16
+    // 8-bit writes with 8, 16 and 32 tokens: 20000 tokens of 8 heads 27, 27 and 31 us (the last blocks run alone), 32761 40, 39 and 38,
+    // 65536 76, 69 and 70, 32761 of 2 heads 33, 29 and 27. Norms alike from 9 to 16.
     p.v.tokens = a.q != nullptr ? 12 : 16;
-    p.v.each = 4;  // gradient: groups of a slice (8191 tokens of 18 heads of 256: 49 us with two or four, 62 with eight, which 18 heads do not fill)
-    p.u = f32 ? 1 : 2;  // groups of a warp on their way: 16 registers each (bf16 norms as above 59 us with two, 62 with one; 8-bit writes 39, 42)
+    p.v.each = 4;  // gradient: groups of a slice (8191 tokens of 18 heads of 256: 49 us with two or four, 63 with eight, which 18 heads do not fill)
+    p.u = f32 ? 1 : 2;  // groups of a warp on their way: 16 registers each (bf16 norms of 2 x 8192 tokens 60 us with two, 62 with one; 8-bit writes 38, 42)
     // few tokens: a warp for each group of heads, and as few tokens in a block as keep its warps busy (8 single tokens into the
     // cache: 4.4 us, and 11 with twelve tokens in a block)
     const int64_t sms = sm_count();
@@ -928,9 +929,10 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
         if (a.seqs.rows * groups < 4 * sms * kVecWarps * 4) p.v.each = p.u = 1;
     }
     p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
-    // With norms and angles, blocks that stay and go through shares of all tokens (norms as above 59 us, and 64 with a block for
-    // each 12 tokens); rows that are only written, 16 tokens a block (39 us, and 41 with blocks that stay).
-    p.blocks = (unsigned)(a.q == nullptr || p.v.batches < 3 * sms ? p.v.batches : 3 * sms);
+    // With norms and angles, blocks that stay and go through shares of all tokens (bf16 norms of 2 x 4096 tokens of 40 heads of 128 33 us, and 35
+    // with a block for each 12 tokens; 2 x 8192 60 both ways; 2 x 30000 of 10 heads 88 and 90), but not in fp32 (2 x 8192 tokens 121 us,
+    // and 111 with a block for each 12); rows that are only written, 16 tokens a block (38 us, and 40 with blocks that stay).
+    p.blocks = (unsigned)(a.q == nullptr || f32 || p.v.batches < 3 * sms ? p.v.batches : 3 * sms);
     p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 32 * p.lpr) * sizeof(float);  // at most 26 KB
     return p;
 }
