@@ -5,21 +5,28 @@
 // short side N: S^T = K Q^T (16 keys x rows), O^T += V^T P^T (channels x rows). K is read from the ring as it lies, V
 // through the transposing load; the accumulator of S^T becomes the operand P^T by a transpose of 8 x 8 blocks
 // in registers. A row's statistics are shared by the 8 lanes that hold its keys, but the sum is kept per
-// lane and the reference m of the exponentials moves only when some score passes it by 2^8 or more, so that
+// lane and the reference m of the exponentials moves only when a score of the row is more than 8 (base 2) above it, so that
 // most steps exchange nothing between lanes.
 //
+// Probabilities are rounded to bf16, the one type that a product with bf16 values takes; the sum l is not. Against 64 bits the
+// result for 131071 tokens is off by 2.4e-3 of its norm, with fp32 probabilities by 1.7e-3, which is the rounding of the result.
+// A second product with what that rounding left would take it back at as many matrix instructions again.
+//
 // What bounds it is the stream of keys and values where they are many: 64 sequences of up to 16384 tokens, 8 key heads of 128 in
-// 8 bits, 186 us, 95 % of what a copy moves (three blocks of four warps on an SM, each warp 24 KB ahead; tensor pipes 18 % busy,
-// so larger matrix instructions would change nothing); one sequence of 131071 in bf16 91 us, 87 % with the start and
-// the join. With many rows it is the instructions, about 650 for a warp's 32 keys and 8 rows in 8 bits: 4 new tokens
-// of 8 heads a key head, 16 sequences of up to 8192: 42 us, 23 %.
+// 8 bits, 187 us, 95 % of what a copy moves (three blocks of four warps on an SM, each warp 24 KB ahead; tensor pipes 18 % busy,
+// so larger matrix instructions would change nothing); one sequence of 131071 in bf16 92 us, 86 % with the start and
+// the join. With many rows it is the instructions, 680 for a warp's 32 keys and 8 rows in 8 bits (all of a launch's over the
+// number of such units): 4 new tokens of 8 heads a key head, 16 sequences of up to 8192: 41 us, 24 %. 64 rows of 128 channels
+// have more live than the registers of three blocks hold (176 bytes spilled over 8 bits, 72 in bf16; elsewhere at most 32).
 //
 // 8-bit cache: e4m3 numbers are exact in fp16, so K and V are widened in registers and the products run in fp16
 // (one conversion per two numbers; widening to bf16 takes four to five instructions). Q goes to fp16 times a power of two per
 // row that puts its largest entry at 2^14: entries down to 2^-28 of it stay exact. The power of two of a key multiplies
 // its scores, that of a value its probability: P' = 2^(score + sv - M) with a reference M of its own, between 2^-24 and
 // 2^14 in fp16 (11 bits), while the sum l keeps the plain 2^(score - m). Both references are watched by one
-// comparison per score, with min(m + 2^8, M's border - the largest sv so far).
+// comparison per score, with min(m + 8, M + 14 - the largest sv so far). That sv may belong to a key of no weight, and then
+// each unit takes the longer way without a move (a value 2^6 to 2^14 above the others and of no weight in every 64 keys: 64
+// sequences of up to 16384 tokens 177 us instead of 173, the new tokens above 45 instead of 41).
 #include <type_traits>
 
 #include "attn_common.cuh"

@@ -931,7 +931,7 @@ VecPlan vec_plan(const HeadArgs &a, bool f32) {
     p.v.batches = (int)ceil_div(a.seqs.rows, p.v.tokens);
     // With norms and angles, blocks that stay and go through shares of all tokens (bf16 norms of 2 x 4096 tokens of 40 heads of 128 33 us, and 35
     // with a block for each 12 tokens; 2 x 8192 60 both ways; 2 x 30000 of 10 heads 88 and 90), but not in fp32 (2 x 8192 tokens 121 us,
-    // and 111 with a block for each 12); rows that are only written, 16 tokens a block (38 us, and 40 with blocks that stay).
+    // and 111 with a block for each 12; 2 x 30000 of 10 heads 102 and 104); rows that are only written, 16 tokens a block (38 us, and 40 with blocks that stay).
     p.blocks = (unsigned)(a.q == nullptr || f32 || p.v.batches < 3 * sms ? p.v.batches : 3 * sms);
     p.smem = ((size_t)p.v.tokens * (a.R / 2) * 3 + 32 * p.lpr) * sizeof(float);  // at most 26 KB
     return p;
