@@ -17,16 +17,17 @@
 // so larger matrix instructions would change nothing); one sequence of 131071 in bf16 92 us, 86 % with the start and
 // the join. With many rows it is the instructions, 680 for a warp's 32 keys and 8 rows in 8 bits (all of a launch's over the
 // number of such units): 4 new tokens of 8 heads a key head, 16 sequences of up to 8192: 41 us, 24 %. 64 rows of 128 channels
-// have more live than the registers of three blocks hold (176 bytes spilled over 8 bits, 72 in bf16; elsewhere at most 32).
+// have more live than the registers of three blocks hold (172 bytes spilled over 8 bits, 72 in bf16; elsewhere at most 68).
 //
 // 8-bit cache: e4m3 numbers are exact in fp16, so K and V are widened in registers and the products run in fp16
 // (one conversion per two numbers; widening to bf16 takes four to five instructions). Q goes to fp16 times a power of two per
 // row that puts its largest entry at 2^14: entries down to 2^-28 of it stay exact. The power of two of a key multiplies
 // its scores, that of a value its probability: P' = 2^(score + sv - M) with a reference M of its own, between 2^-24 and
-// 2^14 in fp16 (11 bits), while the sum l keeps the plain 2^(score - m). Both references are watched by one
+// 2^14 in fp16 (11 bits), while the sum l keeps the plain 2^(score - m). M is kept as M - m: beside a large score a value's
+// power of two would be lost. Both references are watched by one
 // comparison per score, with min(m + 8, M + 14 - the largest sv so far). That sv may belong to a key of no weight, and then
 // each unit takes the longer way without a move (a value 2^6 to 2^14 above the others and of no weight in every 64 keys: 64
-// sequences of up to 16384 tokens 177 us instead of 173, the new tokens above 45 instead of 41).
+// sequences of up to 16384 tokens 178 us instead of 173, the new tokens above 45 to 46 instead of 41).
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -38,6 +39,7 @@ namespace {
 
 constexpr float kGrow = 8.f;  // a score may pass its reference by so much before it moves: exponentials up to 2^8
 constexpr float kMost = 14.f;  // 8-bit: P' up to 2^14, within fp16
+constexpr float kWatch = kMost - 0.01f;  // looked after from here on, so that no rounding hides what passes kMost
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
     unsigned char *own = mem + worker * S::kBytes;
     S st(a, own, mem + M::kSc + worker * S::kScaleBytes, lane, warp, walk);
     uint2 *qmem = reinterpret_cast<uint2 *>(mem + M::kQ + warp * M::kQBytes) + lane;  // [NT][kSteps], 32 apart
-    // of each row: what its scores are multiplied with, the references m and M, the factor of the last move
+    // of each row: what its scores are multiplied with, the reference m, M - m, the factor of the last move
     float *stats = reinterpret_cast<float *>(mem + M::kStat) + warp * M::kStats;
     float *row_m = stats + kRows, *row_mv = row_m + kRows, *row_back = row_mv + kRows;
     const int D = a.cache.D;
@@ -218,21 +220,30 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[k][n][i] = 0.f;
         }
-        float my_m = 0.f, my_mv = 0.f;
-        // the borders of all rows from the references, after those or sv_top have moved
+        float my_m = 0.f, my_mv = 0.f;  // of my_row: m, and 8-bit M - m
+        // -m of all rows, after it has moved
+        auto references = [&] {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 m2 = *reinterpret_cast<const float2 *>(row_m + 8 * n + 2 * c);
+                ref[n] = pk(m2.x == -INFINITY ? 0.f : -m2.x, m2.y == -INFINITY ? 0.f : -m2.y);
+            }
+        };
+        // the borders of all rows, after the references or sv_top have moved; rounded down, so that a score that has to move a
+        // reference is seen whatever its size
         auto borders = [&](bool moved) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float2 m2 = *reinterpret_cast<const float2 *>(row_m + 8 * n + 2 * c);
-                if (moved) ref[n] = pk(m2.x == -INFINITY ? 0.f : -m2.x, m2.y == -INFINITY ? 0.f : -m2.y);
-                lim[n][0] = m2.x + kGrow;
-                lim[n][1] = m2.y + kGrow;
+                float over[2] = {kGrow, kGrow};
                 if constexpr (M::kScaled) {
                     const float2 v2 = *reinterpret_cast<const float2 *>(row_mv + 8 * n + 2 * c);
-                    lim[n][0] = fminf(lim[n][0], v2.x + kMost - sv_top);
-                    lim[n][1] = fminf(lim[n][1], v2.y + kMost - sv_top);
-                    if (moved) turn[n] = pk(m2.x == -INFINITY ? 1.f : tc5::ex2(m2.x - v2.x), m2.y == -INFINITY ? 1.f : tc5::ex2(m2.y - v2.y));
+                    over[0] = fminf(kGrow, v2.x + kWatch - sv_top);
+                    over[1] = fminf(kGrow, v2.y + kWatch - sv_top);
+                    if (moved) turn[n] = pk(tc5::ex2(-v2.x), tc5::ex2(-v2.y));
                 }
+                lim[n][0] = __fadd_rd(m2.x, over[0]);
+                lim[n][1] = __fadd_rd(m2.y, over[1]);
             }
         };
         if (lane < kRows) {
@@ -356,40 +367,53 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                         if constexpr (kJoint == 2) v[i] = fmaxf(v[i], fmaxf(x[1][i / 2][i & 1], x[1][i / 2][(i & 1) + 2]));
                     }
                     const float top = spread_max(v, lane);
-                    float back = 1.f, back_l = 1.f;
+                    float back = 1.f;
                     const bool first = nothing;
-                    if (top > (first ? -INFINITY : my_m + kGrow)) {
-                        back_l = first ? 0.f : tc5::ex2(my_m - top);
+                    if (first ? top > -INFINITY : top - my_m > kGrow) {
+                        back = first ? 0.f : tc5::ex2(my_m - top);
+                        my_mv -= first ? 0.f : top - my_m;
                         my_m = top;
                         nothing = false;
                     }
-                    back = back_l;
+                    row_m[my_row] = nothing ? -INFINITY : my_m;
+                    (M::kScaled ? stats : row_back)[my_row] = back;
+                    __syncwarp();
+                    references();
                     if constexpr (M::kScaled) {
+                        // from the differences to m, as the scores may be so large that a value's power of two is lost beside them
                         float ev[kJoint][2];
 #pragma unroll
                         for (int h = 0; h < kJoint; ++h)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) ev[h][i] = (float)((int)(__float_as_uint(fv[h][i]) >> 23) - 127);
 #pragma unroll
-                        for (int i = 0; i < 2 * NT; ++i) {
-                            v[i] = fmaxf(x[0][i / 2][i & 1] + ev[0][0], x[0][i / 2][(i & 1) + 2] + ev[0][1]);
-                            if constexpr (kJoint == 2) v[i] = fmaxf(v[i], fmaxf(x[1][i / 2][i & 1] + ev[1][0], x[1][i / 2][(i & 1) + 2] + ev[1][1]));
+                        for (int n = 0; n < NT; ++n) {
+                            float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int h = 0; h < kJoint; ++h)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    float lo, hi;
+                                    upk(add2(pk(x[h][n][2 * i], x[h][n][2 * i + 1]), ref[n]), lo, hi);
+                                    y[0] = fmaxf(y[0], lo + ev[h][i]);
+                                    y[1] = fmaxf(y[1], hi + ev[h][i]);
+                                }
+                            v[2 * n] = y[0];
+                            v[2 * n + 1] = y[1];
                         }
                         // the largest P' at 2^6, so that none passes 2^kMost soon; rows of zeros (sv = -126) alone leave it lower, or
                         // 2^(score - M), with a score of up to m + 8, would pass what fp32 holds
                         const float top_v = spread_max(v, lane);
                         back = 1.f;
                         if (!nothing) {
-                            const float to = fmaxf(first || top_v > my_mv + kMost ? top_v - 6.f : my_mv, my_m - 119.f);
+                            const float to = fmaxf(first || top_v > my_mv + kMost ? top_v - 6.f : my_mv, -119.f);
                             back = first ? 0.f : tc5::ex2(my_mv - to);
                             my_mv = to;
                         }
                         row_mv[my_row] = my_mv;
-                        stats[my_row] = back_l;
+                        row_back[my_row] = back;
+                        __syncwarp();
                     }
-                    row_m[my_row] = nothing ? -INFINITY : my_m;
-                    row_back[my_row] = back;
-                    __syncwarp();
                     borders(true);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -525,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, Mma<C, DP, NT, SLOTS, TEAM>::kBlocks
                 const int r = 8 * n + 2 * c + j;
                 if (r >= p.rows) continue;
                 const float top = row_m[r];
-                float f = M::kScaled && top > -INFINITY ? tc5::ex2(row_mv[r] - top) : 1.f;
+                float f = M::kScaled ? tc5::ex2(row_mv[r]) : 1.f;
                 const bool empty = whole && sum[j] == 0.f;  // zeros, whatever the values are
                 if (whole) f = f / sum[j];
                 const int64_t row = out_row(a, p, r);

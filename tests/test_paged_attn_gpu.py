@@ -548,3 +548,27 @@ def test_an_infinity_of_an_8_bit_cache_counts_as_the_number_it_is_held_as(dtype,
     want, _ = aref.attention(q, cache, table, lens, 0.125)
     o = paged_attn_step(q.to(dev), to_gpu(cache), table.to(dev), _int32(lens))
     ref.check("o", o, want, dtype, WORK[dtype])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("kbyte", [128, 130, 132, 134, 136, 138, 146, 200, 240])
+@pytest.mark.parametrize("vbyte", [86, 106, 113, 121, 145])
+def test_large_scores_over_an_8_bit_cache(dtype, sign, kbyte, vbyte):
+    """Scores of 2^13 to 2^33, of which one key's is far above the others' (they differ by parts of themselves): the result is
+    that key's value, however large or small the values are."""
+    g = torch.Generator().manual_seed(23)
+    lens = [70, 300]
+    cache, table = filled(g, lens, 16, 1, 64, E4M3)
+    q = torch.zeros(2, 2, 4, 64)
+    q[..., 0] = sign * 2.0 ** 13 / 2.0 ** max(0, kbyte - 140)
+    for b, n in enumerate(lens):
+        for pos in range(n):
+            at = _places(table, b, pos)
+            x = (448.0 if pos == 37 else 20.0 + pos % 17) if sign > 0 else (20.0 if pos == 37 else 400.0 + 10 * (pos % 3))
+            index(cache.k)[(*at, 0)] = torch.tensor(x).to(E4M3).view(torch.uint8)
+            index(cache.k_scale)[at] = kbyte
+            index(cache.v_scale)[at] = vbyte
+    want = aref.attention(q, cache, table, lens, 0.125)[0]
+    o = paged_attn_step(q.to(dtype).to(dev), to_gpu(cache), table.to(dev), _int32(lens))
+    ref.check("o", o, want, dtype, WORK[dtype])
